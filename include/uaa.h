@@ -306,6 +306,108 @@ int uaa_ulysses_attn_bwd(const void* q, const void* k, const void* v, const void
 int uaa_assemble_key_mask(const uint8_t* gathered, uint8_t* mask, int P, const int* shard_lens,
                           int cap, int B, uaa_stream_t stream);
 
+/* Element types of the calls that take more than bf16. */
+enum { UAA_BF16 = 0, UAA_FP16 = 1, UAA_FP32 = 2 };
+
+/* ------------------------------------------------------------------ rotary positions
+ * Pair i of every head is turned by 2 pi * position * turns_i: columns i and
+ * i + rot/2 (UAA_ROTARY_HALF) or 2i and 2i + 1 (UAA_ROTARY_INTERLEAVED); columns
+ * rot..D-1 are copied.  A token has one position per axis (frame, row and column of
+ * a video token; a text token has one axis), and the plan says which axis a pair
+ * follows. */
+enum { UAA_ROTARY_HALF = 0, UAA_ROTARY_INTERLEAVED = 1 };
+enum {
+  UAA_ROTARY_NONE = 0,
+  UAA_ROTARY_LINEAR = 1,  /* every frequency / factor */
+  UAA_ROTARY_NTK = 2,     /* base * factor^(w / (w - 2)) for an axis of w columns */
+  UAA_ROTARY_PARTS = 3    /* pairs that turn more than beta times over `original` positions stay, those
+                             below alpha are divided by factor, a linear blend between; the result is
+                             multiplied by 0.1 ln(factor) + 1 */
+};
+#define UAA_ROTARY_MAX_PAIRS 128
+#define UAA_ROTARY_MAX_AXES 4
+
+/* A host structure: the frequencies, as 64-bit fixed-point fractions of a turn per position. */
+typedef struct {
+  int rot;    /* rotated columns of a head */
+  int layout;
+  int axes;
+  float magnitude;
+  uint64_t turns[UAA_ROTARY_MAX_PAIRS];
+  uint8_t axis[UAA_ROTARY_MAX_PAIRS];
+} uaa_rotary_plan;
+
+/* Fills *plan (host memory, no GPU needed).  widths[x]: rotated columns that follow axis x (even;
+ * 2 * UAA_ROTARY_MAX_PAIRS in all at most); pair j of an axis of w columns turns by base^(-2j/w)
+ * radians per position before scaling.  factor is read unless scaling is UAA_ROTARY_NONE;
+ * original, alpha and beta only for UAA_ROTARY_PARTS.  Returns UAA_OK or UAA_ERR_INVALID_ARG. */
+int uaa_rotary_plan_init(uaa_rotary_plan* plan, int layout, int axes, const int* widths, double base,
+                         int scaling, double factor, double original, double alpha, double beta);
+
+/* A (B, S, H, D) operand and its result: device pointers and strides in elements; the D columns of a
+ * head are contiguous.  y may be x (with x's strides); otherwise the two must not overlap. */
+typedef struct {
+  const void* x;
+  void* y;
+  long long x_batch, x_token, x_head, y_batch, y_token, y_head;
+  int H;
+} uaa_rotary_tensor;
+
+/* Rotates q and, if it is not NULL, k (which may have another head count) in one launch.
+ *   plan      : host, read during the call
+ *   positions : device, int32 (pos64 = 0) or int64, axis x of token (b, s) at
+ *               b * pos_batch_stride + s * pos_token_stride + x; NULL: position start + s on every axis
+ *   dtype     : UAA_BF16, UAA_FP16 or UAA_FP32; computed in 32 bits, rounded once
+ *   inverse   : nonzero applies the transposed map: the gradients of q and k from those of the results
+ * Returns UAA_OK or a negative uaa_status. */
+int uaa_rotary(const uaa_rotary_plan* plan, const uaa_rotary_tensor* q, const uaa_rotary_tensor* k,
+               const void* positions, int pos64, long long pos_batch_stride, long long pos_token_stride,
+               long long start, int B, int S, int D, int dtype, int inverse, uaa_stream_t stream);
+
+/* ------------------------------------------------------------------ activation checkpoints in 8 bits
+ * Each row of D values becomes D signed codes and one fp32 step: step = max|x| / 127, code =
+ * round(127 x / max|x|), ties to even; the value taken back is code * step in the tensor's type.  A row
+ * with an infinity or a NaN comes back as NaN; a row whose largest magnitude is below 2^-119 comes back
+ * as zeros.  Up to UAA_ACT8_MAX_TENSORS tensors per launch.
+ *   x, y  : host arrays of n device pointers, contiguous (rows[i], D), 16-byte aligned
+ *   codes : host array of n device pointers to int8 (rows[i], D), 16-byte aligned
+ *   steps : host array of n device pointers to fp32 (rows[i])
+ *   D     : a multiple of 16 up to 512
+ * Returns UAA_OK or a negative uaa_status. */
+#define UAA_ACT8_MAX_TENSORS 8
+int uaa_act8_pack(int n, const void* const* x, int8_t* const* codes, float* const* steps, const long long* rows,
+                  int D, int dtype, uaa_stream_t stream);
+int uaa_act8_unpack(int n, const int8_t* const* codes, const float* const* steps, void* const* y,
+                    const long long* rows, int D, int dtype, uaa_stream_t stream);
+
+/* ------------------------------------------------------------------ differential attention
+ * Each head has two softmax maps over the same keys, one from the first D/2 columns of q and k and one from
+ * the last D/2, and the values of all D columns are read by their difference:
+ *   A_m = softmax(scale * q_m k_m^T + bias),  out = (A_1 - lambda_h A_2) v,  out2 = A_2 v.
+ *   q, out, out2 : device, bf16 (B, Sq, H, D); k, v: bf16 (B, Sk, H, D); D = 64 or 128 (maps of 32 or 64)
+ *   lambda       : device, (H), bf16 or fp32 (lambda_dtype)
+ *   key_mask     : device, uint8 (B, Sk) or NULL, nonzero = attend; a row without an attended key gets
+ *                  out = out2 = 0, lse = -inf and no gradient
+ *   out2         : what the backward needs next to out; NULL when no gradient is wanted
+ *   lse          : device, fp32 (B, H, 2, Sq)
+ * scale is usually 1/sqrt(D/2).  Returns UAA_OK or a negative uaa_status. */
+int uaa_diff_attn_fwd(const void* q, const void* k, const void* v, const void* lambda, int lambda_dtype,
+                      const uint8_t* key_mask, void* out, void* out2, float* lse, int B, int Sq, int Sk, int H, int D,
+                      float scale, uaa_stream_t stream);
+
+/* Bytes of device workspace that uaa_diff_attn_bwd needs: per query row and map the row dot of dout with the
+ * map's output and -LSE*log2(e), rows padded to 128.  Returns 0 for invalid sizes. */
+size_t uaa_diff_attn_bwd_workspace_bytes(int B, int Sq, int H, int D);
+
+/* Gradients of uaa_diff_attn_fwd; deterministic (no atomics).
+ *   dq, dk, dv : bf16, written, in the layouts of q, k, v; dlambda: (H) in lambda's type
+ *   workspace  : device, at least uaa_diff_attn_bwd_workspace_bytes() bytes, 256-byte aligned
+ * Sq and Sk must both be positive (or B*H = 0).  Returns UAA_OK or a negative uaa_status. */
+int uaa_diff_attn_bwd(const void* q, const void* k, const void* v, const void* lambda, int lambda_dtype,
+                      const void* out, const void* out2, const void* dout, const float* lse, const uint8_t* key_mask,
+                      void* dq, void* dk, void* dv, void* dlambda, int B, int Sq, int Sk, int H, int D, float scale,
+                      void* workspace, size_t workspace_bytes, uaa_stream_t stream);
+
 /* Synchronises `stream`, then reads and clears the library's device status
  * words.  Returns UAA_OK, UAA_ERR_TIMEOUT (a bounded device wait ran out in
  * some kernel since the last check), UAA_ERR_DEBUG_CHECK (debug builds: a

@@ -1,0 +1,137 @@
+"""float64 definitions of the operators around attention: rotary positions, 8-bit activation
+checkpoints and differential attention, with the error each result may carry.
+
+Plain NumPy, no code shared with the library.  The error bounds count the roundings that the
+kernels make: a value rounded to bf16 is off by at most 2^-8 of itself (``BF16``), the exponentials
+on the FMA pipe by 8e-5 (``EXP``); 32-bit sums and products are covered by ``F32`` times the sum of
+the terms' magnitudes.
+"""
+import numpy as np
+
+BF16 = 2.0 ** -8
+EXP = 8e-5
+F32 = 2.0 ** -20
+
+
+# --------------------------------------------------------------------------- rotary positions
+def rotary_rates(widths, base=10000.0, scaling="none", factor=1.0, original=8192, alpha=1.0, beta=32.0):
+    """Radians per position of every pair, and the axis it follows."""
+    rates, axis = [], []
+    for a, w in enumerate(widths):
+        for j in range(w // 2):
+            b = base * factor ** (w / (w - 2.0)) if scaling == "ntk" and w > 2 else base
+            f = b ** (-2.0 * j / w)
+            if scaling == "linear":
+                f /= factor
+            elif scaling == "parts":
+                keep = min(1.0, max(0.0, (original * f / (2 * np.pi) - alpha) / (beta - alpha)))
+                f = keep * f + (1 - keep) * f / factor
+            rates.append(f)
+            axis.append(a)
+    return np.array(rates), np.array(axis, dtype=int)
+
+
+def rotary(x, positions, rates, axis, layout, magnitude=1.0, inverse=False):
+    """x (B, S, H, D), positions (B, S, axes): returns the rotated x and the magnitude of each result's terms."""
+    R = 2 * len(rates)
+    angle = (positions[..., axis].astype(np.float64) * rates)[:, :, None, :]
+    c, s = magnitude * np.cos(angle), magnitude * np.sin(angle) * (-1.0 if inverse else 1.0)
+    lo, hi = (np.arange(R // 2), np.arange(R // 2) + R // 2) if layout == "half" else (np.arange(0, R, 2),
+                                                                                      np.arange(1, R, 2))
+    y, size = x.astype(np.float64).copy(), np.zeros(x.shape)
+    y[..., lo], y[..., hi] = x[..., lo] * c - x[..., hi] * s, x[..., lo] * s + x[..., hi] * c
+    size[..., lo] = size[..., hi] = magnitude * (np.abs(x[..., lo]) + np.abs(x[..., hi]))
+    return y, size
+
+
+# --------------------------------------------------------------------------- 8-bit checkpoints
+def act8_codes(x):
+    """Codes (whole numbers) of finite rows x (..., D), ties to even."""
+    x = x.astype(np.float64)
+    top = np.abs(x).max(-1, keepdims=True)
+    codes = np.rint(127.0 * x / np.where(top > 0, top, 1.0))
+    return np.where(top < 2.0 ** -119, 0.0, codes) + 0.0, top[..., 0]  # a code is an integer: no -0
+
+
+# --------------------------------------------------------------------------- differential attention
+def _maps(q, k, mask, scale):
+    """Softmax maps and LSE of one batch element: q (Sq, H, D), k (Sk, H, D) -> (2, H, Sq, Sk), (2, H, Sq)."""
+    w = q.shape[-1] // 2
+    a, lse = [], []
+    for m in range(2):
+        s = scale * np.einsum("ihd,jhd->hij", q[..., m * w:m * w + w], k[..., m * w:m * w + w])
+        if mask is not None:
+            s = np.where(mask[None, None, :], s, -np.inf)
+        top = s.max(-1, keepdims=True)
+        e = np.exp(s - np.where(np.isinf(top), 0.0, top))
+        total = e.sum(-1, keepdims=True)
+        a.append(e / np.where(total > 0, total, 1.0))
+        with np.errstate(divide="ignore"):
+            lse.append((np.where(np.isinf(top), 0.0, top) + np.log(total))[..., 0])
+    return np.stack(a), np.stack(lse)
+
+
+def diff_attn(q, k, v, lam, mask=None, scale=None, dout=None):
+    """Outputs and, with ``dout``, gradients; each as ``name: (value, error bound)``."""
+    B, Sq, H, D = q.shape
+    Sk, w = k.shape[1], D // 2
+    scale = w ** -0.5 if scale is None else scale
+    P = BF16 + EXP  # a probability that a matrix product reads
+    names = ["out", "out2", "lse"] + ([] if dout is None else ["dq", "dk", "dv", "dlam"])
+    shapes = {"out": q.shape, "out2": q.shape, "lse": (B, H, 2, Sq), "dq": q.shape, "dk": k.shape, "dv": k.shape,
+              "dlam": (H,)}
+    res = {n: (np.zeros(shapes[n]), np.zeros(shapes[n])) for n in names}
+
+    def put(n, at, value, bound):
+        res[n][0][at], res[n][1][at] = value, bound
+
+    L = lam[:, None, None]
+    for b in range(B):
+        a, lse = _maps(q[b], k[b], None if mask is None else mask[b], scale)
+        vb = v[b]
+        both = a[0] + np.abs(L) * a[1]
+        o = np.einsum("hij,jhd->ihd", a[0] - L * a[1], vb)
+        o2 = np.einsum("hij,jhd->ihd", a[1], vb)
+        size = np.einsum("hij,jhd->ihd", both, np.abs(vb))
+        size2 = np.einsum("hij,jhd->ihd", a[1], np.abs(vb))
+        eo, eo2 = (P + F32) * size + BF16 * np.abs(o), (P + F32) * size2 + BF16 * np.abs(o2)
+        put("out", b, o, eo)
+        put("out2", b, o2, eo2)
+        # 32-bit scores: their terms' magnitudes, and the exponentials' own error
+        es = F32 * scale * np.stack([np.einsum("ihd,jhd->hij", np.abs(q[b][..., m * w:m * w + w]),
+                                               np.abs(k[b][..., m * w:m * w + w])).max(-1) for m in range(2)])
+        put("lse", b, np.moveaxis(lse, 0, 1), np.moveaxis(es + EXP + F32 * np.where(np.isinf(lse), 0, np.abs(lse)),
+                                                          0, 1))
+        if dout is None:
+            continue
+        g = dout[b]
+        da = np.einsum("ihd,jhd->hij", g, vb)
+        eda = F32 * np.einsum("ihd,jhd->hij", np.abs(g), np.abs(vb))
+        rows = np.einsum("mhij,hij->mhi", a, da)
+        erow2 = np.einsum("ihd,ihd->hi", np.abs(g), eo2) + F32 * np.einsum("ihd,ihd->hi", np.abs(g), np.abs(o2))
+        erow1 = (np.einsum("ihd,ihd->hi", np.abs(g), eo) + F32 * np.einsum("ihd,ihd->hi", np.abs(g), np.abs(o))
+                 + np.abs(lam)[:, None] * erow2)
+        weight = np.stack([np.ones_like(L), -L])
+        ds = weight * a * (da - rows[..., None])
+        # an entry of dS: its probability, its rounding to bf16, and the row dots' error
+        eds = (np.abs(ds) * (P + EXP + 2 * es[..., None] + F32)
+               + np.abs(weight) * a * (eda + np.stack([erow1, erow2])[..., None]))
+        pv = a[0] - L * a[1]
+        epv = BF16 * np.abs(pv) + both * (EXP + F32 + es.max(0)[..., None])
+        dv = np.einsum("hij,ihd->jhd", pv, g)
+        edv = np.einsum("hij,ihd->jhd", epv + F32 * np.abs(pv), np.abs(g))
+        put("dv", b, dv, edv + BF16 * np.abs(dv))
+        for m in range(2):
+            c = slice(m * w, m * w + w)
+            e = eds[m] + F32 * np.abs(ds[m])
+            dq = scale * np.einsum("hij,jhd->ihd", ds[m], k[b][..., c])
+            dk = scale * np.einsum("hij,ihd->jhd", ds[m], q[b][..., c])
+            put("dq", (b, slice(None), slice(None), c), dq,
+                scale * np.einsum("hij,jhd->ihd", e, np.abs(k[b][..., c])) + BF16 * np.abs(dq))
+            put("dk", (b, slice(None), slice(None), c), dk,
+                scale * np.einsum("hij,ihd->jhd", e, np.abs(q[b][..., c])) + BF16 * np.abs(dk))
+        res["dlam"][0][:] -= rows[1].sum(-1)
+        res["dlam"][1][:] += erow2.sum(-1) + F32 * np.abs(rows[1]).sum(-1)
+    if dout is not None:
+        res["dlam"][1][:] += BF16 * np.abs(res["dlam"][0])  # lambda in bf16
+    return res

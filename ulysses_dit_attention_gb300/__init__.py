@@ -28,6 +28,8 @@ __all__ = [
     "assemble_key_mask", "check_device_status", "watchdog_selftest", "set_wait_timeout_ms", "debug_drop_load",
     "set_bwd_profile_events", "Attention", "attn_fwd_groups", "attn_bwd_groups",
     "attention", "UlyssesAttention", "ulysses_attention", "STATUS", "debug_build", "debug_exp2_fma2",
+    "RotaryPlan", "rotary_fwd", "rotary_bwd", "Rotary", "rotary", "shard_positions", "Act8", "act8_pack", "act8_unpack",
+    "diff_attn_fwd", "diff_attn_bwd", "diff_attn_bwd_workspace_bytes", "DiffAttention", "diff_attention",
 ]
 
 STATUS = {0: "UAA_OK", -1: "UAA_ERR_INVALID_ARG", -2: "UAA_ERR_UNSUPPORTED", -3: "UAA_ERR_PER_HEAD_MASK",
@@ -45,7 +47,30 @@ _lib_lock = threading.Lock()
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_longlong
+
+
+class _RotaryPlan(ctypes.Structure):  # uaa_rotary_plan
+    _fields_ = [("rot", _I), ("layout", _I), ("axes", _I), ("magnitude", ctypes.c_float),
+                ("turns", ctypes.c_uint64 * 128), ("axis", ctypes.c_uint8 * 128)]
+
+
+class _RotaryTensor(ctypes.Structure):  # uaa_rotary_tensor
+    _fields_ = [("x", _P), ("y", _P), ("x_batch", _L), ("x_token", _L), ("x_head", _L), ("y_batch", _L),
+                ("y_token", _L), ("y_head", _L), ("H", _I)]
+
+
 _SIGS = {
+    "uaa_rotary_plan_init": (_I, [ctypes.POINTER(_RotaryPlan), _I, _I, _P, ctypes.c_double, _I, ctypes.c_double,
+                                  ctypes.c_double, ctypes.c_double, ctypes.c_double]),
+    "uaa_rotary": (_I, [ctypes.POINTER(_RotaryPlan), ctypes.POINTER(_RotaryTensor), ctypes.POINTER(_RotaryTensor), _P,
+                        _I, _L, _L, _L, _I, _I, _I, _I, _I, _P]),
+    "uaa_act8_pack": (_I, [_I, _P, _P, _P, _P, _I, _I, _P]),
+    "uaa_act8_unpack": (_I, [_I, _P, _P, _P, _P, _I, _I, _P]),
+    "uaa_diff_attn_fwd": (_I, [_P, _P, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, ctypes.c_float, _P]),
+    "uaa_diff_attn_bwd_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I]),
+    "uaa_diff_attn_bwd": (_I, [_P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I,
+                               ctypes.c_float, _P, ctypes.c_size_t, _P]),
     "uaa_attn_fwd": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, ctypes.c_float, _P]),
     "uaa_attn_fwd_cross": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, ctypes.c_float, _P]),
     "uaa_attn_bwd_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I]),
@@ -303,13 +328,36 @@ def attn_bwd_groups(q, k, v, out, dout, lse, key_mask=None, scale=None, dq=None,
     return dq, dk, dv
 
 
+def _save(ctx, saved, tensors, *others):
+    """Keeps ``tensors`` for the backward pass, as they are or (``saved="int8"``) as an 8-bit checkpoint."""
+    if saved not in (None, "int8"):
+        raise ValueError(f"saved must be None or 'int8', got {saved!r}")
+    ctx.packed = None
+    if saved == "int8" and any(ctx.needs_input_grad):
+        packed = act8_pack(tensors)
+        ctx.packed = packed._meta()
+        tensors = (packed.codes, packed.steps)
+    ctx.save_for_backward(*tensors, *others)
+
+
+def _saved(ctx, n):
+    """The ``n`` tensors that :func:`_save` kept, and the others."""
+    kept = ctx.saved_tensors
+    if ctx.packed is None:
+        return list(kept[:n]), kept[n:]
+    return act8_unpack(Act8(kept[0], kept[1], *ctx.packed)), kept[2:]
+
+
 class Attention(torch.autograd.Function):
-    """Autograd pairing of ``attn_fwd`` / ``attn_bwd``; ``lse`` is non-differentiable."""
+    """Autograd pairing of ``attn_fwd`` / ``attn_bwd``; ``lse`` is non-differentiable.
+
+    ``saved="int8"`` keeps Q, K, V and O for the backward pass as an 8-bit checkpoint
+    (:func:`act8_pack`): half the memory, gradients of the values that the codes stand for."""
 
     @staticmethod
-    def forward(ctx, q, k, v, key_mask=None, scale=None):
+    def forward(ctx, q, k, v, key_mask=None, scale=None, saved=None):
         out, lse = attn_fwd(q, k, v, key_mask, scale)
-        ctx.save_for_backward(q, k, v, out, lse)
+        _save(ctx, saved, (q, k, v, out), lse)
         ctx.key_mask = key_mask
         ctx.scale = scale
         ctx.mark_non_differentiable(lse)
@@ -317,13 +365,349 @@ class Attention(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dout, _dlse):
-        q, k, v, out, lse = ctx.saved_tensors
+        (q, k, v, out), (lse,) = _saved(ctx, 4)
         dq, dk, dv = attn_bwd(q, k, v, out, dout.contiguous(), lse, ctx.key_mask, ctx.scale)
-        return dq, dk, dv, None, None
+        return dq, dk, dv, None, None, None
 
 
-def attention(q, k, v, key_mask=None, scale=None):
-    return Attention.apply(q, k, v, key_mask, scale)
+def attention(q, k, v, key_mask=None, scale=None, saved=None):
+    return Attention.apply(q, k, v, key_mask, scale, saved)
+
+
+# --------------------------------------------------------------------------- shared checks of the calls below
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _same_device(*ts):
+    first = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("uaa kernels run on CUDA tensors only (no CPU fallback)")
+        if first is None:
+            first = t.device
+        elif t.device != first:
+            raise ValueError(f"tensors are on {first} and {t.device}")
+    return first
+
+
+def _call(device, name, *args):
+    """Calls the library on the tensors' device, on its current stream."""
+    if device.index == torch.cuda.current_device():
+        _check(getattr(lib(), name)(*args, _stream(device)))
+    else:
+        with torch.cuda.device(device):
+            _check(getattr(lib(), name)(*args, _stream(device)))
+
+
+def _result(name, t, shape, dtype, device):
+    """An output of the caller's, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)} on {device}")
+    return t
+
+
+# --------------------------------------------------------------------------- rotary positions
+class RotaryPlan:
+    """The frequencies of a rotary position code (``uaa_rotary_plan``), made once and kept by the model.
+
+    ``widths``: rotated columns of a head per position axis -- ``[128]`` for one axis, ``[44, 42, 42]``
+    for frame, row and column; the columns behind them are copied.  ``layout``: ``"half"`` pairs column
+    ``i`` with ``i + R/2`` (``R = sum(widths)``), ``"interleaved"`` pairs ``2i`` with ``2i + 1``.
+    ``scaling`` for contexts longer than the trained one: ``"linear"`` divides every frequency by
+    ``factor``; ``"ntk"`` raises the base; ``"parts"`` keeps pairs that turn more than ``beta`` times over
+    ``original`` positions, divides those below ``alpha`` by ``factor``, blends between, and multiplies
+    the result by ``0.1 ln(factor) + 1``.
+    """
+
+    LAYOUTS = {"half": 0, "interleaved": 1}
+    SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
+
+    def __init__(self, widths, layout="half", base=10000.0, scaling="none", factor=1.0, original=8192, alpha=1.0,
+                 beta=32.0):
+        widths = [int(w) for w in ([widths] if isinstance(widths, int) else widths)]
+        if layout not in self.LAYOUTS:
+            raise ValueError(f"layout must be one of {sorted(self.LAYOUTS)}, got {layout!r}")
+        if scaling not in self.SCALINGS:
+            raise ValueError(f"scaling must be one of {sorted(self.SCALINGS)}, got {scaling!r}")
+        self._c = _RotaryPlan()
+        _check(lib().uaa_rotary_plan_init(ctypes.byref(self._c), self.LAYOUTS[layout], len(widths),
+                                          (ctypes.c_int * len(widths))(*widths), float(base), self.SCALINGS[scaling],
+                                          float(factor), float(original), float(alpha), float(beta)))
+        self._ref = ctypes.byref(self._c)
+        self.axes, self.rot, self.magnitude = self._c.axes, self._c.rot, self._c.magnitude
+
+    @property
+    def turns(self):
+        """Turns per position of each pair, as numbers below 1."""
+        return [self._c.turns[i] / 2.0 ** 64 for i in range(self.rot // 2)]
+
+
+def shard_positions(shard_lens, cap, B, device, dtype=torch.int32):
+    """Positions ``(P*B, cap)`` of the rows of ``(P, B, cap, H, D)`` shards seen as ``(P*B, cap, H, D)``: row s of
+    shard p stands at ``sum(shard_lens[:p]) + s`` (padding rows run on)."""
+    starts = torch.tensor([sum(shard_lens[:p]) for p in range(len(shard_lens))], dtype=dtype)
+    at = starts[:, None, None] + torch.arange(cap, dtype=dtype)
+    return at.expand(len(shard_lens), B, cap).reshape(len(shard_lens) * B, cap).contiguous().to(device)
+
+
+def _rotary_tensor(name, x, y):
+    sx, sy = x.stride(), y.stride()
+    return _RotaryTensor(x.data_ptr(), y.data_ptr(), sx[0], sx[1], sx[2], sy[0], sy[1], sy[2], x.shape[2])
+
+
+def _rotate(q, k, plan, positions, start, inverse, out_q, out_k):
+    if not isinstance(plan, RotaryPlan):
+        raise TypeError("plan must be a RotaryPlan")
+    dev = _same_device(q, k, positions)
+    for n, t in (("q", q), ("k", k)):
+        if t is None:
+            continue
+        if t.dim() != 4:
+            raise ValueError(f"{n} must be (B, S, H, D), got {tuple(t.shape)}")
+        if t.dtype not in _DTYPES or t.dtype != q.dtype:
+            raise TypeError(f"{n} must be bfloat16, float16 or float32, q and k alike")
+        if t.shape[3] > 1 and t.stride(3) != 1:
+            raise ValueError(f"the columns of {n} must be contiguous")
+        if t.shape[:2] != q.shape[:2] or t.shape[3] != q.shape[3]:
+            raise ValueError(f"{n} shape {tuple(t.shape)} does not fit {tuple(q.shape)}")
+    B, S, _, D = q.shape
+    pos, wide, pb, ps = None, 0, 0, 0
+    if positions is not None:
+        tail = () if plan.axes == 1 else (plan.axes,)
+        if tuple(positions.shape) not in ((S,) + tail, (B, S) + tail):
+            raise ValueError(f"positions must be {(S,) + tail} or {(B, S) + tail}, got {tuple(positions.shape)}")
+        if positions.dtype not in (torch.int32, torch.int64):
+            raise TypeError("positions must be int32 or int64")
+        if tail and positions.stride(-1) != 1:
+            raise ValueError("the axes of positions must be contiguous")
+        if start:
+            raise ValueError("start goes with positions=None")
+        at = positions.stride()
+        pb, ps = (at[0], at[1]) if positions.dim() == 2 + len(tail) else (0, at[0])
+        pos, wide = positions.data_ptr(), int(positions.dtype == torch.int64)
+    outs = []
+    for n, t, y in (("out_q", q, out_q), ("out_k", k, out_k)):
+        if t is None:
+            outs.append(None)
+        elif y is None:
+            outs.append(torch.empty(t.shape, dtype=t.dtype, device=dev))
+        elif y.shape != t.shape or y.dtype != t.dtype or y.device != dev or (D > 1 and y.stride(3) != 1):
+            raise ValueError(f"{n} must be {t.dtype} {tuple(t.shape)} on {dev} with contiguous columns")
+        else:
+            outs.append(y)
+    tq = _rotary_tensor("q", q, outs[0])
+    tk = None if k is None else ctypes.byref(_rotary_tensor("k", k, outs[1]))
+    _call(dev, "uaa_rotary", plan._ref, ctypes.byref(tq), tk, pos, wide, pb, ps, int(start), B, S, D,
+          _DTYPES[q.dtype], inverse)
+    return outs[0], outs[1]
+
+
+def rotary_fwd(q, k, plan, positions=None, start=0, out_q=None, out_k=None):
+    """``uaa_rotary``: returns ``(q, k)`` rotated; ``k`` may be None or have another head count.
+
+    ``q``, ``k``: ``(B, S, H, D)`` bf16, fp16 or fp32 with contiguous columns -- slices of a packed
+    projection are fine.  ``positions``: int32 or int64 ``(S,)`` or ``(B, S)``, with a last dimension of
+    ``plan.axes`` when the plan has several; None stands for ``start, start + 1, ...``.  ``out_q=q`` rotates
+    in place.
+    """
+    return _rotate(q, k, plan, positions, start, 0, out_q, out_k)
+
+
+def rotary_bwd(dq, dk, plan, positions=None, start=0, out_q=None, out_k=None):
+    """The gradients of :func:`rotary_fwd`'s ``q`` and ``k`` from those of its results (the transposed map)."""
+    return _rotate(dq, dk, plan, positions, start, 1, out_q, out_k)
+
+
+class Rotary(torch.autograd.Function):
+    """Autograd pairing of ``rotary_fwd`` / ``rotary_bwd``; keeps nothing but the positions."""
+
+    @staticmethod
+    def forward(ctx, q, k, plan, positions=None, start=0):
+        ctx.plan, ctx.start = plan, start
+        ctx.save_for_backward(positions)
+        ctx.set_materialize_grads(False)
+        return _rotate(q, k, plan, positions, start, 0, None, None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq, dk):
+        (positions,) = ctx.saved_tensors
+        dq, dk = (t if t is None or t.stride(-1) == 1 else t.contiguous() for t in (dq, dk))
+        if dq is None and dk is None:
+            return None, None, None, None, None
+        if dq is None:
+            dk, dq = _rotate(dk, None, ctx.plan, positions, ctx.start, 1, None, None)
+        else:
+            dq, dk = _rotate(dq, dk, ctx.plan, positions, ctx.start, 1, None, None)
+        return dq, dk, None, None, None
+
+
+def rotary(q, k, plan, positions=None, start=0):
+    """Differentiable :func:`rotary_fwd`."""
+    return Rotary.apply(q, k, plan, positions, start)
+
+
+# --------------------------------------------------------------------------- activation checkpoints in 8 bits
+class Act8:
+    """Tensors kept in 8 bits: the codes and the steps of all of them, one behind the other."""
+
+    __slots__ = ("codes", "steps", "shapes", "dtype", "single")
+
+    def __init__(self, codes, steps, shapes, dtype, single):
+        self.codes, self.steps, self.shapes, self.dtype, self.single = codes, steps, shapes, dtype, single
+
+    def _meta(self):
+        return self.shapes, self.dtype, self.single
+
+    @property
+    def nbytes(self):
+        return self.codes.numel() + 4 * self.steps.numel()
+
+
+def _act8_call(name, tensors, codes, steps, swap):
+    n, D = len(tensors), tensors[0].shape[-1]
+    rows = [t.numel() // D for t in tensors]
+    base_c, base_s = codes.data_ptr(), steps.data_ptr()
+    at, pc, ps = 0, [], []
+    for r in rows:
+        pc.append(base_c + at * D)
+        ps.append(base_s + at * 4)
+        at += r
+    arr = ctypes.c_void_p * n
+    x = arr(*[t.data_ptr() for t in tensors])
+    pc, ps = arr(*pc), arr(*ps)
+    first = (pc, ps, x) if swap else (x, pc, ps)
+    _call(codes.device, name, n, *first, (_L * n)(*rows), D, _DTYPES[tensors[0].dtype])
+
+
+def act8_pack(x):
+    """``uaa_act8_pack``: puts a tensor, or up to eight of one type and last dimension, away in 8 bits.
+
+    Each row of the last dimension D (a multiple of 16 up to 512) becomes int8 codes and one fp32 step,
+    ``max|row| / 127``.  Returns an :class:`Act8` for :func:`act8_unpack`.
+    """
+    single = isinstance(x, torch.Tensor)
+    xs = [x] if single else list(x)
+    if not 1 <= len(xs) <= 8:
+        raise ValueError(f"one to eight tensors at a time, got {len(xs)}")
+    dev = _same_device(*xs)
+    for t in xs:
+        if t.dtype not in _DTYPES or t.dtype != xs[0].dtype:
+            raise TypeError("tensors must be bfloat16, float16 or float32, all alike")
+        if t.dim() < 1 or t.shape[-1] != xs[0].shape[-1] or not t.is_contiguous():
+            raise ValueError("tensors must be contiguous, with one last dimension")
+    D = xs[0].shape[-1]
+    if D < 1:
+        raise ValueError("the last dimension is empty")
+    total = sum(t.numel() for t in xs)
+    codes = torch.empty(total, dtype=torch.int8, device=dev)
+    steps = torch.empty(total // D, dtype=torch.float32, device=dev)
+    _act8_call("uaa_act8_pack", xs, codes, steps, False)
+    return Act8(codes, steps, tuple(tuple(t.shape) for t in xs), xs[0].dtype, single)
+
+
+def act8_unpack(packed):
+    """``uaa_act8_unpack``: the values that the codes stand for, in the shapes and type of the tensors packed."""
+    dev = _same_device(packed.codes, packed.steps)
+    ys = [torch.empty(s, dtype=packed.dtype, device=dev) for s in packed.shapes]
+    _act8_call("uaa_act8_unpack", ys, packed.codes, packed.steps, True)
+    return ys[0] if packed.single else ys
+
+
+# --------------------------------------------------------------------------- differential attention
+def _diff_args(q, k, v, lam, key_mask, scale):
+    _bshd("q", q)
+    _bshd("k", k, q, same_s=False)
+    _bshd("v", v, k)
+    B, Sq, H, D = q.shape
+    Sk = k.shape[1]
+    if lam.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("lam must be bfloat16 or float32")
+    if tuple(lam.shape) != (H,) or not lam.is_contiguous():
+        raise ValueError(f"lam must be contiguous (H,) = ({H},), got {tuple(lam.shape)}")
+    mask = normalize_key_mask(key_mask, B, Sk)
+    dev = _same_device(q, k, v, lam, mask)
+    return B, Sq, Sk, H, D, mask, float(1.0 / math.sqrt(D / 2) if scale is None else scale), dev
+
+
+def diff_attn_fwd(q, k, v, lam, key_mask=None, scale=None, need_out2=True, out=None, out2=None, lse=None):
+    """``uaa_diff_attn_fwd``: returns ``(out, out2, lse)``.
+
+    ``q`` ``(B, Sq, H, D)``, ``k``, ``v`` ``(B, Sk, H, D)``: bf16 BSHD as for :func:`attn_fwd`; the first D/2 columns
+    of ``q`` and ``k`` are the first softmax map's, the others the second's.  ``lam`` ``(H,)``: bf16 or fp32.
+    ``out = (A1 - lam A2) v``; ``out2 = A2 v`` (None with ``need_out2=False``, when no gradient is wanted);
+    ``lse`` fp32 ``(B, H, 2, Sq)``.  ``scale`` defaults to ``1/sqrt(D/2)``.
+    """
+    B, Sq, Sk, H, D, mask, scale, dev = _diff_args(q, k, v, lam, key_mask, scale)
+    out = _result("out", out, q.shape, q.dtype, dev)
+    out2 = _result("out2", out2, q.shape, q.dtype, dev) if need_out2 or out2 is not None else None
+    lse = _result("lse", lse, (B, H, 2, Sq), torch.float32, dev)
+    _call(dev, "uaa_diff_attn_fwd", _ptr(q), _ptr(k), _ptr(v), _ptr(lam), _DTYPES[lam.dtype], _ptr(mask), _ptr(out),
+          _ptr(out2), _ptr(lse), B, Sq, Sk, H, D, scale)
+    return out, out2, lse
+
+
+def diff_attn_bwd_workspace_bytes(B, Sq, H, D) -> int:
+    return int(lib().uaa_diff_attn_bwd_workspace_bytes(B, Sq, H, D))
+
+
+def diff_attn_bwd(q, k, v, lam, out, out2, dout, lse, key_mask=None, scale=None, dq=None, dk=None, dv=None, dlam=None,
+                  workspace=None):
+    """``uaa_diff_attn_bwd``: returns ``(dq, dk, dv, dlam)``, ``dlam`` in ``lam``'s type."""
+    B, Sq, Sk, H, D, mask, scale, dev = _diff_args(q, k, v, lam, key_mask, scale)
+    for n, t in (("out", out), ("out2", out2), ("dout", dout)):
+        _bshd(n, t, q)
+    if lse.dtype != torch.float32 or tuple(lse.shape) != (B, H, 2, Sq) or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous fp32 (B, H, 2, Sq)")
+    _same_device(q, out, out2, dout, lse, workspace)
+    dq = _result("dq", dq, q.shape, q.dtype, dev)
+    dk = _result("dk", dk, k.shape, q.dtype, dev)
+    dv = _result("dv", dv, k.shape, q.dtype, dev)
+    dlam = _result("dlam", dlam, lam.shape, lam.dtype, dev)
+    if B * Sq == 0:
+        if Sk and B:
+            raise ValueError("keys without queries (Sq = 0)")
+        return dq, dk, dv, dlam.zero_()
+    nbytes = diff_attn_bwd_workspace_bytes(B, Sq, H, D)
+    if workspace is None:
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+    _call(dev, "uaa_diff_attn_bwd", _ptr(q), _ptr(k), _ptr(v), _ptr(lam), _DTYPES[lam.dtype], _ptr(out), _ptr(out2),
+          _ptr(dout), _ptr(lse), _ptr(mask), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dlam), B, Sq, Sk, H, D, scale,
+          _ptr(workspace), workspace.numel() * workspace.element_size())
+    return dq, dk, dv, dlam
+
+
+class DiffAttention(torch.autograd.Function):
+    """Autograd pairing of ``diff_attn_fwd`` / ``diff_attn_bwd``; ``lse`` is non-differentiable.
+
+    ``saved="int8"`` keeps Q, K, V, O and O2 for the backward pass as an 8-bit checkpoint."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, lam, key_mask=None, scale=None, saved=None):
+        grad = any(ctx.needs_input_grad)
+        out, out2, lse = diff_attn_fwd(q, k, v, lam, key_mask, scale, need_out2=grad)
+        if grad:
+            _save(ctx, saved, (q, k, v, out, out2), lam, lse)
+        ctx.key_mask = key_mask
+        ctx.scale = scale
+        ctx.mark_non_differentiable(lse)
+        return out, lse
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout, _dlse):
+        (q, k, v, out, out2), (lam, lse) = _saved(ctx, 5)
+        dq, dk, dv, dlam = diff_attn_bwd(q, k, v, lam, out, out2, dout.contiguous(), lse, ctx.key_mask, ctx.scale)
+        return dq, dk, dv, dlam, None, None, None
+
+
+def diff_attention(q, k, v, lam, key_mask=None, scale=None, saved=None):
+    """Differentiable differential attention: returns ``(out, lse)``."""
+    return DiffAttention.apply(q, k, v, lam, key_mask, scale, saved)
 
 
 # --------------------------------------------------------------------------- Ulysses re-layout
@@ -447,7 +831,7 @@ class UlyssesAttention(torch.autograd.Function):
     """
 
     @staticmethod
-    def forward(ctx, q_sh, k_sh, v_sh, shard_lens, key_mask=None, scale=None):
+    def forward(ctx, q_sh, k_sh, v_sh, shard_lens, key_mask=None, scale=None, saved=None):
         cap, H = q_sh.shape[2], q_sh.shape[3]
         yq, yk, yv = (seq_to_head(t, shard_lens) for t in (q_sh, k_sh, v_sh))
         P = yq.shape[0]
@@ -455,22 +839,24 @@ class UlyssesAttention(torch.autograd.Function):
         # emulated ranks
         o, lse = attn_fwd_groups(yq, yk, yv, key_mask, scale)
         o_sh = head_to_seq(o, shard_lens, cap, H)
-        ctx.save_for_backward(yq, yk, yv, o, lse)
+        _save(ctx, saved, (yq, yk, yv, o), lse)
         ctx.shard_lens, ctx.key_mask, ctx.scale, ctx.cap, ctx.H = tuple(shard_lens), key_mask, scale, cap, H
         ctx.mark_non_differentiable(lse)
         return o_sh, lse
 
     @staticmethod
     def backward(ctx, do_sh, _dlse):
-        yq, yk, yv, o, lse = ctx.saved_tensors
+        (yq, yk, yv, o), (lse,) = _saved(ctx, 4)
         ydo = seq_to_head(do_sh.contiguous(), ctx.shard_lens)
         dq, dk, dv = attn_bwd_groups(yq, yk, yv, o, ydo, lse, ctx.key_mask, ctx.scale)
         return (head_to_seq(dq, ctx.shard_lens, ctx.cap, ctx.H), head_to_seq(dk, ctx.shard_lens, ctx.cap, ctx.H),
-                head_to_seq(dv, ctx.shard_lens, ctx.cap, ctx.H), None, None, None)
+                head_to_seq(dv, ctx.shard_lens, ctx.cap, ctx.H), None, None, None, None)
 
 
-def ulysses_attention(q_sh, k_sh, v_sh, shard_lens, key_mask=None, scale=None):
-    return UlyssesAttention.apply(q_sh, k_sh, v_sh, tuple(shard_lens), key_mask, scale)
+def ulysses_attention(q_sh, k_sh, v_sh, shard_lens, key_mask=None, scale=None, saved=None):
+    """Differentiable Ulysses attention; ``saved="int8"`` keeps the head groups of Q, K, V and O for the
+    backward pass as an 8-bit checkpoint."""
+    return UlyssesAttention.apply(q_sh, k_sh, v_sh, tuple(shard_lens), key_mask, scale, saved)
 
 
 # --------------------------------------------------------------------------- Ulysses, exchanges fused
@@ -553,20 +939,20 @@ class FusedUlyssesAttention(torch.autograd.Function):
     :class:`UlyssesAttention` up to rounding; ``lse`` is ``(B, H, N)``, non-differentiable)."""
 
     @staticmethod
-    def forward(ctx, q_sh, k_sh, v_sh, shard_lens, key_mask=None, scale=None):
+    def forward(ctx, q_sh, k_sh, v_sh, shard_lens, key_mask=None, scale=None, saved=None):
         out, lse = ulysses_attn_fwd(q_sh, k_sh, v_sh, shard_lens, key_mask, scale)
-        ctx.save_for_backward(q_sh, k_sh, v_sh, out, lse)
+        _save(ctx, saved, (q_sh, k_sh, v_sh, out), lse)
         ctx.shard_lens, ctx.key_mask, ctx.scale = tuple(shard_lens), key_mask, scale
         ctx.mark_non_differentiable(lse)
         return out, lse
 
     @staticmethod
     def backward(ctx, dout, _dlse):
-        q_sh, k_sh, v_sh, out, lse = ctx.saved_tensors
+        (q_sh, k_sh, v_sh, out), (lse,) = _saved(ctx, 4)
         dq, dk, dv = ulysses_attn_bwd(q_sh, k_sh, v_sh, out, dout.contiguous(), lse, ctx.shard_lens, ctx.key_mask,
                                       ctx.scale)
-        return dq, dk, dv, None, None, None
+        return dq, dk, dv, None, None, None, None
 
 
-def ulysses_attention_fused(q_sh, k_sh, v_sh, shard_lens, key_mask=None, scale=None):
-    return FusedUlyssesAttention.apply(q_sh, k_sh, v_sh, tuple(shard_lens), key_mask, scale)
+def ulysses_attention_fused(q_sh, k_sh, v_sh, shard_lens, key_mask=None, scale=None, saved=None):
+    return FusedUlyssesAttention.apply(q_sh, k_sh, v_sh, tuple(shard_lens), key_mask, scale, saved)
