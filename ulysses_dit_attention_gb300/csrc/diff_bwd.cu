@@ -1,30 +1,11 @@
-// Differential attention: every head has two softmax maps over the same keys and
-// reads the values by their difference,
-//   A_m = softmax(scale q_m k_m^T + bias)      (m = 1, 2; D/2 columns each)
-//   O   = (A_1 - lambda_h A_2) V,   O2 = A_2 V (kept for the backward).
-// With dA = dO V^T the gradients are
-//   Delta_2 = dO . O2,  Delta_1 = dO . O + lambda Delta_2     (= A_m dA per row)
-//   dS_1 = A_1 (dA - Delta_1),  dS_2 = -lambda A_2 (dA - Delta_2)
-//   dQ_m = scale dS_m K_m,  dK_m = scale dS_m^T Q_m,  dV = (A_1 - lambda A_2)^T dO
-//   dlambda_h = -sum_{b, i} Delta_2.
-// Sums, softmax statistics and accumulators are 32-bit.
-#include <math.h>
-
-#include "uaa_common.cuh"
+// Differential attention, backward (the formulas stand in diff_shared.cuh).
+#include "diff_shared.cuh"
 
 namespace uaa {
-
-int validate_attn_sizes(const char* fn, int B, int Sq, int Sk, int H, int D, float scale);
-int check_dev_ptr(const char* fn, const char* name, const void* p);
-
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-
-__device__ __forceinline__ float load_lambda(const void* lam, int bf16, int h) {
-  return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(lam)[h]) : static_cast<const float*>(lam)[h];
-}
 
 // The E consecutive columns of a row that one lane holds (a row is spread over a warp: lanes 0-15 hold map 1).
 template <int E>
@@ -60,60 +41,9 @@ __device__ __forceinline__ float warp_sum(float s) {
   return s + __shfl_xor_sync(0xffffffffu, s, 16);
 }
 
-__host__ __device__ __forceinline__ int row_tiles(int S) { return (S + 127) / 128; }
 // Row vectors of the backward: (B, H, tiles, 2 maps, 128)
 __host__ __device__ __forceinline__ size_t row_at(size_t bh, int Sq, int m, int i) {
-  return ((bh * row_tiles(Sq) + i / 128) * 2 + m) * 128 + i % 128;
-}
-
-// One warp per (b, h, query row), keys in order.
-template <int D>
-__global__ void __launch_bounds__(kThreads) diff_fwd_kernel(
-    const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
-    const void* __restrict__ lam, int lam_bf16, const uint8_t* __restrict__ mask, __nv_bfloat16* __restrict__ out,
-    __nv_bfloat16* __restrict__ out2, float* __restrict__ lse, int B, int Sq, int Sk, int H, float scale_log2) {
-  constexpr int E = D / 32;
-  constexpr float kLn2 = 0.6931471805599453f;
-  const int lane = threadIdx.x & 31;
-  const size_t rows = (size_t)B * H * Sq;
-  for (size_t r = (size_t)blockIdx.x * kWarps + (threadIdx.x >> 5); r < rows; r += (size_t)gridDim.x * kWarps) {
-    const int i = r % Sq, h = r / Sq % H, b = r / Sq / H;
-    const size_t at = (((size_t)b * Sq + i) * H + h) * D + lane * E;
-    float qv[E], o1[E] = {}, o2[E] = {};
-    load_cols<E>(q + at, qv);
-    float mx = -INFINITY, sum = 0.f;  // of the lane's own map
-    for (int j = 0; j < Sk; ++j) {
-      if (mask && !mask[(size_t)b * Sk + j]) continue;
-      const size_t kat = (((size_t)b * Sk + j) * H + h) * D + lane * E;
-      float kv[E], vv[E];
-      load_cols<E>(k + kat, kv);
-      load_cols<E>(v + kat, vv);
-      const float s = map_sum(dot_cols<E>(qv, kv)) * scale_log2;
-      const float m = fmaxf(mx, s);
-      const float alpha = exp2f(mx - m), p = exp2f(s - m);
-      mx = m;
-      sum = sum * alpha + p;
-      const float a1 = __shfl_sync(0xffffffffu, alpha, 0), a2 = __shfl_sync(0xffffffffu, alpha, 16);
-      const float p1 = __shfl_sync(0xffffffffu, p, 0), p2 = __shfl_sync(0xffffffffu, p, 16);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        o1[e] = fmaf(p1, vv[e], o1[e] * a1);
-        o2[e] = fmaf(p2, vv[e], o2[e] * a2);
-      }
-    }
-    const float l1 = __shfl_sync(0xffffffffu, sum, 0), l2 = __shfl_sync(0xffffffffu, sum, 16);
-    const float c1 = l1 > 0.f ? 1.f / l1 : 0.f, c2 = l2 > 0.f ? 1.f / l2 : 0.f;
-    const float lm = load_lambda(lam, lam_bf16, h);
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      o2[e] *= c2;
-      o1[e] = o1[e] * c1 - lm * o2[e];
-    }
-    store_cols<E>(out + at, o1, 1.f);
-    if (out2) store_cols<E>(out2 + at, o2, 1.f);
-    if ((lane & 15) == 0)
-      lse[(((size_t)b * H + h) * 2 + (lane >> 4)) * Sq + i] = sum > 0.f ? mx * kLn2 + logf(sum) : -INFINITY;
-  }
+  return ((bh * tiles_of(Sq) + i / 128) * 2 + m) * 128 + i % 128;
 }
 
 // Delta_m and -LSE_m * log2(e) of every query row; rows past Sq get 0 and -inf (P = 0).
@@ -124,7 +54,7 @@ __global__ void __launch_bounds__(kThreads) diff_rows_kernel(
     float* __restrict__ delta, float* __restrict__ nl2, int B, int Sq, int H) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
-  const int pad = row_tiles(Sq) * 128;
+  const int pad = tiles_of(Sq) * 128;
   const size_t rows = (size_t)B * pad * H;
   for (size_t r = (size_t)blockIdx.x * kWarps + (threadIdx.x >> 5); r < rows; r += (size_t)gridDim.x * kWarps) {
     const int h = r % H, i = r / H % pad, b = r / H / pad;
@@ -151,7 +81,7 @@ __global__ void __launch_bounds__(kThreads) diff_rows_kernel(
 __global__ void __launch_bounds__(1024) diff_dlambda_kernel(const float* __restrict__ delta, void* __restrict__ dlam,
                                                             int lam_bf16, int B, int Sq, int H) {
   __shared__ float part[32];
-  const int h = blockIdx.x, tiles = row_tiles(Sq);
+  const int h = blockIdx.x, tiles = tiles_of(Sq);
   float s = 0.f;
   for (int b = 0; b < B; ++b)
     for (int i = threadIdx.x; i < tiles * 128; i += blockDim.x) s += delta[row_at((size_t)b * H + h, Sq, 1, i)];
@@ -239,32 +169,9 @@ __global__ void __launch_bounds__(kThreads) diff_dkdv_kernel(
   }
 }
 
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) !=
-                                                cudaSuccess || n <= 0)
-    return 148;
-  return n;
-}
-
 int grid_for(size_t rows) {
-  const size_t need = (rows + kWarps - 1) / kWarps, cap = (size_t)sm_count() * 8;
+  const size_t need = (rows + kWarps - 1) / kWarps, cap = (size_t)device_sms() * 8;
   return (int)(need < cap ? need : cap);
-}
-
-int check_lambda(const char* fn, const void* lam, int dtype) {
-  if (dtype != UAA_BF16 && dtype != UAA_FP32)
-    return set_error(UAA_ERR_INVALID_ARG, "%s: lambda must be bf16 or fp32 (dtype %d)", fn, dtype);
-  if (!lam) return set_error(UAA_ERR_INVALID_ARG, "%s: lambda is NULL", fn);
-  if (reinterpret_cast<uintptr_t>(lam) & (dtype == UAA_BF16 ? 1u : 3u))
-    return set_error(UAA_ERR_INVALID_ARG, "%s: lambda is not aligned to its element", fn);
-  return UAA_OK;
-}
-
-int check_lse(const char* fn, const void* lse) {
-  if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3u))
-    return set_error(UAA_ERR_INVALID_ARG, "%s: lse is NULL or not 4-byte aligned", fn);
-  return UAA_OK;
 }
 
 using bf = __nv_bfloat16;
@@ -275,9 +182,9 @@ template <int D>
 int launch_bwd(const void* q, const void* k, const void* v, const void* lam, int lam_bf16, const void* out,
                const void* out2, const void* dout, const float* lse, const uint8_t* mask, void* dq, void* dk, void* dv,
                void* dlam, int B, int Sq, int Sk, int H, float scale, float* delta, cudaStream_t s) {
-  float* nl2 = delta + (size_t)B * H * row_tiles(Sq) * 256;
+  float* nl2 = delta + (size_t)B * H * tiles_of(Sq) * 256;
   int st;
-  diff_rows_kernel<D><<<grid_for((size_t)B * H * row_tiles(Sq) * 128), kThreads, 0, s>>>(
+  diff_rows_kernel<D><<<grid_for((size_t)B * H * tiles_of(Sq) * 128), kThreads, 0, s>>>(
       in(out), in(out2), in(dout), lse, lam, lam_bf16, delta, nl2, B, Sq, H);
   if ((st = check_launch("uaa_diff_attn_bwd (rows)"))) return st;
   diff_dlambda_kernel<<<H, 1024, 0, s>>>(delta, dlam, lam_bf16, B, Sq, H);
@@ -297,29 +204,10 @@ int launch_bwd(const void* q, const void* k, const void* v, const void* lam, int
 
 using namespace uaa;
 
-extern "C" int uaa_diff_attn_fwd(const void* q, const void* k, const void* v, const void* lambda, int lambda_dtype,
-                                 const uint8_t* key_mask, void* out, void* out2, float* lse, int B, int Sq, int Sk,
-                                 int H, int D, float scale, uaa_stream_t stream) {
-  const char* fn = "uaa_diff_attn_fwd";
-  int st = validate_attn_sizes(fn, B, Sq, Sk, H, D, scale);
-  if (st) return st;
-  if ((uint64_t)B * Sq * H == 0) return UAA_OK;
-  if ((st = check_dev_ptr(fn, "q", q)) || (st = check_dev_ptr(fn, "k", k)) || (st = check_dev_ptr(fn, "v", v)) ||
-      (st = check_dev_ptr(fn, "out", out)) || (out2 && (st = check_dev_ptr(fn, "out2", out2))) ||
-      (st = check_lambda(fn, lambda, lambda_dtype)) || (st = check_lse(fn, lse)))
-    return st;
-  const int grid = grid_for((size_t)B * H * Sq), lb = lambda_dtype == UAA_BF16;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  auto kern = D == 64 ? diff_fwd_kernel<64> : diff_fwd_kernel<128>;
-  kern<<<grid, kThreads, 0, s>>>(in(q), in(k), in(v), lambda, lb, key_mask, to(out), to(out2), lse, B, Sq, Sk, H,
-                                 scale * kLog2e);
-  return check_launch(fn);
-}
-
 extern "C" size_t uaa_diff_attn_bwd_workspace_bytes(int B, int Sq, int H, int D) {
   if (B < 0 || Sq < 0 || H < 0 || (D != 64 && D != 128)) return 0;
   // Delta and -LSE*log2(e), each (B, H, tiles, 2, 128) fp32
-  return (size_t)B * H * row_tiles(Sq) * 2048;
+  return (size_t)B * H * tiles_of(Sq) * 2048;
 }
 
 extern "C" int uaa_diff_attn_bwd(const void* q, const void* k, const void* v, const void* lambda, int lambda_dtype,
