@@ -76,8 +76,8 @@ def test_refusals_of_the_call():
     assert bwd(out2=None) == -1 and "out2" in err()
     assert bwd(dlam=None) == -1 and "lambda" in err()
     assert bwd(Sq=0) == -1 and "queries" in err()
-    # Delta and -LSE*log2(e), two maps, rows padded to 128
-    assert L.uaa_diff_attn_bwd_workspace_bytes(2, 130, 3, 128) == 2 * 3 * 256 * 2 * 2 * 4
+    # per head Delta and -LSE*log2(e) of two maps, rows padded to 128, and a sum per 64 rows
+    assert L.uaa_diff_attn_bwd_workspace_bytes(2, 130, 3, 128) == 2 * 3 * (256 * 4 + 4) * 4 // 256 * 256 + 256
     assert L.uaa_diff_attn_bwd_workspace_bytes(2, 130, 3, 96) == 0
 
 
