@@ -117,7 +117,8 @@ def diff_attn(q, k, v, lam, mask=None, scale=None, dout=None):
         eds = (np.abs(ds) * (P + EXP + 2 * es[..., None] + F32)
                + np.abs(weight) * a * (eda + np.stack([erow1, erow2])[..., None]))
         pv = a[0] - L * a[1]
-        epv = BF16 * np.abs(pv) + both * (EXP + F32 + es.max(0)[..., None])
+        # each map's probability is rounded to bf16 by itself: |A1 2^-8| + |lambda A2 2^-8|
+        epv = both * (BF16 + EXP + F32 + es.max(0)[..., None])
         dv = np.einsum("hij,ihd->jhd", pv, g)
         edv = np.einsum("hij,ihd->jhd", epv + F32 * np.abs(pv), np.abs(g))
         put("dv", b, dv, edv + BF16 * np.abs(dv))

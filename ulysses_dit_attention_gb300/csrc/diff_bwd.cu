@@ -3,35 +3,44 @@
 //  1. diff_rows_kernel: Delta_m and -LSE_m log2(e) of every query row, and the
 //     sum of Delta_2 over 64 rows, the summands of dlambda.
 //  2. diff_dlambda_kernel: dlambda_h from those sums, in a fixed order.
-//  3. diff_dkdv_kernel, key-tile-major: 128 keys against steps of 64 queries.
-//  4. diff_dq_kernel, query-tile-major: 128 queries against steps of 64 keys.
-//
-// Both matrix kernels run on the tensor cores with a step of 64 columns, so that
-// two steps fit into TMEM next to the accumulators and one warpgroup works on
-// each: while warpgroup 0 takes the exponentials of step g, the tensor cores run
-// the products of step g + 1 for warpgroup 1, and the other way round.  The maps
-// share dA = dO V^T, and both maps' probabilities enter dV in one product, so
-// the products cost what plain attention's backward costs; the exponentials are
-// twice as many.
+//  3. diff_dkdv_kernel, key-tile-major: dK and dV of 128 keys.
+//  4. diff_dq_kernel, query-tile-major: dQ of 128 queries.
+// -lambda enters as |lambda| = 2^(log2 |lambda|), added to map 2's exponents with its LSE, and a sign: the negated
+// A operand of map 2's dV product, and the sign of dQ_2 and dK_2 when they are written.
+// Both matrix kernels: warps 0-15 compute (TMEM lane quadrant = warp % 4, 32 of a tile's 128 columns = warp / 4;
+// four warps on each scheduler, because with two the latencies of TMEM and barriers lay open: dK/dV 1640 -> 1455 us,
+// dQ 1067 -> 933 us at S = 8191, H = 24, D = 128), warp 16 loads by TMA, warp 17 issues the tcgen05 products from one elected lane.  MMAs of one thread run in order; two that read A
+// from TMEM for different products are only relied on with equal shapes or with another product between them.
 #include "diff_shared.cuh"
 
 namespace uaa {
 namespace {
 
-constexpr int kStep = 64;  // queries (dK/dV) or keys (dQ) of a step
-constexpr int kThreads = 320;
-constexpr int kProducerWarp = 8;
-constexpr int kMmaWarp = 9;
-constexpr int kStepChunk = kStep * 128;  // 64 rows x 128 bytes: 64 columns of a step's operand
+constexpr int kThreads = 576;
+constexpr int kCompute = 512;  // warps 0-15
+constexpr int kProducerWarp = 16;
+constexpr int kMmaWarp = 17;
+// Named barriers between the compute warps (which arrive) and the issuer (which syncs): the issuer waits on these
+// within an item, because an mbarrier test would be held behind the MMAs that it has queued.
+constexpr uint32_t kBarP = 1, kBarDS = 2, kBarCount = kCompute + 32;
+constexpr int kRowBytes = 4 * kTile * 4;
+constexpr uint32_t kIdescNegateA = 1u << 13;  // instruction descriptor: the A operand is negated
 
-__host__ __device__ __forceinline__ int steps_of(int S) { return 2 * tiles_of(S); }
-// Row vectors, (B, H, steps, 4, 64): -LSE_1 log2(e), -LSE_2 log2(e), Delta_1, Delta_2 of a step's queries
+// Row vectors, (B, H, tiles, 4, 128): -LSE_1 log2(e), -LSE_2 log2(e) + log2 |lambda|, Delta_1, Delta_2 of a tile's
+// queries
 __host__ __device__ __forceinline__ size_t rows_at(size_t bh, int Sq, int i) {
-  return (bh * steps_of(Sq) + i / kStep) * (4 * kStep) + i % kStep;
+  return (bh * tiles_of(Sq) + i / kTile) * (4 * kTile) + i % kTile;
 }
 
-// 16 / 8 packed columns of this thread's TMEM lane, then a wait for the store.
-__device__ __forceinline__ void tmem_st16_bits(uint32_t taddr, const uint32_t (&v)[16]) {
+// TMEM column of the A operand for 16-element step kk: each warpgroup's 32 packed elements lie in the first 16
+// columns of its own 32.
+__device__ __forceinline__ uint32_t packed_col(int kk) { return 32 * (kk >> 1) + 8 * (kk & 1); }
+
+// 32 values as bf16 pairs into 16 columns of this thread's TMEM lane, then a wait for the store.
+__device__ __forceinline__ void store_packed32(uint32_t taddr, const float (&x)[32]) {
+  uint32_t v[16];
+#pragma unroll
+  for (int c = 0; c < 16; ++c) v[c] = pack_bf16(x[2 * c], x[2 * c + 1]);
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n\t"
       "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
@@ -39,12 +48,14 @@ __device__ __forceinline__ void tmem_st16_bits(uint32_t taddr, const uint32_t (&
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st8_bits(uint32_t taddr, const uint32_t (&v)[8]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\t"
-      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-      : "memory");
+
+// Are these barriers' phases complete?  Both are tested before either answer is used; the slow path waits in turn.
+template <typename Ctl>
+__device__ __forceinline__ bool wait_two(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, const DevCtx& ctx,
+                                         Ctl* ctl) {
+  const bool ra = mbar_try_wait(a, pa), rb = mbar_try_wait(b, pb);
+  if (ra && rb) return true;
+  return wait_or_abort(a, pa, ctx, ctl) && wait_or_abort(b, pb, ctx, ctl);
 }
 
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v, float c) {
@@ -57,6 +68,8 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v, float c
 // that neighbouring reads follow each other and a head's results are written as runs.
 constexpr int kRowThreads = 256;
 constexpr int kRowHeads = 4;
+constexpr int kStep = 64;
+__host__ __device__ __forceinline__ int steps_of(int S) { return 2 * tiles_of(S); }
 
 template <int D>
 __global__ void __launch_bounds__(kRowThreads) diff_rows_kernel(
@@ -105,8 +118,9 @@ __global__ void __launch_bounds__(kRowThreads) diff_rows_kernel(
         if (sub < 2) {
           const float l = i < Sq ? lse[(bh * 2 + sub) * Sq + i] : -INFINITY;
           x = l == -INFINITY ? -INFINITY : -l * kLog2e;  // rows past Sq, or without a key: P = 0
+          if (sub == 1 && l != -INFINITY) x += log2f(fabsf(lm));
         }
-        rows[rows_at(bh, Sq, i) + sub * kStep] = x;
+        rows[rows_at(bh, Sq, i) + sub * kTile] = x;
       }
     }
     if (sub == 0) sums[group] = sum;
@@ -159,35 +173,37 @@ __device__ __forceinline__ Item decode_item(int item, int tiles, int H, bool hea
 }
 
 // ---------------------------------------------------------------------------
-// 3. dK, dV.  A persistent CTA takes 128 keys of one (batch, head) and loops over steps of 64 queries:
-//     S_m^T = K_m Q_m^T, P^T = A_1^T - lambda A_2^T, dA^T = V dO^T       (M = keys, N = 64)
-//     dV += P^T dO, dK_m += dS_m^T Q_m
-// TMEM, per step parity 128 columns: X holds S_1^T, then P^T (32 packed columns) and dS_2^T (columns 32..63);
-// Y holds S_2^T, then dA^T (formed once both S have been read), then dS_1^T.  dV is at 256, dK_m at 384 + 64 m
-// (64 columns each; with D = 64 the product runs over all 64 columns of Q and map m's 32 are kept).
-// One elected lane issues, per step g: dA_g dV_g after p_ready(g), dK_g S_{g+2} after ds_ready(g).
-// MMAs of one thread run in order, but two that read A from TMEM for different products are only relied on
-// with equal shapes: dV_g (N = D) has completed before dK_g (N = 64) is issued.
+// 3. dK, dV.  A persistent CTA takes 128 keys of one (batch, head); its steps are the maps of the query tiles in
+// turn, (i, 1) (i, 2) (i + 1, 1) ...:
+//     S^T = K_m Q_m^T, P^T = w_m A_m^T (w = 1, -lambda), dA^T = V dO^T    (M = keys, N = 128 queries)
+//     dV += P^T dO, dS^T = P^T (dA^T - Delta_m), dK_m += dS^T Q_m
+// One elected lane issues, per step: dV_s S_{s+1} after P_s, dK_s dA_{s+1} after dS_s; so the tensor cores work
+// while the eight compute warps take the exponentials of the next step or form dS of this one.  dA is formed anew
+// for the second map: 3072 cycles of products per pair of tiles against 2048 without, but the TMEM that keeping it
+// would take is not there, and with steps of 64 queries, whose two buffers would fit, a product with both operands
+// in shared memory takes as long as one with 128 (its A operand is read just the same): measured 2052 us
+// against 1640 for B = 1, S = 8191, H = 24, D = 128 (1455 with sixteen compute warps).
+// TMEM: S^T at column 0, dA^T at 128 (P^T and dS^T, packed, over the first 16 columns of each warpgroup's 32),
+// dV at 256, dK_m at 384 + 64 m (with D = 64 the product runs over all 64 columns of Q and map m's 32 are kept).
 template <int D>
 struct DkdvLayout {
   static constexpr int kTileBytes = 128 * D * 2;
-  static constexpr int kStepBytes = kStep * D * 2;
-  static constexpr int kRing = D == 128 ? 4 : 6;
+  static constexpr int kRing = D == 128 ? 2 : 4;
   static constexpr int kK = 0;
   static constexpr int kV = kK + kTileBytes;
-  static constexpr int kQ = kV + kTileBytes;           // Q steps, then dO steps, then row vectors
-  static constexpr int kDO = kQ + kRing * kStepBytes;
-  static constexpr int kRows = kDO + kRing * kStepBytes;
-  static constexpr int kCtl = kRows + kRing * 4 * kStep * 4;
+  static constexpr int kQ = kV + kTileBytes;
+  static constexpr int kDO = kQ + kRing * kTileBytes;
+  static constexpr int kRows = kDO + kRing * kTileBytes;
+  static constexpr int kCtl = kRows + kRing * kRowBytes;
   static constexpr int kSmem = kCtl + 256;
   static_assert(kSmem <= 232448, "shared memory exceeds the per-CTA limit");
 };
 
 struct DkdvCtl {
   uint64_t bar_kv_full, bar_kv_empty;
-  uint64_t bar_full[6], bar_empty[6];
-  uint64_t bar_s_full[2], bar_dp_full[2], bar_p_ready[2], bar_ds_ready[2];
-  uint64_t bar_dv_done, bar_acc_done, bar_acc_free, bar_final;
+  uint64_t bar_full[4], bar_empty[4];
+  uint64_t bar_s_full, bar_dp_full, bar_dv_done;
+  uint64_t bar_acc_done, bar_acc_free, bar_final;
   uint32_t tmem_base;
   int abort;
 };
@@ -216,10 +232,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   using L = DkdvLayout<D>;
   constexpr int kChunks = D / 64;
   constexpr int R = L::kRing;
-  constexpr uint32_t kIdescS = idesc_bf16_f32(128, kStep, false, false);  // S^T, dA^T
+  constexpr uint32_t kIdescS = idesc_bf16_f32(128, kTile, false, false);  // S^T, dA^T
   constexpr uint32_t kIdescV = idesc_bf16_f32(128, D, false, true);       // dV (A in TMEM)
   constexpr uint32_t kIdescK = idesc_bf16_f32(128, 64, false, true);      // dK_m (A in TMEM)
-  constexpr uint32_t kX = 0, kY = 64, kStage = 128, kColDV = 256, kColDK = 384;
+  constexpr uint32_t kColS = 0, kColDP = 128, kColDV = 256, kColDK = 384;
 
   extern __shared__ __align__(1024) uint8_t smem[];
   DkdvCtl* ctl = reinterpret_cast<DkdvCtl*>(smem + L::kCtl);
@@ -231,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int nkt = tiles_of(Sk);
-  const int n = (Sq + kStep - 1) / kStep;  // steps of an item
+  const int nqt = tiles_of(Sq);
 
   if (threadIdx.x == 0) {
     mbar_init(&ctl->bar_kv_full, 1);
@@ -240,15 +256,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->bar_full[s], 1);
       mbar_init(&ctl->bar_empty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&ctl->bar_s_full[s], 1);
-      mbar_init(&ctl->bar_dp_full[s], 1);
-      mbar_init(&ctl->bar_p_ready[s], 128);
-      mbar_init(&ctl->bar_ds_ready[s], 128);
-    }
+    mbar_init(&ctl->bar_s_full, 1);
+    mbar_init(&ctl->bar_dp_full, 1);
     mbar_init(&ctl->bar_dv_done, 1);
     mbar_init(&ctl->bar_acc_done, 1);
-    mbar_init(&ctl->bar_acc_free, 256);
+    mbar_init(&ctl->bar_acc_free, kCompute);
     mbar_init(&ctl->bar_final, 1);
     ctl->abort = 0;
     fence_mbar_init();
@@ -270,13 +282,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const MmaGuard mg = mma_guard(ctx, sbase, L::kSmem, tmem, 512);  // debug builds' operand checks
   const size_t k_extent = (size_t)B * Sk * H * D;
 
-  uint32_t armed[6] = {}, kv_armed = 0;
+  uint32_t armed[4] = {}, kv_armed = 0;
   bool mma_issued = false;
 
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer
     bool ok = true;
-    uint32_t G = 0, it = 0;  // steps and items so far
+    uint32_t T = 0, it = 0;  // query tiles and items so far
     for (int item = blockIdx.x; ok && item < num_items; item += gridDim.x) {
       const Item w = decode_item(item, nkt, H, head_inner);
       if (kMask && !tile_any(key_mask, w.b, w.t, Sk)) continue;
@@ -292,22 +304,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           kv_armed = it + 1;
         }
         const float* rsrc = rows + rows_at((size_t)w.b * H + w.h, Sq, 0);
-        for (int g = 0; ok && g < n; ++g, ++G) {
-          const int slot = G % R;
-          const uint32_t use = G / R;
+        for (int i = 0; ok && i < nqt; ++i, ++T) {
+          const int slot = T % R;
+          const uint32_t use = T / R;
           if (use > 0) ok = wait_or_abort(&ctl->bar_empty[slot], (use - 1) & 1, ctx, ctl);
           if (!ok) break;
-          if ((int)G == ctx.drop_load) continue;
-          mbar_arrive_expect_tx(&ctl->bar_full[slot], 2 * L::kStepBytes + 4 * kStep * 4);
+          if ((int)T == ctx.drop_load) continue;
+          mbar_arrive_expect_tx(&ctl->bar_full[slot], 2 * L::kTileBytes + kRowBytes);
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
-            tma_load_4d(smem + L::kQ + slot * L::kStepBytes + c * kStepChunk, &tmQ, &ctl->bar_full[slot], c * 64, w.h,
-                        g * kStep, w.b);
-            tma_load_4d(smem + L::kDO + slot * L::kStepBytes + c * kStepChunk, &tmDO, &ctl->bar_full[slot], c * 64,
-                        w.h, g * kStep, w.b);
+            tma_load_4d(smem + L::kQ + slot * L::kTileBytes + c * kChunkBytes, &tmQ, &ctl->bar_full[slot], c * 64, w.h,
+                        i * kTile, w.b);
+            tma_load_4d(smem + L::kDO + slot * L::kTileBytes + c * kChunkBytes, &tmDO, &ctl->bar_full[slot], c * 64,
+                        w.h, i * kTile, w.b);
           }
-          bulk_load(smem + L::kRows + slot * 4 * kStep * 4, rsrc + (size_t)g * 4 * kStep, 4 * kStep * 4,
-                    &ctl->bar_full[slot]);
+          bulk_load(smem + L::kRows + slot * kRowBytes, rsrc + (size_t)i * 4 * kTile, kRowBytes, &ctl->bar_full[slot]);
           armed[slot] = use + 1;
         }
       }
@@ -319,89 +330,94 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t el_lane;
     const bool el = elect_one_sync(&el_lane);
     bool ok = true;
-    uint32_t G0 = 0, it = 0;
+    uint32_t T0 = 0, it = 0;
     auto wait_el = [&](uint64_t* bar, uint32_t parity) {
       bool w = true;
       if (el) w = wait_or_abort(bar, parity, ctx, ctl);
       return __shfl_sync(0xffffffffu, w ? 1 : 0, el_lane) != 0;
     };
-    auto sq = [&](uint32_t G) { return sbase + L::kQ + (G % R) * L::kStepBytes; };
-    auto sdo = [&](uint32_t G) { return sbase + L::kDO + (G % R) * L::kStepBytes; };
-    // 16-column step kk of a 64-row operand of D columns
-    auto step_off = [](int kk) { return (uint32_t)((kk >> 2) * kStepChunk + (kk & 3) * 32); };
-    auto tile_off = [](int kk) { return (uint32_t)((kk >> 2) * kChunkBytes + (kk & 3) * 32); };
-    auto issue_s = [&](uint32_t G) {
-      const uint64_t a0 = sdesc_sw128(sbase + L::kK, 16, 1024), b0 = sdesc_sw128(sq(G), 16, 1024);
-      const uint32_t d = tmem + (G & 1) * kStage;
+    auto sq = [&](uint32_t T) { return sbase + L::kQ + (T % R) * L::kTileBytes; };
+    auto sdo = [&](uint32_t T) { return sbase + L::kDO + (T % R) * L::kTileBytes; };
+    auto issue_s = [&](uint32_t T, int m) {
+      const uint64_t a0 = sdesc_sw128(sbase + L::kK, 16, 1024), b0 = sdesc_sw128(sq(T), 16, 1024);
+#pragma unroll
+      for (int kk = 0; kk < D / 32; ++kk) {
+        const uint32_t off = m ? map_step<D>(1, kk) : map_step<D>(0, kk);
+        const uint64_t a = desc_add(a0, off), b = desc_add(b0, off);
+        if (el) mma_ss_checked(mg, tmem + kColS, a, b, kIdescS, kk > 0, kTile);
+      }
+      if (el) mma_commit(&ctl->bar_s_full);
+    };
+    auto issue_dp = [&](uint32_t T) {
+      const uint64_t a0 = sdesc_sw128(sbase + L::kV, 16, 1024), b0 = sdesc_sw128(sdo(T), 16, 1024);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        const int m = kk >= D / 32;
-        const uint64_t a = desc_add(a0, tile_off(kk)), b = desc_add(b0, step_off(kk));
-        if (el) mma_ss_checked(mg, d + (m ? kY : kX), a, b, kIdescS, kk % (D / 32) > 0, kStep);
+        const uint32_t off = (kk >> 2) * kChunkBytes + (kk & 3) * 32;
+        const uint64_t a = desc_add(a0, off), b = desc_add(b0, off);
+        if (el) mma_ss_checked(mg, tmem + kColDP, a, b, kIdescS, kk > 0, kTile);
       }
-      if (el) mma_commit(&ctl->bar_s_full[G & 1]);
+      if (el) mma_commit(&ctl->bar_dp_full);
     };
-    auto issue_dp = [&](uint32_t G) {
-      const uint64_t a0 = sdesc_sw128(sbase + L::kV, 16, 1024), b0 = sdesc_sw128(sdo(G), 16, 1024);
-      const uint32_t d = tmem + (G & 1) * kStage + kY;
+    auto issue_dv = [&](uint32_t T, bool first, bool last, uint32_t idesc) {
+      const uint64_t b0 = sdesc_sw128(sdo(T), kChunkBytes, 1024);
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint64_t a = desc_add(a0, tile_off(kk)), b = desc_add(b0, step_off(kk));
-        if (el) mma_ss_checked(mg, d, a, b, kIdescS, kk > 0, kStep);
-      }
-      if (el) mma_commit(&ctl->bar_dp_full[G & 1]);
-    };
-    auto issue_dv = [&](uint32_t G, bool first) {
-      const uint64_t b0 = sdesc_sw128(sdo(G), kStepChunk, 1024);
-      const uint32_t a = tmem + (G & 1) * kStage + kX;
-#pragma unroll
-      for (int kk = 0; kk < kStep / 16; ++kk) {
+      for (int kk = 0; kk < kTile / 16; ++kk) {
         const uint64_t b = desc_add(b0, kk * 2048);
-        if (el) mma_ts_checked(mg, tmem + kColDV, a + kk * 8, b, kIdescV, (!first || kk > 0) ? 1u : 0u, D);
+        if (el)
+          mma_ts_checked(mg, tmem + kColDV, tmem + kColS + packed_col(kk), b, idesc, (!first || kk > 0) ? 1u : 0u, D);
       }
-      if (el) mma_commit(&ctl->bar_dv_done);
+      if (el && last) mma_commit(&ctl->bar_dv_done);
     };
-    auto issue_dk = [&](uint32_t G, bool first) {
+    auto issue_dk = [&](uint32_t T, int m, bool first) {
+      const uint64_t b0 = sdesc_sw128(sq(T) + (D == 128 ? m * kChunkBytes : 0), kChunkBytes, 1024);
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const uint64_t b0 = sdesc_sw128(sq(G) + (D == 128 ? m * kStepChunk : 0), kStepChunk, 1024);
-        const uint32_t a = tmem + (G & 1) * kStage + (m ? kX + 32 : kY);
-#pragma unroll
-        for (int kk = 0; kk < kStep / 16; ++kk) {
-          const uint64_t b = desc_add(b0, kk * 2048);
-          if (el)
-            mma_ts_checked(mg, tmem + kColDK + 64 * m, a + kk * 8, b, kIdescK, (!first || kk > 0) ? 1u : 0u, 64);
-        }
+      for (int kk = 0; kk < kTile / 16; ++kk) {
+        const uint64_t b = desc_add(b0, kk * 2048);
+        if (el)
+          mma_ts_checked(mg, tmem + kColDK + 64 * m, tmem + kColDP + packed_col(kk), b, kIdescK,
+                         (!first || kk > 0) ? 1u : 0u, 64);
       }
-      if (el) mma_commit(&ctl->bar_empty[G % R]);
+      if (el && m == 1) mma_commit(&ctl->bar_empty[T % R]);
     };
-    auto full = [&](uint32_t G) { return wait_el(&ctl->bar_full[G % R], (G / R) & 1); };
-    for (int item = blockIdx.x; ok && item < num_items; item += gridDim.x) {
+    for (int item = blockIdx.x; item < num_items; item += gridDim.x) {
       const Item w = decode_item(item, nkt, H, head_inner);
       if (kMask && !tile_any(key_mask, w.b, w.t, Sk)) continue;
-      ok = wait_el(&ctl->bar_kv_full, it & 1);
-      for (int g = 0; ok && g < 2 && g < n; ++g) {
-        if (!(ok = full(G0 + g))) break;
+      // After a failure anywhere in the CTA this warp stops issuing but still meets the compute warps at
+      // every named barrier of the schedule.
+      if (ok && *reinterpret_cast<volatile int*>(&ctl->abort)) ok = false;
+      // map 2's probabilities enter dV with the sign of -lambda
+      const uint32_t idesc2 = kIdescV | (load_lambda(lam, lam_bf16, w.h) > 0.f ? kIdescNegateA : 0u);
+      if (ok) ok = wait_el(&ctl->bar_kv_full, it & 1);
+      if (ok) ok = wait_el(&ctl->bar_full[T0 % R], (T0 / R) & 1);
+      if (ok) {
         tc_fence_after();
-        issue_s(G0 + g);
+        issue_s(T0, 0);
+        issue_dp(T0);
         if (el) mma_issued = true;
       }
-      for (int g = 0; ok && g < n; ++g) {
-        const uint32_t G = G0 + g, st = G & 1, ph = (G >> 1) & 1;
-        if (!(ok = wait_el(&ctl->bar_p_ready[st], ph))) break;
-        // the previous item's epilogue must have read dV and dK
-        if (g == 0 && it > 0 && !(ok = wait_el(&ctl->bar_acc_free, (it - 1) & 1))) break;
-        tc_fence_after();
-        issue_dp(G);
-        issue_dv(G, g == 0);
-        if (!(ok = wait_el(&ctl->bar_ds_ready[st], ph))) break;
-        if (!(ok = wait_el(&ctl->bar_dv_done, G & 1))) break;
-        tc_fence_after();
-        issue_dk(G, g == 0);
-        if (g + 2 < n) {
-          if (!(ok = full(G + 2))) break;
-          tc_fence_after();
-          issue_s(G + 2);
+      for (int i = 0; i < nqt; ++i) {
+        const uint32_t T = T0 + i;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const bool more = m == 0 || i + 1 < nqt;
+          const uint32_t T1 = T + m;  // the next step's tile
+          // P is in TMEM, and the next step's Q has landed: the compute warps waited for it
+          named_sync(kBarP, kBarCount);
+          // the previous item's epilogue must have read dV and dK
+          if (ok && i == 0 && m == 0 && it > 0) ok = wait_el(&ctl->bar_acc_free, (it - 1) & 1);
+          if (ok) {
+            tc_fence_after();
+            issue_dv(T, i == 0 && m == 0, !more, m ? idesc2 : kIdescV);
+            if (more) issue_s(T1, 1 - m);
+          }
+          __syncwarp();
+          named_sync(kBarDS, kBarCount);
+          if (ok) {
+            tc_fence_after();
+            issue_dk(T, m, i == 0);
+            if (more) issue_dp(T1);
+          }
+          __syncwarp();
         }
       }
       if (el) {
@@ -413,116 +429,121 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      G0 += n;
+      T0 += nqt;
       ++it;
     }
   } else {
-    // ------------------------------------------------------------ compute: warpgroup wg takes steps of its parity
-    const int wg = warp >> 2;
+    // ------------------------------------------------------------ compute: quarter cq of the queries of every step
+    const int cq = warp >> 2;
     const int jrow = (warp & 3) * 32 + lane;  // key row = TMEM lane
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t tX = tl + wg * kStage + kX, tY = tl + wg * kStage + kY;
+    const uint32_t tS = tl + kColS + 32 * cq, tP = tl + kColDP + 32 * cq;
     bool ok = true;
-    uint32_t G0 = 0, it = 0;
-    for (int item = blockIdx.x; ok && item < num_items; item += gridDim.x) {
+    uint32_t T0 = 0, G = 0, it = 0;  // G: steps so far
+    for (int item = blockIdx.x; item < num_items; item += gridDim.x) {
       const Item w = decode_item(item, nkt, H, head_inner);
       const int j = w.t * kTile + jrow;
       const bool exists = j < Sk;
-      // this thread writes half of the row's columns: half wg
-      const size_t off = (((size_t)w.b * Sk + (exists ? j : 0)) * H + w.h) * D + wg * (D / 2);
-      const bool store = exists && guard_store(ctx, off, D / 2, k_extent);
+      // this thread writes a quarter of the row's columns
+      const size_t off = (((size_t)w.b * Sk + (exists ? j : 0)) * H + w.h) * D + cq * (D / 4);
+      const bool store = exists && guard_store(ctx, off, D / 4, k_extent);
       if (kMask && !tile_any(key_mask, w.b, w.t, Sk)) {
         // no attended key in this tile: dK = dV = 0
         if (store) {
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
+          for (int c = 0; c < D / 32; ++c) {
             *reinterpret_cast<uint4*>(dk + off + 8 * c) = make_uint4(0u, 0u, 0u, 0u);
             *reinterpret_cast<uint4*>(dv + off + 8 * c) = make_uint4(0u, 0u, 0u, 0u);
           }
         }
         continue;
       }
-      const bool attended = exists && (!kMask || key_mask[(size_t)w.b * Sk + j] != 0);
-      const float neg_lam = -load_lambda(lam, lam_bf16, w.h);
-      const float2 nl = make_float2(neg_lam, neg_lam), c2 = make_float2(scale_log2, scale_log2);
-      for (int g = 0; g < n; ++g) {
-        const uint32_t G = G0 + g, ph = (G >> 1) & 1;
-        if ((G & 1) != (uint32_t)wg) continue;
-        const float* rv = reinterpret_cast<const float*>(smem + L::kRows + (G % R) * 4 * kStep * 4);
-        bool okw = wait_or_abort(&ctl->bar_full[G % R], (G / R) & 1, ctx, ctl);
-        if (okw) okw = wait_or_abort(&ctl->bar_s_full[wg], ph, ctx, ctl);
-        if (!(ok = __all_sync(0xffffffffu, okw))) break;
-        tc_fence_after();
-        float p1[kStep], p2[kStep];  // A_1 and -lambda A_2
+      const float2 c2 = make_float2(scale_log2, scale_log2);
+      for (int i = 0; i < nqt; ++i) {
+        const uint32_t T = T0 + i, slot = T % R;
+        const bool last = i + 1 == nqt;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float s[64];
-          tmem_ld32x2(tX + 32 * c, tY + 32 * c, s);
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int q = 32 * c + 2 * i;
-            const float2 x1 = fma2(make_float2(s[2 * i], s[2 * i + 1]), c2, *reinterpret_cast<const float2*>(rv + q));
-            const float2 x2 = fma2(make_float2(s[32 + 2 * i], s[33 + 2 * i]), c2,
-                                   *reinterpret_cast<const float2*>(rv + kStep + q));
-            const float2 a = make_float2(ex2(x1.x), ex2(x1.y));
-            const float2 b = mul2(make_float2(ex2(x2.x), ex2(x2.y)), nl);
-            p1[q] = a.x, p1[q + 1] = a.y, p2[q] = b.x, p2[q + 1] = b.y;
-            pk[i] = pack_bf16(a.x + b.x, a.y + b.y);
+        for (int m = 0; m < 2; ++m, ++G) {
+          const float* rv = reinterpret_cast<const float*>(smem + L::kRows + slot * kRowBytes) + m * kTile + 32 * cq;
+          if (ok) {
+            // S, and the row vectors with this tile (m = 0), or the next tile, which the product released by this
+            // step's first arrival reads
+            const uint32_t Tw = m == 0 || last ? T : T + 1;
+            ok = __all_sync(0xffffffffu, wait_two(&ctl->bar_s_full, G & 1, &ctl->bar_full[Tw % R], (Tw / R) & 1, ctx,
+                                                  ctl));
           }
-          tmem_st16_bits(tX + 16 * c, pk);  // P^T, over columns of S_1^T that were read
-        }
-        tc_fence_before();
-        mbar_arrive(&ctl->bar_p_ready[wg]);
-        if (!(ok = __all_sync(0xffffffffu, wait_or_abort(&ctl->bar_dp_full[wg], ph, ctx, ctl)))) break;
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float dp[16];
-          tmem_ld16(tY + 16 * c, dp);
-          uint32_t k1[8], k2[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int q = 16 * c + 2 * i;
-            const float2 d = make_float2(dp[2 * i], dp[2 * i + 1]);
-            const float2 a = mul2(make_float2(p1[q], p1[q + 1]),
-                                  sub2(d, *reinterpret_cast<const float2*>(rv + 2 * kStep + q)));
-            const float2 b = mul2(make_float2(p2[q], p2[q + 1]),
-                                  sub2(d, *reinterpret_cast<const float2*>(rv + 3 * kStep + q)));
-            k1[i] = pack_bf16(a.x, a.y);
-            k2[i] = pack_bf16(b.x, b.y);
+          if (!ok) {
+            // after a failure: keep meeting the issuer, a rendezvous at every step of the schedule
+            named_sync(kBarP, kBarCount);
+            named_sync(kBarDS, kBarCount);
+            continue;
           }
-          tmem_st8_bits(tY + 8 * c, k1);        // dS_1^T, over columns of dA^T that were read
-          tmem_st8_bits(tX + 32 + 8 * c, k2);   // dS_2^T, beside P^T
+          tc_fence_after();
+          float p[32];  // A_1 or |lambda| A_2
+          tmem_ld32(tS, p);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float4 r = *reinterpret_cast<const float4*>(rv + 4 * c);
+            const float2 x = fma2(make_float2(p[4 * c], p[4 * c + 1]), c2, make_float2(r.x, r.y));
+            const float2 y = fma2(make_float2(p[4 * c + 2], p[4 * c + 3]), c2, make_float2(r.z, r.w));
+            p[4 * c] = ex2(x.x), p[4 * c + 1] = ex2(x.y), p[4 * c + 2] = ex2(y.x), p[4 * c + 3] = ex2(y.y);
+          }
+          store_packed32(tS, p);
+          tc_fence_before();
+          named_arrive(kBarP, kBarCount);
+          ok = __all_sync(0xffffffffu, wait_or_abort(&ctl->bar_dp_full, G & 1, ctx, ctl));
+          if (!ok) {
+            named_sync(kBarDS, kBarCount);
+            continue;
+          }
+          tc_fence_after();
+          float dp[32];
+          tmem_ld32(tP, dp);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float4 r = *reinterpret_cast<const float4*>(rv + 2 * kTile + 4 * c);
+            const float2 x = mul2(make_float2(p[4 * c], p[4 * c + 1]),
+                                  sub2(make_float2(dp[4 * c], dp[4 * c + 1]), make_float2(r.x, r.y)));
+            const float2 y = mul2(make_float2(p[4 * c + 2], p[4 * c + 3]),
+                                  sub2(make_float2(dp[4 * c + 2], dp[4 * c + 3]), make_float2(r.z, r.w)));
+            dp[4 * c] = x.x, dp[4 * c + 1] = x.y, dp[4 * c + 2] = y.x, dp[4 * c + 3] = y.y;
+          }
+          store_packed32(tP, dp);
+          // dV's and dK's products both read A from TMEM and differ in shape: where no other product stands
+          // between them, dV has to have completed
+          if (m == 1 && last) ok = __all_sync(0xffffffffu, wait_or_abort(&ctl->bar_dv_done, it & 1, ctx, ctl));
+          tc_fence_before();
+          named_arrive(kBarDS, kBarCount);
         }
-        tc_fence_before();
-        mbar_arrive(&ctl->bar_ds_ready[wg]);
       }
-      if (!ok) break;
-      G0 += n;
+      T0 += nqt;
       // epilogue: dV, and dK = scale * (dS^T Q).  A key outside the mask gets zeros, whatever its rows hold.
-      if (!(ok = __all_sync(0xffffffffu, wait_or_abort(&ctl->bar_acc_done, it & 1, ctx, ctl)))) break;
+      if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(&ctl->bar_acc_done, it & 1, ctx, ctl));
+      ++it;
+      if (!ok) continue;
       tc_fence_after();
-      const uint32_t cV = tl + kColDV + wg * (D / 2), cK = tl + kColDK + 64 * wg + (D == 64 ? 32 * wg : 0);
-#pragma unroll 1
+      const bool attended = exists && (!kMask || key_mask[(size_t)w.b * Sk + j] != 0);
+      const float ck = cq >= 2 && load_lambda(lam, lam_bf16, w.h) > 0.f ? -scale : scale;
+      const uint32_t cV = tl + kColDV + cq * (D / 4);
+      const uint32_t cK = tl + kColDK + cq * (D / 4) + (D == 64 ? (cq >> 1) * 64 : 0);
+#pragma unroll
       for (int c = 0; c < D / 64; ++c) {
-        float gv[64];
-        tmem_ld32x2(cV + 32 * c, cK + 32 * c, gv);
+        float gv[16], gk[16];
+        tmem_ld16(cV + 16 * c, gv);
+        tmem_ld16(cK + 16 * c, gk);
         if (!attended) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i) gv[i] = 0.f;
+          for (int x = 0; x < 16; ++x) gv[x] = gk[x] = 0.f;
         }
         if (store) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            store8(dv + off + 32 * c + 8 * i, gv + 8 * i, 1.f);
-            store8(dk + off + 32 * c + 8 * i, gv + 32 + 8 * i, scale);
-          }
+          store8(dv + off + 16 * c, gv, 1.f);
+          store8(dv + off + 16 * c + 8, gv + 8, 1.f);
+          store8(dk + off + 16 * c, gk, ck);
+          store8(dk + off + 16 * c + 8, gk + 8, ck);
         }
       }
       tc_fence_before();
       mbar_arrive(&ctl->bar_acc_free);
-      ++it;
     }
   }
 
@@ -547,34 +568,35 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// 4. dQ.  A persistent CTA takes 128 queries of one (batch, head), Q and dO in shared memory, and loops over steps
-// of 64 keys: S_m = Q_m K_m^T, dA = dO V^T (M = queries, N = 64), then dQ_m += dS_m K_m.
-// TMEM, per step parity 192 columns: S_1 (then dS_1), S_2 (then dS_2), dA; dQ_m at 384 + 64 m (with D = 64 the
-// product runs over all 64 columns of K and map m's 32 are kept).  One elected lane issues dQ_g and the three
-// products of step g + 2 after ds_ready(g).
+// 4. dQ.  A persistent CTA takes 128 queries of one (batch, head), Q and dO in shared memory, and walks the key
+// tiles: S_m = Q_m K_m^T, dA = dO V^T (M = queries, N = 128 keys), then dQ_m += dS_m K_m.  The maps take turns:
+// while the compute warps work on map 2 of tile g, the tensor cores form dQ_1 of tile g and S_1 of tile g + 1;
+// then dA of tile g + 1, dQ_2 and S_2 while they take map 1's exponentials.
+// TMEM: S_1 at column 0, S_2 at 128 (dS_m, packed, over the first 16 columns of each warpgroup's 32), dA at 256,
+// dQ_m at 384 + 64 m (with D = 64 the product runs over all 64 columns of K and map m's 32 are kept).
 template <int D>
 struct DqLayout {
   static constexpr int kTileBytes = 128 * D * 2;
-  static constexpr int kStepBytes = kStep * D * 2;
-  static constexpr int kRing = D == 128 ? 5 : 8;
+  static constexpr int kKRing = D == 128 ? 3 : 6;  // a K slot is freed by dQ_2, a V slot already by dA
+  static constexpr int kVRing = D == 128 ? 2 : 5;
   static constexpr int kQ = 0;
   static constexpr int kDO = kQ + kTileBytes;
   static constexpr int kK = kDO + kTileBytes;
-  static constexpr int kV = kK + kRing * kStepBytes;
-  static constexpr int kCtl = kV + kRing * kStepBytes;
-  static constexpr int kCnt = kCtl + 384;  // attended steps per mask row
+  static constexpr int kV = kK + kKRing * kTileBytes;
+  static constexpr int kCtl = kV + kVRing * kTileBytes;
+  static constexpr int kCnt = kCtl + 384;  // attended key tiles per mask row
   static constexpr int kSmem = kCnt + kMaxCntRows * 4;
   static_assert(kSmem <= 232448, "shared memory exceeds the per-CTA limit");
 };
 
 struct DqCtl {
   uint64_t bar_q_full, bar_q_empty;
-  uint64_t bar_full[8], bar_empty[8];
-  uint64_t bar_s_full[2], bar_ds_ready[2];
+  uint64_t bar_k_full[6], bar_k_empty[6], bar_v_full[5], bar_v_empty[5];
+  uint64_t bar_s_full[2], bar_dp_full;
   uint64_t bar_dq_done, bar_dq_free, bar_final;
   uint32_t tmem_base;
   int abort;
-  uint32_t mask_words[8][2];  // per ring slot: the attended keys of its step
+  uint32_t mask_words[6][4];  // per K slot: the attended keys of its tile
 };
 static_assert(sizeof(DqCtl) <= 384, "control block");
 
@@ -587,10 +609,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                    int num_items, float scale, float scale_log2, DevCtx ctx) {
   using L = DqLayout<D>;
   constexpr int kChunks = D / 64;
-  constexpr int R = L::kRing;
-  constexpr uint32_t kIdescS = idesc_bf16_f32(128, kStep, false, false);  // S, dA
+  constexpr int KR = L::kKRing, VR = L::kVRing;
+  constexpr uint32_t kIdescS = idesc_bf16_f32(128, kTile, false, false);  // S, dA
   constexpr uint32_t kIdescQ = idesc_bf16_f32(128, 64, false, true);      // dQ_m (A in TMEM)
-  constexpr uint32_t kStage = 192, kColDP = 128, kColDQ = 384;
+  constexpr uint32_t kColDP = 256, kColDQ = 384;
 
   extern __shared__ __align__(1024) uint8_t smem[];
   DqCtl* ctl = reinterpret_cast<DqCtl*>(smem + L::kCtl);
@@ -602,21 +624,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int nqt = tiles_of(Sq);
-  const int nks = (Sk + kStep - 1) / kStep;
+  const int nkt = tiles_of(Sk);
 
   if (threadIdx.x == 0) {
     mbar_init(&ctl->bar_q_full, 1);
     mbar_init(&ctl->bar_q_empty, 1);
-    for (int s = 0; s < R; ++s) {
-      mbar_init(&ctl->bar_full[s], 1);
-      mbar_init(&ctl->bar_empty[s], 1);
+    for (int s = 0; s < KR; ++s) {
+      mbar_init(&ctl->bar_k_full[s], 1);
+      mbar_init(&ctl->bar_k_empty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&ctl->bar_s_full[s], 1);
-      mbar_init(&ctl->bar_ds_ready[s], 128);
+    for (int s = 0; s < VR; ++s) {
+      mbar_init(&ctl->bar_v_full[s], 1);
+      mbar_init(&ctl->bar_v_empty[s], 1);
     }
+    mbar_init(&ctl->bar_s_full[0], 1);
+    mbar_init(&ctl->bar_s_full[1], 1);
+    mbar_init(&ctl->bar_dp_full, 1);
     mbar_init(&ctl->bar_dq_done, 1);
-    mbar_init(&ctl->bar_dq_free, 256);
+    mbar_init(&ctl->bar_dq_free, kCompute);
     mbar_init(&ctl->bar_final, 1);
     ctl->abort = 0;
     fence_mbar_init();
@@ -631,31 +656,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&ctl->tmem_base, 512);
     tmem_relinquish();
   }
-  // Attended steps per mask row: every role takes its step count from this table, which no one writes after the
-  // start; only the producer reads the mask itself and leaves each step's bits with its ring slot.
-  int* step_cnt = reinterpret_cast<int*>(smem + L::kCnt);
+  // Attended key tiles per mask row: every role takes its tile count from this table, which no one writes after the
+  // start; only the producer reads the mask itself and leaves each tile's bits with its K slot.
+  int* tile_cnt = reinterpret_cast<int*>(smem + L::kCnt);
   const bool skip = kMask && B <= kMaxCntRows;
   if (skip) {
-    for (int r = threadIdx.x; r < B; r += kThreads) step_cnt[r] = 0;
+    for (int r = threadIdx.x; r < B; r += kThreads) tile_cnt[r] = 0;
     __syncthreads();
-    const int pairs = B * nks;
-    for (int p0 = warp * 4; p0 < pairs; p0 += (kThreads / 32) * 4) {
-      bool any[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int pr = p0 + u;
-        bool hit = false;
-        if (pr < pairs) {
-          const int r = pr / nks, k0 = (pr - r * nks) * kStep;
-          const uint8_t* row = key_mask + (size_t)r * Sk + k0;
-          hit = (k0 + lane < Sk && row[lane] != 0) || (k0 + 32 + lane < Sk && row[32 + lane] != 0);
-        }
-        any[u] = hit;
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (__any_sync(0xffffffffu, any[u]) && lane == 0 && p0 + u < pairs) atomicAdd(&step_cnt[(p0 + u) / nks], 1);
-    }
+    for (int pr = warp; pr < B * nkt; pr += kThreads / 32)
+      if (tile_any(key_mask, pr / nkt, pr % nkt, Sk) && lane == 0) atomicAdd(&tile_cnt[pr / nkt], 1);
   }
   tc_fence_before();
   __syncthreads();
@@ -663,9 +672,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = ctl->tmem_base;
   const MmaGuard mg = mma_guard(ctx, sbase, L::kSmem, tmem, 512);  // debug builds' operand checks
   const size_t q_extent = (size_t)B * Sq * H * D;
-  auto item_steps = [&](int b) { return skip ? step_cnt[b] : nks; };
+  auto item_tiles = [&](int b) { return skip ? tile_cnt[b] : nkt; };
 
-  uint32_t armed[8] = {}, q_armed = 0;
+  uint32_t k_armed[6] = {}, v_armed[5] = {}, q_armed = 0;
   bool mma_issued = false;
 
   if (warp == kProducerWarp) {
@@ -674,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t G = 0, it = 0;
     for (int item = blockIdx.x; ok && item < num_items; item += gridDim.x) {
       const Item w = decode_item(item, nqt, H, false);
-      if (item_steps(w.b) == 0) continue;  // no attended key: the compute warps write dQ = 0
+      if (item_tiles(w.b) == 0) continue;  // no attended key: the compute warps write dQ = 0
       if (lane == 0) {
         if (it > 0) ok = wait_or_abort(&ctl->bar_q_empty, (it - 1) & 1, ctx, ctl);
         if (ok) {
@@ -689,34 +698,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
       ++it;
-      for (int j = 0; ok && j < nks; ++j) {
-        uint32_t words[2] = {0u, 0u};
+      for (int j = 0; ok && j < nkt; ++j) {
+        uint32_t words[4] = {0u, 0u, 0u, 0u};
         if (kMask) {
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const int c = j * kStep + 32 * t + lane;
+          for (int t = 0; t < 4; ++t) {
+            const int c = j * kTile + 32 * t + lane;
             words[t] = __ballot_sync(0xffffffffu, c < Sk && key_mask[(size_t)w.b * Sk + c] != 0);
           }
-          if (skip && (words[0] | words[1]) == 0) continue;
+          if (skip && (words[0] | words[1] | words[2] | words[3]) == 0) continue;
         }
-        const int slot = G % R;
-        const uint32_t use = G / R;
         if (lane == 0) {
-          if (use > 0) ok = wait_or_abort(&ctl->bar_empty[slot], (use - 1) & 1, ctx, ctl);
+          const int ks = G % KR, vs = G % VR;
+          if (G / KR > 0) ok = wait_or_abort(&ctl->bar_k_empty[ks], (G / KR - 1) & 1, ctx, ctl);
           if (ok) {
-            ctl->mask_words[slot][0] = words[0];
-            ctl->mask_words[slot][1] = words[1];
-            if ((int)G != ctx.drop_load) {
-              mbar_arrive_expect_tx(&ctl->bar_full[slot], 2 * L::kStepBytes);
 #pragma unroll
-              for (int c = 0; c < kChunks; ++c) {
-                tma_load_4d(smem + L::kK + slot * L::kStepBytes + c * kStepChunk, &tmK, &ctl->bar_full[slot], c * 64,
-                            w.h, j * kStep, w.b);
-                tma_load_4d(smem + L::kV + slot * L::kStepBytes + c * kStepChunk, &tmV, &ctl->bar_full[slot], c * 64,
-                            w.h, j * kStep, w.b);
-              }
-              armed[slot] = use + 1;
+            for (int t = 0; t < 4; ++t) ctl->mask_words[ks][t] = words[t];
+            if ((int)G != ctx.drop_load) {
+              mbar_arrive_expect_tx(&ctl->bar_k_full[ks], L::kTileBytes);
+#pragma unroll
+              for (int c = 0; c < kChunks; ++c)
+                tma_load_4d(smem + L::kK + ks * L::kTileBytes + c * kChunkBytes, &tmK, &ctl->bar_k_full[ks], c * 64,
+                            w.h, j * kTile, w.b);
+              k_armed[ks] = G / KR + 1;
             }
+            if (G / VR > 0) ok = wait_or_abort(&ctl->bar_v_empty[vs], (G / VR - 1) & 1, ctx, ctl);
+          }
+          if (ok) {
+            mbar_arrive_expect_tx(&ctl->bar_v_full[vs], L::kTileBytes);
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c)
+              tma_load_4d(smem + L::kV + vs * L::kTileBytes + c * kChunkBytes, &tmV, &ctl->bar_v_full[vs], c * 64, w.h,
+                          j * kTile, w.b);
+            v_armed[vs] = G / VR + 1;
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -734,67 +748,86 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (el) w = wait_or_abort(bar, parity, ctx, ctl);
       return __shfl_sync(0xffffffffu, w ? 1 : 0, el_lane) != 0;
     };
-    auto sk = [&](uint32_t G) { return sbase + L::kK + (G % R) * L::kStepBytes; };
-    auto sv = [&](uint32_t G) { return sbase + L::kV + (G % R) * L::kStepBytes; };
-    auto step_off = [](int kk) { return (uint32_t)((kk >> 2) * kStepChunk + (kk & 3) * 32); };
-    auto tile_off = [](int kk) { return (uint32_t)((kk >> 2) * kChunkBytes + (kk & 3) * 32); };
-    // S_1, S_2 and dA of step G
-    auto issue_kk = [&](uint32_t G) {
-      const uint32_t d = tmem + (G & 1) * kStage;
+    auto sk = [&](uint32_t G) { return sbase + L::kK + (G % KR) * L::kTileBytes; };
+    auto issue_s = [&](uint32_t G, int m) {
       const uint64_t a0 = sdesc_sw128(sbase + L::kQ, 16, 1024), b0 = sdesc_sw128(sk(G), 16, 1024);
-      const uint64_t a1 = sdesc_sw128(sbase + L::kDO, 16, 1024), b1 = sdesc_sw128(sv(G), 16, 1024);
+#pragma unroll
+      for (int kk = 0; kk < D / 32; ++kk) {
+        const uint32_t off = m ? map_step<D>(1, kk) : map_step<D>(0, kk);
+        const uint64_t a = desc_add(a0, off), b = desc_add(b0, off);
+        if (el) mma_ss_checked(mg, tmem + m * kTile, a, b, kIdescS, kk > 0, kTile);
+      }
+      if (el) mma_commit(&ctl->bar_s_full[m]);
+    };
+    auto issue_dp = [&](uint32_t G) {
+      const uint64_t a0 = sdesc_sw128(sbase + L::kDO, 16, 1024);
+      const uint64_t b0 = sdesc_sw128(sbase + L::kV + (G % VR) * L::kTileBytes, 16, 1024);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        const int m = kk >= D / 32;
-        const uint64_t a = desc_add(a0, tile_off(kk)), b = desc_add(b0, step_off(kk));
-        if (el) mma_ss_checked(mg, d + (m ? 64 : 0), a, b, kIdescS, kk % (D / 32) > 0, kStep);
+        const uint32_t off = (kk >> 2) * kChunkBytes + (kk & 3) * 32;
+        const uint64_t a = desc_add(a0, off), b = desc_add(b0, off);
+        if (el) mma_ss_checked(mg, tmem + kColDP, a, b, kIdescS, kk > 0, kTile);
       }
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint64_t a = desc_add(a1, tile_off(kk)), b = desc_add(b1, step_off(kk));
-        if (el) mma_ss_checked(mg, d + kColDP, a, b, kIdescS, kk > 0, kStep);
+      if (el) {
+        mma_commit(&ctl->bar_dp_full);
+        mma_commit(&ctl->bar_v_empty[G % VR]);
       }
-      if (el) mma_commit(&ctl->bar_s_full[G & 1]);
     };
-    auto issue_dq = [&](uint32_t G, bool first) {
+    auto issue_dq = [&](uint32_t G, int m, bool first) {
+      const uint64_t b0 = sdesc_sw128(sk(G) + (D == 128 ? m * kChunkBytes : 0), kChunkBytes, 1024);
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const uint64_t b0 = sdesc_sw128(sk(G) + (D == 128 ? m * kStepChunk : 0), kStepChunk, 1024);
-        const uint32_t a = tmem + (G & 1) * kStage + 64 * m;
-#pragma unroll
-        for (int kk = 0; kk < kStep / 16; ++kk) {
-          const uint64_t b = desc_add(b0, kk * 2048);
-          if (el)
-            mma_ts_checked(mg, tmem + kColDQ + 64 * m, a + kk * 8, b, kIdescQ, (!first || kk > 0) ? 1u : 0u, 64);
-        }
+      for (int kk = 0; kk < kTile / 16; ++kk) {
+        const uint64_t b = desc_add(b0, kk * 2048);
+        if (el)
+          mma_ts_checked(mg, tmem + kColDQ + 64 * m, tmem + m * kTile + packed_col(kk), b, kIdescQ,
+                         (!first || kk > 0) ? 1u : 0u, 64);
       }
-      if (el) mma_commit(&ctl->bar_empty[G % R]);
+      if (el && m == 1) mma_commit(&ctl->bar_k_empty[G % KR]);
     };
-    for (int item = blockIdx.x; ok && item < num_items; item += gridDim.x) {
+    for (int item = blockIdx.x; item < num_items; item += gridDim.x) {
       const Item w = decode_item(item, nqt, H, false);
-      const int n = item_steps(w.b);
+      const int n = item_tiles(w.b);
       if (n == 0) continue;
-      ok = wait_el(&ctl->bar_q_full, it & 1);
-      for (int g = 0; ok && g < 2 && g < n; ++g) {
-        if (!(ok = wait_el(&ctl->bar_full[(G0 + g) % R], ((G0 + g) / R) & 1))) break;
+      if (ok && *reinterpret_cast<volatile int*>(&ctl->abort)) ok = false;  // see the dK/dV kernel
+      if (ok) ok = wait_el(&ctl->bar_q_full, it & 1);
+      if (ok) ok = wait_el(&ctl->bar_k_full[G0 % KR], (G0 / KR) & 1);
+      if (ok) {
         tc_fence_after();
-        issue_kk(G0 + g);
+        issue_s(G0, 0);
         if (el) mma_issued = true;
+        ok = wait_el(&ctl->bar_v_full[G0 % VR], (G0 / VR) & 1);
       }
-      if (ok && el && n <= 2) mma_commit(&ctl->bar_q_empty);
-      for (int g = 0; ok && g < n; ++g) {
-        const uint32_t G = G0 + g;
-        if (!(ok = wait_el(&ctl->bar_ds_ready[G & 1], (G >> 1) & 1))) break;
-        // the previous item's epilogue must have read dQ
-        if (g == 0 && it > 0 && !(ok = wait_el(&ctl->bar_dq_free, (it - 1) & 1))) break;
+      if (ok) {
         tc_fence_after();
-        issue_dq(G, g == 0);
-        if (g + 2 < n) {
-          if (!(ok = wait_el(&ctl->bar_full[(G + 2) % R], ((G + 2) / R) & 1))) break;
+        issue_dp(G0);
+        issue_s(G0, 1);
+        if (el && n == 1) mma_commit(&ctl->bar_q_empty);
+      }
+      for (int g = 0; g < n; ++g) {
+        const uint32_t G = G0 + g;
+        const bool more = g + 1 < n;
+        // dS_1 is in TMEM and the next K tile has landed: the compute warps waited for it
+        named_sync(kBarP, kBarCount);
+        // the previous item's epilogue must have read dQ
+        if (ok && g == 0 && it > 0) ok = wait_el(&ctl->bar_dq_free, (it - 1) & 1);
+        if (ok) {
           tc_fence_after();
-          issue_kk(G + 2);
-          if (el && g + 3 == n) mma_commit(&ctl->bar_q_empty);  // the item's last products with Q and dO
+          issue_dq(G, 0, g == 0);
+          if (more) issue_s(G + 1, 0);
         }
+        __syncwarp();
+        // dS_2 is in TMEM, dA has been read, and the next V tile has landed
+        named_sync(kBarDS, kBarCount);
+        if (ok) {
+          tc_fence_after();
+          if (more) issue_dp(G + 1);
+          issue_dq(G, 1, g == 0);
+          if (more) {
+            issue_s(G + 1, 1);
+            if (el && g + 2 == n) mma_commit(&ctl->bar_q_empty);  // the item's last products with Q and dO
+          }
+        }
+        __syncwarp();
       }
       if (el) {
         if (ok)
@@ -807,108 +840,128 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++it;
     }
   } else {
-    // ------------------------------------------------------------ compute: warpgroup wg takes steps of its parity
-    const int wg = warp >> 2;
+    // ------------------------------------------------------------ compute: quarter cq of the keys of every tile
+    const int cq = warp >> 2;
     const int row = (warp & 3) * 32 + lane;  // query row = TMEM lane
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t tS = tl + wg * kStage;
+    const uint32_t tS = tl + 32 * cq;
     bool ok = true;
     uint32_t G0 = 0, it = 0;
-    for (int item = blockIdx.x; ok && item < num_items; item += gridDim.x) {
+    for (int item = blockIdx.x; item < num_items; item += gridDim.x) {
       const Item w = decode_item(item, nqt, H, false);
-      const int n = item_steps(w.b);
+      const int n = item_tiles(w.b);
       const int i = w.t * kTile + row;
-      // this thread writes half of the row's columns: map wg's
-      const size_t off = (((size_t)w.b * Sq + (i < Sq ? i : 0)) * H + w.h) * D + wg * (D / 2);
-      const bool store = i < Sq && guard_store(ctx, off, D / 2, q_extent);
+      // this thread writes a quarter of the row's columns
+      const size_t off = (((size_t)w.b * Sq + (i < Sq ? i : 0)) * H + w.h) * D + cq * (D / 4);
+      const bool store = i < Sq && guard_store(ctx, off, D / 4, q_extent);
       if (n == 0) {
         if (store) {
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) *reinterpret_cast<uint4*>(dq + off + 8 * c) = make_uint4(0u, 0u, 0u, 0u);
+          for (int c = 0; c < D / 32; ++c) *reinterpret_cast<uint4*>(dq + off + 8 * c) = make_uint4(0u, 0u, 0u, 0u);
         }
         continue;
       }
       const float* rv = rows + rows_at((size_t)w.b * H + w.h, Sq, i);  // rows past Sq: -inf and 0
-      const float n1 = rv[0], n2 = rv[kStep], d1 = rv[2 * kStep], d2 = rv[3 * kStep];
-      const float neg_lam = -load_lambda(lam, lam_bf16, w.h);
-      const float2 c2 = make_float2(scale_log2, scale_log2), nl = make_float2(neg_lam, neg_lam);
+      const float2 c2 = make_float2(scale_log2, scale_log2);
+      const float nl2[2] = {rv[0], rv[kTile]}, delta[2] = {rv[2 * kTile], rv[3 * kTile]};
       for (int g = 0; g < n; ++g) {
-        const uint32_t G = G0 + g;
-        if ((G & 1) != (uint32_t)wg) continue;
-        const int slot = G % R;
-        bool okw = wait_or_abort(&ctl->bar_full[slot], (G / R) & 1, ctx, ctl);
-        if (okw) okw = wait_or_abort(&ctl->bar_s_full[wg], (G >> 1) & 1, ctx, ctl);
-        if (!(ok = __all_sync(0xffffffffu, okw))) break;
-        tc_fence_after();
-        uint32_t words[2] = {0xffffffffu, 0xffffffffu};
+        const uint32_t G = G0 + g, ks = G % KR;
+        const bool more = g + 1 < n;
+        if (ok) {
+          // S_1, and the next K tile, which the product released by this tile's first arrival reads
+          const uint32_t Gw = more ? G + 1 : G;
+          ok = __all_sync(0xffffffffu, wait_two(&ctl->bar_s_full[0], G & 1, &ctl->bar_k_full[Gw % KR], (Gw / KR) & 1,
+                                                ctx, ctl));
+        }
+        if (!ok) {
+          // after a failure: keep meeting the issuer
+          named_sync(kBarP, kBarCount);
+          named_sync(kBarDS, kBarCount);
+          continue;
+        }
+        uint32_t word = 0xffffffffu;  // the attended keys of this quarter
         if (kMask) {
-          words[0] = ctl->mask_words[slot][0];
-          words[1] = ctl->mask_words[slot][1];
-        } else if (g == n - 1 && Sk % kStep) {  // keys past the end
-          const int left = Sk % kStep;
-          words[0] = left >= 32 ? 0xffffffffu : (1u << left) - 1u;
-          words[1] = left > 32 ? (1u << (left - 32)) - 1u : 0u;
-        }
+          if (g == 0) ok = __all_sync(0xffffffffu, wait_or_abort(&ctl->bar_k_full[ks], (G / KR) & 1, ctx, ctl));
+          word = ctl->mask_words[ks][cq];
+          // K's rows outside the mask are read as zeros by the dQ products; where S_2 is still being formed, it
+          // is only masked columns that change
+          const int r = threadIdx.x >> 2;
+          if (!((ctl->mask_words[ks][r >> 5] >> (r & 31)) & 1u)) {
+            const int x = (threadIdx.x & 3) * (D / 2);  // byte of the row's 2 D, in 128-byte chunks
+            uint8_t* z = smem + L::kK + ks * L::kTileBytes + (x >> 7) * kChunkBytes + r * 128 + (x & 127);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float s[64], dp[32];
-          tmem_ld32x2(tS + 32 * c, tS + 64 + 32 * c, s);
-          tmem_ld32(tS + kColDP + 32 * c, dp);
-          uint32_t k1[16], k2[16];
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            const float2 x1 = fma2(make_float2(s[2 * x], s[2 * x + 1]), c2, make_float2(n1, n1));
-            const float2 x2 = fma2(make_float2(s[32 + 2 * x], s[33 + 2 * x]), c2, make_float2(n2, n2));
-            const float2 d = make_float2(dp[2 * x], dp[2 * x + 1]);
-            float2 a = mul2(make_float2(ex2(x1.x), ex2(x1.y)), sub2(d, make_float2(d1, d1)));
-            float2 b = mul2(mul2(make_float2(ex2(x2.x), ex2(x2.y)), nl), sub2(d, make_float2(d2, d2)));
-            s[2 * x] = a.x, s[2 * x + 1] = a.y, s[32 + 2 * x] = b.x, s[33 + 2 * x] = b.y;
-          }
-          if (words[c] != 0xffffffffu) {
-            // keys outside the mask, or past the end: dS = 0 whatever their rows hold
-#pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (!((words[c] >> x) & 1u)) s[x] = s[32 + x] = 0.f;
-          }
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            k1[x] = pack_bf16(s[2 * x], s[2 * x + 1]);
-            k2[x] = pack_bf16(s[32 + 2 * x], s[33 + 2 * x]);
-          }
-          tmem_st16_bits(tS + 16 * c, k1);       // over columns of S_1 that were read
-          tmem_st16_bits(tS + 64 + 16 * c, k2);  // and of S_2
-        }
-        if (kMask && (words[0] & words[1]) != 0xffffffffu) {
-          // K's rows outside the mask are read as zeros by the dQ product; S_1 and S_2 have been formed
-          const int r = (threadIdx.x & 127) >> 1, half = threadIdx.x & 1;
-          if (!((words[r >> 5] >> (r & 31)) & 1u)) {
-            uint8_t* p = smem + L::kK + slot * L::kStepBytes + r * 128 + (D == 128 ? half * kStepChunk : half * 64);
-#pragma unroll
-            for (int x = 0; x < D / 16; ++x) *reinterpret_cast<uint4*>(p + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
+            for (int c = 0; c < D / 32; ++c) *reinterpret_cast<uint4*>(z + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
+        } else if (!more) {  // keys past the end
+          const int left = Sk - (nkt - 1) * kTile - 32 * cq;
+          word = left >= 32 ? 0xffffffffu : (left > 0 ? (1u << left) - 1u : 0u);
         }
-        tc_fence_before();
-        mbar_arrive(&ctl->bar_ds_ready[wg]);
+        bool met = false;  // this tile's first arrival has been made
+        float dp[32];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          if (m == 1) {
+            met = true;
+            const uint32_t Gw = more ? G + 1 : G;  // the next V tile, read by the product that dS_2 releases
+            ok = __all_sync(0xffffffffu, wait_two(&ctl->bar_s_full[1], G & 1, &ctl->bar_v_full[Gw % VR],
+                                                  (Gw / VR) & 1, ctx, ctl));
+            if (!ok) break;
+          }
+          tc_fence_after();
+          float p[32];  // A_1 or |lambda| A_2
+          tmem_ld32(tS + m * kTile, p);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float2 x = fma2(make_float2(p[2 * c], p[2 * c + 1]), c2, make_float2(nl2[m], nl2[m]));
+            p[2 * c] = ex2(x.x), p[2 * c + 1] = ex2(x.y);
+          }
+          if (m == 0) {
+            ok = __all_sync(0xffffffffu, wait_or_abort(&ctl->bar_dp_full, G & 1, ctx, ctl));
+            if (!ok) break;
+            tc_fence_after();
+            tmem_ld32(tl + kColDP + 32 * cq, dp);
+          }
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float2 x = mul2(make_float2(p[2 * c], p[2 * c + 1]),
+                                  sub2(make_float2(dp[2 * c], dp[2 * c + 1]), make_float2(delta[m], delta[m])));
+            p[2 * c] = x.x, p[2 * c + 1] = x.y;
+          }
+          if (word != 0xffffffffu) {
+            // keys outside the mask, or past the end: dS = 0 whatever their rows hold
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!((word >> c) & 1u)) p[c] = 0.f;
+          }
+          store_packed32(tS + m * kTile, p);
+          tc_fence_before();
+          named_arrive(m == 0 ? kBarP : kBarDS, kBarCount);
+        }
+        if (!ok) {
+          if (!met) named_sync(kBarP, kBarCount);
+          named_sync(kBarDS, kBarCount);
+        }
       }
-      if (!ok) break;
       G0 += n;
       // epilogue: dQ = scale * (dS K)
-      if (!(ok = __all_sync(0xffffffffu, wait_or_abort(&ctl->bar_dq_done, it & 1, ctx, ctl)))) break;
+      if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(&ctl->bar_dq_done, it & 1, ctx, ctl));
+      ++it;
+      if (!ok) continue;
       tc_fence_after();
-      const uint32_t cQ = tl + kColDQ + 64 * wg + (D == 64 ? 32 * wg : 0);
-#pragma unroll 1
-      for (int c = 0; c < D / 64; ++c) {
-        float gv[32];
-        tmem_ld32(cQ + 32 * c, gv);
-        if (store) {
+      const float cs = cq >= 2 && load_lambda(lam, lam_bf16, w.h) > 0.f ? -scale : scale;
+      const uint32_t cQ = tl + kColDQ + cq * (D / 4) + (D == 64 ? (cq >> 1) * 64 : 0);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) store8(dq + off + 32 * c + 8 * x, gv + 8 * x, scale);
+      for (int c = 0; c < D / 64; ++c) {
+        float gv[16];
+        tmem_ld16(cQ + 16 * c, gv);
+        if (store) {
+          store8(dq + off + 16 * c, gv, cs);
+          store8(dq + off + 16 * c + 8, gv + 8, cs);
         }
       }
       tc_fence_before();
       mbar_arrive(&ctl->bar_dq_free);
-      ++it;
     }
   }
 
@@ -921,8 +974,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == kProducerWarp && lane == 0) {
     if (q_armed) settle(&ctl->bar_q_full, (q_armed - 1) & 1, ctx);
-    for (int s = 0; s < R; ++s)
-      if (armed[s]) settle(&ctl->bar_full[s], (armed[s] - 1) & 1, ctx);
+    for (int s = 0; s < KR; ++s)
+      if (k_armed[s]) settle(&ctl->bar_k_full[s], (k_armed[s] - 1) & 1, ctx);
+    for (int s = 0; s < VR; ++s)
+      if (v_armed[s]) settle(&ctl->bar_v_full[s], (v_armed[s] - 1) & 1, ctx);
   }
   tc_fence_before();
   __syncthreads();
@@ -940,7 +995,7 @@ int prepare(K kern, int smem) {
   return UAA_OK;
 }
 
-size_t row_floats(int B, int Sq, int H) { return (size_t)B * H * steps_of(Sq) * 4 * kStep; }
+size_t row_floats(int B, int Sq, int H) { return (size_t)B * H * tiles_of(Sq) * 4 * kTile; }
 
 template <int D, bool kMask>
 int launch_bwd(const void* q, const void* k, const void* v, const void* lam, int lam_bf16, const void* out,
@@ -954,14 +1009,12 @@ int launch_bwd(const void* q, const void* k, const void* v, const void* lam, int
   if (items_k > INT32_MAX || items_q > INT32_MAX || row_blocks > INT32_MAX)
     return set_error(UAA_ERR_UNSUPPORTED, "uaa_diff_attn_bwd: too many work items");
   DevCtx ctx;
-  SegMaps mq, mk, mv, mdo, sq, sk, sv, sdo;  // tiles of 128 rows, steps of 64
+  SegMaps mq, mk, mv, mdo;
   const SeqDesc qd = seq_plain(Sq), kd = seq_plain(Sk);
   int st;
   if ((st = get_dev_ctx(&ctx)) || (st = encode_seq_maps(&mq, q, qd, B, H, D, kTile)) ||
       (st = encode_seq_maps(&mk, k, kd, B, H, D, kTile)) || (st = encode_seq_maps(&mv, v, kd, B, H, D, kTile)) ||
-      (st = encode_seq_maps(&mdo, dout, qd, B, H, D, kTile)) || (st = encode_seq_maps(&sq, q, qd, B, H, D, kStep)) ||
-      (st = encode_seq_maps(&sk, k, kd, B, H, D, kStep)) || (st = encode_seq_maps(&sv, v, kd, B, H, D, kStep)) ||
-      (st = encode_seq_maps(&sdo, dout, qd, B, H, D, kStep)))
+      (st = encode_seq_maps(&mdo, dout, qd, B, H, D, kTile)))
     return st;
   diff_rows_kernel<D><<<(int)row_blocks, kRowThreads, 0, s>>>(static_cast<const bf*>(out), static_cast<const bf*>(out2),
                                                              static_cast<const bf*>(dout), lse, lam, lam_bf16, rows,
@@ -977,14 +1030,14 @@ int launch_bwd(const void* q, const void* k, const void* v, const void* lam, int
     // tiles spread evenly over the CTAs (as in the plain backward)
     const int head_inner = mask != nullptr && 4LL * H * Sq * D <= (64LL << 20);
     kern<<<(int)(items_k < sms ? items_k : sms), kThreads, DkdvLayout<D>::kSmem, s>>>(
-        sq.m[0], mk.m[0], mv.m[0], sdo.m[0], lam, lam_bf16, rows, mask, static_cast<bf*>(dk), static_cast<bf*>(dv), B,
+        mq.m[0], mk.m[0], mv.m[0], mdo.m[0], lam, lam_bf16, rows, mask, static_cast<bf*>(dk), static_cast<bf*>(dv), B,
         H, Sq, Sk, (int)items_k, head_inner, scale, scale * kLog2e, ctx);
     if ((st = check_launch("uaa_diff_attn_bwd (dK/dV)"))) return st;
   }
   auto kern = diff_dq_kernel<D, kMask>;
   if ((st = prepare(kern, DqLayout<D>::kSmem))) return st;
   kern<<<(int)(items_q < sms ? items_q : sms), kThreads, DqLayout<D>::kSmem, s>>>(
-      mq.m[0], sk.m[0], sv.m[0], mdo.m[0], lam, lam_bf16, rows, mask, static_cast<bf*>(dq), B, H, Sq, Sk, (int)items_q,
+      mq.m[0], mk.m[0], mv.m[0], mdo.m[0], lam, lam_bf16, rows, mask, static_cast<bf*>(dq), B, H, Sq, Sk, (int)items_q,
       scale, scale * kLog2e, ctx);
   return check_launch("uaa_diff_attn_bwd (dQ)");
 }
