@@ -104,6 +104,21 @@ def test_borders_and_special_rows(dtype):
 
 
 @pytest.mark.gpu
+def test_every_bf16_pair():
+    """Every significand under every top's, at every scale where it has a code."""
+    X = torch.cat([torch.arange(128, 256).double() * 2.0 ** -s for s in range(11)])
+    X = torch.cat((X, -X))
+    rows = []
+    for T in range(128, 256):
+        x = X[X.abs() <= T]
+        x = torch.cat((x, torch.zeros(-len(x) % 511))).view(-1, 511)
+        rows.append(torch.cat((torch.full((len(x), 1), float(T)), x), 1))
+    x = torch.cat(rows).bfloat16().to(DEV)
+    assert torch.equal(x.cpu().double(), torch.cat(rows).double())
+    _check(uaa.act8_pack([x]), [x])
+
+
+@pytest.mark.gpu
 def test_what_is_not_finite_shows():
     x = torch.randn(6, 128, device=DEV)
     x[1, 3], x[2, 127], x[4, 0] = math.inf, math.nan, -math.inf

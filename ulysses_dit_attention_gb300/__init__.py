@@ -133,11 +133,12 @@ def _check(status: int):
 
 
 def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    index = torch.device(device).index
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _need_cuda(*ts):
@@ -361,10 +362,13 @@ class Attention(torch.autograd.Function):
         ctx.key_mask = key_mask
         ctx.scale = scale
         ctx.mark_non_differentiable(lse)
+        ctx.set_materialize_grads(False)  # no zeros for lse
         return out, lse
 
     @staticmethod
     def backward(ctx, dout, _dlse):
+        if dout is None:
+            return None, None, None, None, None, None
         (q, k, v, out), (lse,) = _saved(ctx, 4)
         dq, dk, dv = attn_bwd(q, k, v, out, dout.contiguous(), lse, ctx.key_mask, ctx.scale)
         return dq, dk, dv, None, None, None
@@ -383,22 +387,26 @@ def _same_device(*ts):
     for t in ts:
         if t is None:
             continue
-        if not t.is_cuda:
-            raise ValueError("uaa kernels run on CUDA tensors only (no CPU fallback)")
         if first is None:
             first = t.device
+            if first.type != "cuda":
+                raise ValueError("uaa kernels run on CUDA tensors only (no CPU fallback)")
         elif t.device != first:
-            raise ValueError(f"tensors are on {first} and {t.device}")
+            raise ValueError(f"tensors are on {first} and {t.device}: uaa kernels run on CUDA tensors of one device")
     return first
 
 
 def _call(device, name, *args):
     """Calls the library on the tensors' device, on its current stream."""
-    if device.index == torch.cuda.current_device():
-        _check(getattr(lib(), name)(*args, _stream(device)))
+    i = device.index
+    fn = getattr(_lib or lib(), name)
+    if i == torch._C._cuda_getDevice():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(i))
     else:
         with torch.cuda.device(device):
-            _check(getattr(lib(), name)(*args, _stream(device)))
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    if st != 0:
+        _check(st)
 
 
 def _result(name, t, shape, dtype, device):
@@ -454,31 +462,40 @@ def shard_positions(shard_lens, cap, B, device, dtype=torch.int32):
     return at.expand(len(shard_lens), B, cap).reshape(len(shard_lens) * B, cap).contiguous().to(device)
 
 
-def _rotary_tensor(name, x, y):
-    sx, sy = x.stride(), y.stride()
-    return _RotaryTensor(x.data_ptr(), y.data_ptr(), sx[0], sx[1], sx[2], sy[0], sy[1], sy[2], x.shape[2])
+def _rotary_operand(name, t, ref, out):
+    """Checks an operand and its result; returns the library's view of both, and the result."""
+    shape, dtype = t.shape, t.dtype
+    if len(shape) != 4:
+        raise ValueError(f"{name} must be (B, S, H, D), got {tuple(shape)}")
+    if dtype not in _DTYPES or dtype != ref.dtype:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, q and k alike")
+    if t is not ref and (shape[:2] != ref.shape[:2] or shape[3] != ref.shape[3]):
+        raise ValueError(f"{name} shape {tuple(shape)} does not fit {tuple(ref.shape)}")
+    x0, x1, x2, x3 = t.stride()
+    if x3 != 1 and shape[3] > 1:
+        raise ValueError(f"the columns of {name} must be contiguous")
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=t.device)
+    elif out.shape != shape or out.dtype != dtype or out.device != t.device or (shape[3] > 1 and out.stride(3) != 1):
+        raise ValueError(f"out_{name} must be {dtype} {tuple(shape)} on {t.device} with contiguous columns")
+    y0, y1, y2, _ = out.stride()
+    return _RotaryTensor(t.data_ptr(), out.data_ptr(), x0, x1, x2, y0, y1, y2, shape[2]), out
 
 
 def _rotate(q, k, plan, positions, start, inverse, out_q, out_k):
     if not isinstance(plan, RotaryPlan):
         raise TypeError("plan must be a RotaryPlan")
     dev = _same_device(q, k, positions)
-    for n, t in (("q", q), ("k", k)):
-        if t is None:
-            continue
-        if t.dim() != 4:
-            raise ValueError(f"{n} must be (B, S, H, D), got {tuple(t.shape)}")
-        if t.dtype not in _DTYPES or t.dtype != q.dtype:
-            raise TypeError(f"{n} must be bfloat16, float16 or float32, q and k alike")
-        if t.shape[3] > 1 and t.stride(3) != 1:
-            raise ValueError(f"the columns of {n} must be contiguous")
-        if t.shape[:2] != q.shape[:2] or t.shape[3] != q.shape[3]:
-            raise ValueError(f"{n} shape {tuple(t.shape)} does not fit {tuple(q.shape)}")
+    tq, out_q = _rotary_operand("q", q, q, out_q)
+    tk = None
+    if k is not None:
+        tk, out_k = _rotary_operand("k", k, q, out_k)
+        tk = ctypes.byref(tk)
     B, S, _, D = q.shape
     pos, wide, pb, ps = None, 0, 0, 0
     if positions is not None:
         tail = () if plan.axes == 1 else (plan.axes,)
-        if tuple(positions.shape) not in ((S,) + tail, (B, S) + tail):
+        if positions.shape != (B, S) + tail and positions.shape != (S,) + tail:
             raise ValueError(f"positions must be {(S,) + tail} or {(B, S) + tail}, got {tuple(positions.shape)}")
         if positions.dtype not in (torch.int32, torch.int64):
             raise TypeError("positions must be int32 or int64")
@@ -489,21 +506,9 @@ def _rotate(q, k, plan, positions, start, inverse, out_q, out_k):
         at = positions.stride()
         pb, ps = (at[0], at[1]) if positions.dim() == 2 + len(tail) else (0, at[0])
         pos, wide = positions.data_ptr(), int(positions.dtype == torch.int64)
-    outs = []
-    for n, t, y in (("out_q", q, out_q), ("out_k", k, out_k)):
-        if t is None:
-            outs.append(None)
-        elif y is None:
-            outs.append(torch.empty(t.shape, dtype=t.dtype, device=dev))
-        elif y.shape != t.shape or y.dtype != t.dtype or y.device != dev or (D > 1 and y.stride(3) != 1):
-            raise ValueError(f"{n} must be {t.dtype} {tuple(t.shape)} on {dev} with contiguous columns")
-        else:
-            outs.append(y)
-    tq = _rotary_tensor("q", q, outs[0])
-    tk = None if k is None else ctypes.byref(_rotary_tensor("k", k, outs[1]))
     _call(dev, "uaa_rotary", plan._ref, ctypes.byref(tq), tk, pos, wide, pb, ps, int(start), B, S, D,
           _DTYPES[q.dtype], inverse)
-    return outs[0], outs[1]
+    return out_q, out_k
 
 
 def rotary_fwd(q, k, plan, positions=None, start=0, out_q=None, out_k=None):
@@ -568,20 +573,21 @@ class Act8:
         return self.codes.numel() + 4 * self.steps.numel()
 
 
-def _act8_call(name, tensors, codes, steps, swap):
-    n, D = len(tensors), tensors[0].shape[-1]
-    rows = [t.numel() // D for t in tensors]
-    base_c, base_s = codes.data_ptr(), steps.data_ptr()
-    at, pc, ps = 0, [], []
+_ACT8_ARRAYS = [(ctypes.c_void_p * n, _L * n) for n in range(9)]
+
+
+def _act8_call(name, dev, tensors, rows, codes, steps, D, swap):
+    n = len(tensors)
+    ptrs, longs = _ACT8_ARRAYS[n]
+    c, s, pc, ps = codes.data_ptr(), steps.data_ptr(), [], []
     for r in rows:
-        pc.append(base_c + at * D)
-        ps.append(base_s + at * 4)
-        at += r
-    arr = ctypes.c_void_p * n
-    x = arr(*[t.data_ptr() for t in tensors])
-    pc, ps = arr(*pc), arr(*ps)
+        pc.append(c)
+        ps.append(s)
+        c += r * D
+        s += r * 4
+    x, pc, ps = ptrs(*[t.data_ptr() for t in tensors]), ptrs(*pc), ptrs(*ps)
     first = (pc, ps, x) if swap else (x, pc, ps)
-    _call(codes.device, name, n, *first, (_L * n)(*rows), D, _DTYPES[tensors[0].dtype])
+    _call(dev, name, n, *first, longs(*rows), D, _DTYPES[tensors[0].dtype])
 
 
 def act8_pack(x):
@@ -591,30 +597,36 @@ def act8_pack(x):
     ``max|row| / 127``.  Returns an :class:`Act8` for :func:`act8_unpack`.
     """
     single = isinstance(x, torch.Tensor)
-    xs = [x] if single else list(x)
+    xs = (x,) if single else tuple(x)
     if not 1 <= len(xs) <= 8:
         raise ValueError(f"one to eight tensors at a time, got {len(xs)}")
     dev = _same_device(*xs)
-    for t in xs:
-        if t.dtype not in _DTYPES or t.dtype != xs[0].dtype:
-            raise TypeError("tensors must be bfloat16, float16 or float32, all alike")
-        if t.dim() < 1 or t.shape[-1] != xs[0].shape[-1] or not t.is_contiguous():
-            raise ValueError("tensors must be contiguous, with one last dimension")
-    D = xs[0].shape[-1]
-    if D < 1:
+    dtype, shapes = xs[0].dtype, tuple([t.shape for t in xs])
+    if dtype not in _DTYPES:
+        raise TypeError("tensors must be bfloat16, float16 or float32, all alike")
+    if not shapes[0] or not shapes[0][-1]:
         raise ValueError("the last dimension is empty")
-    total = sum(t.numel() for t in xs)
-    codes = torch.empty(total, dtype=torch.int8, device=dev)
-    steps = torch.empty(total // D, dtype=torch.float32, device=dev)
-    _act8_call("uaa_act8_pack", xs, codes, steps, False)
-    return Act8(codes, steps, tuple(tuple(t.shape) for t in xs), xs[0].dtype, single)
+    D = shapes[0][-1]
+    for t, s in zip(xs, shapes):
+        if t.dtype != dtype:
+            raise TypeError("tensors must be bfloat16, float16 or float32, all alike")
+        if not s or s[-1] != D or not t.is_contiguous():
+            raise ValueError("tensors must be contiguous, with one last dimension")
+    rows = [s.numel() // D for s in shapes]
+    total = sum(rows)
+    codes = torch.empty(total * D, dtype=torch.int8, device=dev)
+    steps = torch.empty(total, dtype=torch.float32, device=dev)
+    _act8_call("uaa_act8_pack", dev, xs, rows, codes, steps, D, False)
+    return Act8(codes, steps, shapes, dtype, single)
 
 
 def act8_unpack(packed):
     """``uaa_act8_unpack``: the values that the codes stand for, in the shapes and type of the tensors packed."""
     dev = _same_device(packed.codes, packed.steps)
-    ys = [torch.empty(s, dtype=packed.dtype, device=dev) for s in packed.shapes]
-    _act8_call("uaa_act8_unpack", ys, packed.codes, packed.steps, True)
+    dtype, shapes = packed.dtype, packed.shapes
+    D = shapes[0][-1]
+    ys = [torch.empty(s, dtype=dtype, device=dev) for s in shapes]
+    _act8_call("uaa_act8_unpack", dev, ys, [s.numel() // D for s in shapes], packed.codes, packed.steps, D, True)
     return ys[0] if packed.single else ys
 
 
@@ -695,11 +707,14 @@ class DiffAttention(torch.autograd.Function):
         ctx.key_mask = key_mask
         ctx.scale = scale
         ctx.mark_non_differentiable(lse)
+        ctx.set_materialize_grads(False)  # no zeros for lse
         return out, lse
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dout, _dlse):
+        if dout is None:
+            return None, None, None, None, None, None, None
         (q, k, v, out, out2), (lam, lse) = _saved(ctx, 5)
         dq, dk, dv, dlam = diff_attn_bwd(q, k, v, lam, out, out2, dout.contiguous(), lse, ctx.key_mask, ctx.scale)
         return dq, dk, dv, dlam, None, None, None
