@@ -1,6 +1,7 @@
 """Differential attention against the float64 definition, within the error that the operands' roundings allow."""
 import ctypes
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -319,6 +320,35 @@ def test_captured_step_and_two_streams():
     again = step(x)
     for a, n in zip((out,) + grads, ("out", "dq", "dk", "dv", "dlam")):
         assert np.array_equal(bits(a), bits(again[n])), n
+
+
+@pytest.mark.gpu
+def test_from_threads_that_made_no_cuda_call():
+    """The library binds the device's context itself; two threads at once, each on its own stream."""
+    xs = [on_gpu(draw(1, 150, 160, 2, 64, None, seed=s)) for s in (30, 31)]
+    want = [step(x) for x in xs]
+    got, streams = [None, None], [torch.cuda.Stream() for _ in xs]
+    bufs = [{n: torch.empty_like(t) for n, t in w.items()} for w in want]  # so that the threads allocate nothing
+    ws = [torch.empty(uaa.diff_attn_bwd_workspace_bytes(1, 150, 2, 64), dtype=torch.uint8, device=DEV) for _ in xs]
+    torch.cuda.synchronize()
+
+    def work(i):
+        x, b = xs[i], bufs[i]
+        with torch.cuda.stream(streams[i]):
+            out, out2, lse = uaa.diff_attn_fwd(x["q"], x["k"], x["v"], x["lam"], out=b["out"], out2=b["out2"],
+                                               lse=b["lse"])
+            uaa.diff_attn_bwd(x["q"], x["k"], x["v"], x["lam"], out, out2, x["do"], lse, dq=b["dq"], dk=b["dk"],
+                              dv=b["dv"], dlam=b["dlam"], workspace=ws[i])
+        got[i] = b
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert g is not None and all(np.array_equal(bits(g[n]), bits(w[n])) for n in w)
 
 
 @pytest.mark.gpu

@@ -2,9 +2,9 @@
 // No atomics: two runs on the same inputs give the same bits.
 //  1. diff_rows_kernel: Delta_m and -LSE_m log2(e) of every query row, and the
 //     sum of Delta_2 over 64 rows, the summands of dlambda.
-//  2. diff_dlambda_kernel: dlambda_h from those sums, in a fixed order.
-//  3. diff_dkdv_kernel, key-tile-major: dK and dV of 128 keys.
-//  4. diff_dq_kernel, query-tile-major: dQ of 128 queries.
+//  2. diff_dkdv_kernel, key-tile-major: dK and dV of 128 keys.
+//  3. diff_dq_kernel, query-tile-major: dQ of 128 queries; its loading warps, when they have loaded all, add up
+//     dlambda, in a fixed order.
 // -lambda enters as |lambda| = 2^(log2 |lambda|), added to map 2's exponents with its LSE, and a sign: the negated
 // A operand of map 2's dV product, and the sign of dQ_2 and dK_2 when they are written.
 // Both matrix kernels: warps 0-15 compute (TMEM lane quadrant = warp % 4, 32 of a tile's 128 columns = warp / 4;
@@ -41,12 +41,7 @@ __device__ __forceinline__ void store_packed32(uint32_t taddr, const float (&x)[
   uint32_t v[16];
 #pragma unroll
   for (int c = 0; c < 16; ++c) v[c] = pack_bf16(x[2 * c], x[2 * c + 1]);
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n\t"
-      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
+  tmem_st16_bits(taddr, v);
 }
 
 // Are these barriers' phases complete?  Both are tested before either answer is used; the slow path waits in turn.
@@ -64,10 +59,10 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v, float c
 }
 
 // ---------------------------------------------------------------------------
-// 1. Row vectors.  A block takes 64 rows of kRowHeads heads: D/8 lanes of 16 bytes a row, the heads in turn, so
-// that neighbouring reads follow each other and a head's results are written as runs.
+// 1. Row vectors.  Bound: reading O, O2 and dO once.  A block takes 64 rows of one head, D/8 lanes of 16 bytes a row
+// and all of a lane's rows in flight; neighbouring blocks take neighbouring heads, whose rows lie side by side.
+// 29 us at B = 1, S = 8191, H = 24, D = 128 (5.3 TB/s; four heads a block one after the other: 47 us).
 constexpr int kRowThreads = 256;
-constexpr int kRowHeads = 4;
 constexpr int kStep = 64;
 __host__ __device__ __forceinline__ int steps_of(int S) { return 2 * tiles_of(S); }
 
@@ -80,74 +75,63 @@ __global__ void __launch_bounds__(kRowThreads) diff_rows_kernel(
   constexpr int kGroups = kRowThreads / G;
   __shared__ float sums[kGroups];
   const int group = threadIdx.x / G, sub = threadIdx.x % G;
-  const int steps = steps_of(Sq), hgroups = (H + kRowHeads - 1) / kRowHeads;
-  const long long unit = blockIdx.x;
-  const int h0 = (int)(unit % hgroups) * kRowHeads;
-  const int t = (int)(unit / hgroups % steps), b = (int)(unit / hgroups / steps);
-  for (int h = h0; h < min(H, h0 + kRowHeads); ++h) {
-    const size_t bh = (size_t)b * H + h;
-    const float lm = load_lambda(lam, lam_bf16, h);
-    float sum = 0.f;
+  const int steps = steps_of(Sq);
+  const int h = blockIdx.x % H, t = blockIdx.x / H % steps, b = blockIdx.x / H / steps;
+  const size_t bh = (size_t)b * H + h;
+  const float lm = load_lambda(lam, lam_bf16, h);
+  float sum = 0.f;
 #pragma unroll
-    for (int r = 0; r < kStep / kGroups; ++r) {
-      const int i = t * kStep + r * kGroups + group;
-      float d1 = 0.f, d2 = 0.f;
-      if (i < Sq) {
-        const size_t at = (((size_t)b * Sq + i) * H + h) * D + 8 * sub;
-        const uint4 o = __ldg(reinterpret_cast<const uint4*>(out + at));
-        const uint4 p = __ldg(reinterpret_cast<const uint4*>(out2 + at));
-        const uint4 g = __ldg(reinterpret_cast<const uint4*>(dout + at));
-        const __nv_bfloat162* o2 = reinterpret_cast<const __nv_bfloat162*>(&o);
-        const __nv_bfloat162* p2 = reinterpret_cast<const __nv_bfloat162*>(&p);
-        const __nv_bfloat162* g2 = reinterpret_cast<const __nv_bfloat162*>(&g);
+  for (int r = 0; r < kStep / kGroups; ++r) {
+    const int i = t * kStep + r * kGroups + group;
+    float d1 = 0.f, d2 = 0.f;
+    if (i < Sq) {
+      const size_t at = (((size_t)b * Sq + i) * H + h) * D + 8 * sub;
+      const uint4 o = __ldg(reinterpret_cast<const uint4*>(out + at));
+      const uint4 p = __ldg(reinterpret_cast<const uint4*>(out2 + at));
+      const uint4 g = __ldg(reinterpret_cast<const uint4*>(dout + at));
+      const __nv_bfloat162* o2 = reinterpret_cast<const __nv_bfloat162*>(&o);
+      const __nv_bfloat162* p2 = reinterpret_cast<const __nv_bfloat162*>(&p);
+      const __nv_bfloat162* g2 = reinterpret_cast<const __nv_bfloat162*>(&g);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 of = __bfloat1622float2(o2[e]), pf = __bfloat1622float2(p2[e]), gf = __bfloat1622float2(g2[e]);
-          d1 = fmaf(of.x, gf.x, fmaf(of.y, gf.y, d1));
-          d2 = fmaf(pf.x, gf.x, fmaf(pf.y, gf.y, d2));
-        }
-      }
-#pragma unroll
-      for (int o = G / 2; o > 0; o /= 2) {
-        d1 += __shfl_xor_sync(0xffffffffu, d1, o);
-        d2 += __shfl_xor_sync(0xffffffffu, d2, o);
-      }
-      sum += d2;
-      if (sub < 4) {
-        float x = sub == 2 ? fmaf(lm, d2, d1) : d2;
-        if (sub < 2) {
-          const float l = i < Sq ? lse[(bh * 2 + sub) * Sq + i] : -INFINITY;
-          x = l == -INFINITY ? -INFINITY : -l * kLog2e;  // rows past Sq, or without a key: P = 0
-          if (sub == 1 && l != -INFINITY) x += log2f(fabsf(lm));
-        }
-        rows[rows_at(bh, Sq, i) + sub * kTile] = x;
+      for (int e = 0; e < 4; ++e) {
+        const float2 of = __bfloat1622float2(o2[e]), pf = __bfloat1622float2(p2[e]), gf = __bfloat1622float2(g2[e]);
+        d1 = fmaf(of.x, gf.x, fmaf(of.y, gf.y, d1));
+        d2 = fmaf(pf.x, gf.x, fmaf(pf.y, gf.y, d2));
       }
     }
-    if (sub == 0) sums[group] = sum;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      float s = 0.f;
-      for (int x = 0; x < kGroups; ++x) s += sums[x];
-      part[(size_t)h * B * steps + (size_t)b * steps + t] = s;
+#pragma unroll
+    for (int o = G / 2; o > 0; o /= 2) {
+      d1 += __shfl_xor_sync(0xffffffffu, d1, o);
+      d2 += __shfl_xor_sync(0xffffffffu, d2, o);
     }
-    __syncthreads();
+    sum += d2;
+    if (sub < 4) {
+      float x = sub == 2 ? fmaf(lm, d2, d1) : d2;
+      if (sub < 2) {
+        const float l = i < Sq ? lse[(bh * 2 + sub) * Sq + i] : -INFINITY;
+        x = l == -INFINITY ? -INFINITY : -l * kLog2e;  // rows past Sq, or without a key: P = 0
+        if (sub == 1 && l != -INFINITY) x += log2f(fabsf(lm));
+      }
+      rows[rows_at(bh, Sq, i) + sub * kTile] = x;
+    }
+  }
+  if (sub == 0) sums[group] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float s = 0.f;
+    for (int x = 0; x < kGroups; ++x) s += sums[x];
+    part[(size_t)h * B * steps + (size_t)b * steps + t] = s;
   }
 }
 
-// 2. dlambda_h = -sum of Delta_2 over the head's rows, one block per head.
-__global__ void __launch_bounds__(256) diff_dlambda_kernel(const float* __restrict__ part, void* __restrict__ dlam,
-                                                           int lam_bf16, int n) {
-  __shared__ float sums[8];
-  const int h = blockIdx.x;
+// dlambda_h = -sum of Delta_2 over the head's rows, by one warp, in a fixed order.
+__device__ __forceinline__ void sum_dlambda(const float* __restrict__ part, void* __restrict__ dlam, int lam_bf16, int h,
+                                            int n, int lane) {
   float s = 0.f;
-  for (int i = threadIdx.x; i < n; i += 256) s += part[(size_t)h * n + i];
+  for (int i = lane; i < n; i += 32) s += part[(size_t)h * n + i];
 #pragma unroll
   for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = s;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    s = 0.f;
-    for (int x = 0; x < 8; ++x) s += sums[x];
+  if (lane == 0) {
     if (lam_bf16)
       static_cast<__nv_bfloat16*>(dlam)[h] = __float2bfloat16_rn(-s);
     else
@@ -173,7 +157,7 @@ __device__ __forceinline__ Item decode_item(int item, int tiles, int H, bool hea
 }
 
 // ---------------------------------------------------------------------------
-// 3. dK, dV.  A persistent CTA takes 128 keys of one (batch, head); its steps are the maps of the query tiles in
+// 2. dK, dV.  A persistent CTA takes 128 keys of one (batch, head); its steps are the maps of the query tiles in
 // turn, (i, 1) (i, 2) (i + 1, 1) ...:
 //     S^T = K_m Q_m^T, P^T = w_m A_m^T (w = 1, -lambda), dA^T = V dO^T    (M = keys, N = 128 queries)
 //     dV += P^T dO, dS^T = P^T (dA^T - Delta_m), dK_m += dS^T Q_m
@@ -568,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// 4. dQ.  A persistent CTA takes 128 queries of one (batch, head), Q and dO in shared memory, and walks the key
+// 3. dQ.  A persistent CTA takes 128 queries of one (batch, head), Q and dO in shared memory, and walks the key
 // tiles: S_m = Q_m K_m^T, dA = dO V^T (M = queries, N = 128 keys), then dQ_m += dS_m K_m.  The maps take turns:
 // while the compute warps work on map 2 of tile g, the tensor cores form dQ_1 of tile g and S_1 of tile g + 1;
 // then dA of tile g + 1, dQ_2 and S_2 while they take map 1's exponentials.
@@ -605,7 +589,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     diff_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
                    const void* __restrict__ lam, int lam_bf16, const float* __restrict__ rows,
-                   const uint8_t* __restrict__ key_mask, __nv_bfloat16* __restrict__ dq, int B, int H, int Sq, int Sk,
+                   const uint8_t* __restrict__ key_mask, __nv_bfloat16* __restrict__ dq,
+                   const float* __restrict__ part, void* __restrict__ dlam, int B, int H, int Sq, int Sk,
                    int num_items, float scale, float scale_log2, DevCtx ctx) {
   using L = DqLayout<D>;
   constexpr int kChunks = D / 64;
@@ -737,6 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++G;
       }
     }
+    for (int h = blockIdx.x; h < H; h += gridDim.x) sum_dlambda(part, dlam, lam_bf16, h, B * steps_of(Sq), lane);
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
     uint32_t el_lane;
@@ -1005,7 +991,7 @@ int launch_bwd(const void* q, const void* k, const void* v, const void* lam, int
   float* part = rows + row_floats(B, Sq, H);
   const int steps = steps_of(Sq);
   const long long items_k = (long long)tiles_of(Sk) * H * B, items_q = (long long)tiles_of(Sq) * H * B;
-  const long long row_blocks = (long long)B * steps * ((H + kRowHeads - 1) / kRowHeads);
+  const long long row_blocks = (long long)B * steps * H;
   if (items_k > INT32_MAX || items_q > INT32_MAX || row_blocks > INT32_MAX)
     return set_error(UAA_ERR_UNSUPPORTED, "uaa_diff_attn_bwd: too many work items");
   DevCtx ctx;
@@ -1020,8 +1006,6 @@ int launch_bwd(const void* q, const void* k, const void* v, const void* lam, int
                                                              static_cast<const bf*>(dout), lse, lam, lam_bf16, rows,
                                                              part, B, Sq, H);
   if ((st = check_launch("uaa_diff_attn_bwd (rows)"))) return st;
-  diff_dlambda_kernel<<<H, 256, 0, s>>>(part, dlam, lam_bf16, B * steps);
-  if ((st = check_launch("uaa_diff_attn_bwd (dlambda)"))) return st;
   const int sms = device_sms();
   if (items_k > 0) {
     auto kern = diff_dkdv_kernel<D, kMask>;
@@ -1037,8 +1021,8 @@ int launch_bwd(const void* q, const void* k, const void* v, const void* lam, int
   auto kern = diff_dq_kernel<D, kMask>;
   if ((st = prepare(kern, DqLayout<D>::kSmem))) return st;
   kern<<<(int)(items_q < sms ? items_q : sms), kThreads, DqLayout<D>::kSmem, s>>>(
-      mq.m[0], mk.m[0], mv.m[0], mdo.m[0], lam, lam_bf16, rows, mask, static_cast<bf*>(dq), B, H, Sq, Sk, (int)items_q,
-      scale, scale * kLog2e, ctx);
+      mq.m[0], mk.m[0], mv.m[0], mdo.m[0], lam, lam_bf16, rows, mask, static_cast<bf*>(dq), part, dlam, B, H, Sq, Sk,
+      (int)items_q, scale, scale * kLog2e, ctx);
   return check_launch("uaa_diff_attn_bwd (dQ)");
 }
 
