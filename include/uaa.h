@@ -380,6 +380,18 @@ int uaa_act8_pack(int n, const void* const* x, int8_t* const* codes, float* cons
 int uaa_act8_unpack(int n, const int8_t* const* codes, const float* const* steps, void* const* y,
                     const long long* rows, int D, int dtype, uaa_stream_t stream);
 
+/* Attention backward from an 8-bit checkpoint: uaa_attn_bwd_cross on the values that the codes of q, k, v and out
+ * stand for, which the call takes back into its workspace (one launch, then the backward).
+ *   codes, steps : host arrays of 4 device pointers, of q, k, v and out as uaa_act8_pack wrote them from bf16
+ *                  (B, S, H, D) tensors, rows of D
+ *   lse          : the forward's
+ *   workspace    : device, at least uaa_attn_bwd_act8_workspace_bytes() bytes, 256-byte aligned
+ * The other arguments and the refusals are uaa_attn_bwd_cross's. */
+size_t uaa_attn_bwd_act8_workspace_bytes(int B, int Sq, int Sk, int H, int D);
+int uaa_attn_bwd_act8(const int8_t* const* codes, const float* const* steps, const void* dout, const float* lse,
+                      const uint8_t* key_mask, void* dq, void* dk, void* dv, int B, int Sq, int Sk, int H, int D,
+                      float scale, void* workspace, size_t workspace_bytes, uaa_stream_t stream);
+
 /* ------------------------------------------------------------------ differential attention
  * Each head has two softmax maps over the same keys, one from the first D/2 columns of q and k and one from
  * the last D/2, and the values of all D columns are read by their difference:

@@ -31,6 +31,18 @@ def test_refusals_of_the_call():
     assert pack(D=0) == -1 and pack(D=40) == -2 and pack(D=528) == -2 and pack(dtype=9) == -1
     assert pack(n=9) == -1 and pack(n=-1) == -1 and pack(r=-1) == -1
     assert pack(r=0, x=None) == 0 and pack(n=0) == 0
+    # the backward from a checkpoint: its own workspace holds the four tensors and the backward's
+    B, Sq, Sk, H, D = 1, 130, 300, 2, 64
+    need = L.uaa_attn_bwd_act8_workspace_bytes(B, Sq, Sk, H, D)
+    assert need == 4 * (Sq + Sk) * H * D + L.uaa_attn_bwd_workspace_bytes(B, Sq, H, D)
+    f, four = ctypes.c_void_p(1 << 20), (ctypes.c_void_p * 4)(*[1 << 20] * 4)
+
+    def bwd(codes=four, dout=f, lse=f, D=D, Sq=Sq, ws=f, n=need):
+        return L.uaa_attn_bwd_act8(codes, four, dout, lse, None, f, f, f, B, Sq, Sk, H, D, ctypes.c_float(0.1), ws, n, None)
+
+    assert bwd(n=need - 1) == -1 and "workspace" in err()
+    assert bwd(ws=ctypes.c_void_p((1 << 20) + 64)) == -1 and "256-byte" in err()
+    assert bwd(codes=None) == -1 and bwd(dout=None) == -1 and bwd(lse=None) == -1 and bwd(D=96) == -2 and bwd(Sq=0) == -1
     assert L.uaa_act8_unpack(1, arr(4096), arr(4096), arr(None), rows(4), 64, 0, None) == -1
 
 
@@ -174,11 +186,30 @@ def test_attention_backward_from_the_checkpoint(B, S, H, D, masked):
     want = uaa.attn_bwd(*kept, do, lse, mask)
     for name, a, w in zip(("dq", "dk", "dv"), grads, want):
         assert np.array_equal(bits(a), bits(w)), name
+    packed = uaa.act8_pack([t.detach() for t in (q, k, v, out)])
+    for a, w in zip(uaa.attn_bwd_act8(packed, do, lse, mask), want):
+        assert np.array_equal(bits(a), bits(w))
+    with pytest.raises(ValueError):
+        uaa.attn_bwd_act8(uaa.act8_pack([q.detach()] * 3), do, lse, mask)
     m = inp["mask"].numpy().astype(bool) if masked else None
     ref = oracle.attn_bwd(*(f64(t) for t in (q, k, v, do)), m, 1 / math.sqrt(D))
     for a, r in zip(grads, ref):
         # 0.6 % of rms in each of q, k, v, o; two of them meet in a product, and dS = P (dP - Delta)
         assert np.linalg.norm(f64(a) - r) <= 0.05 * np.linalg.norm(r)
+
+
+@pytest.mark.gpu
+def test_attention_across_lengths_from_the_checkpoint():
+    q, do = (torch.randn(2, 70, 3, 64, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    k, v = (torch.randn(2, 200, 3, 64, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    mask = torch.rand(2, 200, device=DEV) < 0.5
+    leaves = [t.requires_grad_() for t in (q, k, v)]
+    out, lse = uaa.attention(*leaves, mask, 0.2, saved="int8")
+    got = torch.autograd.grad(out, leaves, do)
+    want = uaa.attn_bwd(*(_values(t.detach()) for t in (q, k, v, out)), do, lse, mask, 0.2)
+    for a, w in zip(got, want):
+        assert np.array_equal(bits(a), bits(w))
+    assert torch.equal(uaa.attention(*(t.detach() for t in leaves), mask, 0.2, saved="int8")[0], out)  # nothing to keep
 
 
 @pytest.mark.gpu

@@ -46,15 +46,12 @@ def test_refusals_without_gpu():
 
 
 def _raw(plan=None, q=None, k=None, pos=None, B=1, S=2, D=64, dtype=0):
-    import ctypes
-
     plan = plan or uaa.RotaryPlan([64])
-    return uaa.lib().uaa_rotary(plan._ref, ctypes.byref(q), None if k is None else ctypes.byref(k), pos, 0, 0, 0, 0, B,
-                                S, D, dtype, 0, None)
+    return uaa.lib().uaa_rotary(plan._ref, q, k, pos, 0, 0, 0, 0, B, S, D, dtype, 0, None)
 
 
 def _tensor(x=4096, y=4096, strides=(512, 256, 64, 512, 256, 64), H=4):
-    return uaa._RotaryTensor(x, y, *strides, H)
+    return uaa._ROTARY_TENSOR.pack(x or 0, y, *strides, H)
 
 
 def test_refusals_of_the_call():

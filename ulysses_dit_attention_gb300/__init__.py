@@ -17,6 +17,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 import threading
 
 import torch
@@ -29,6 +30,7 @@ __all__ = [
     "set_bwd_profile_events", "Attention", "attn_fwd_groups", "attn_bwd_groups",
     "attention", "UlyssesAttention", "ulysses_attention", "STATUS", "debug_build", "debug_exp2_fma2",
     "RotaryPlan", "rotary_fwd", "rotary_bwd", "Rotary", "rotary", "shard_positions", "Act8", "act8_pack", "act8_unpack",
+    "attn_bwd_act8",
     "diff_attn_fwd", "diff_attn_bwd", "diff_attn_bwd_workspace_bytes", "DiffAttention", "diff_attention",
 ]
 
@@ -55,16 +57,17 @@ class _RotaryPlan(ctypes.Structure):  # uaa_rotary_plan
                 ("turns", ctypes.c_uint64 * 128), ("axis", ctypes.c_uint8 * 128)]
 
 
-class _RotaryTensor(ctypes.Structure):  # uaa_rotary_tensor
-    _fields_ = [("x", _P), ("y", _P), ("x_batch", _L), ("x_token", _L), ("x_head", _L), ("y_batch", _L),
-                ("y_token", _L), ("y_head", _L), ("H", _I)]
-
+# uaa_rotary_tensor, as bytes: x, y, their batch, token and head strides, H
+_ROTARY_TENSOR = struct.Struct("@PP6qi0q")
 
 _SIGS = {
     "uaa_rotary_plan_init": (_I, [ctypes.POINTER(_RotaryPlan), _I, _I, _P, ctypes.c_double, _I, ctypes.c_double,
                                   ctypes.c_double, ctypes.c_double, ctypes.c_double]),
-    "uaa_rotary": (_I, [ctypes.POINTER(_RotaryPlan), ctypes.POINTER(_RotaryTensor), ctypes.POINTER(_RotaryTensor), _P,
+    "uaa_rotary": (_I, [ctypes.POINTER(_RotaryPlan), _P, _P, _P,
                         _I, _L, _L, _L, _I, _I, _I, _I, _I, _P]),
+    "uaa_attn_bwd_act8_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I]),
+    "uaa_attn_bwd_act8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, ctypes.c_float, _P, ctypes.c_size_t,
+                               _P]),
     "uaa_act8_pack": (_I, [_I, _P, _P, _P, _P, _I, _I, _P]),
     "uaa_act8_unpack": (_I, [_I, _P, _P, _P, _P, _I, _I, _P]),
     "uaa_diff_attn_fwd": (_I, [_P, _P, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, ctypes.c_float, _P]),
@@ -337,7 +340,7 @@ def _save(ctx, saved, tensors, *others):
     if saved == "int8" and any(ctx.needs_input_grad):
         packed = act8_pack(tensors)
         ctx.packed = packed._meta()
-        tensors = (packed.codes, packed.steps)
+        tensors = (packed.data,)
     ctx.save_for_backward(*tensors, *others)
 
 
@@ -346,7 +349,7 @@ def _saved(ctx, n):
     kept = ctx.saved_tensors
     if ctx.packed is None:
         return list(kept[:n]), kept[n:]
-    return act8_unpack(Act8(kept[0], kept[1], *ctx.packed)), kept[2:]
+    return act8_unpack(Act8(kept[0], *ctx.packed)), kept[1:]
 
 
 class Attention(torch.autograd.Function):
@@ -369,9 +372,13 @@ class Attention(torch.autograd.Function):
     def backward(ctx, dout, _dlse):
         if dout is None:
             return None, None, None, None, None, None
-        (q, k, v, out), (lse,) = _saved(ctx, 4)
-        dq, dk, dv = attn_bwd(q, k, v, out, dout.contiguous(), lse, ctx.key_mask, ctx.scale)
-        return dq, dk, dv, None, None, None
+        if ctx.packed is not None:
+            data, lse = ctx.saved_tensors
+            grads = attn_bwd_act8(Act8(data, *ctx.packed), dout.contiguous(), lse, ctx.key_mask, ctx.scale)
+        else:
+            q, k, v, out, lse = ctx.saved_tensors
+            grads = attn_bwd(q, k, v, out, dout.contiguous(), lse, ctx.key_mask, ctx.scale)
+        return *grads, None, None, None
 
 
 def attention(q, k, v, key_mask=None, scale=None, saved=None):
@@ -479,7 +486,7 @@ def _rotary_operand(name, t, ref, out):
     elif out.shape != shape or out.dtype != dtype or out.device != t.device or (shape[3] > 1 and out.stride(3) != 1):
         raise ValueError(f"out_{name} must be {dtype} {tuple(shape)} on {t.device} with contiguous columns")
     y0, y1, y2, _ = out.stride()
-    return _RotaryTensor(t.data_ptr(), out.data_ptr(), x0, x1, x2, y0, y1, y2, shape[2]), out
+    return _ROTARY_TENSOR.pack(t.data_ptr(), out.data_ptr(), x0, x1, x2, y0, y1, y2, shape[2]), out
 
 
 def _rotate(q, k, plan, positions, start, inverse, out_q, out_k):
@@ -490,24 +497,27 @@ def _rotate(q, k, plan, positions, start, inverse, out_q, out_k):
     tk = None
     if k is not None:
         tk, out_k = _rotary_operand("k", k, q, out_k)
-        tk = ctypes.byref(tk)
     B, S, _, D = q.shape
     pos, wide, pb, ps = None, 0, 0, 0
     if positions is not None:
-        tail = () if plan.axes == 1 else (plan.axes,)
-        if positions.shape != (B, S) + tail and positions.shape != (S,) + tail:
-            raise ValueError(f"positions must be {(S,) + tail} or {(B, S) + tail}, got {tuple(positions.shape)}")
-        if positions.dtype not in (torch.int32, torch.int64):
-            raise TypeError("positions must be int32 or int64")
-        if tail and positions.stride(-1) != 1:
-            raise ValueError("the axes of positions must be contiguous")
         if start:
             raise ValueError("start goes with positions=None")
-        at = positions.stride()
-        pb, ps = (at[0], at[1]) if positions.dim() == 2 + len(tail) else (0, at[0])
-        pos, wide = positions.data_ptr(), int(positions.dtype == torch.int64)
-    _call(dev, "uaa_rotary", plan._ref, ctypes.byref(tq), tk, pos, wide, pb, ps, int(start), B, S, D,
-          _DTYPES[q.dtype], inverse)
+        axes, at, dtype = plan.axes, positions.stride(), positions.dtype
+        tail = () if axes == 1 else (axes,)
+        if positions.shape == (B, S) + tail:
+            pb, ps = at[0], at[1]
+        elif positions.shape == (S,) + tail:
+            ps = at[0]
+        else:
+            raise ValueError(f"positions must be {(S,) + tail} or {(B, S) + tail}, got {tuple(positions.shape)}")
+        if dtype == torch.int64:
+            wide = 1
+        elif dtype != torch.int32:
+            raise TypeError("positions must be int32 or int64")
+        if axes > 1 and at[-1] != 1:
+            raise ValueError("the axes of positions must be contiguous")
+        pos = positions.data_ptr()
+    _call(dev, "uaa_rotary", plan._ref, tq, tk, pos, wide, pb, ps, start, B, S, D, _DTYPES[q.dtype], inverse)
     return out_q, out_k
 
 
@@ -558,36 +568,49 @@ def rotary(q, k, plan, positions=None, start=0):
 
 # --------------------------------------------------------------------------- activation checkpoints in 8 bits
 class Act8:
-    """Tensors kept in 8 bits: the codes and the steps of all of them, one behind the other."""
+    """Tensors kept in 8 bits: one buffer with the codes of all of them, one behind the other, then their steps."""
 
-    __slots__ = ("codes", "steps", "shapes", "dtype", "single")
+    __slots__ = ("data", "shapes", "dtype", "single")
 
-    def __init__(self, codes, steps, shapes, dtype, single):
-        self.codes, self.steps, self.shapes, self.dtype, self.single = codes, steps, shapes, dtype, single
+    def __init__(self, data, shapes, dtype, single):
+        self.data, self.shapes, self.dtype, self.single = data, shapes, dtype, single
 
     def _meta(self):
         return self.shapes, self.dtype, self.single
 
     @property
+    def _numel(self):
+        return sum(s.numel() for s in self.shapes)
+
+    @property
+    def codes(self):
+        return self.data[:self._numel].view(torch.int8)
+
+    @property
+    def steps(self):
+        return self.data[self._numel:].view(torch.float32)
+
+    @property
     def nbytes(self):
-        return self.codes.numel() + 4 * self.steps.numel()
+        return self.data.numel()
 
 
 _ACT8_ARRAYS = [(ctypes.c_void_p * n, _L * n) for n in range(9)]
 
 
-def _act8_call(name, dev, tensors, rows, codes, steps, D, swap):
-    n = len(tensors)
-    ptrs, longs = _ACT8_ARRAYS[n]
-    c, s, pc, ps = codes.data_ptr(), steps.data_ptr(), [], []
+def _act8_layout(data, shapes):
+    """Arrays of the tensors' code and step pointers and of their rows; D."""
+    ptrs, longs = _ACT8_ARRAYS[len(shapes)]
+    D = shapes[0][-1]
+    rows = [s.numel() // D for s in shapes]
+    c = data.data_ptr()
+    s, pc, ps = c + sum(rows) * D, [], []
     for r in rows:
         pc.append(c)
         ps.append(s)
         c += r * D
         s += r * 4
-    x, pc, ps = ptrs(*[t.data_ptr() for t in tensors]), ptrs(*pc), ptrs(*ps)
-    first = (pc, ps, x) if swap else (x, pc, ps)
-    _call(dev, name, n, *first, longs(*rows), D, _DTYPES[tensors[0].dtype])
+    return ptrs(*pc), ptrs(*ps), longs(*rows), D
 
 
 def act8_pack(x):
@@ -606,28 +629,58 @@ def act8_pack(x):
         raise TypeError("tensors must be bfloat16, float16 or float32, all alike")
     if not shapes[0] or not shapes[0][-1]:
         raise ValueError("the last dimension is empty")
-    D = shapes[0][-1]
+    D, total = shapes[0][-1], 0
     for t, s in zip(xs, shapes):
         if t.dtype != dtype:
             raise TypeError("tensors must be bfloat16, float16 or float32, all alike")
         if not s or s[-1] != D or not t.is_contiguous():
             raise ValueError("tensors must be contiguous, with one last dimension")
-    rows = [s.numel() // D for s in shapes]
-    total = sum(rows)
-    codes = torch.empty(total * D, dtype=torch.int8, device=dev)
-    steps = torch.empty(total, dtype=torch.float32, device=dev)
-    _act8_call("uaa_act8_pack", dev, xs, rows, codes, steps, D, False)
-    return Act8(codes, steps, shapes, dtype, single)
+        total += s.numel()
+    data = torch.empty(total + total // D * 4, dtype=torch.uint8, device=dev)
+    pc, ps, rows, D = _act8_layout(data, shapes)
+    _call(dev, "uaa_act8_pack", len(xs), _ACT8_ARRAYS[len(xs)][0](*[t.data_ptr() for t in xs]), pc, ps, rows, D,
+          _DTYPES[dtype])
+    return Act8(data, shapes, dtype, single)
 
 
 def act8_unpack(packed):
     """``uaa_act8_unpack``: the values that the codes stand for, in the shapes and type of the tensors packed."""
-    dev = _same_device(packed.codes, packed.steps)
-    dtype, shapes = packed.dtype, packed.shapes
-    D = shapes[0][-1]
+    dev, dtype, shapes = _same_device(packed.data), packed.dtype, packed.shapes
     ys = [torch.empty(s, dtype=dtype, device=dev) for s in shapes]
-    _act8_call("uaa_act8_unpack", dev, ys, [s.numel() // D for s in shapes], packed.codes, packed.steps, D, True)
+    pc, ps, rows, D = _act8_layout(packed.data, shapes)
+    _call(dev, "uaa_act8_unpack", len(ys), pc, ps, _ACT8_ARRAYS[len(ys)][0](*[t.data_ptr() for t in ys]), rows, D,
+          _DTYPES[dtype])
     return ys[0] if packed.single else ys
+
+
+def attn_bwd_act8(packed, dout, lse, key_mask=None, scale=None, dq=None, dk=None, dv=None, workspace=None):
+    """``uaa_attn_bwd_act8``: the gradients of :func:`attn_bwd` from an 8-bit checkpoint of ``[q, k, v, out]``."""
+    shapes = packed.shapes
+    if len(shapes) != 4 or packed.dtype != torch.bfloat16 or any(len(s) != 4 for s in shapes):
+        raise ValueError("packed must hold the bf16 BSHD tensors q, k, v and out")
+    qs, ks = shapes[0], shapes[1]
+    if shapes[2] != ks or shapes[3] != qs or ks[0] != qs[0] or ks[2:] != qs[2:]:
+        raise ValueError(f"the packed shapes do not fit: {[tuple(s) for s in shapes]}")
+    _bshd("dout", dout)
+    B, Sq, H, D = qs
+    Sk = ks[1]
+    if dout.shape != qs:
+        raise ValueError(f"dout shape {tuple(dout.shape)} does not fit {tuple(qs)}")
+    if lse.dtype != torch.float32 or lse.shape != (B, H, Sq) or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous fp32 (B, H, Sq)")
+    mask = normalize_key_mask(key_mask, B, Sk)
+    dev = _same_device(packed.data, dout, lse, mask, workspace)
+    dq = _result("dq", dq, qs, torch.bfloat16, dev)
+    dk = _result("dk", dk, ks, torch.bfloat16, dev)
+    dv = _result("dv", dv, ks, torch.bfloat16, dev)
+    if workspace is None:
+        nbytes = int(lib().uaa_attn_bwd_act8_workspace_bytes(B, Sq, Sk, H, D))
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+    pc, ps, _, _ = _act8_layout(packed.data, shapes)
+    _call(dev, "uaa_attn_bwd_act8", pc, ps, dout.data_ptr(), lse.data_ptr(), _ptr(mask), dq.data_ptr(), dk.data_ptr(),
+          dv.data_ptr(), B, Sq, Sk, H, D, float(1.0 / math.sqrt(D) if scale is None else scale), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
+    return dq, dk, dv
 
 
 # --------------------------------------------------------------------------- differential attention

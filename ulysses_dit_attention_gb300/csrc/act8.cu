@@ -41,6 +41,9 @@
 #include "uaa_common.cuh"
 
 namespace uaa {
+
+int validate_attn_sizes(const char* fn, int B, int Sq, int Sk, int H, int D, float scale);
+
 namespace {
 
 constexpr int kThreads = 256;
@@ -291,4 +294,44 @@ extern "C" int uaa_act8_unpack(int n, const int8_t* const* codes, const float* c
                                const long long* rows, int D, int dtype, uaa_stream_t stream) {
   return uaa::act8("uaa_act8_unpack", false, n, y, const_cast<int8_t* const*>(codes), const_cast<float* const*>(steps),
                    rows, D, dtype, stream);
+}
+
+extern "C" size_t uaa_attn_bwd_act8_workspace_bytes(int B, int Sq, int Sk, int H, int D) {
+  if (B < 0 || Sq < 0 || Sk < 0 || H < 0 || (D != 64 && D != 128)) return 0;
+  // q, k, v, out in bf16 (each B * S * H * D * 2 bytes, rounded up to 256), then the backward's own workspace
+  const size_t q = ((size_t)B * Sq * H * D * 2 + 255) & ~(size_t)255, k = ((size_t)B * Sk * H * D * 2 + 255) & ~(size_t)255;
+  return 2 * q + 2 * k + uaa_attn_bwd_workspace_bytes(B, Sq, H, D);
+}
+
+extern "C" int uaa_attn_bwd_act8(const int8_t* const* codes, const float* const* steps, const void* dout,
+                                 const float* lse, const uint8_t* key_mask, void* dq, void* dk, void* dv, int B, int Sq,
+                                 int Sk, int H, int D, float scale, void* workspace, size_t workspace_bytes,
+                                 uaa_stream_t stream) {
+  const char* fn = "uaa_attn_bwd_act8";
+  int st = uaa::validate_attn_sizes(fn, B, Sq, Sk, H, D, scale);
+  if (st) return st;
+  if ((uint64_t)B * H == 0 || (uint64_t)Sq + Sk == 0) return UAA_OK;
+  if (Sq == 0) return uaa::set_error(UAA_ERR_INVALID_ARG, "%s: keys without queries (Sq = 0)", fn);
+  if (!codes || !steps) return uaa::set_error(UAA_ERR_INVALID_ARG, "%s: codes or steps is NULL", fn);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return uaa::set_error(UAA_ERR_INVALID_ARG, "%s: workspace is NULL or not 256-byte aligned", fn);
+  const size_t need = uaa_attn_bwd_act8_workspace_bytes(B, Sq, Sk, H, D);
+  if (workspace_bytes < need)
+    return uaa::set_error(UAA_ERR_INVALID_ARG, "%s: workspace has %zu bytes, %zu needed", fn, workspace_bytes, need);
+  // the backward's other operands are checked before anything is launched
+  for (const void* p : {dout, static_cast<const void*>(dq), static_cast<const void*>(dk), static_cast<const void*>(dv)})
+    if (!p || (reinterpret_cast<uintptr_t>(p) & 15u))
+      return uaa::set_error(UAA_ERR_INVALID_ARG, "%s: dout, dq, dk or dv is NULL or not 16-byte aligned", fn);
+  if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return uaa::set_error(UAA_ERR_INVALID_ARG, "%s: lse is NULL or not 4-byte aligned", fn);
+  const long long rows[4] = {(long long)B * Sq * H, (long long)B * Sk * H, (long long)B * Sk * H, (long long)B * Sq * H};
+  void* y[4];
+  char* at = static_cast<char*>(workspace);
+  for (int i = 0; i < 4; ++i) {
+    y[i] = at;
+    at += ((size_t)rows[i] * D * 2 + 255) & ~(size_t)255;
+  }
+  if ((st = uaa_act8_unpack(4, codes, steps, y, rows, D, UAA_BF16, stream))) return st;
+  return uaa_attn_bwd_cross(y[0], y[1], y[2], y[3], dout, lse, key_mask, dq, dk, dv, B, Sq, Sk, H, D, scale, at,
+                            workspace_bytes - (at - static_cast<char*>(workspace)), stream);
 }

@@ -540,8 +540,10 @@ int launch_tiles(const void* q, const void* k, const void* v, const void* lam, i
 // fixed order: one launch, no workspace.
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
-constexpr int kRowUnroll = 4;   // keys in flight per lane
 constexpr int kMaxCluster = 8;
+// Keys in flight per lane: as many as leave two CTAs on an SM (B = 4, Sk = 16389, H = 24, D = 128: one row 158 us with 4,
+// 134 with 8, 222 with 12; two rows 172 us with 4, 136 with 6, 390 with 8: 6.0 TB/s).
+__host__ __device__ constexpr int row_unroll(int nq) { return nq == 1 ? 8 : 6; }
 
 template <int D, int NQ>
 struct RowPart {  // a CTA's (or warp's) share of NQ rows
@@ -561,6 +563,7 @@ __global__ void __launch_bounds__(kRowThreads) diff_fwd_rows_kernel(
     float scale_log2) {
   constexpr int G = D / 8;       // lanes of a row
   constexpr int KW = 32 / G;     // keys of a warp's load
+  constexpr int kRowUnroll = row_unroll(NQ);
   constexpr float kLn2 = 0.6931471805599453f;
   using Part = RowPart<D, NQ>;
   extern __shared__ __align__(16) uint8_t raw[];
@@ -787,9 +790,9 @@ int launch_rows(const void* q, const void* k, const void* v, const void* lam, in
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return set_error(UAA_ERR_CUDA, "%s: smem attribute: %s", fn, cudaGetErrorString(e));
   const long long units = (long long)B * H * ((Sq + NQ - 1) / NQ);
-  // as many CTAs per unit as fill the SMs twice, each with at least two loads of keys per warp
-  const int least = 2 * kRowWarps * (256 / D) * kRowUnroll;
-  long long c = 2LL * device_sms() / units;
+  // as many CTAs per unit as fill the SMs twice (two are resident), each with at least two loads of keys per warp
+  const int least = 2 * kRowWarps * (256 / D) * row_unroll(NQ);
+  long long c = (4LL * device_sms() / units + 1) / 2;
   const long long most = (Sk + least - 1) / least;
   c = c > most ? most : c;
   const int cluster = c < 1 ? 1 : (c > kMaxCluster ? kMaxCluster : (int)c);
@@ -815,10 +818,15 @@ int launch_rows(const void* q, const void* k, const void* v, const void* lam, in
 template <int D, bool kMask>
 int launch_fwd(const void* q, const void* k, const void* v, const void* lam, int lam_bf16, const uint8_t* mask,
                void* out, void* out2, float* lse, int B, int Sq, int Sk, int H, float scale, cudaStream_t s) {
-  auto go = Sq == 1   ? launch_rows<D, 1, kMask>
-            : Sq == 2 ? launch_rows<D, 2, kMask>
-            : Sq <= 4 ? launch_rows<D, 4, kMask>
-                      : launch_tiles<D, kMask>;
+  // Few rows or tiles?  Per 128 keys and head, reading them for two rows takes about 11 ns of the whole card (D = 128;
+  // half of it with D = 64), and a wave of query tiles about 1.45 us: the first is the faster for up to 128 such pairs
+  // of rows a wave.  Measured both ways at Sk = 16389, D = 128, us (rows, tiles): B H = 96, Sq = 2: 136, 195; Sq = 3:
+  // 277, 195; B H = 24, Sq = 8: 117, 180; Sq = 16: 258, 181; B H = 8, Sq = 32: 164, 177; D = 64, B H = 24, Sq = 16:
+  // 137, 158.  One or two rows need one reading only: B H = 1536, Sk = 1000, Sq = 1: 144, 163.
+  const long long bh = (long long)B * H, groups = (Sq + 1) / 2, sms = device_sms();
+  const long long waves = (bh * tiles_of(Sq) + sms - 1) / sms;
+  const bool rows = Sq <= 2 || groups * bh * D <= 16384 * waves;
+  auto go = !rows ? launch_tiles<D, kMask> : Sq == 1 ? launch_rows<D, 1, kMask> : launch_rows<D, 2, kMask>;
   return go(q, k, v, lam, lam_bf16, mask, out, out2, lse, B, Sq, Sk, H, scale, s);
 }
 
