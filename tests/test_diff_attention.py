@@ -371,3 +371,30 @@ def test_empty_sizes_and_outputs_of_the_caller():
     assert uaa.diff_attn_fwd(x["q"], x["k"], x["v"], x["lam"], out=out)[0] is out
     with pytest.raises(ValueError):
         uaa.diff_attn_fwd(x["q"], x["k"], x["v"], x["lam"], out=out[:, 1:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,mask", [(128, None), (64, "prefix"), (64, None), (128, "prefix")])
+@pytest.mark.parametrize("n", [0, 1, 2, 5])
+def test_a_load_that_never_comes(D, mask, n):
+    """The n-th ring load of every CTA is not issued: the waits for it run out, every role meets the others to the end of
+    its schedule, the status says so, and the next call, issued before it was read, is right."""
+    x = on_gpu(draw(1, 300, 700, 2, D, mask, seed=40))
+    want = step(x)
+    uaa.set_wait_timeout_ms(20)
+    uaa.debug_drop_load(n)
+    try:
+        uaa.diff_attn_fwd(x["q"], x["k"], x["v"], x["lam"], x["mask"])
+        uaa.diff_attn_bwd(x["q"], x["k"], x["v"], x["lam"], want["out"], want["out2"], x["do"], want["lse"], x["mask"])
+    finally:
+        uaa.debug_drop_load(-1)
+        uaa.set_wait_timeout_ms(0)
+    out, out2, lse = uaa.diff_attn_fwd(x["q"], x["k"], x["v"], x["lam"], x["mask"])
+    grads = uaa.diff_attn_bwd(x["q"], x["k"], x["v"], x["lam"], out, out2, x["do"], lse, x["mask"])
+    torch.cuda.synchronize()
+    with pytest.raises(uaa.UAAError) as e:
+        uaa.check_device_status()
+    assert e.value.status == -5
+    uaa.check_device_status()
+    for a, name in zip((out, out2, lse) + grads, ("out", "out2", "lse", "dq", "dk", "dv", "dlam")):
+        assert np.array_equal(bits(a), bits(want[name])), name

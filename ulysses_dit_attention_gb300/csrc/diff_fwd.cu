@@ -3,21 +3,29 @@
 // query rows against many keys, which is bound by reading K and V.
 //
 // Tiles.  A persistent CTA per SM walks items; an item is one 128-row query tile
-// of one (batch, head), both maps.  The two maps of a tile take the places that
-// two query tiles would have: one softmax warpgroup each, working while the
-// tensor cores run the other map's products.
-//   warp 8     TMA: the item's Q tile (twice buffered when two fit), then K_j,
-//              V_j through a ring; V_j is loaded once and read by both maps.
+// of one (batch, head), both maps, against tiles of 80 keys (D = 64: 128).
+//   warp 8     TMA: the item's Q tile (two buffers), then K_j, V_j through a
+//              ring; V_j is loaded once and read by both maps.
 //   warp 9     tcgen05, one elected lane:
-//                S1_0 S2_0 | PV1_0 S1_1 | PV2_0 S2_1 | PV1_1 S1_2 | ...
+//                S1_0 S2_0 | S1_1 | S2_1 | PV1_0 | S1_2 | PV2_0 | S2_2 | PV1_1 | ...
 //              S_m = Q_m K_m^T takes D/2 columns (half the steps of a full
 //              product), PV_m reads P_m from TMEM and V from shared memory.
 //   warps 0-3  softmax of map 1, warps 4-7 of map 2: a thread owns a query row
 //              (a TMEM lane), one pass with a running maximum; the accumulator
 //              is rescaled only when the maximum grew by more than 2^8.
+//   warps 10, 11  wait for copies and products on behalf of map 1 and map 2.
 //   epilogue   the warpgroups exchange 1/l_1 and lambda/l_2 through shared
 //              memory and write half of O's columns each.
-// TMEM: S1/P1 at column 0, S2/P2 at 128, O1 at 256, O2 at 256 + D.
+// P_m has columns of its own, so S_m of the next tile is formed as soon as the
+// warpgroup has read this one's, and a map's loop is its softmax alone.  That is
+// what 80 keys are for at D = 128: with 128 the two S and the two O fill TMEM,
+// P_m lies over S_m, and every tile waits for PV_m and the next S_m in turn.
+// Time at B = 1, S = 8191, H = 24, D = 128 (and at B = 2, Sq = 4096, Sk = 777 with a
+// key mask): 960 us (128) that way; 980 (124) with columns of its own for P_m; 795
+// (104) with the relay warps, 0.70 of the tensor time at the issue rate of 51 to 64
+// cycles a product.  What bounds it now is the issuer, whose bursts of four or five
+// products stand 160 to 300 cycles apart.
+// TMEM: S_1, S_2, P_1, P_2 from column 0; O_1, O_2 in the last 2 D.
 // Keys outside the mask get P = 0; their rows of V are zeroed in shared memory
 // before the product reads them, so an infinity or a NaN there leaves no trace.
 #include <cooperative_groups.h>
@@ -31,24 +39,36 @@ namespace cg = cooperative_groups;
 
 // ---------------------------------------------------------------------------
 // Tiles of 128 query rows
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;
+constexpr int kRelayWarp = 10;  // + m
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-// One column pair in sixteen takes its exponentials on the FMA pipe (without, and with one in eight: 135 and 137 us
-// against 128 at B = 2, Sq = 4096, Sk = 777, H = 24, D = 128 with a key mask; 954 and 945 against 960 at S = 8191).
-constexpr int kFmaEvery = 16;
-constexpr uint32_t kBarP = 1;              // kBarP + m: P_m is in TMEM (the warpgroup arrives, the issuer syncs)
-constexpr uint32_t kBarPCount = 128 + 32;
-constexpr uint32_t kBarL = 3;              // the two warpgroups exchange their sums
+// Named barriers.  For the issuer, from a map's warpgroup and relay warp: kBarS + m: S_m has been read and the next K
+// tile has landed; kBarP + m: P_m is in TMEM and the V tile has landed.  For a warpgroup, from its relay warp: kBarF + m:
+// S_m is complete and the V tile has landed; kBarE + m: P's buffer is free.  kBarL: the two warpgroups exchange their sums.
+constexpr uint32_t kBarS = 1, kBarP = 3, kBarIssue = 128 + 32 + 32;
+constexpr uint32_t kBarF = 5, kBarE = 7, kBarRelay = 128 + 32, kBarL = 9;
 
 template <int D>
 struct FwdLayout {
   static constexpr int kTileBytes = 128 * D * 2;
-  static constexpr int kRing = D == 128 ? 5 : 8;
+  static constexpr int kKeys = D == 128 ? 80 : 128;  // keys of a tile
+  static constexpr int kWords = (kKeys + 31) / 32;
+  static constexpr int kKeyBytes = kKeys * D * 2;  // a K or V tile
+  static constexpr int kKeyChunk = kKeys * 128;    // 64 columns of it
+  static constexpr int kRing = 8;
   static constexpr int kQ = 0;  // two Q tiles
   static constexpr int kRingOff = kQ + 2 * kTileBytes;
-  static constexpr int kCtl = kRingOff + kRing * kTileBytes;
+  static constexpr int kCtl = kRingOff + kRing * kKeyBytes;
+  __host__ __device__ static constexpr uint32_t col_s(int m) { return kKeys * m; }
+  __host__ __device__ static constexpr uint32_t col_p(int m) { return 2 * kKeys + kKeys / 2 * m; }
+  __host__ __device__ static constexpr uint32_t col_o(int m) { return 512 - 2 * D + D * m; }
+  static_assert(3 * kKeys <= 512 - 2 * D, "S, P and O of both maps exceed TMEM");
+  // the bits of a full tile in mask word t
+  __host__ __device__ static constexpr uint32_t full(int t) {
+    return kKeys - 32 * t >= 32 ? 0xffffffffu : (1u << (kKeys - 32 * t)) - 1u;
+  }
   static constexpr int kSum = kCtl + 512;          // 1/l of both maps, per row
   static constexpr int kCnt = kSum + 2 * 128 * 4;  // attended key tiles per mask row
   static constexpr int kSmem = kCnt + kMaxCntRows * 4;
@@ -62,7 +82,7 @@ struct FwdCtl {
   uint64_t bar_o_free, bar_final;
   uint32_t tmem_base;
   int abort;
-  uint32_t mask_words[8][4];  // per ring slot (filled with the V tile)
+  alignas(16) uint32_t mask_words[8][4];  // per ring slot (filled with the V tile)
 };
 static_assert(sizeof(FwdCtl) <= 512, "control block");
 
@@ -87,8 +107,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                           int num_items, float scale_log2, DevCtx ctx) {
   using L = FwdLayout<D>;
   constexpr int kChunks = D / 64;
-  constexpr int R = L::kRing;
-  constexpr uint32_t kIdescS = idesc_bf16_f32(128, kTile, false, false);
+  constexpr int R = L::kRing, kKeys = L::kKeys, W = L::kWords;
+  constexpr uint32_t kIdescS = idesc_bf16_f32(128, kKeys, false, false);
   constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, false, true);
   constexpr float kLn2 = 0.6931471805599453f;
 
@@ -104,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int nqt = tiles_of(Sq);
-  const int nkt = tiles_of(Sk);
+  const int nkt = (Sk + kKeys - 1) / kKeys;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -146,12 +166,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int pr = p0 + u;
         bool hit = false;
         if (pr < pairs) {
-          const int r = pr / nkt, k0 = (pr - r * nkt) * kTile;
+          const int r = pr / nkt, k0 = (pr - r * nkt) * kKeys;
           const uint8_t* row = key_mask + (size_t)r * Sk + k0;
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
+          for (int t = 0; t < W; ++t) {
             const int c = 32 * t + lane;
-            hit |= k0 + c < Sk && row[c] != 0;
+            hit |= c < kKeys && k0 + c < Sk && row[c] != 0;
           }
         }
         any[u] = hit;
@@ -194,14 +214,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
       ++ne;
+      // the mask bytes of a tile, a lane's of each word, read one tile ahead: their latency is longer than a tile's time
+      uint8_t bytes[W];
+      auto read_mask = [&](int j) {
+#pragma unroll
+        for (int t = 0; t < W; ++t) {
+          const int c = j * kKeys + 32 * t + lane;
+          bytes[t] = 32 * t + lane < kKeys && c < Sk ? key_mask[(size_t)w.b * Sk + c] : (uint8_t)0;
+        }
+      };
+      if (kMask) read_mask(0);
       for (int j = 0; ok && j < nkt; ++j) {
         uint32_t words[4] = {0u, 0u, 0u, 0u};  // bit c of word t: key 32t + c of the tile is attended
         if (kMask) {
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const int c = j * kTile + 32 * t + lane;
-            words[t] = __ballot_sync(0xffffffffu, c < Sk && key_mask[(size_t)w.b * Sk + c] != 0);
-          }
+          for (int t = 0; t < W; ++t) words[t] = __ballot_sync(0xffffffffu, bytes[t] != 0);
+          read_mask(j + 1);
           if (skip && (words[0] | words[1] | words[2] | words[3]) == 0) continue;
         }
 #pragma unroll
@@ -213,15 +241,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           if (kMask && kind == 1 && lane == 0) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) ctl->mask_words[slot][t] = words[t];
+            for (int t = 0; t < W; ++t) ctl->mask_words[slot][t] = words[t];
           }
           if (lane == 0 && (int)n != ctx.drop_load) {
-            mbar_arrive_expect_tx(&ctl->bar_kv_full[slot], L::kTileBytes);
+            mbar_arrive_expect_tx(&ctl->bar_kv_full[slot], L::kKeyBytes);
             const CUtensorMap* map = kind == 0 ? &tmK : &tmV;
 #pragma unroll
             for (int c = 0; c < kChunks; ++c)
-              tma_load_4d(smem + L::kRingOff + slot * L::kTileBytes + c * kChunkBytes, map, &ctl->bar_kv_full[slot],
-                          c * 64, w.h, j * kTile, w.b);
+              tma_load_4d(smem + L::kRingOff + slot * L::kKeyBytes + c * L::kKeyChunk, map, &ctl->bar_kv_full[slot],
+                          c * 64, w.h, j * kKeys, w.b);
             kv_armed[slot] = use + 1;
           }
         }
@@ -230,33 +258,47 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
     // The whole warp runs the schedule and computes the descriptors, one elected lane waits and
-    // issues.  Within an item this warp learns that P_m is in TMEM from named barrier kBarP + m.
+    // issues.  Within an item this warp waits on named barriers only.
     uint32_t el_lane;
     const bool el = elect_one_sync(&el_lane);
     bool ok = true;
     uint32_t g = 0;   // key tiles across items (phase index of s / pv barriers)
     uint32_t ne = 0;  // items with at least one attended key tile
-    auto ring_addr = [&](uint32_t n) { return sbase + L::kRingOff + (n % R) * L::kTileBytes; };
-    auto issue_s = [&](int m, uint32_t nk, uint32_t qs) {
+    auto ring_addr = [&](uint32_t n) { return sbase + L::kRingOff + (n % R) * L::kKeyBytes; };
+    // byte offset of 16-column step kk of map m in a K tile (map_step in a Q tile, whose chunks are longer)
+    auto key_step = [](int m, int kk) {
+      const int col = m * (D / 2) + 16 * kk;
+      return (uint32_t)((col / 64) * L::kKeyChunk + (col % 64) * 2);
+    };
+    // S_m of key tile t; the second map's releases K's slot
+    auto issue_s = [&](int m, uint32_t t, uint32_t qs) {
       const uint64_t a0 = sdesc_sw128(sbase + L::kQ + qs * L::kTileBytes, 16, 1024);
-      const uint64_t b0 = sdesc_sw128(ring_addr(nk), 16, 1024);
+      const uint64_t b0 = sdesc_sw128(ring_addr(2 * t), 16, 1024);
 #pragma unroll
       for (int kk = 0; kk < D / 32; ++kk) {
-        const uint32_t off = m == 0 ? map_step<D>(0, kk) : map_step<D>(1, kk);
-        const uint64_t a = desc_add(a0, off), b = desc_add(b0, off);
-        if (el) mma_ss_checked(mg, tmem + m * kTile, a, b, kIdescS, kk > 0, kTile);
+        const uint64_t a = desc_add(a0, m == 0 ? map_step<D>(0, kk) : map_step<D>(1, kk));
+        const uint64_t b = desc_add(b0, key_step(m, kk));
+        if (el) mma_ss_checked(mg, tmem + L::col_s(m), a, b, kIdescS, kk > 0, kKeys);
       }
-      if (el) mma_commit(&ctl->bar_s_full[m]);
+      if (el) {
+        mma_commit(&ctl->bar_s_full[m]);
+        if (m == 1) mma_commit(&ctl->bar_kv_empty[(2 * t) % R]);
+      }
     };
-    auto issue_pv = [&](int m, uint32_t nv, bool acc) {
-      const uint64_t b0 = sdesc_sw128(ring_addr(nv), kChunkBytes, 1024);
+    // O_m += P_m V_t; the second map's releases V's slot
+    auto issue_pv = [&](int m, uint32_t t, bool first) {
+      const uint64_t b0 = sdesc_sw128(ring_addr(2 * t + 1), L::kKeyChunk, 1024);
 #pragma unroll
-      for (int kk = 0; kk < kTile / 16; ++kk) {
+      for (int kk = 0; kk < kKeys / 16; ++kk) {
         const uint64_t b = desc_add(b0, kk * 2048);
         if (el)
-          mma_ts_checked(mg, tmem + 256 + m * D, tmem + m * kTile + kk * 8, b, kIdescPV, (acc || kk > 0) ? 1u : 0u, D);
+          mma_ts_checked(mg, tmem + L::col_o(m), tmem + L::col_p(m) + kk * 8, b, kIdescPV, (!first || kk > 0) ? 1u : 0u,
+                         D);
       }
-      if (el) mma_commit(&ctl->bar_pv_done[m]);
+      if (el) {
+        mma_commit(&ctl->bar_pv_done[m]);
+        if (m == 1) mma_commit(&ctl->bar_kv_empty[(2 * t + 1) % R]);
+      }
     };
     for (int item = blockIdx.x; item < num_items; item += gridDim.x) {
       const int nt = item_tiles(decode_item(item, nqt, H).b);
@@ -264,65 +306,113 @@ __global__ void __launch_bounds__(kThreads, 1)
       // After a failure anywhere in the CTA this warp stops issuing but still meets the softmax
       // warpgroups at every named barrier of the schedule.
       if (ok && *reinterpret_cast<volatile int*>(&ctl->abort)) ok = false;
-      const uint32_t nk = 2 * g, qs = ne & 1;
+      const uint32_t qs = ne & 1;
       if (ok) {
         bool w = true;
         if (el) {
           w = wait_or_abort(&ctl->bar_q_full[qs], (ne >> 1) & 1, ctx, ctl);
-          if (w) w = wait_or_abort(&ctl->bar_kv_full[nk % R], (nk / R) & 1, ctx, ctl);
+          if (w) w = wait_or_abort(&ctl->bar_kv_full[(2 * g) % R], ((2 * g) / R) & 1, ctx, ctl);
         }
         ok = __shfl_sync(0xffffffffu, w, el_lane);
         if (ok) {
           tc_fence_after();
-          issue_s(0, nk, qs);
-          issue_s(1, nk, qs);
+          issue_s(0, g, qs);
+          issue_s(1, g, qs);
           if (el) {
-            mma_commit(&ctl->bar_kv_empty[nk % R]);
+            if (nt == 1) mma_commit(&ctl->bar_q_empty[qs]);
             mma_issued = true;
           }
         }
       }
-      for (int j = 0; j < nt; ++j) {
-        const uint32_t nv = 2 * (g + j) + 1, nk1 = nv + 1;
+      for (int j = 0; j <= nt; ++j) {
+        const uint32_t t = g + j;
         const bool more = j + 1 < nt;
-        // map 1: PV1_j, then S1_{j+1}.  V_j and K_{j+1} have landed: the warpgroups waited for them.
-        named_sync(kBarP + 0, kBarPCount);
-        if (ok && j == 0 && ne > 0) {
-          // the previous item's epilogue must have read O before PV1_0 overwrites it
-          bool w = true;
-          if (el) w = wait_or_abort(&ctl->bar_o_free, (ne - 1) & 1, ctx, ctl);
-          ok = __shfl_sync(0xffffffffu, w, el_lane);
-        }
-        if (ok) {
-          tc_fence_after();
-          issue_pv(0, nv, j > 0);
-          if (more) issue_s(0, nk1, qs);
-        }
-        __syncwarp();
-        named_sync(kBarP + 1, kBarPCount);
-        if (ok) {
-          tc_fence_after();
-          issue_pv(1, nv, j > 0);
-          if (el) mma_commit(&ctl->bar_kv_empty[nv % R]);
-          if (more) {
-            issue_s(1, nk1, qs);
-            if (el) mma_commit(&ctl->bar_kv_empty[nk1 % R]);
+        // A product's operands have landed when its barrier passes: the warpgroups waited for them.
+        if (j < nt) {
+          named_sync(kBarS + 0, kBarIssue);
+          if (ok && more) {
+            tc_fence_after();
+            issue_s(0, t + 1, qs);
           }
+          __syncwarp();
         }
-        __syncwarp();
+        if (j > 0) {
+          named_sync(kBarP + 1, kBarIssue);
+          if (ok) {
+            tc_fence_after();
+            issue_pv(1, t - 1, j == 1);
+          }
+          __syncwarp();
+        }
+        if (j < nt) {
+          named_sync(kBarS + 1, kBarIssue);
+          if (ok && more) {
+            tc_fence_after();
+            issue_s(1, t + 1, qs);
+            if (el && j + 2 == nt) mma_commit(&ctl->bar_q_empty[qs]);  // the item's last S
+          }
+          __syncwarp();
+          named_sync(kBarP + 0, kBarIssue);
+          if (ok && j == 0 && ne > 0) {
+            // the previous item's epilogue must have read O before PV1_0 overwrites it
+            bool w = true;
+            if (el) w = wait_or_abort(&ctl->bar_o_free, (ne - 1) & 1, ctx, ctl);
+            ok = __shfl_sync(0xffffffffu, w, el_lane);
+          }
+          if (ok) {
+            tc_fence_after();
+            issue_pv(0, t, j == 0);
+          }
+          __syncwarp();
+        }
       }
-      if (ok && el) mma_commit(&ctl->bar_q_empty[qs]);
-      __syncwarp();
       g += nt;
       ++ne;
+    }
+  } else if (warp >= kRelayWarp) {
+    // ------------------------------------------------------------ relay warps
+    // All waits for copies and products of map m's loop: a test of an mbarrier takes 150 to 300 cycles beside the
+    // matrix instructions' shared-memory reads, even when it passes, and a named barrier about 30; so this warp does
+    // the first and the softmax warps only the second.  After a failure it keeps meeting the others, one
+    // rendezvous after the other.
+    const int m = warp - kRelayWarp;
+    bool ok = true;
+    uint32_t g = 0;
+    auto wait = [&](uint64_t* bar, uint32_t phase) {
+      if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bar, phase & 1, ctx, ctl));
+    };
+    auto meet = [&](uint32_t id, uint32_t count) {
+      if (ok)
+        named_arrive(id, count);
+      else
+        named_sync(id, count);
+    };
+    for (int item = blockIdx.x; item < num_items; item += gridDim.x) {
+      const int nt = item_tiles(decode_item(item, nqt, H).b);
+      for (int j = 0; j < nt; ++j) {
+        const uint32_t gj = g + j, nv = 2 * gj + 1, nk1 = nv + 1;
+        // V_j first: it has mostly landed long before S_m is complete, and its mask words come with it
+        wait(&ctl->bar_kv_full[nv % R], nv / R);
+        wait(&ctl->bar_s_full[m], gj);
+        meet(kBarF + m, kBarRelay);
+        if (j + 1 < nt) wait(&ctl->bar_kv_full[nk1 % R], nk1 / R);
+        meet(kBarS + m, kBarIssue);
+        if (j > 0) {
+          // PV_{j-1} has read P's buffer.  That also says that the last kBarP has been passed, so this warp's arrivals
+          // on it cannot overtake.
+          wait(&ctl->bar_pv_done[m], gj - 1);
+          meet(kBarE + m, kBarRelay);
+        }
+        meet(kBarP + m, kBarIssue);
+      }
+      g += nt;
     }
   } else {
     // ------------------------------------------------------------ softmax warpgroups
     const int m = warp >> 2;                 // map
     const int row = (warp & 3) * 32 + lane;  // TMEM lane = query row within the tile
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t colS = (uint32_t)(m * kTile);
-    const uint32_t colO = 256 + (uint32_t)(m * D);
+    const uint32_t tS = tl + L::col_s(m), tP = tl + L::col_p(m), tO = tl + L::col_o(m);
     bool ok = true;
     uint32_t g = 0;
     for (int item = blockIdx.x; item < num_items; item += gridDim.x) {
@@ -349,54 +439,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       float mu = -INFINITY;  // log2-domain offset in use (scaled max, possibly stale by < 2^8)
       float l_run = 0.f;
       for (int j = 0; j < nt; ++j) {
-        const uint32_t gj = g + j;
-        if (ok) {
-          // V_j and K_{j+1}, read by the MMAs that this step's arrival releases
-          const uint32_t nv = 2 * gj + 1, nk1 = nv + 1;
-          bool okw = wait_or_abort(&ctl->bar_kv_full[nv % R], (nv / R) & 1, ctx, ctl);
-          if (okw && j + 1 < nt) okw = wait_or_abort(&ctl->bar_kv_full[nk1 % R], (nk1 / R) & 1, ctx, ctl);
-          if (okw) okw = wait_or_abort(&ctl->bar_s_full[m], gj & 1, ctx, ctl);
-          ok = __all_sync(0xffffffffu, okw);
-        }
-        if (!ok) {
-          named_sync(kBarP + m, kBarPCount);  // after a failure: keep meeting the issuer
-          continue;
-        }
+        const uint32_t gj = g + j, nv = 2 * gj + 1;
+        named_sync(kBarF + m, kBarRelay);
         tc_fence_after();
-        float s[kTile];
-        tmem_ld32x2(tl + colS, tl + colS + 32, *reinterpret_cast<float(*)[64]>(&s[0]));
-        tmem_ld32x2(tl + colS + 64, tl + colS + 96, *reinterpret_cast<float(*)[64]>(&s[64]));
+        // the tile's mask words, asked for ahead of S: the answer takes as long
+        uint4 words;
+        if (kMask) words = *reinterpret_cast<const uint4*>(ctl->mask_words[nv % R]);
+        float s[kKeys];
+        tmem_ld32x2(tS, tS + 32, *reinterpret_cast<float(*)[64]>(&s[0]));
+        if constexpr (kKeys == 128)
+          tmem_ld32x2(tS + 64, tS + 96, *reinterpret_cast<float(*)[64]>(&s[64]));
+        else
+          tmem_ld16(tS + 64, *reinterpret_cast<float(*)[16]>(&s[64]));
+        tc_fence_before();
+        named_arrive(kBarS + m, kBarIssue);
         if (kMask) {
-          const int vs = (2 * gj + 1) % R;
-          uint32_t mw[4];
+          const int vs = nv % R;
+          const uint32_t mw[4] = {words.x, words.y, words.z, words.w};
+          bool whole = true;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) mw[q] = ctl->mask_words[vs][q];
-          if ((mw[0] & mw[1] & mw[2] & mw[3]) != 0xffffffffu) {
+          for (int q = 0; q < W; ++q) whole = whole && mw[q] == L::full(q);
+          if (!whole) {
 #pragma unroll
-            for (int c = 0; c < kTile; ++c)
+            for (int c = 0; c < kKeys; ++c)
               if (!((mw[c >> 5] >> (c & 31)) & 1u)) s[c] = -INFINITY;
             // V_j's rows outside the mask: read as zeros by both maps' products, the second of which is
             // issued behind the first
             if (m == 0) {
-              if (!((mw[warp & 3] >> lane) & 1u)) {
+              if (row < kKeys && !((ctl->mask_words[vs][row >> 5] >> lane) & 1u)) {
 #pragma unroll
                 for (int c = 0; c < kChunks * 8; ++c)
-                  *reinterpret_cast<uint4*>(smem + L::kRingOff + vs * L::kTileBytes + (c >> 3) * kChunkBytes +
+                  *reinterpret_cast<uint4*>(smem + L::kRingOff + vs * L::kKeyBytes + (c >> 3) * L::kKeyChunk +
                                             row * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
               }
               fence_proxy_async_smem();
             }
           }
-        } else if (j == nkt - 1 && Sk - j * kTile < kTile) {
+        } else if (j == nkt - 1 && Sk - j * kKeys < kKeys) {
 #pragma unroll
-          for (int c = 0; c < kTile; ++c)
-            if (c >= Sk - j * kTile) s[c] = -INFINITY;
+          for (int c = 0; c < kKeys; ++c)
+            if (c >= Sk - j * kKeys) s[c] = -INFINITY;
         }
         float m8[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) m8[q] = fmaxf(s[q], s[q + 8]);
 #pragma unroll
-        for (int c = 16; c < kTile; c += 16)
+        for (int c = 16; c < kKeys; c += 16)
 #pragma unroll
           for (int q = 0; q < 8; ++q) m8[q] = max3(m8[q], s[c + q], s[c + q + 8]);
         const float mt = fmaxf(max3(m8[0], m8[1], m8[2]), max3(max3(m8[3], m8[4], m8[5]), m8[6], m8[7]));
@@ -407,37 +495,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           mu = mt2;
         }
         const float mu_use = (mu == -INFINITY) ? 0.f : mu;
-        // PV_{j-1} of this map, which reads the P columns about to be overwritten, has completed: it was
-        // issued before S_j, and the commit behind s_full covers every earlier MMA of the issuing thread
         const float2 c2 = make_float2(scale_log2, scale_log2);
         const float2 nm2 = make_float2(-mu_use, -mu_use);
         float2 rs2 = make_float2(0.f, 0.f);
+        uint32_t pk[kKeys / 2];
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const float2 x = fma2(make_float2(s[64 * hh + 2 * c], s[64 * hh + 2 * c + 1]), c2, nm2);
-            const float2 e = (c % kFmaEvery == kFmaEvery - 1) ? exp2_fma2(x) : make_float2(ex2(x.x), ex2(x.y));
-            rs2 = add2(rs2, e);
-            pk[c] = pack_bf16(e.x, e.y);
-          }
-          // P (bf16 pairs) over the first 64 columns of this map's S buffer
-          tmem_st32_bits(tl + colS + 32 * hh, pk);
+        for (int c = 0; c < kKeys / 2; ++c) {
+          const float2 x = fma2(make_float2(s[2 * c], s[2 * c + 1]), c2, nm2);
+          const float2 e = make_float2(ex2(x.x), ex2(x.y));
+          rs2 = add2(rs2, e);
+          pk[c] = pack_bf16(e.x, e.y);
         }
         l_run = l_run * alpha + (rs2.x + rs2.y);
+        if (j > 0) named_sync(kBarE + m, kBarRelay);  // PV_{j-1} is done: P's buffer is free, and O may be rescaled
+        tc_fence_after();
+        tmem_st32_bits(tP, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
+        if constexpr (kKeys == 128)
+          tmem_st32_bits(tP + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
+        else
+          tmem_st8_bits(tP + 32, *reinterpret_cast<const uint32_t(*)[8]>(&pk[32]));
         if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             float o[32];
-            tmem_ld32(tl + colO + 32 * c, o);
+            tmem_ld32(tO + 32 * c, o);
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] *= alpha;
-            tmem_st32(tl + colO + 32 * c, o);
+            tmem_st32(tO + 32 * c, o);
           }
         }
         tc_fence_before();
-        named_arrive(kBarP + m, kBarPCount);
+        named_arrive(kBarP + m, kBarIssue);
       }
       if (ok) {
         bool okw = wait_or_abort(&ctl->bar_pv_done[0], (g + nt - 1) & 1, ctx, ctl);
@@ -455,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int c = 0; c < D / 64; ++c) {
         float o[64];  // 32 columns of O1, then of O2
-        tmem_ld32x2(tl + 256 + m * (D / 2) + 32 * c, tl + 256 + D + m * (D / 2) + 32 * c, o);
+        tmem_ld32x2(tl + L::col_o(0) + m * (D / 2) + 32 * c, tl + L::col_o(1) + m * (D / 2) + 32 * c, o);
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           o[32 + i] *= c2;
@@ -511,8 +599,8 @@ int launch_tiles(const void* q, const void* k, const void* v, const void* lam, i
   SegMaps mq, mk, mv;
   int st;
   if ((st = get_dev_ctx(&ctx)) || (st = encode_seq_maps(&mq, q, seq_plain(Sq), B, H, D, kTile)) ||
-      (st = encode_seq_maps(&mk, k, seq_plain(Sk), B, H, D, kTile)) ||
-      (st = encode_seq_maps(&mv, v, seq_plain(Sk), B, H, D, kTile)))
+      (st = encode_seq_maps(&mk, k, seq_plain(Sk), B, H, D, FwdLayout<D>::kKeys)) ||
+      (st = encode_seq_maps(&mv, v, seq_plain(Sk), B, H, D, FwdLayout<D>::kKeys)))
     return st;
   auto kern = diff_fwd_tiles_kernel<D, kMask>;
   const int smem = FwdLayout<D>::kSmem;
