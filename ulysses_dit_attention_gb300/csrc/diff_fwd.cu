@@ -14,16 +14,21 @@
 //              (a TMEM lane), one pass with a running maximum; the accumulator
 //              is rescaled only when the maximum grew by more than 2^8.
 //   warps 10, 11  wait for copies and products on behalf of map 1 and map 2.
-//   epilogue   the warpgroups exchange 1/l_1 and lambda/l_2 through shared
-//              memory and write half of O's columns each.
+//   epilogue   the warpgroups exchange 1/l_1 and 1/l_2 through shared memory and
+//              round half of the columns each into shared memory, over the item's
+//              Q, whose last product is done: O_2, which every warp reads back in
+//              whole lines and stores, then O, which warp 10 sends out by TMA.
+//              (Stored from the registers, a row's 16 bytes a lane, every store
+//              touches 32 lines.)
 // P_m has columns of its own, so S_m of the next tile is formed as soon as the
 // warpgroup has read this one's, and a map's loop is its softmax alone.  That is
 // what 80 keys are for at D = 128: with 128 the two S and the two O fill TMEM,
 // P_m lies over S_m, and every tile waits for PV_m and the next S_m in turn.
 // Time at B = 1, S = 8191, H = 24, D = 128 (and at B = 2, Sq = 4096, Sk = 777 with a
 // key mask): 960 us (128) that way; 980 (124) with columns of its own for P_m; 795
-// (104) with the relay warps, 0.70 of the tensor time at the issue rate of 51 to 64
-// cycles a product.  What bounds it now is the issuer, whose bursts of four or five
+// (104) with the relay warps; 779 (86) with the outputs sent out of shared memory,
+// 0.7 of it tensor time at the issue rate of 51 to 64 cycles a product.  What bounds
+// the loop now is the issuer, whose bursts of four or five
 // products stand 160 to 300 cycles apart.
 // TMEM: S_1, S_2, P_1, P_2 from column 0; O_1, O_2 in the last 2 D.
 // Keys outside the mask get P = 0; their rows of V are zeroed in shared memory
@@ -46,9 +51,11 @@ constexpr int kRelayWarp = 10;  // + m
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 // Named barriers.  For the issuer, from a map's warpgroup and relay warp: kBarS + m: S_m has been read and the next K
 // tile has landed; kBarP + m: P_m is in TMEM and the V tile has landed.  For a warpgroup, from its relay warp: kBarF + m:
-// S_m is complete and the V tile has landed; kBarE + m: P's buffer is free.  kBarL: the two warpgroups exchange their sums.
+// S_m is complete and the V tile has landed; kBarE + m: P's buffer is free.  kBarL: the two warpgroups exchange their
+// sums.  kBarO: O lies in shared memory.
 constexpr uint32_t kBarS = 1, kBarP = 3, kBarIssue = 128 + 32 + 32;
-constexpr uint32_t kBarF = 5, kBarE = 7, kBarRelay = 128 + 32, kBarL = 9;
+constexpr uint32_t kBarF = 5, kBarE = 7, kBarRelay = 128 + 32;
+constexpr uint32_t kBarL = 9, kBarO = 10, kBarOut = 256 + 32;
 
 template <int D>
 struct FwdLayout {
@@ -58,7 +65,7 @@ struct FwdLayout {
   static constexpr int kKeyBytes = kKeys * D * 2;  // a K or V tile
   static constexpr int kKeyChunk = kKeys * 128;    // 64 columns of it
   static constexpr int kRing = 8;
-  static constexpr int kQ = 0;  // two Q tiles
+  static constexpr int kQ = 0;  // two Q tiles, each of them its item's O_2 and O at the end
   static constexpr int kRingOff = kQ + 2 * kTileBytes;
   static constexpr int kCtl = kRingOff + kRing * kKeyBytes;
   __host__ __device__ static constexpr uint32_t col_s(int m) { return kKeys * m; }
@@ -101,13 +108,14 @@ __device__ __forceinline__ Item decode_item(int item, int tiles, int H) {
 template <int D, bool kMask>
 __global__ void __launch_bounds__(kThreads, 1)
     diff_fwd_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                          const __grid_constant__ CUtensorMap tmV, const void* __restrict__ lam, int lam_bf16,
-                          const uint8_t* __restrict__ key_mask, __nv_bfloat16* __restrict__ out,
+                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                          const void* __restrict__ lam, int lam_bf16, const uint8_t* __restrict__ key_mask, __nv_bfloat16* __restrict__ out,
                           __nv_bfloat16* __restrict__ out2, float* __restrict__ lse, int B, int H, int Sq, int Sk,
                           int num_items, float scale_log2, DevCtx ctx) {
   using L = FwdLayout<D>;
   constexpr int kChunks = D / 64;
   constexpr int R = L::kRing, kKeys = L::kKeys, W = L::kWords;
+  constexpr int kPieces = D / 16;  // 16-byte pieces of half a row
   constexpr uint32_t kIdescS = idesc_bf16_f32(128, kKeys, false, false);
   constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, false, true);
   constexpr float kLn2 = 0.6931471805599453f;
@@ -318,10 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           issue_s(0, g, qs);
           issue_s(1, g, qs);
-          if (el) {
-            if (nt == 1) mma_commit(&ctl->bar_q_empty[qs]);
-            mma_issued = true;
-          }
+          if (el) mma_issued = true;
         }
       }
       for (int j = 0; j <= nt; ++j) {
@@ -349,7 +354,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok && more) {
             tc_fence_after();
             issue_s(1, t + 1, qs);
-            if (el && j + 2 == nt) mma_commit(&ctl->bar_q_empty[qs]);  // the item's last S
           }
           __syncwarp();
           named_sync(kBarP + 0, kBarIssue);
@@ -375,9 +379,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // matrix instructions' shared-memory reads, even when it passes, and a named barrier about 30; so this warp does
     // the first and the softmax warps only the second.  After a failure it keeps meeting the others, one
     // rendezvous after the other.
+    // Map 1's also sends O out at the end of an item.  The copy has left the Q tile, which the producer may then fill,
+    // before the next item has come to its first P.
     const int m = warp - kRelayWarp;
     bool ok = true;
-    uint32_t g = 0;
+    uint32_t g = 0, ne = 0;  // key tiles, and items with at least one
     auto wait = [&](uint64_t* bar, uint32_t phase) {
       if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bar, phase & 1, ctx, ctl));
     };
@@ -388,7 +394,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         named_sync(id, count);
     };
     for (int item = blockIdx.x; item < num_items; item += gridDim.x) {
-      const int nt = item_tiles(decode_item(item, nqt, H).b);
+      const Item w = decode_item(item, nqt, H);
+      const int nt = item_tiles(w.b);
+      if (nt == 0) continue;
       for (int j = 0; j < nt; ++j) {
         const uint32_t gj = g + j, nv = 2 * gj + 1, nk1 = nv + 1;
         // V_j first: it has mostly landed long before S_m is complete, and its mask words come with it
@@ -404,9 +412,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           meet(kBarE + m, kBarRelay);
         }
         meet(kBarP + m, kBarIssue);
+        if (m == 0 && j == 0 && ne > 0) {
+          if (lane == 0) {
+            bulk_wait_read_all();
+            mbar_arrive(&ctl->bar_q_empty[(ne - 1) & 1]);
+          }
+          __syncwarp();
+        }
+      }
+      if (m == 0) {
+        named_sync(kBarO, kBarOut);
+        if (lane == 0 && ok && !*reinterpret_cast<volatile int*>(&ctl->abort)) {
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+            tma_store_4d(smem + L::kQ + (ne & 1) * L::kTileBytes + c * kChunkBytes, &tmO, c * 64, w.h, w.t * kTile,
+                         w.b);
+          bulk_commit_group();
+        }
+        __syncwarp();
       }
       g += nt;
+      ++ne;
     }
+    if (m == 0 && lane == 0) bulk_wait_read_all();  // shared memory is read until then
   } else {
     // ------------------------------------------------------------ softmax warpgroups
     const int m = warp >> 2;                 // map
@@ -414,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t tS = tl + L::col_s(m), tP = tl + L::col_p(m), tO = tl + L::col_o(m);
     bool ok = true;
-    uint32_t g = 0;
+    uint32_t g = 0, ne = 0;
     for (int item = blockIdx.x; item < num_items; item += gridDim.x) {
       const Item w = decode_item(item, nqt, H);
       const int nt = item_tiles(w.b);
@@ -535,34 +563,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       // both maps' products are done, which the previous item's readers of these sums allowed (bar_o_free)
       sSum[m * kTile + row] = l_run > 0.f ? 1.f / l_run : 0.f;
       named_sync(kBarL, 256);
+      const uint32_t qs = ne & 1;
       g += nt;
-      if (!ok) continue;
+      ++ne;
+      if (!ok) {
+        named_arrive(kBarO, kBarOut);
+        continue;
+      }
       tc_fence_after();
       const float c1 = sSum[row], c2 = sSum[kTile + row];
       const float lm = load_lambda(lam, lam_bf16, w.h);
+      // this warp's 32 rows and half of the columns, in 16-byte pieces of the swizzled tile
+      auto at = [&](int r, int i) {
+        const int piece = m * kPieces + i;
+        return reinterpret_cast<uint4*>(smem + L::kQ + qs * L::kTileBytes + (piece >> 3) * kChunkBytes + r * 128 +
+                                        (((piece ^ r) & 7) << 4));
+      };
+      auto put = [&](int i, const float* x, float c) {
+        *at(row, i) = make_uint4(pack_bf16(x[0] * c, x[1] * c), pack_bf16(x[2] * c, x[3] * c),
+                                 pack_bf16(x[4] * c, x[5] * c), pack_bf16(x[6] * c, x[7] * c));
+      };
+      if (out2) {
+#pragma unroll 1
+        for (int c = 0; c < D / 64; ++c) {
+          float o[32];
+          tmem_ld32(tl + L::col_o(1) + m * (D / 2) + 32 * c, o);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) put(4 * c + i, o + 8 * i, c2);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int x = 0; x < kPieces; ++x) {
+          const int r = (warp & 3) * 32 + x * (32 / kPieces) + lane / kPieces, i = lane % kPieces;
+          const uint4 v = *at(r, i);
+          const size_t o = (((size_t)w.b * Sq + w.t * kTile + r) * H + w.h) * D + m * (D / 2) + 8 * i;
+          if (w.t * kTile + r < Sq && guard_store(ctx, o, 8, o_extent)) *reinterpret_cast<uint4*>(out2 + o) = v;
+        }
+        __syncwarp();
+      }
 #pragma unroll 1
       for (int c = 0; c < D / 64; ++c) {
         float o[64];  // 32 columns of O1, then of O2
         tmem_ld32x2(tl + L::col_o(0) + m * (D / 2) + 32 * c, tl + L::col_o(1) + m * (D / 2) + 32 * c, o);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          o[32 + i] *= c2;
-          o[i] = o[i] * c1 - lm * o[32 + i];
-        }
-        if (ostore) {
+        for (int i = 0; i < 32; ++i) o[i] = o[i] * c1 - lm * (o[32 + i] * c2);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            *reinterpret_cast<uint4*>(out + oo + 32 * c + 8 * i) =
-                make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
-                           pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
-            if (out2) {
-              const float* p = o + 32 + 8 * i;
-              *reinterpret_cast<uint4*>(out2 + oo + 32 * c + 8 * i) =
-                  make_uint4(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
-            }
-          }
-        }
+        for (int i = 0; i < 4; ++i) put(4 * c + i, o + 8 * i, 1.f);
       }
+      fence_proxy_async_smem();
+      named_arrive(kBarO, kBarOut);
       tc_fence_before();
       mbar_arrive(&ctl->bar_o_free);
       if (ostore) lse[lo] = l_run > 0.f ? mu * kLn2 + logf(l_run) : -INFINITY;
@@ -596,11 +645,12 @@ int launch_tiles(const void* q, const void* k, const void* v, const void* lam, i
                  void* out, void* out2, float* lse, int B, int Sq, int Sk, int H, float scale, cudaStream_t s) {
   const char* fn = "uaa_diff_attn_fwd";
   DevCtx ctx;
-  SegMaps mq, mk, mv;
+  SegMaps mq, mk, mv, mo;
   int st;
   if ((st = get_dev_ctx(&ctx)) || (st = encode_seq_maps(&mq, q, seq_plain(Sq), B, H, D, kTile)) ||
       (st = encode_seq_maps(&mk, k, seq_plain(Sk), B, H, D, FwdLayout<D>::kKeys)) ||
-      (st = encode_seq_maps(&mv, v, seq_plain(Sk), B, H, D, FwdLayout<D>::kKeys)))
+      (st = encode_seq_maps(&mv, v, seq_plain(Sk), B, H, D, FwdLayout<D>::kKeys)) ||
+      (st = encode_seq_maps(&mo, out, seq_plain(Sq), B, H, D, kTile)))
     return st;
   auto kern = diff_fwd_tiles_kernel<D, kMask>;
   const int smem = FwdLayout<D>::kSmem;
@@ -609,9 +659,9 @@ int launch_tiles(const void* q, const void* k, const void* v, const void* lam, i
   const long long items = (long long)tiles_of(Sq) * H * B;
   if (items > INT32_MAX) return set_error(UAA_ERR_UNSUPPORTED, "%s: too many work items", fn);
   const int grid = (int)(items < device_sms() ? items : device_sms());
-  kern<<<grid, kThreads, smem, s>>>(mq.m[0], mk.m[0], mv.m[0], lam, lam_bf16, mask, static_cast<__nv_bfloat16*>(out),
-                                    static_cast<__nv_bfloat16*>(out2), lse, B, H, Sq, Sk, (int)items, scale * kLog2e,
-                                    ctx);
+  kern<<<grid, kThreads, smem, s>>>(mq.m[0], mk.m[0], mv.m[0], mo.m[0], lam, lam_bf16, mask,
+                                    static_cast<__nv_bfloat16*>(out), static_cast<__nv_bfloat16*>(out2), lse, B, H, Sq,
+                                    Sk, (int)items, scale * kLog2e, ctx);
   return check_launch(fn);
 }
 

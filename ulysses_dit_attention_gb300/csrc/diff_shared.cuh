@@ -25,6 +25,16 @@ namespace {
 constexpr int kTile = 128;              // query rows and keys of a tile
 constexpr int kChunkBytes = 128 * 128;  // 128 rows x 128 bytes: 64 columns of a tile, 128-byte swizzled
 
+// 4-D tiled tensor store from shared memory (bulk-group completion; out-of-range rows of the box are not written).
+__device__ __forceinline__ void tma_store_4d(const void* smem_src, const CUtensorMap* map, int c0, int c1, int c2,
+                                             int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(smem_u32(smem_src)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
 __device__ __forceinline__ float load_lambda(const void* lam, int bf16, int h) {
   return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(lam)[h]) : static_cast<const float*>(lam)[h];
 }
