@@ -53,9 +53,48 @@ __device__ __forceinline__ bool wait_two(uint64_t* a, uint32_t pa, uint64_t* b, 
   return wait_or_abort(a, pa, ctx, ctl) && wait_or_abort(b, pb, ctx, ctl);
 }
 
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v, float c) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(v[0] * c, v[1] * c), pack_bf16(v[2] * c, v[3] * c),
-                                            pack_bf16(v[4] * c, v[5] * c), pack_bf16(v[6] * c, v[7] * c));
+// Pieces of 16 bytes, N of this lane's row, to piece lane % N of the N rows of its group of N lanes: a store of the warp
+// then writes 32 / N rows, 16 N bytes each, instead of 16 bytes in each of 32 rows.
+template <int N>
+__device__ __forceinline__ void swap_pieces(uint4 (&x)[N], int lane) {
+#pragma unroll
+  for (int bit = 1; bit < N; bit *= 2) {
+    const bool hi = lane & bit;
+#pragma unroll
+    for (int p = 0; p < N; ++p) {
+      if (p & bit) continue;
+      uint4 v = hi ? x[p] : x[p | bit];
+      v.x = __shfl_xor_sync(0xffffffffu, v.x, bit), v.y = __shfl_xor_sync(0xffffffffu, v.y, bit);
+      v.z = __shfl_xor_sync(0xffffffffu, v.z, bit), v.w = __shfl_xor_sync(0xffffffffu, v.w, bit);
+      (hi ? x[p] : x[p | bit]) = v;
+    }
+  }
+}
+
+// Warp-collective: 8 N accumulator columns of 32 rows, times c (zero where `zero`), as bf16; row 0 of them at `at`, the
+// rows `pitch` elements apart, `left` of them to be written.
+template <int N>
+__device__ __forceinline__ void store_rows(__nv_bfloat16* base, size_t at, size_t pitch, int left, uint32_t col, float c,
+                                           bool zero, int lane, const DevCtx& ctx, size_t extent) {
+  uint4 x[N];
+#pragma unroll
+  for (int h = 0; h < N / 2; ++h) {
+    float v[16];
+    tmem_ld16(col + 16 * h, v);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = zero ? 0.f : v[i] * c;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      x[2 * h + i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                                pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+  }
+  swap_pieces<N>(x, lane);
+  const int q = lane % N, r0 = lane - q;
+#pragma unroll
+  for (int r = 0; r < N; ++r) {
+    const size_t to = at + (r0 + r) * pitch + 8 * q;
+    if (r0 + r < left && guard_store(ctx, to, 8, extent)) *reinterpret_cast<uint4*>(base + to) = x[r];
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -523,22 +562,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float ck = cq >= 2 && load_lambda(lam, lam_bf16, w.h) > 0.f ? -scale : scale;
       const uint32_t cV = tl + kColDV + cq * (D / 4);
       const uint32_t cK = tl + kColDK + cq * (D / 4) + (D == 64 ? (cq >> 1) * 64 : 0);
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        float gv[16], gk[16];
-        tmem_ld16(cV + 16 * c, gv);
-        tmem_ld16(cK + 16 * c, gk);
-        if (!attended) {
-#pragma unroll
-          for (int x = 0; x < 16; ++x) gv[x] = gk[x] = 0.f;
-        }
-        if (store) {
-          store8(dv + off + 16 * c, gv, 1.f);
-          store8(dv + off + 16 * c + 8, gv + 8, 1.f);
-          store8(dk + off + 16 * c, gk, ck);
-          store8(dk + off + 16 * c + 8, gk + 8, ck);
-        }
-      }
+      const int j0 = w.t * kTile + (warp & 3) * 32;
+      const size_t to = (((size_t)w.b * Sk + j0) * H + w.h) * D + cq * (D / 4), pitch = (size_t)H * D;
+      store_rows<D / 32>(dv, to, pitch, Sk - j0, cV, 1.f, !attended, lane, ctx, k_extent);
+      store_rows<D / 32>(dk, to, pitch, Sk - j0, cK, ck, !attended, lane, ctx, k_extent);
       tc_fence_before();
       mbar_arrive(&ctl->bar_acc_free);
     }
@@ -951,15 +978,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const float cs = cq >= 2 && load_lambda(lam, lam_bf16, w.h) > 0.f ? -scale : scale;
       const uint32_t cQ = tl + kColDQ + cq * (D / 4) + (D == 64 ? (cq >> 1) * 64 : 0);
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        float gv[16];
-        tmem_ld16(cQ + 16 * c, gv);
-        if (store) {
-          store8(dq + off + 16 * c, gv, cs);
-          store8(dq + off + 16 * c + 8, gv + 8, cs);
-        }
-      }
+      const int i0 = w.t * kTile + (warp & 3) * 32;
+      store_rows<D / 32>(dq, (((size_t)w.b * Sq + i0) * H + w.h) * D + cq * (D / 4), (size_t)H * D, Sq - i0, cQ, cs, false,
+                         lane, ctx, q_extent);
       tc_fence_before();
       mbar_arrive(&ctl->bar_dq_free);
     }
