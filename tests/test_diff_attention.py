@@ -207,18 +207,99 @@ def test_forward_without_gradient(D):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("Sq", [1, 200])
-def test_what_is_masked_does_not_matter(D, Sq):
-    """Infinities and NaN... in masked keys' rows would meet P = 0; finite extremes must leave no trace."""
+@pytest.mark.parametrize("Sq", [1, 4, 200, 600])
+@pytest.mark.parametrize("value", [3e4, float("inf"), float("nan")])
+def test_what_is_masked_does_not_matter(D, Sq, value):
+    """Whatever a masked key's rows of K and V hold, infinities and NaN too: every result has the same bits."""
     x = draw(1, Sq, 333, 2, D, "random", seed=8)
     y = {n: None if t is None else t.clone() for n, t in x.items()}
     dead = ~x["mask"][0]
-    y["k"][0, dead] = 3e4
-    y["v"][0, dead] = -3e4
+    y["k"][0, dead] = value
+    y["v"][0, dead] = -value
     a, b = step(on_gpu(x)), step(on_gpu(y))
     for n in a:
-        if n not in ("dk", "dv"):
-            assert np.array_equal(bits(a[n]), bits(b[n])), n
+        assert np.array_equal(bits(a[n]), bits(b[n])), n
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Sq", [1, 3, 130, 1030])
+def test_keys_past_32_bits(Sq):
+    """Offsets of K, V, dK and dV past 2^31 elements: only the last keys are attended, and the results are those of
+    the short problem that has no others.  Its start is a border between tiles of both kernels (80 and 128 keys)."""
+    Sk, start, H, D = 139008, 133120, 128, 128
+    assert start * H * D > 2**31 and start % 640 == 0
+    g = torch.Generator(DEV).manual_seed(41)
+    new = lambda n: torch.randn(1, n, H, D, generator=g, device=DEV, dtype=torch.bfloat16)  # noqa: E731
+    q, do, k, v = new(Sq), new(Sq), new(Sk), new(Sk)
+    lam = torch.rand(H, generator=g, device=DEV)
+    mask = torch.zeros(1, Sk, dtype=torch.bool, device=DEV)
+    mask[:, start:] = True
+    mask[:, -3] = False
+    long = step(dict(q=q, k=k, v=v, do=do, lam=lam, mask=mask))
+    cut = lambda t: t[:, start:].contiguous()  # noqa: E731
+    short = step(dict(q=q, k=cut(k), v=cut(v), do=do, lam=lam, mask=cut(mask)))
+    for n in ("dk", "dv"):
+        assert not long[n][:, :start].any(), n
+        long[n] = cut(long[n])
+    if Sq <= 2:
+        # The few-row kernel splits the keys by their number, so the forward's sums have another order.  A lane group
+        # adds at most 400 of the products A v (5888 keys over 16 groups) and eight joins follow, so a sum is within
+        # 408 * 2^-24 * sum A |v| < 2^-11, as |v| < 8 and the weights sum to 1 + lambda < 2; then a step of bf16.
+        assert v.abs().max() < 8
+        for n in ("out", "out2", "lse"):
+            assert torch.allclose(long[n].float(), short[n].float(), rtol=2**-7, atol=2**-11), n
+        short.update(zip(("dq", "dk", "dv", "dlam"),
+                         uaa.diff_attn_bwd(q, cut(k), cut(v), lam, long["out"], long["out2"], do, long["lse"], cut(mask))))
+    for n in ("out", "out2", "lse", "dq", "dk", "dv", "dlam"):
+        if Sq > 2 or n[0] == "d":
+            assert torch.equal(long[n], short[n]), n
+
+
+@pytest.mark.gpu
+def test_queries_past_32_bits():
+    """Offsets of Q, O, dO and dQ past 2^31 elements: the last rows are those of the short problem."""
+    Sq, start, H, D, Sk = 136000, 133120, 128, 128, 100
+    assert start * H * D > 2**31 and start % 128 == 0
+    g = torch.Generator(DEV).manual_seed(42)
+    new = lambda n: torch.randn(1, n, H, D, generator=g, device=DEV, dtype=torch.bfloat16)  # noqa: E731
+    q, do, k, v = new(Sq), new(Sq), new(Sk), new(Sk)
+    lam = torch.rand(H, generator=g, device=DEV)
+    long = step(dict(q=q, k=k, v=v, do=do, lam=lam, mask=None))
+    cut = lambda t: t[:, start:].contiguous()  # noqa: E731
+    short = step(dict(q=cut(q), k=k, v=v, do=cut(do), lam=lam, mask=None))
+    for n in ("out", "out2", "dq"):
+        assert torch.equal(cut(long[n]), short[n]), n
+    assert torch.equal(long["lse"][..., start:], short["lse"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("saved", [None, "int8"])
+def test_captured_autograd_step(saved):
+    """Forward and gradients by autograd, captured after a warm-up on another stream, replayed on new inputs."""
+    x = on_gpu(draw(2, 200, 210, 2, 128, "prefix", seed=43))
+    leaves = [x[n].requires_grad_() for n in ("q", "k", "v", "lam")]
+
+    def run():
+        out, _ = uaa.diff_attention(*leaves, x["mask"], saved=saved)
+        return (out.detach(),) + torch.autograd.grad(out, leaves, x["do"])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    with torch.no_grad():
+        for n in ("q", "k", "v", "do"):
+            x[n].normal_()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, w in zip(got, run()):
+        assert np.array_equal(bits(a), bits(w))
+    uaa.check_device_status()
 
 
 @pytest.mark.gpu
