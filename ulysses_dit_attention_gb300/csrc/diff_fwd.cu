@@ -957,13 +957,14 @@ template <int D, bool kMask>
 int launch_fwd(const void* q, const void* k, const void* v, const void* lam, int lam_bf16, const uint8_t* mask,
                void* out, void* out2, float* lse, int B, int Sq, int Sk, int H, float scale, cudaStream_t s) {
   // Few rows or tiles?  Per 128 keys and head, reading them for two rows takes about 11 ns of the whole card (D = 128;
-  // half of it with D = 64), and a wave of query tiles about 1.45 us: the first is the faster for up to 128 such pairs
-  // of rows a wave.  Measured both ways at Sk = 16389, D = 128, us (rows, tiles): B H = 96, Sq = 2: 136, 195; Sq = 3:
-  // 277, 195; B H = 24, Sq = 8: 117, 180; Sq = 16: 258, 181; B H = 8, Sq = 32: 164, 177; D = 64, B H = 24, Sq = 16:
-  // 137, 158.  One or two rows need one reading only: B H = 1536, Sk = 1000, Sq = 1: 144, 163.
+  // half of it with D = 64), and a wave of query tiles about 1.1 us: the first is the faster for up to 96 such pairs of
+  // rows a wave.  Measured both ways at Sk = 16389, D = 128, us (rows, tiles): B H = 96, Sq = 2: 136, 158; Sq = 3: 279,
+  // 158; B H = 24, Sq = 8: 117, 141; Sq = 16: 258, 141; B H = 8, Sq = 16: 115, 138; Sq = 32: 165, 138; D = 64,
+  // B H = 24, Sq = 16: 138, 145; Sq = 32: 252, 145; B H = 1536, Sk = 1000, Sq = 2: 158, 144.  One row needs less of
+  // the kernel: Sq = 1 there: 143, 146.
   const long long bh = (long long)B * H, groups = (Sq + 1) / 2, sms = device_sms();
   const long long waves = (bh * tiles_of(Sq) + sms - 1) / sms;
-  const bool rows = Sq <= 2 || groups * bh * D <= 16384 * waves;
+  const bool rows = Sq == 1 || groups * bh * D <= 12288 * waves;
   auto go = !rows ? launch_tiles<D, kMask> : Sq == 1 ? launch_rows<D, 1, kMask> : launch_rows<D, 2, kMask>;
   return go(q, k, v, lam, lam_bf16, mask, out, out2, lse, B, Sq, Sk, H, scale, s);
 }
