@@ -840,14 +840,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) {
           tc_fence_after();
           issue_dq(G, 0, g == 0);
-          if (more) issue_s(G + 1, 0);
+          if (more) {
+            issue_s(G + 1, 0);
+            issue_dp(G + 1);
+          }
         }
         __syncwarp();
         // dS_2 is in TMEM, dA has been read, and the next V tile has landed
         named_sync(kBarDS, kBarCount);
         if (ok) {
           tc_fence_after();
-          if (more) issue_dp(G + 1);
           issue_dq(G, 1, g == 0);
           if (more) {
             issue_s(G + 1, 1);
@@ -930,9 +932,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int m = 0; m < 2; ++m) {
           if (m == 1) {
             met = true;
-            const uint32_t Gw = more ? G + 1 : G;  // the next V tile, read by the product that dS_2 releases
-            ok = __all_sync(0xffffffffu, wait_two(&ctl->bar_s_full[1], G & 1, &ctl->bar_v_full[Gw % VR],
-                                                  (Gw / VR) & 1, ctx, ctl));
+            ok = __all_sync(0xffffffffu, wait_or_abort(&ctl->bar_s_full[1], G & 1, ctx, ctl));
             if (!ok) break;
           }
           tc_fence_after();
@@ -944,7 +944,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             p[2 * c] = ex2(x.x), p[2 * c + 1] = ex2(x.y);
           }
           if (m == 0) {
-            ok = __all_sync(0xffffffffu, wait_or_abort(&ctl->bar_dp_full, G & 1, ctx, ctl));
+            // dA, and the next V tile, which the next dA's product reads as soon as this one has been read
+            const uint32_t Gw = more ? G + 1 : G;
+            ok = __all_sync(0xffffffffu, wait_two(&ctl->bar_dp_full, G & 1, &ctl->bar_v_full[Gw % VR], (Gw / VR) & 1,
+                                                  ctx, ctl));
             if (!ok) break;
             tc_fence_after();
             tmem_ld32(tl + kColDP + 32 * cq, dp);
