@@ -111,6 +111,12 @@ CASES = [
     (1, 50, 1, 3, 256, [256], "half", torch.bfloat16, "none"),
     (1, 5, 2, 2, 64, [0, 0], "half", torch.bfloat16, "none"),  # nothing is rotated: a copy
     (1, 3, 2, 2, 7, [6], "interleaved", torch.float32, "none"),
+    # rows of whole 16-byte vectors whose runs of pairs are not
+    (2, 40, 5, 3, 80, [50], "half", torch.bfloat16, "none"),
+    (1, 33, 3, 2, 256, [250], "interleaved", torch.float16, "none"),
+    (1, 21, 2, 9, 128, [100, 26], "half", torch.float32, "none"),
+    (2, 19, 1, 2, 8, [6], "half", torch.bfloat16, "none"),
+    (1, 19, 3, 0, 264, [250], "half", torch.bfloat16, "none"),  # more vectors than a warp has lanes
 ]
 
 
@@ -147,6 +153,27 @@ def test_default_positions_one_tensor_and_in_place():
     z = q.clone()
     assert uaa.rotary_fwd(z, None, plan, start=1000, out_q=z)[0] is z
     assert torch.equal(z, y)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("D,rot", [(64, 50), (80, 78), (256, 130), (128, 20)])
+def test_partial_rows_in_place_strided_and_off_the_grid(layout, D, rot):
+    """Every access width gives the same bits; a row that lies between others is turned where it is."""
+    plan = uaa.RotaryPlan([rot], layout=layout)
+    B, S, H = 2, 45, 3
+    x = torch.randn(B, S, H, D, device=DEV, dtype=torch.bfloat16)
+    want = uaa.rotary_fwd(x, None, plan, start=9)[0]
+    for off in (1, 2, 4, 8):
+        flat = torch.zeros(x.numel() + 8, device=DEV, dtype=torch.bfloat16)
+        y = flat[off:off + x.numel()].view(B, S, H, D).copy_(x)
+        assert torch.equal(uaa.rotary_fwd(y, None, plan, start=9)[0], want), off
+    packed = torch.randn(B, S, 3, H, D, device=DEV, dtype=torch.bfloat16)
+    packed[:, :, 1] = x
+    keep = packed.clone()
+    uaa.rotary_fwd(packed[:, :, 1], None, plan, start=9, out_q=packed[:, :, 1])
+    assert torch.equal(packed[:, :, 1], want)
+    assert torch.equal(packed[:, :, 0], keep[:, :, 0]) and torch.equal(packed[:, :, 2], keep[:, :, 2])
 
 
 @pytest.mark.gpu

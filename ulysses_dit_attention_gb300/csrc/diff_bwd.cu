@@ -9,8 +9,12 @@
 // A operand of map 2's dV product, and the sign of dQ_2 and dK_2 when they are written.
 // Both matrix kernels: warps 0-15 compute (TMEM lane quadrant = warp % 4, 32 of a tile's 128 columns = warp / 4;
 // four warps on each scheduler, because with two the latencies of TMEM and barriers lay open: dK/dV 1640 -> 1455 us,
-// dQ 1067 -> 933 us at S = 8191, H = 24, D = 128), warp 16 loads by TMA, warp 17 issues the tcgen05 products from one elected lane.  MMAs of one thread run in order; two that read A
-// from TMEM for different products are only relied on with equal shapes or with another product between them.
+// dQ 1067 -> 933 us at S = 8191, H = 24, D = 128), warp 16 loads by TMA, warp 17 issues the tcgen05 products from one
+// elected lane.  MMAs of one thread run in order; two that read A from TMEM for different products are only relied on
+// with equal shapes or with another product between them.
+// At that size: 29 us, 1434 us (tensor pipe active 79 % of the time) and 905 us; 2366 us together.  What bounds the
+// matrix kernels is the chain S -> P -> dS -> next S through TMEM and barriers, which one tile's products and the
+// compute warps take in turns; two tiles half a step apart would need 640 columns of TMEM.
 #include "diff_shared.cuh"
 
 namespace uaa {
@@ -212,11 +216,12 @@ __device__ __forceinline__ Item decode_item(int item, int tiles, int H, bool hea
 //     S^T = K_m Q_m^T, P^T = w_m A_m^T (w = 1, -lambda), dA^T = V dO^T    (M = keys, N = 128 queries)
 //     dV += P^T dO, dS^T = P^T (dA^T - Delta_m), dK_m += dS^T Q_m
 // One elected lane issues, per step: dV_s S_{s+1} after P_s, dK_s dA_{s+1} after dS_s; so the tensor cores work
-// while the eight compute warps take the exponentials of the next step or form dS of this one.  dA is formed anew
-// for the second map: 3072 cycles of products per pair of tiles against 2048 without, but the TMEM that keeping it
-// would take is not there, and with steps of 64 queries, whose two buffers would fit, a product with both operands
-// in shared memory takes as long as one with 128 (its A operand is read just the same): measured 2052 us
-// against 1640 for B = 1, S = 8191, H = 24, D = 128 (1455 with sixteen compute warps).
+// while the compute warps take the exponentials of the next step or form dS of this one.  dA is formed anew for the
+// second map.  Kept in the compute warps' registers instead, it saves a seventh of the MMAs and no time: 2401 against
+// 2343 us for the whole backward at B = 1, S = 8191, H = 24, D = 128, 773 against 750 at B = 2, S = 4096 with a mask;
+// nor does one dV product of A_1 - lambda A_2 (2727).  Steps of 64 queries, whose TMEM would hold two buffers, lose
+// too: a product with both operands in shared memory takes as long for 64 columns as for 128 (2052 against 1640 us,
+// with eight compute warps).
 // TMEM: S^T at column 0, dA^T at 128 (P^T and dS^T, packed, over the first 16 columns of each warpgroup's 32),
 // dV at 256, dK_m at 384 + 64 m (with D = 64 the product runs over all 64 columns of Q and map m's 32 are kept).
 template <int D>
@@ -594,8 +599,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------
 // 3. dQ.  A persistent CTA takes 128 queries of one (batch, head), Q and dO in shared memory, and walks the key
 // tiles: S_m = Q_m K_m^T, dA = dO V^T (M = queries, N = 128 keys), then dQ_m += dS_m K_m.  The maps take turns:
-// while the compute warps work on map 2 of tile g, the tensor cores form dQ_1 of tile g and S_1 of tile g + 1;
-// then dA of tile g + 1, dQ_2 and S_2 while they take map 1's exponentials.
+// while the compute warps work on map 2 of tile g, with dA in their registers, the tensor cores form dQ_1 of tile g, S_1
+// and dA of tile g + 1; then dQ_2 and S_2 while they take map 1's exponentials.
 // TMEM: S_1 at column 0, S_2 at 128 (dS_m, packed, over the first 16 columns of each warpgroup's 32), dA at 256,
 // dQ_m at 384 + 64 m (with D = 64 the product runs over all 64 columns of K and map m's 32 are kept).
 template <int D>
@@ -833,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int g = 0; g < n; ++g) {
         const uint32_t G = G0 + g;
         const bool more = g + 1 < n;
-        // dS_1 is in TMEM and the next K tile has landed: the compute warps waited for it
+        // dS_1 is in TMEM, dA has been read, and the next K and V tiles have landed: the compute warps waited for them
         named_sync(kBarP, kBarCount);
         // the previous item's epilogue must have read dQ
         if (ok && g == 0 && it > 0) ok = wait_el(&ctl->bar_dq_free, (it - 1) & 1);
@@ -846,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
-        // dS_2 is in TMEM, dA has been read, and the next V tile has landed
+        // dS_2 is in TMEM
         named_sync(kBarDS, kBarCount);
         if (ok) {
           tc_fence_after();

@@ -17,7 +17,8 @@
 //
 // Bound: HBM.  Every element is read once and written once; the angles are
 // computed once per token by the block (R/2 of them, in shared memory) and used
-// by all heads of Q and K.
+// by all heads of Q and K.  Q and K of 27280 x 40 x 128 in bf16: 196 us a pass
+// interleaved, 189 in halves, 5.7 and 5.9 TB/s, 0.85 and 0.88 of a copy's rate.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -73,6 +74,45 @@ struct alignas(V * sizeof(T)) Vec {
   T e[V];
 };
 
+// One pair, with the same roundings in every kernel; c = (cos a, sin a) * m
+template <typename T>
+__device__ __forceinline__ void turn_pair(float2 c, T& u, T& w) {
+  const float x0 = to_f32<T>(u), x1 = to_f32<T>(w);
+  u = from_f32<T>(fmaf(x0, c.x, -(x1 * c.y)));
+  w = from_f32<T>(fmaf(x0, c.y, x1 * c.x));
+}
+
+// (cos a, sin a) * m of every pair of nt tokens
+__device__ __forceinline__ void angles(const RotArgs& a, uint32_t t0, uint32_t nt, float2* cs) {
+  const int pairs = a.plan.rot / 2;
+  for (uint32_t i = threadIdx.x; i < nt * pairs; i += kThreads) {
+    const uint32_t tok = t0 + i / pairs, p = i % pairs;
+    const uint32_t b = tok / a.S, s = tok - b * a.S;
+    long long pos = a.start + s;
+    if (a.positions) {
+      const long long at = b * a.pb + s * a.ps + a.plan.axis[p];
+      pos = a.pos64 ? static_cast<const long long*>(a.positions)[at] : static_cast<const int*>(a.positions)[at];
+    }
+    const uint64_t turn = static_cast<uint64_t>(pos) * a.plan.turns[p];
+    // the fraction of a turn in (-1/2, 1/2], in half turns: 32 bits, rounded to 24 by the conversion
+    const float half_turns = static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f;
+    float sn, cn;
+    sincospif(half_turns, &sn, &cn);
+    cs[i] = make_float2(cn * a.plan.magnitude, (a.inverse ? -sn : sn) * a.plan.magnitude);
+  }
+}
+
+// Row h of token tok: the tensor that holds it, its input and its output
+template <typename T>
+__device__ __forceinline__ void locate(const RotArgs& a, uint32_t tok, uint32_t h, const T** x, T** y) {
+  const uint32_t b = tok / a.S, s = tok - b * a.S;
+  const bool second = h >= static_cast<uint32_t>(a.t[0].H);
+  const RotTensor& t = a.t[second ? 1 : 0];
+  if (second) h -= a.t[0].H;
+  *x = static_cast<const T*>(t.x) + (b * t.xb + s * t.xs + h * t.xh);
+  *y = static_cast<T*>(t.y) + (b * t.yb + s * t.ys + h * t.yh);
+}
+
 // One thread takes units of V pairs (two runs of V columns) or of V copied columns.
 template <typename T, int V, bool kHalf>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotArgs a) {
@@ -81,61 +121,89 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
   const uint32_t heads = a.t[0].H + a.t[1].H;
   for (uint32_t t0 = blockIdx.x * a.tokens_per_block; t0 < a.tokens; t0 += gridDim.x * a.tokens_per_block) {
     const uint32_t nt = a.tokens - t0 < a.tokens_per_block ? a.tokens - t0 : a.tokens_per_block;
-    for (uint32_t i = threadIdx.x; i < nt * pairs; i += kThreads) {
-      const uint32_t tok = t0 + i / pairs, p = i % pairs;
-      const uint32_t b = tok / a.S, s = tok - b * a.S;
-      long long pos = a.start + s;
-      if (a.positions) {
-        const long long at = b * a.pb + s * a.ps + a.plan.axis[p];
-        pos = a.pos64 ? static_cast<const long long*>(a.positions)[at] : static_cast<const int*>(a.positions)[at];
-      }
-      const uint64_t turn = static_cast<uint64_t>(pos) * a.plan.turns[p];
-      // the fraction of a turn in (-1/2, 1/2], in half turns: 32 bits, rounded to 24 by the conversion
-      const float half_turns = static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f;
-      float sn, cn;
-      sincospif(half_turns, &sn, &cn);
-      cs[i] = make_float2(cn * a.plan.magnitude, (a.inverse ? -sn : sn) * a.plan.magnitude);
-    }
+    angles(a, t0, nt, cs);
     __syncthreads();
     const uint32_t work = nt * heads * a.units;
     for (uint32_t i = threadIdx.x; i < work; i += kThreads) {
       const uint32_t row = i / a.units, u = i - row * a.units;
       const uint32_t lt = row / heads;
-      uint32_t h = row - lt * heads;
-      const uint32_t tok = t0 + lt;
-      const uint32_t b = tok / a.S, s = tok - b * a.S;
-      const bool second = h >= static_cast<uint32_t>(a.t[0].H);
-      const RotTensor& t = a.t[second ? 1 : 0];
-      if (second) h -= a.t[0].H;
-      const T* x = static_cast<const T*>(t.x) + (b * t.xb + s * t.xs + h * t.xh);
-      T* y = static_cast<T*>(t.y) + (b * t.yb + s * t.ys + h * t.yh);
+      const T* x;
+      T* y;
+      locate(a, t0 + lt, row - lt * heads, &x, &y);
       using VT = Vec<T, V>;
       if (u < a.pair_units) {
         const int c0 = kHalf ? u * V : 2 * u * V, c1 = kHalf ? c0 + pairs : c0 + V;
-        const VT v0 = *reinterpret_cast<const VT*>(x + c0), v1 = *reinterpret_cast<const VT*>(x + c1);
+        VT v0 = *reinterpret_cast<const VT*>(x + c0), v1 = *reinterpret_cast<const VT*>(x + c1);
         const float2* w = cs + lt * pairs + u * V;
-        VT o0, o1;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const float2 r = w[e];
           // interleaved: pair e of the unit is elements 2e and 2e + 1 of its 2V columns
-          const float x0 = to_f32<T>(kHalf ? v0.e[e] : (2 * e < V ? v0.e[(2 * e) % V] : v1.e[(2 * e) % V]));
-          const float x1 = to_f32<T>(kHalf ? v1.e[e] : (2 * e + 1 < V ? v0.e[(2 * e + 1) % V] : v1.e[(2 * e + 1) % V]));
-          const T y0 = from_f32<T>(x0 * r.x - x1 * r.y), y1 = from_f32<T>(x0 * r.y + x1 * r.x);
-          if (kHalf) {
-            o0.e[e] = y0;
-            o1.e[e] = y1;
-          } else {
-            (2 * e < V ? o0 : o1).e[(2 * e) % V] = y0;
-            (2 * e + 1 < V ? o0 : o1).e[(2 * e + 1) % V] = y1;
-          }
+          T& u0 = kHalf ? v0.e[e] : (2 * e < V ? v0.e[(2 * e) % V] : v1.e[(2 * e) % V]);
+          T& u1 = kHalf ? v1.e[e] : (2 * e + 1 < V ? v0.e[(2 * e + 1) % V] : v1.e[(2 * e + 1) % V]);
+          turn_pair(w[e], u0, u1);
         }
-        *reinterpret_cast<VT*>(y + c0) = o0;
-        *reinterpret_cast<VT*>(y + c1) = o1;
+        *reinterpret_cast<VT*>(y + c0) = v0;
+        *reinterpret_cast<VT*>(y + c1) = v1;
       } else {
         const int c = a.plan.rot + (u - a.pair_units) * V;
         *reinterpret_cast<VT*>(y + c) = *reinterpret_cast<const VT*>(x + c);
       }
+    }
+    __syncthreads();  // the next tokens' angles replace these
+  }
+}
+
+// Rows of whole 16-byte vectors whose pairs are not: rot / 2 or D - rot is not a multiple of the vector's elements.  A
+// warp takes as many rows as its lanes hold, one vector a lane.  Interleaved pairs lie in one lane; halves are read from
+// and written to the rows in shared memory, pair by pair, so a row may be turned in place.
+template <typename T, bool kHalf>
+__global__ void __launch_bounds__(kThreads) rotary_rows_kernel(const __grid_constant__ RotArgs a) {
+  constexpr int E = 16 / sizeof(T);
+  extern __shared__ float2 cs[];
+  __shared__ Vec<T, E> stage[kHalf ? kThreads : 1];
+  const uint32_t pairs = a.plan.rot / 2, heads = a.t[0].H + a.t[1].H;
+  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t L = a.units, rw = 32 / L, r = lane / L, j = lane % L;  // vectors of a row, rows of a warp
+  Vec<T, E>* mine = stage + warp * 32;
+  for (uint32_t t0 = blockIdx.x * a.tokens_per_block; t0 < a.tokens; t0 += gridDim.x * a.tokens_per_block) {
+    const uint32_t nt = a.tokens - t0 < a.tokens_per_block ? a.tokens - t0 : a.tokens_per_block;
+    angles(a, t0, nt, cs);
+    __syncthreads();
+    const uint32_t rows = nt * heads;
+    for (uint32_t r0 = warp * rw; r0 < rows; r0 += kThreads / 32 * rw) {
+      const uint32_t row = r0 + r, lt = row / heads;
+      const bool active = r < rw && row < rows;
+      const T* x;
+      T* y = nullptr;
+      Vec<T, E> v;
+      if (active) {
+        locate(a, t0 + lt, row - lt * heads, &x, &y);
+        v = *reinterpret_cast<const Vec<T, E>*>(x + j * E);
+      }
+      if constexpr (kHalf) {
+        if (active) mine[lane] = v;
+        __syncwarp();
+        for (uint32_t n = 0; n < rw && r0 + n < rows; ++n) {
+          T* buf = mine[n * L].e;
+          const float2* w = cs + (r0 + n) / heads * pairs;
+          for (uint32_t p = lane; p < pairs; p += 32) {
+            T u = buf[p], o = buf[p + pairs];
+            turn_pair(w[p], u, o);
+            buf[p] = u;
+            buf[p + pairs] = o;
+          }
+        }
+        __syncwarp();
+        if (active) v = mine[lane];
+      } else if (active) {
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          const uint32_t p = j * (E / 2) + e;
+          if (p >= pairs) continue;
+          turn_pair(cs[lt * pairs + p], v.e[2 * e], v.e[2 * e + 1]);
+        }
+      }
+      if (active) *reinterpret_cast<Vec<T, E>*>(y + j * E) = v;
     }
     __syncthreads();  // the next tokens' angles replace these
   }
@@ -158,27 +226,35 @@ int launch_v(const RotArgs& a, int grid, size_t smem, cudaStream_t s) {
   return check_launch("uaa_rotary");
 }
 
+// Do all rows begin at multiples of v elements?
+bool rows_at(const RotArgs& a, int elem, int v) {
+  for (const RotTensor& t : a.t) {
+    if (t.H == 0) continue;
+    if ((reinterpret_cast<uintptr_t>(t.x) | reinterpret_cast<uintptr_t>(t.y)) & (v * elem - 1)) return false;
+    for (long long st : {t.xb, t.xs, t.xh, t.yb, t.ys, t.yh})
+      if (st % v != 0) return false;
+  }
+  return true;
+}
+
 // The widest access that every run of columns, stride and base address allows: 16 bytes in ordinary use, down to
 // one element for odd widths (a unit then moves V-fold less per index computation).
 int pick_vec(const RotArgs& a, int elem) {
-  for (int v = 16 / elem; v > 1; v /= 2) {
-    bool ok = (a.plan.rot / 2) % v == 0 && (a.D - a.plan.rot) % v == 0;
-    for (int i = 0; i < 2 && ok; ++i) {
-      const RotTensor& t = a.t[i];
-      if (t.H == 0) continue;
-      ok = ((reinterpret_cast<uintptr_t>(t.x) | reinterpret_cast<uintptr_t>(t.y)) & (v * elem - 1)) == 0;
-      for (long long st : {t.xb, t.xs, t.xh, t.yb, t.ys, t.yh}) ok = ok && st % v == 0;
-    }
-    if (ok) return v;
-  }
+  for (int v = 16 / elem; v > 1; v /= 2)
+    if ((a.plan.rot / 2) % v == 0 && (a.D - a.plan.rot) % v == 0 && rows_at(a, elem, v)) return v;
   return 1;
 }
 
 template <typename T>
 int launch_t(RotArgs& a, cudaStream_t s) {
+  constexpr int E = 16 / sizeof(T);
   const int v = pick_vec(a, sizeof(T));
+  // Narrower accesses cost more than whole rows' detour: 40000 tokens, 24 + 8 heads of 64, bf16: 50 columns in halves
+  // take 272 us by single elements and 123 by rows, 40 interleaved ones 103 by 8 bytes and 71 by rows.  Where both
+  // move 16 bytes, the units are the faster (27280 x 80 heads of 128 in halves: 189 us, by rows 313).
+  const bool rows = v < E && a.D % E == 0 && a.D / E <= 32 && rows_at(a, sizeof(T), E);
   a.pair_units = a.plan.rot / 2 / v;
-  a.units = a.pair_units + (a.D - a.plan.rot) / v;
+  a.units = rows ? a.D / E : a.pair_units + (a.D - a.plan.rot) / v;
   const uint32_t per_token = (a.t[0].H + a.t[1].H) * a.units;
   // a few units for every thread, as far as the angles fit
   uint32_t nt = 4 * kThreads / per_token;
@@ -186,9 +262,17 @@ int launch_t(RotArgs& a, cudaStream_t s) {
   nt = nt > fit ? fit : nt;
   nt = nt > kMaxTokens ? kMaxTokens : nt;
   a.tokens_per_block = nt < 1 ? 1 : nt;
-  const uint32_t need = (a.tokens - 1) / a.tokens_per_block + 1, cap = sm_count() * 8;
+  // more blocks than fit at once, so that blocks end at different times: with 8 an SM, 247 us instead of those 189
+  const uint32_t need = (a.tokens - 1) / a.tokens_per_block + 1, cap = sm_count() * 64;
   const int grid = need < cap ? need : cap;
   const size_t smem = a.tokens_per_block * (a.plan.rot / 2) * sizeof(float2);
+  if (rows) {
+    if (a.plan.layout == UAA_ROTARY_HALF)
+      rotary_rows_kernel<T, true><<<grid, kThreads, smem, s>>>(a);
+    else
+      rotary_rows_kernel<T, false><<<grid, kThreads, smem, s>>>(a);
+    return check_launch("uaa_rotary");
+  }
   switch (v) {
     case 8:
       if constexpr (sizeof(T) == 2) return launch_v<T, 8>(a, grid, smem, s);
