@@ -404,6 +404,29 @@ def test_captured_step_and_two_streams():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Sq", [1, 2, 5])
+def test_captured_decoding(Sq):
+    """A captured call on a cache whose length, the mask's, grows between replays, on another stream."""
+    x = on_gpu(draw(2, Sq, 900, 4, 128, "prefix", seed=22))
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    uaa.diff_attn_fwd(x["q"], x["k"], x["v"], x["lam"], x["mask"], need_out2=False)
+    with torch.cuda.graph(graph, stream=stream):
+        out, _, lse = uaa.diff_attn_fwd(x["q"], x["k"], x["v"], x["lam"], x["mask"], need_out2=False)
+    for n in (0, 1, 500, 899, 900):
+        x["mask"][0] = torch.arange(900, device=DEV) < n
+        x["q"].normal_()
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            graph.replay()
+        torch.cuda.current_stream().wait_stream(stream)
+        want = uaa.diff_attn_fwd(x["q"], x["k"], x["v"], x["lam"], x["mask"], need_out2=False)
+        assert np.array_equal(bits(out), bits(want[0])) and np.array_equal(bits(lse), bits(want[2]))
+        if n == 0:
+            assert not out[0].any() and torch.isneginf(lse[0]).all()
+    uaa.check_device_status()
+
+
+@pytest.mark.gpu
 def test_from_threads_that_made_no_cuda_call():
     """The library binds the device's context itself; two threads at once, each on its own stream."""
     xs = [on_gpu(draw(1, 150, 160, 2, 64, None, seed=s)) for s in (30, 31)]

@@ -774,7 +774,10 @@ class DiffAttention(torch.autograd.Function):
 
 
 def diff_attention(q, k, v, lam, key_mask=None, scale=None, saved=None):
-    """Differentiable differential attention: returns ``(out, lse)``."""
+    """Differentiable differential attention: returns ``(out, lse)``.
+
+    To capture a step with its gradients in a CUDA graph, warm up on another stream and let no eager autograd graph
+    of the same leaves live: PyTorch ties a leaf's gradients to the stream of the first graph that holds it."""
     return DiffAttention.apply(q, k, v, lam, key_mask, scale, saved)
 
 

@@ -1027,9 +1027,9 @@ int prepare(K kern, int smem) {
 
 size_t row_floats(int B, int Sq, int H) { return (size_t)B * H * tiles_of(Sq) * 4 * kTile; }
 
-// Launches a kernel; with `early`, as soon as all blocks of the one before it on the stream allow it.
+// Launches a kernel that may start as soon as all blocks of the one before it on the stream allow it.
 template <typename K, typename... Args>
-int launch_next(const char* what, bool early, K kern, int grid, int smem, cudaStream_t s, Args... args) {
+int launch_next(const char* what, K kern, int grid, int smem, cudaStream_t s, Args... args) {
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -1039,7 +1039,7 @@ int launch_next(const char* what, bool early, K kern, int grid, int smem, cudaSt
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = &attr;
-  cfg.numAttrs = early ? 1 : 0;
+  cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
   if (e != cudaSuccess) return set_error(UAA_ERR_CUDA, "%s: launch failed: %s", what, cudaGetErrorString(e));
   return check_launch(what);
@@ -1069,24 +1069,20 @@ int launch_bwd(const void* q, const void* k, const void* v, const void* lam, int
                                                              part, B, Sq, H);
   if ((st = check_launch("uaa_diff_attn_bwd (rows)"))) return st;
   const int sms = device_sms();
-  if (items_k > 0) {
-    auto kern = diff_dkdv_kernel<D, kMask>;
-    if ((st = prepare(kern, DkdvLayout<D>::kSmem))) return st;
-    // with a key mask the heads go innermost while one batch's Q and dO fit in half of L2, so that the empty key
-    // tiles spread evenly over the CTAs (as in the plain backward)
-    const int head_inner = mask != nullptr && 4LL * H * Sq * D <= (64LL << 20);
-    if ((st = launch_next("uaa_diff_attn_bwd (dK/dV)", true, kern, (int)(items_k < sms ? items_k : sms),
-                          DkdvLayout<D>::kSmem, s, mq.m[0], mk.m[0], mv.m[0], mdo.m[0], lam, lam_bf16, rows, mask,
-                          static_cast<bf*>(dk), static_cast<bf*>(dv), B, H, Sq, Sk, (int)items_k, head_inner, scale,
-                          scale * kLog2e, ctx)))
-      return st;
-  }
-  auto kern = diff_dq_kernel<D, kMask>;
-  if ((st = prepare(kern, DqLayout<D>::kSmem))) return st;
-  // without keys it follows the row kernel, whose sums it needs from the start
-  return launch_next("uaa_diff_attn_bwd (dQ)", items_k > 0, kern, (int)(items_q < sms ? items_q : sms),
-                     DqLayout<D>::kSmem, s, mq.m[0], mk.m[0], mv.m[0], mdo.m[0], lam, lam_bf16, rows, mask, static_cast<bf*>(dq), part, dlam,
-                     B, H, Sq, Sk, (int)items_q, scale, scale * kLog2e, ctx);
+  // with a key mask the heads go innermost while one batch's Q and dO fit in half of L2, so that the empty key
+  // tiles spread evenly over the CTAs (as in the plain backward)
+  const int head_inner = mask != nullptr && 4LL * H * Sq * D <= (64LL << 20);
+  auto dkdv = diff_dkdv_kernel<D, kMask>;
+  if ((st = prepare(dkdv, DkdvLayout<D>::kSmem)) ||
+      (st = launch_next("uaa_diff_attn_bwd (dK/dV)", dkdv, (int)(items_k < sms ? items_k : sms), DkdvLayout<D>::kSmem, s,
+                        mq.m[0], mk.m[0], mv.m[0], mdo.m[0], lam, lam_bf16, rows, mask, static_cast<bf*>(dk),
+                        static_cast<bf*>(dv), B, H, Sq, Sk, (int)items_k, head_inner, scale, scale * kLog2e, ctx)))
+    return st;
+  auto dqk = diff_dq_kernel<D, kMask>;
+  if ((st = prepare(dqk, DqLayout<D>::kSmem))) return st;
+  return launch_next("uaa_diff_attn_bwd (dQ)", dqk, (int)(items_q < sms ? items_q : sms), DqLayout<D>::kSmem, s, mq.m[0],
+                     mk.m[0], mv.m[0], mdo.m[0], lam, lam_bf16, rows, mask, static_cast<bf*>(dq), part, dlam, B, H, Sq,
+                     Sk, (int)items_q, scale, scale * kLog2e, ctx);
 }
 
 }  // namespace
