@@ -15,6 +15,8 @@
 // At that size: 29 us, 1434 us (tensor pipe active 79 % of the time) and 905 us; 2366 us together.  What bounds the
 // matrix kernels is the chain S -> P -> dS -> next S through TMEM and barriers, which one tile's products and the
 // compute warps take in turns; two tiles half a step apart would need 640 columns of TMEM.
+#include <algorithm>
+
 #include "diff_shared.cuh"
 
 namespace uaa {
@@ -618,6 +620,18 @@ struct DqLayout {
   static_assert(kSmem <= 232448, "shared memory exceeds the per-CTA limit");
 };
 
+// The items of a CTA: one of every `all` rounds over the whole grid, then, for the first `early` CTAs, one of every
+// further round over these.  The first CTAs start on SMs that the dK/dV kernel's last round leaves idle.
+struct DqWalk {
+  int all, early;
+};
+__device__ __forceinline__ int next_item(const DqWalk& w, int item, int num_items) {
+  const int grid = gridDim.x, head = min(w.all, num_items / grid + 1) * grid;  // the items of the first rounds
+  if (item + grid < head) return item + grid;
+  if ((int)blockIdx.x >= w.early) return num_items;
+  return item < head ? head + (int)blockIdx.x : item + w.early;
+}
+
 struct DqCtl {
   uint64_t bar_q_full, bar_q_empty;
   uint64_t bar_k_full[6], bar_k_empty[6], bar_v_full[5], bar_v_empty[5];
@@ -636,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                    const void* __restrict__ lam, int lam_bf16, const float* __restrict__ rows,
                    const uint8_t* __restrict__ key_mask, __nv_bfloat16* __restrict__ dq,
                    const float* __restrict__ part, void* __restrict__ dlam, int B, int H, int Sq, int Sk,
-                   int num_items, float scale, float scale_log2, DevCtx ctx) {
+                   int num_items, DqWalk walk, float scale, float scale_log2, DevCtx ctx) {
   using L = DqLayout<D>;
   constexpr int kChunks = D / 64;
   constexpr int KR = L::kKRing, VR = L::kVRing;
@@ -712,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ producer
     bool ok = true;
     uint32_t G = 0, it = 0;
-    for (int item = blockIdx.x; ok && item < num_items; item += gridDim.x) {
+    for (int item = blockIdx.x; ok && item < num_items; item = next_item(walk, item, num_items)) {
       const Item w = decode_item(item, nqt, H, false);
       if (item_tiles(w.b) == 0) continue;  // no attended key: the compute warps write dQ = 0
       if (lane == 0) {
@@ -816,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (el && m == 1) mma_commit(&ctl->bar_k_empty[G % KR]);
     };
-    for (int item = blockIdx.x; item < num_items; item += gridDim.x) {
+    for (int item = blockIdx.x; item < num_items; item = next_item(walk, item, num_items)) {
       const Item w = decode_item(item, nqt, H, false);
       const int n = item_tiles(w.b);
       if (n == 0) continue;
@@ -881,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tl + 32 * cq;
     bool ok = true;
     uint32_t G0 = 0, it = 0;
-    for (int item = blockIdx.x; item < num_items; item += gridDim.x) {
+    for (int item = blockIdx.x; item < num_items; item = next_item(walk, item, num_items)) {
       const Item w = decode_item(item, nqt, H, false);
       const int n = item_tiles(w.b);
       const int i = w.t * kTile + row;
@@ -1078,11 +1092,26 @@ int launch_bwd(const void* q, const void* k, const void* v, const void* lam, int
                         mq.m[0], mk.m[0], mv.m[0], mdo.m[0], lam, lam_bf16, rows, mask, static_cast<bf*>(dk),
                         static_cast<bf*>(dv), B, H, Sq, Sk, (int)items_k, head_inner, scale, scale * kLog2e, ctx)))
     return st;
+  // dQ's rounds: the CTAs on the `late` SMs that the last round of dK/dV keeps busy start one dK/dV item later, which is
+  // worth 1.66 (D = 64: 1.33) dQ items of as many tiles, and take that much less.  Whole backward with equal shares and
+  // this way: B = 2, Sq = 4096, Sk = 512, H = 24, D = 128: 240 and 192 us; B = 2, S = 1024, H = 24, D = 64: 90 and 85 us
+  const int grid_q = (int)(items_q < sms ? items_q : sms), late = (int)(items_k < sms ? items_k : items_k % sms);
+  DqWalk walk{INT32_MAX, grid_q};
+  if (late > 0 && late < grid_q) {
+    const int early = grid_q - late;
+    const double delay = (D == 128 ? 1.66 : 1.33) * tiles_of(Sq) / tiles_of(Sk);
+    double best = 1e30;
+    for (long long r = items_q / grid_q + 1, k = 0; r >= 1 && k < 64; --r, ++k) {
+      const long long left = items_q - r * grid_q;
+      const double end = std::max(delay + r, (double)(r + (left > 0 ? (left + early - 1) / early : 0)));
+      if (end < best) best = end, walk = DqWalk{(int)r, early};
+    }
+  }
   auto dqk = diff_dq_kernel<D, kMask>;
   if ((st = prepare(dqk, DqLayout<D>::kSmem))) return st;
-  return launch_next("uaa_diff_attn_bwd (dQ)", dqk, (int)(items_q < sms ? items_q : sms), DqLayout<D>::kSmem, s, mq.m[0],
+  return launch_next("uaa_diff_attn_bwd (dQ)", dqk, grid_q, DqLayout<D>::kSmem, s, mq.m[0],
                      mk.m[0], mv.m[0], mdo.m[0], lam, lam_bf16, rows, mask, static_cast<bf*>(dq), part, dlam, B, H, Sq,
-                     Sk, (int)items_q, scale, scale * kLog2e, ctx);
+                     Sk, (int)items_q, walk, scale, scale * kLog2e, ctx);
 }
 
 }  // namespace
