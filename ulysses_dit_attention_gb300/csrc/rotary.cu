@@ -17,8 +17,8 @@
 //
 // Bound: HBM.  Every element is read once and written once; the angles are
 // computed once per token by the block (R/2 of them, in shared memory) and used
-// by all heads of Q and K.  Q and K of 27280 x 40 x 128 in bf16: 196 us a pass
-// interleaved, 189 in halves, 5.7 and 5.9 TB/s, 0.85 and 0.88 of a copy's rate.
+// by all heads of Q and K.  Q and K of 27280 x 40 x 128 in bf16: 184 us a pass
+// interleaved, 170 in halves, 6.1 and 6.6 TB/s, 0.91 and 0.98 of a copy's rate.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -29,7 +29,7 @@
 namespace uaa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;  // small blocks: fewer wait for a token's angles at a time (256: 189 us instead of 170 below)
 constexpr int kMaxPairs = UAA_ROTARY_MAX_PAIRS;
 constexpr int kMaxTokens = 16;       // tokens of one block (shared memory: kMaxTokens * kMaxPairs * 8 bytes at most)
 constexpr int kMaxSmemPairs = 2048;  // pairs whose cosine and sine a block holds: 16 KB
@@ -113,7 +113,8 @@ __device__ __forceinline__ void locate(const RotArgs& a, uint32_t tok, uint32_t 
   *y = static_cast<T*>(t.y) + (b * t.yb + s * t.ys + h * t.yh);
 }
 
-// One thread takes units of V pairs (two runs of V columns) or of V copied columns.
+// One thread takes units: of V pairs in two runs of V columns (halves, or V = 1), of V / 2 interleaved pairs in one run,
+// or of V copied columns.
 template <typename T, int V, bool kHalf>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotArgs a) {
   extern __shared__ float2 cs[];  // (cos a, sin a) * m of this block's tokens
@@ -132,18 +133,21 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
       locate(a, t0 + lt, row - lt * heads, &x, &y);
       using VT = Vec<T, V>;
       if (u < a.pair_units) {
-        const int c0 = kHalf ? u * V : 2 * u * V, c1 = kHalf ? c0 + pairs : c0 + V;
-        VT v0 = *reinterpret_cast<const VT*>(x + c0), v1 = *reinterpret_cast<const VT*>(x + c1);
-        const float2* w = cs + lt * pairs + u * V;
+        if constexpr (kHalf || V == 1) {
+          const int c0 = kHalf ? u * V : 2 * u, c1 = kHalf ? c0 + pairs : c0 + 1;
+          VT v0 = *reinterpret_cast<const VT*>(x + c0), v1 = *reinterpret_cast<const VT*>(x + c1);
+          const float2* w = cs + lt * pairs + u * V;
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          // interleaved: pair e of the unit is elements 2e and 2e + 1 of its 2V columns
-          T& u0 = kHalf ? v0.e[e] : (2 * e < V ? v0.e[(2 * e) % V] : v1.e[(2 * e) % V]);
-          T& u1 = kHalf ? v1.e[e] : (2 * e + 1 < V ? v0.e[(2 * e + 1) % V] : v1.e[(2 * e + 1) % V]);
-          turn_pair(w[e], u0, u1);
+          for (int e = 0; e < V; ++e) turn_pair(w[e], v0.e[e], v1.e[e]);
+          *reinterpret_cast<VT*>(y + c0) = v0;
+          *reinterpret_cast<VT*>(y + c1) = v1;
+        } else {
+          VT v = *reinterpret_cast<const VT*>(x + u * V);
+          const float2* w = cs + lt * pairs + u * (V / 2);
+#pragma unroll
+          for (int e = 0; e < V / 2; ++e) turn_pair(w[e], v.e[2 * e], v.e[2 * e + 1]);
+          *reinterpret_cast<VT*>(y + u * V) = v;
         }
-        *reinterpret_cast<VT*>(y + c0) = v0;
-        *reinterpret_cast<VT*>(y + c1) = v1;
       } else {
         const int c = a.plan.rot + (u - a.pair_units) * V;
         *reinterpret_cast<VT*>(y + c) = *reinterpret_cast<const VT*>(x + c);
@@ -240,8 +244,9 @@ bool rows_at(const RotArgs& a, int elem, int v) {
 // The widest access that every run of columns, stride and base address allows: 16 bytes in ordinary use, down to
 // one element for odd widths (a unit then moves V-fold less per index computation).
 int pick_vec(const RotArgs& a, int elem) {
+  const int run = a.plan.layout == UAA_ROTARY_HALF ? a.plan.rot / 2 : a.plan.rot;
   for (int v = 16 / elem; v > 1; v /= 2)
-    if ((a.plan.rot / 2) % v == 0 && (a.D - a.plan.rot) % v == 0 && rows_at(a, elem, v)) return v;
+    if (run % v == 0 && (a.D - a.plan.rot) % v == 0 && rows_at(a, elem, v)) return v;
   return 1;
 }
 
@@ -250,10 +255,10 @@ int launch_t(RotArgs& a, cudaStream_t s) {
   constexpr int E = 16 / sizeof(T);
   const int v = pick_vec(a, sizeof(T));
   // Narrower accesses cost more than whole rows' detour: 40000 tokens, 24 + 8 heads of 64, bf16: 50 columns in halves
-  // take 272 us by single elements and 123 by rows, 40 interleaved ones 103 by 8 bytes and 71 by rows.  Where both
-  // move 16 bytes, the units are the faster (27280 x 80 heads of 128 in halves: 189 us, by rows 313).
+  // take 272 us by single elements and 122 by rows.  Where both move 16 bytes, the units are the faster (27280 x 80
+  // heads of 128 in halves: 189 us, by rows 313).
   const bool rows = v < E && a.D % E == 0 && a.D / E <= 32 && rows_at(a, sizeof(T), E);
-  a.pair_units = a.plan.rot / 2 / v;
+  a.pair_units = a.plan.layout == UAA_ROTARY_HALF || v == 1 ? a.plan.rot / 2 / v : a.plan.rot / v;
   a.units = rows ? a.D / E : a.pair_units + (a.D - a.plan.rot) / v;
   const uint32_t per_token = (a.t[0].H + a.t[1].H) * a.units;
   // a few units for every thread, as far as the angles fit
@@ -262,8 +267,9 @@ int launch_t(RotArgs& a, cudaStream_t s) {
   nt = nt > fit ? fit : nt;
   nt = nt > kMaxTokens ? kMaxTokens : nt;
   a.tokens_per_block = nt < 1 ? 1 : nt;
-  // more blocks than fit at once, so that blocks end at different times: with 8 an SM, 247 us instead of those 189
-  const uint32_t need = (a.tokens - 1) / a.tokens_per_block + 1, cap = sm_count() * 64;
+  // more blocks than fit at once, so that blocks end at different times (blocks of 256 threads: 247 us with 8 an SM, 189
+  // with 64)
+  const uint32_t need = (a.tokens - 1) / a.tokens_per_block + 1, cap = sm_count() * 128;
   const int grid = need < cap ? need : cap;
   const size_t smem = a.tokens_per_block * (a.plan.rot / 2) * sizeof(float2);
   if (rows) {
