@@ -30,9 +30,10 @@
 // with shuffles.  A lane's 16 values are runs of 16 bytes, one in each part of
 // the row, so that the lanes of a warp read and write whole sectors side by side
 // (16 consecutive values a lane, in two half-sector accesses, took 556 us to
-// pack and 356 us to unpack four bf16 tensors of 27280 x 40 x 128; this takes 295
-// and 249 us, 5.7 and 6.8 TB/s).  The grid holds 64 blocks a SM: with 8, packing
-// takes 379 us and unpacking 276.
+// pack and 356 us to unpack four bf16 tensors of 27280 x 40 x 128; this takes 294
+// and 238 us, 5.7 and 7.1 TB/s).  The grid holds 64 blocks a SM to pack and 1024
+// to unpack: with 8, packing takes 379 us and unpacking 276; with 1024 and 64, 316
+// and 249.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -227,7 +228,7 @@ int sm_count() {
 
 template <typename T, int G>
 int launch_g(const ActArgs& a, bool pack, cudaStream_t s) {
-  const long long need = (a.first[a.n] + kThreads / G - 1) / (kThreads / G), cap = (long long)sm_count() * 64;
+  const long long need = (a.first[a.n] + kThreads / G - 1) / (kThreads / G), cap = (long long)sm_count() * (pack ? 64 : 1024);
   const int grid = (int)(need < cap ? need : cap);
   if (pack)
     act8_pack_kernel<T, G><<<grid, kThreads, 0, s>>>(a);
