@@ -30,10 +30,10 @@
 // with shuffles.  A lane's 16 values are runs of 16 bytes, one in each part of
 // the row, so that the lanes of a warp read and write whole sectors side by side
 // (16 consecutive values a lane, in two half-sector accesses, took 556 us to
-// pack and 356 us to unpack four bf16 tensors of 27280 x 40 x 128; this takes 294
-// and 238 us, 5.7 and 7.1 TB/s).  The grid holds 64 blocks a SM to pack and 1024
-// to unpack: with 8, packing takes 379 us and unpacking 276; with 1024 and 64, 316
-// and 249.
+// pack and 356 us to unpack four bf16 tensors of 27280 x 40 x 128; this takes 264
+// and 238 us, 6.3 and 7.1 TB/s).  The grid holds 64 blocks a SM to pack and 1024
+// to unpack: with 8, packing took 379 us (294 with 64, before the quotients below)
+// and unpacking 276; with 1024 and 64, 316 and 249.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -117,6 +117,25 @@ __device__ __forceinline__ int exact_code(float x, float top, float u) {
   return x < 0.f ? -(c + up) : c + up;
 }
 
+// top / 127 toward zero and 127 / top upward, exactly: a quotient q of 24 bits with one Newton step lies within half a
+// last place and a little of the true one, the remainder fmaf(-q, d, n) is exact, and its sign says on which side; so
+// the neighbour is the answer or q is.  (The directed divisions of the language, made for any operands, took 30 us of
+// 294 at the size above.)
+__device__ __forceinline__ float step_of(float top) {
+  const float c = 1.f / 127.f;
+  float q = top * c;
+  q = fmaf(fmaf(-127.f, q, top), c, q);
+  return fmaf(-127.f, q, top) < 0.f ? __uint_as_float(__float_as_uint(q) - 1u) : q;
+}
+__device__ __forceinline__ float inverse_of(float top) {
+  if (top > 0x1p100f) return __fdiv_ru(127.f, top);  // 1 / top is no longer exact enough, or below the normal numbers
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(top));
+  float q = 127.f * y;
+  q = fmaf(fmaf(-q, top, 127.f), y, q);
+  return fmaf(-q, top, 127.f) > 0.f ? __uint_as_float(__float_as_uint(q) + 1u) : q;
+}
+
 // (bf16: 32 registers, so that every thread of the SM holds a row's share in flight: 311 -> 295 us at the size above)
 template <typename T, int G>
 __global__ void __launch_bounds__(kThreads, std::is_same<T, __nv_bfloat16>::value ? 8 : 4) act8_pack_kernel(const __grid_constant__ ActArgs a) {
@@ -146,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, std::is_same<T, __nv_bfloat16>::valu
     for (int o = G / 2; o > 0; o /= 2) top_bits = max(top_bits, __shfl_xor_sync(0xffffffffu, top_bits, o));
     const float top = __uint_as_float(top_bits);
     const bool finite = top_bits < 0x7f800000u, some = top >= 0x1p-119f;
-    const float inv = finite && some ? __fdiv_ru(127.f, top) : 0.f;
+    const float inv = finite && some ? inverse_of(top) : 0.f;
     uint32_t packed[4] = {0u, 0u, 0u, 0u};
     if (inv > 0.f) {
       const float2 inv2 = make_float2(inv, inv), magic = make_float2(12582912.f, 12582912.f);
@@ -182,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, std::is_same<T, __nv_bfloat16>::valu
         else
           __stcs(reinterpret_cast<uint32_t*>(c), packed[i]);
       }
-      if (lane == 0) a.steps[t][row] = !finite ? __uint_as_float(0x7fc00000u) : some ? __fdiv_rz(top, 127.f) : 0.f;
+      if (lane == 0) a.steps[t][row] = !finite ? __uint_as_float(0x7fc00000u) : some ? step_of(top) : 0.f;
     }
   }
 }
