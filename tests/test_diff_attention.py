@@ -312,6 +312,22 @@ def test_same_bits_every_time():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("case", [(4, 700, 300, 24, 64, None), (3, 300, 900, 30, 128, "prefix"),
+                                  (2, 520, 130, 60, 128, None), (5, 130, 1100, 20, 64, "empty")],
+                         ids=["queries", "masked", "few-keys", "empty"])
+def test_many_items_a_block(case):
+    """More tiles than the device has SMs, shared out in several ways: every sequence's results are those of a call of
+    its own."""
+    B, Sq, Sk, H, D, mask = case
+    x = on_gpu(draw(B, Sq, Sk, H, D, mask, seed=50))
+    whole = step(x)
+    for b in range(B):
+        one = step({n: t if t is None or n == "lam" else t[b:b + 1].contiguous() for n, t in x.items()})
+        for n in ("out", "out2", "lse", "dq", "dk", "dv"):
+            assert np.array_equal(bits(whole[n][b:b + 1]), bits(one[n])), (b, n)
+
+
+@pytest.mark.gpu
 def test_many_mask_rows():
     x = draw(300, 40, 140, 1, 64, "random", seed=11)
     x["mask"][7] = False

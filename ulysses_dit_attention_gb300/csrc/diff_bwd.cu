@@ -12,7 +12,7 @@
 // dQ 1067 -> 933 us at S = 8191, H = 24, D = 128), warp 16 loads by TMA, warp 17 issues the tcgen05 products from one
 // elected lane.  MMAs of one thread run in order; two that read A from TMEM for different products are only relied on
 // with equal shapes or with another product between them.
-// At that size: 29 us, 1434 us (tensor pipe active 79 % of the time) and 905 us; 2366 us together.  What bounds the
+// At that size: 29 us, 1435 us (tensor pipe active 78 % of the time) and 862 us (66 %); 2.32 ms together.  What bounds the
 // matrix kernels is the chain S -> P -> dS -> next S through TMEM and barriers, which one tile's products and the
 // compute warps take in turns; two tiles half a step apart would need 640 columns of TMEM.
 #include <algorithm>
