@@ -408,8 +408,9 @@ int uaa_diff_attn_fwd(const void* q, const void* k, const void* v, const void* l
                       float scale, uaa_stream_t stream);
 
 /* Bytes of device workspace that uaa_diff_attn_bwd needs: per query row and map the row dot of dout with the
- * map's output and -LSE*log2(e), rows padded to 128, and a sum per 64 rows.  Returns 0 for invalid sizes. */
-size_t uaa_diff_attn_bwd_workspace_bytes(int B, int Sq, int H, int D);
+ * map's output and -LSE*log2(e), rows padded to 128, a sum per 64 rows and one per 128 keys.  Returns 0 for
+ * invalid sizes. */
+size_t uaa_diff_attn_bwd_workspace_bytes(int B, int Sq, int Sk, int H, int D);
 
 /* Gradients of uaa_diff_attn_fwd; deterministic (no atomics).
  *   dq, dk, dv : bf16, written, in the layouts of q, k, v; dlambda: (H) in lambda's type

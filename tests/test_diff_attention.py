@@ -77,9 +77,9 @@ def test_refusals_of_the_call():
     assert bwd(out2=None) == -1 and "out2" in err()
     assert bwd(dlam=None) == -1 and "lambda" in err()
     assert bwd(Sq=0) == -1 and "queries" in err()
-    # per head Delta and -LSE*log2(e) of two maps, rows padded to 128, and a sum per 64 rows
-    assert L.uaa_diff_attn_bwd_workspace_bytes(2, 130, 3, 128) == 2 * 3 * (256 * 4 + 4) * 4 // 256 * 256 + 256
-    assert L.uaa_diff_attn_bwd_workspace_bytes(2, 130, 3, 96) == 0
+    # per head Delta and -LSE*log2(e) of two maps, rows padded to 128, a sum per 64 rows and one per 128 keys
+    assert L.uaa_diff_attn_bwd_workspace_bytes(2, 130, 300, 3, 128) == 2 * 3 * (256 * 4 + 4 + 3) * 4 // 256 * 256 + 256
+    assert L.uaa_diff_attn_bwd_workspace_bytes(2, 130, 300, 3, 96) == 0
 
 
 def test_refusals_without_gpu():
@@ -196,6 +196,31 @@ def test_lambda_values_and_types(lam):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D,mask", [(64, None), (128, "random")])
+def test_dlambda_does_not_hang_on_the_rounding_of_out2(D, mask):
+    """dlambda is a sum of A_2 dA, whatever out2 holds: with the forward's, and with zeros in its place."""
+    x = draw(2, 500, 400, 3, D, mask, seed=16)
+    x["lam"] = torch.tensor([0.5, -0.3, 1e-3])
+    g = on_gpu(x)
+    out, out2, lse = uaa.diff_attn_fwd(g["q"], g["k"], g["v"], g["lam"], g["mask"])
+    q2, k2 = (f64(x[n])[..., D // 2:].transpose(0, 2, 1, 3) for n in "qk")
+    s = q2 @ k2.transpose(0, 1, 3, 2) / math.sqrt(D / 2)
+    if mask:
+        s = np.where(x["mask"].numpy()[:, None, None], s, -np.inf)
+    a2 = np.exp(s - s.max(-1, keepdims=True))
+    a2 /= a2.sum(-1, keepdims=True)
+    da = f64(x["do"]).transpose(0, 2, 1, 3) @ f64(x["v"]).transpose(0, 2, 3, 1)
+    want = -(a2 * da).sum((0, 2, 3))
+    # a probability is off by 2^-18 (an exponent below 32 in 32 bits, ex2 2^-22), so A_2 sums to 1 within that and a row
+    # sum is off by so much of its summands; adding up 400 keys and 1000 rows in 32 bits, in parts of at most 64: 2^-17
+    bound = 2.0 ** -16 * (a2 * np.abs(da)).sum((0, 2, 3))
+    for o2 in (out2, torch.zeros_like(out2)):
+        dlam = uaa.diff_attn_bwd(g["q"], g["k"], g["v"], g["lam"], out, o2, g["do"], lse, g["mask"])[3]
+        err = np.abs(dlam.cpu().double().numpy() - want)
+        assert (err <= bound).all(), (err, bound)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("D", [64, 128])
 def test_forward_without_gradient(D):
     for Sq in (1, 2, 130):
@@ -250,9 +275,14 @@ def test_keys_past_32_bits(Sq):
             assert torch.allclose(long[n].float(), short[n].float(), rtol=2**-7, atol=2**-11), n
         short.update(zip(("dq", "dk", "dv", "dlam"),
                          uaa.diff_attn_bwd(q, cut(k), cut(v), lam, long["out"], long["out2"], do, long["lse"], cut(mask))))
-    for n in ("out", "out2", "lse", "dq", "dk", "dv", "dlam"):
+    for n in ("out", "out2", "lse", "dq", "dk", "dv"):
         if Sq > 2 or n[0] == "d":
             assert torch.equal(long[n], short[n]), n
+    # dlambda adds the same sums of key tiles in another order, at most eight of them that are not 0 on the way of one:
+    # 2 * 8 * 2^-24 of their magnitudes, which come to 2 max_j |dA_ij| a row at most (A_2 sums to 1, Delta_2 is a mean of
+    # dA), and |dA_ij| <= |do_i| |v_j|
+    size = 2 * do.float().norm(dim=-1).sum((0, 1)) * v.float().norm(dim=-1).max()
+    assert ((long["dlam"] - short["dlam"]).abs() <= 2**-20 * size).all()
 
 
 @pytest.mark.gpu
@@ -449,7 +479,7 @@ def test_from_threads_that_made_no_cuda_call():
     want = [step(x) for x in xs]
     got, streams = [None, None], [torch.cuda.Stream() for _ in xs]
     bufs = [{n: torch.empty_like(t) for n, t in w.items()} for w in want]  # so that the threads allocate nothing
-    ws = [torch.empty(uaa.diff_attn_bwd_workspace_bytes(1, 150, 2, 64), dtype=torch.uint8, device=DEV) for _ in xs]
+    ws = [torch.empty(uaa.diff_attn_bwd_workspace_bytes(1, 150, 160, 2, 64), dtype=torch.uint8, device=DEV) for _ in xs]
     torch.cuda.synchronize()
 
     def work(i):

@@ -71,7 +71,7 @@ _SIGS = {
     "uaa_act8_pack": (_I, [_I, _P, _P, _P, _P, _I, _I, _P]),
     "uaa_act8_unpack": (_I, [_I, _P, _P, _P, _P, _I, _I, _P]),
     "uaa_diff_attn_fwd": (_I, [_P, _P, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, ctypes.c_float, _P]),
-    "uaa_diff_attn_bwd_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I]),
+    "uaa_diff_attn_bwd_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I]),
     "uaa_diff_attn_bwd": (_I, [_P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I,
                                ctypes.c_float, _P, ctypes.c_size_t, _P]),
     "uaa_attn_fwd": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, ctypes.c_float, _P]),
@@ -716,8 +716,8 @@ def diff_attn_fwd(q, k, v, lam, key_mask=None, scale=None, need_out2=True, out=N
     return out, out2, lse
 
 
-def diff_attn_bwd_workspace_bytes(B, Sq, H, D) -> int:
-    return int(lib().uaa_diff_attn_bwd_workspace_bytes(B, Sq, H, D))
+def diff_attn_bwd_workspace_bytes(B, Sq, Sk, H, D) -> int:
+    return int(lib().uaa_diff_attn_bwd_workspace_bytes(B, Sq, Sk, H, D))
 
 
 def diff_attn_bwd(q, k, v, lam, out, out2, dout, lse, key_mask=None, scale=None, dq=None, dk=None, dv=None, dlam=None,
@@ -737,7 +737,7 @@ def diff_attn_bwd(q, k, v, lam, out, out2, dout, lse, key_mask=None, scale=None,
         if Sk and B:
             raise ValueError("keys without queries (Sq = 0)")
         return dq, dk, dv, dlam.zero_()
-    nbytes = diff_attn_bwd_workspace_bytes(B, Sq, H, D)
+    nbytes = diff_attn_bwd_workspace_bytes(B, Sq, Sk, H, D)
     if workspace is None:
         workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
     _call(dev, "uaa_diff_attn_bwd", _ptr(q), _ptr(k), _ptr(v), _ptr(lam), _DTYPES[lam.dtype], _ptr(out), _ptr(out2),

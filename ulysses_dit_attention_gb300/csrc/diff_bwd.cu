@@ -3,8 +3,8 @@
 //  1. diff_rows_kernel: Delta_m and -LSE_m log2(e) of every query row, and the
 //     sum of Delta_2 over 64 rows, the summands of dlambda.
 //  2. diff_dkdv_kernel, key-tile-major: dK and dV of 128 keys.
-//  3. diff_dq_kernel, query-tile-major: dQ of 128 queries; its loading warps, when they have loaded all, add up
-//     dlambda, in a fixed order.
+//  3. diff_dq_kernel, query-tile-major: dQ of 128 queries; its loading warps, when they have loaded all and the
+//     dK/dV kernel has ended, add up dlambda, in a fixed order.
 // -lambda enters as |lambda| = 2^(log2 |lambda|), added to map 2's exponents with its LSE, and a sign: the negated
 // A operand of map 2's dV product, and the sign of dQ_2 and dK_2 when they are written.
 // Both matrix kernels: warps 0-15 compute (TMEM lane quadrant = warp % 4, 32 of a tile's 128 columns = warp / 4;
@@ -29,6 +29,7 @@ constexpr int kMmaWarp = 17;
 // Named barriers between the compute warps (which arrive) and the issuer (which syncs): the issuer waits on these
 // within an item, because an mbarrier test would be held behind the MMAs that it has queued.
 constexpr uint32_t kBarP = 1, kBarDS = 2, kBarCount = kCompute + 32;
+constexpr uint32_t kBarSum = 3;  // the compute warps of the dK/dV kernel exchange their sums of dS_2
 constexpr int kRowBytes = 4 * kTile * 4;
 constexpr uint32_t kIdescNegateA = 1u << 13;  // instruction descriptor: the A operand is negated
 
@@ -114,8 +115,8 @@ __host__ __device__ __forceinline__ int steps_of(int S) { return 2 * tiles_of(S)
 // The three kernels of a call overlap at their ends (programmatic dependent launch): when all blocks of a kernel have
 // called allow_next(), the next one's start wherever an SM has room; await_previous() returns when the previous kernel
 // has completed and its writes can be read.  The dK/dV kernel waits for the row vectors before it lets the dQ kernel
-// start, and the dQ kernel, which needs nothing of the dK/dV kernel's and reads the row
-// kernel's sums past L1, waits for it at its end, so that a call is
+// start, and the dQ kernel, which needs nothing of the dK/dV kernel's but
+// sums for dlambda and reads the row kernel's values past L1, waits for it at its end, so that a call is
 // complete when its last kernel is.  One launch after the other against this: 69.6 -> 56.8 us at B = 2, S = 1000, H = 12,
 // D = 64; 807 -> 775 us at B = 2, S = 4096, H = 24, D = 128 with a mask; 2473 -> 2405 us at S = 8191, H = 24, D = 128.
 __device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -180,11 +181,17 @@ __global__ void __launch_bounds__(kRowThreads) diff_rows_kernel(
   }
 }
 
-// dlambda_h = -sum of Delta_2 over the head's rows, by one warp, in a fixed order.
-__device__ __forceinline__ void sum_dlambda(const float* __restrict__ part, void* __restrict__ dlam, int lam_bf16, int h,
-                                            int n, int lane) {
+// dlambda_h = -sum of Delta_2 over the head's rows, by one warp, in a fixed order.  The row kernel's Delta_2 (part) holds
+// the rounding of O_2 to bf16, which the sum, often small against its summands, would show: 0.4 % and more.  But
+// sum_j dS_2 of a row is -lambda (Delta_2 - that value), as A_2 sums to 1, so the dK/dV kernel, which has dS_2 in 32
+// bits, leaves what is missing in its items' sums (rest).
+__device__ __forceinline__ void sum_dlambda(const float* part, int n, const float* rest, int n_rest,
+                                            void* __restrict__ dlam, int lam_bf16, int h, int lane) {
   float s = 0.f;
+#pragma unroll 4
   for (int i = lane; i < n; i += 32) s += __ldcg(part + (size_t)h * n + i);
+#pragma unroll 4
+  for (int i = lane; i < n_rest; i += 32) s += __ldcg(rest + (size_t)h * n_rest + i);
 #pragma unroll
   for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (lane == 0) {
@@ -247,6 +254,7 @@ struct DkdvCtl {
   uint64_t bar_acc_done, bar_acc_free, bar_final;
   uint32_t tmem_base;
   int abort;
+  float sums[16];  // a warp's sum of dS_2 over an item
 };
 static_assert(sizeof(DkdvCtl) <= 256, "control block");
 
@@ -268,7 +276,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
                      const void* __restrict__ lam, int lam_bf16, const float* __restrict__ rows,
                      const uint8_t* __restrict__ key_mask, __nv_bfloat16* __restrict__ dk,
-                     __nv_bfloat16* __restrict__ dv, int B, int H, int Sq, int Sk, int num_items, int head_inner,
+                     __nv_bfloat16* __restrict__ dv, float* __restrict__ rest, int B, int H, int Sq, int Sk,
+                     int num_items, int head_inner,
                      float scale, float scale_log2, DevCtx ctx) {
   using L = DkdvLayout<D>;
   constexpr int kChunks = D / 64;
@@ -490,8 +499,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // this thread writes a quarter of the row's columns
       const size_t off = (((size_t)w.b * Sk + (exists ? j : 0)) * H + w.h) * D + cq * (D / 4);
       const bool store = exists && guard_store(ctx, off, D / 4, k_extent);
+      float* const rest_at = rest + ((size_t)w.h * B + w.b) * nkt + w.t;
       if (kMask && !tile_any(key_mask, w.b, w.t, Sk)) {
         // no attended key in this tile: dK = dV = 0
+        if (threadIdx.x == 0) *rest_at = 0.f;
         if (store) {
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
@@ -502,6 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       const float2 c2 = make_float2(scale_log2, scale_log2);
+      float2 sum = make_float2(0.f, 0.f);  // of this key's dS_2, with |lambda|
       for (int i = 0; i < nqt; ++i) {
         const uint32_t T = T0 + i, slot = T % R;
         const bool last = i + 1 == nqt;
@@ -557,15 +569,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (m == 1 && last) ok = __all_sync(0xffffffffu, wait_or_abort(&ctl->bar_dv_done, it & 1, ctx, ctl));
           tc_fence_before();
           named_arrive(kBarDS, kBarCount);
+          if (m == 1) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) sum = add2(sum, make_float2(dp[2 * c], dp[2 * c + 1]));
+          }
         }
       }
       T0 += nqt;
+      const bool attended = exists && (!kMask || key_mask[(size_t)w.b * Sk + j] != 0);
+      float total = attended ? sum.x + sum.y : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o /= 2) total += __shfl_xor_sync(0xffffffffu, total, o);
+      if (lane == 0) ctl->sums[warp] = total;
+      named_sync(kBarSum, kCompute);
+      if (threadIdx.x == 0) {
+        // where lambda is 0, or so small that dS_2 may be, the row kernel's sum stands
+        const float l = fabsf(load_lambda(lam, lam_bf16, w.h));
+        total = 0.f;
+        for (int x = 0; x < kCompute / 32; ++x) total += ctl->sums[x];
+        *rest_at = l >= 0x1p-60f ? total / l : 0.f;
+      }
       // epilogue: dV, and dK = scale * (dS^T Q).  A key outside the mask gets zeros, whatever its rows hold.
       if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(&ctl->bar_acc_done, it & 1, ctx, ctl));
       ++it;
       if (!ok) continue;
       tc_fence_after();
-      const bool attended = exists && (!kMask || key_mask[(size_t)w.b * Sk + j] != 0);
       const float ck = cq >= 2 && load_lambda(lam, lam_bf16, w.h) > 0.f ? -scale : scale;
       const uint32_t cV = tl + kColDV + cq * (D / 4);
       const uint32_t cK = tl + kColDK + cq * (D / 4) + (D == 64 ? (cq >> 1) * 64 : 0);
@@ -649,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
                    const void* __restrict__ lam, int lam_bf16, const float* __restrict__ rows,
                    const uint8_t* __restrict__ key_mask, __nv_bfloat16* __restrict__ dq,
-                   const float* __restrict__ part, void* __restrict__ dlam, int B, int H, int Sq, int Sk,
+                   const float* part, const float* rest, void* __restrict__ dlam, int B, int H, int Sq, int Sk,
                    int num_items, DqWalk walk, float scale, float scale_log2, DevCtx ctx) {
   using L = DqLayout<D>;
   constexpr int kChunks = D / 64;
@@ -782,7 +810,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++G;
       }
     }
-    for (int h = blockIdx.x; h < H; h += gridDim.x) sum_dlambda(part, dlam, lam_bf16, h, B * steps_of(Sq), lane);
+    if (blockIdx.x < H) await_previous();  // the sums of the dK/dV kernel
+    for (int h = blockIdx.x; h < H; h += gridDim.x)
+      sum_dlambda(part, B * steps_of(Sq), rest, B * nkt, dlam, lam_bf16, h, lane);
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
     uint32_t el_lane;
@@ -1064,8 +1094,9 @@ int launch_bwd(const void* q, const void* k, const void* v, const void* lam, int
                const void* out2, const void* dout, const float* lse, const uint8_t* mask, void* dq, void* dk, void* dv,
                void* dlam, int B, int Sq, int Sk, int H, float scale, float* rows, cudaStream_t s) {
   using bf = __nv_bfloat16;
-  float* part = rows + row_floats(B, Sq, H);
   const int steps = steps_of(Sq);
+  float* part = rows + row_floats(B, Sq, H);
+  float* rest = part + (size_t)B * H * steps;
   const long long items_k = (long long)tiles_of(Sk) * H * B, items_q = (long long)tiles_of(Sq) * H * B;
   const long long row_blocks = (long long)B * steps * H;
   if (items_k > INT32_MAX || items_q > INT32_MAX || row_blocks > INT32_MAX)
@@ -1090,7 +1121,7 @@ int launch_bwd(const void* q, const void* k, const void* v, const void* lam, int
   if ((st = prepare(dkdv, DkdvLayout<D>::kSmem)) ||
       (st = launch_next("uaa_diff_attn_bwd (dK/dV)", dkdv, (int)(items_k < sms ? items_k : sms), DkdvLayout<D>::kSmem, s,
                         mq.m[0], mk.m[0], mv.m[0], mdo.m[0], lam, lam_bf16, rows, mask, static_cast<bf*>(dk),
-                        static_cast<bf*>(dv), B, H, Sq, Sk, (int)items_k, head_inner, scale, scale * kLog2e, ctx)))
+                        static_cast<bf*>(dv), rest, B, H, Sq, Sk, (int)items_k, head_inner, scale, scale * kLog2e, ctx)))
     return st;
   // dQ's rounds: the CTAs on the `late` SMs that the last round of dK/dV keeps busy start one dK/dV item later, which is
   // worth 1.66 (D = 64: 1.33) dQ items of as many tiles, and take that much less.  Whole backward with equal shares and
@@ -1110,7 +1141,7 @@ int launch_bwd(const void* q, const void* k, const void* v, const void* lam, int
   auto dqk = diff_dq_kernel<D, kMask>;
   if ((st = prepare(dqk, DqLayout<D>::kSmem))) return st;
   return launch_next("uaa_diff_attn_bwd (dQ)", dqk, grid_q, DqLayout<D>::kSmem, s, mq.m[0],
-                     mk.m[0], mv.m[0], mdo.m[0], lam, lam_bf16, rows, mask, static_cast<bf*>(dq), part, dlam, B, H, Sq,
+                     mk.m[0], mv.m[0], mdo.m[0], lam, lam_bf16, rows, mask, static_cast<bf*>(dq), part, rest, dlam, B, H, Sq,
                      Sk, (int)items_q, walk, scale, scale * kLog2e, ctx);
 }
 
@@ -1119,10 +1150,10 @@ int launch_bwd(const void* q, const void* k, const void* v, const void* lam, int
 
 using namespace uaa;
 
-extern "C" size_t uaa_diff_attn_bwd_workspace_bytes(int B, int Sq, int H, int D) {
-  if (B < 0 || Sq < 0 || H < 0 || (D != 64 && D != 128)) return 0;
-  // the row vectors, and the sums of 64 rows' Delta_2
-  return ((row_floats(B, Sq, H) + (size_t)B * H * steps_of(Sq)) * 4 + 255) & ~(size_t)255;
+extern "C" size_t uaa_diff_attn_bwd_workspace_bytes(int B, int Sq, int Sk, int H, int D) {
+  if (B < 0 || Sq < 0 || Sk < 0 || H < 0 || (D != 64 && D != 128)) return 0;
+  // the row vectors, the sums of 64 rows' Delta_2, and a sum per 128 keys
+  return ((row_floats(B, Sq, H) + (size_t)B * H * (steps_of(Sq) + tiles_of(Sk))) * 4 + 255) & ~(size_t)255;
 }
 
 extern "C" int uaa_diff_attn_bwd(const void* q, const void* k, const void* v, const void* lambda, int lambda_dtype,
@@ -1144,7 +1175,7 @@ extern "C" int uaa_diff_attn_bwd(const void* q, const void* k, const void* v, co
     return st;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return set_error(UAA_ERR_INVALID_ARG, "%s: workspace is NULL or not 256-byte aligned", fn);
-  const size_t need = uaa_diff_attn_bwd_workspace_bytes(B, Sq, H, D);
+  const size_t need = uaa_diff_attn_bwd_workspace_bytes(B, Sq, Sk, H, D);
   if (workspace_bytes < need)
     return set_error(UAA_ERR_INVALID_ARG, "%s: workspace has %zu bytes, %zu needed", fn, workspace_bytes, need);
   auto go = D == 64 ? (key_mask ? launch_bwd<64, true> : launch_bwd<64, false>)
