@@ -138,7 +138,8 @@ __device__ __forceinline__ float inverse_of(float top) {
 
 // (bf16: 32 registers, so that every thread of the SM holds a row's share in flight: 311 -> 295 us at the size above)
 template <typename T, int G>
-__global__ void __launch_bounds__(kThreads, std::is_same<T, __nv_bfloat16>::value ? 8 : 4) act8_pack_kernel(const __grid_constant__ ActArgs a) {
+__global__ void __launch_bounds__(kThreads, std::is_same<T, __nv_bfloat16>::value ? 8 : 4)
+    act8_pack_kernel(const __grid_constant__ ActArgs a) {
   constexpr int kRun = Runs<T>::kRun, kRuns = Runs<T>::kRuns;
   constexpr bool kBorders = !std::is_same<T, __nv_bfloat16>::value;
   const int lane = threadIdx.x % G;
@@ -247,7 +248,8 @@ int sm_count() {
 
 template <typename T, int G>
 int launch_g(const ActArgs& a, bool pack, cudaStream_t s) {
-  const long long need = (a.first[a.n] + kThreads / G - 1) / (kThreads / G), cap = (long long)sm_count() * (pack ? 64 : 1024);
+  const long long need = (a.first[a.n] + kThreads / G - 1) / (kThreads / G);
+  const long long cap = (long long)sm_count() * (pack ? 64 : 1024);
   const int grid = (int)(need < cap ? need : cap);
   if (pack)
     act8_pack_kernel<T, G><<<grid, kThreads, 0, s>>>(a);

@@ -115,10 +115,10 @@ __host__ __device__ __forceinline__ int steps_of(int S) { return 2 * tiles_of(S)
 // The three kernels of a call overlap at their ends (programmatic dependent launch): when all blocks of a kernel have
 // called allow_next(), the next one's start wherever an SM has room; await_previous() returns when the previous kernel
 // has completed and its writes can be read.  The dK/dV kernel waits for the row vectors before it lets the dQ kernel
-// start, and the dQ kernel, which needs nothing of the dK/dV kernel's but
-// sums for dlambda and reads the row kernel's values past L1, waits for it at its end, so that a call is
-// complete when its last kernel is.  One launch after the other against this: 69.6 -> 56.8 us at B = 2, S = 1000, H = 12,
-// D = 64; 807 -> 775 us at B = 2, S = 4096, H = 24, D = 128 with a mask; 2473 -> 2405 us at S = 8191, H = 24, D = 128.
+// start, and the dQ kernel, which needs nothing of the dK/dV kernel's but sums for dlambda and reads the row kernel's
+// values past L1, waits for it at its end, so that a call is complete when its last kernel is.  One launch after the
+// other against this: 69.6 -> 56.8 us at B = 2, S = 1000, H = 12, D = 64; 807 -> 775 us at B = 2, S = 4096, H = 24,
+// D = 128 with a mask; 2473 -> 2405 us at S = 8191, H = 24, D = 128.
 __device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -29,7 +29,7 @@
 namespace uaa {
 namespace {
 
-constexpr int kThreads = 128;  // small blocks: fewer wait for a token's angles at a time (256: 189 us instead of 170 below)
+constexpr int kThreads = 128;  // fewer threads wait for a token's angles at a time (256: 189 us instead of those 170)
 constexpr int kMaxPairs = UAA_ROTARY_MAX_PAIRS;
 constexpr int kMaxTokens = 16;       // tokens of one block (shared memory: kMaxTokens * kMaxPairs * 8 bytes at most)
 constexpr int kMaxSmemPairs = 2048;  // pairs whose cosine and sine a block holds: 16 KB
