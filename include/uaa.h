@@ -448,6 +448,13 @@ void uaa_set_wait_timeout_ms(unsigned int ms);
  * with a bad address: the load is simply not issued.  n < 0 turns it off. */
 void uaa_debug_drop_load(int n);
 
+/* Diagnostic of the debug build, for tests of the order of waits: while warp >= 0,
+ * that warp of every block of the attention kernels launched afterwards comes `ns`
+ * nanoseconds (1000000 at most) late to each of its waits for a copy or a product.
+ * Results must not change.  warp < 0 turns it off.  Returns UAA_OK,
+ * UAA_ERR_INVALID_ARG, or UAA_ERR_UNSUPPORTED from the other builds. */
+int uaa_debug_late_warp(int warp, unsigned int ns);
+
 /* Diagnostic (the pages have no counterpart): evaluates on the device, for
  * tests, the exponential the forward kernel takes on the FMA pipe for one
  * column pair of P in eight: 2^x by rounding x (clamped at -127) to n + f,

@@ -27,6 +27,7 @@ from .build import DEBUG_LIB_PATH, LIB_PATH
 __all__ = [
     "UAAError", "lib", "attn_fwd", "attn_bwd", "attn_bwd_workspace_bytes", "attn_bwd_fused_workspace_bytes", "seq_to_head", "head_to_seq",
     "assemble_key_mask", "check_device_status", "watchdog_selftest", "set_wait_timeout_ms", "debug_drop_load",
+    "debug_late_warp",
     "set_bwd_profile_events", "Attention", "attn_fwd_groups", "attn_bwd_groups",
     "attention", "UlyssesAttention", "ulysses_attention", "STATUS", "debug_build", "debug_exp2_fma2",
     "RotaryPlan", "rotary_fwd", "rotary_bwd", "Rotary", "rotary", "shard_positions", "Act8", "act8_pack", "act8_unpack",
@@ -100,6 +101,7 @@ _SIGS = {
     "uaa_watchdog_selftest": (_I, [ctypes.c_uint, _P]),
     "uaa_set_wait_timeout_ms": (None, [ctypes.c_uint]),
     "uaa_debug_drop_load": (None, [_I]),
+    "uaa_debug_late_warp": (_I, [_I, ctypes.c_uint]),
     "uaa_set_bwd_profile_events": (None, [_P, _P, _P]),
     "uaa_last_error": (ctypes.c_char_p, []),
     "uaa_version": (ctypes.c_char_p, []),
@@ -879,6 +881,11 @@ def set_wait_timeout_ms(ms: int):
 def debug_drop_load(n: int):
     """Diagnostic: the attention kernels' producers skip their n-th ring load (-1: off)."""
     lib().uaa_debug_drop_load(int(n))
+
+
+def debug_late_warp(warp: int = -1, ns: int = 0):
+    """Diagnostic of the debug build: that warp of the attention kernels comes late to each of its waits (-1: off)."""
+    _check(lib().uaa_debug_late_warp(int(warp), int(ns)))
 
 
 def set_bwd_profile_events(events=None):

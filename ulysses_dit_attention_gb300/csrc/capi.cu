@@ -32,6 +32,9 @@ std::atomic<unsigned long long> g_timeout_ns{kDefaultTimeoutNs};
 std::atomic<unsigned int> g_epoch{0};
 // Diagnostic: the ring load that the attention kernels' producers skip (-1: none).
 std::atomic<int> g_drop_load{-1};
+// Diagnostic of debug builds: the warp that comes late to its waits (-1: none), and by how much.
+std::atomic<int> g_late_warp{-1};
+std::atomic<unsigned int> g_late_ns{0};
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
@@ -75,6 +78,8 @@ int get_dev_ctx(DevCtx* ctx) {
   if (ep == 0) ep = ++g_epoch;
   ctx->epoch = ep;
   ctx->drop_load = g_drop_load.load();
+  ctx->late_warp = g_late_warp.load();
+  ctx->late_ns = g_late_ns.load();
   return UAA_OK;
 }
 
@@ -196,6 +201,15 @@ void uaa_set_wait_timeout_ms(unsigned int ms) {
 }
 
 void uaa_debug_drop_load(int n) { g_drop_load.store(n < 0 ? -1 : n); }
+
+int uaa_debug_late_warp(int warp, unsigned int ns) {
+  if (warp >= 0 && !uaa_debug_build())
+    return set_error(UAA_ERR_UNSUPPORTED, "uaa_debug_late_warp: only the debug build's warps can be made late");
+  if (ns > 1000000u) return set_error(UAA_ERR_INVALID_ARG, "uaa_debug_late_warp: %u ns (1000000 at most)", ns);
+  g_late_ns.store(ns);
+  g_late_warp.store(warp < 0 ? -1 : warp);
+  return UAA_OK;
+}
 
 int uaa_check_device_status(uaa_stream_t stream) {
   DevCtx ctx;

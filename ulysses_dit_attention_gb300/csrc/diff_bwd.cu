@@ -55,6 +55,7 @@ __device__ __forceinline__ void store_packed32(uint32_t taddr, const float (&x)[
 template <typename Ctl>
 __device__ __forceinline__ bool wait_two(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, const DevCtx& ctx,
                                          Ctl* ctl) {
+  dbg_late(ctx);
   const bool ra = mbar_try_wait(a, pa), rb = mbar_try_wait(b, pb);
   if (ra && rb) return true;
   return wait_or_abort(a, pa, ctx, ctl) && wait_or_abort(b, pb, ctx, ctl);
@@ -993,10 +994,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             p[2 * c] = ex2(x.x), p[2 * c + 1] = ex2(x.y);
           }
           if (m == 0) {
-            // dA, and the next V tile, which the next dA's product reads as soon as this one has been read
-            const uint32_t Gw = more ? G + 1 : G;
-            ok = __all_sync(0xffffffffu, wait_two(&ctl->bar_dp_full, G & 1, &ctl->bar_v_full[Gw % VR], (Gw / VR) & 1,
-                                                  ctx, ctl));
+            // dA, and the next V tile, which the next dA's product reads as soon as this one has been read.  Behind an
+            // item's last tile that is the next item's, and the issuer waits for it: dA has freed this tile's V slot
+            // without any arrival from this step, so the next phases of its barrier may be complete already.
+            ok = __all_sync(0xffffffffu,
+                            more ? wait_two(&ctl->bar_dp_full, G & 1, &ctl->bar_v_full[(G + 1) % VR],
+                                            ((G + 1) / VR) & 1, ctx, ctl)
+                                 : wait_or_abort(&ctl->bar_dp_full, G & 1, ctx, ctl));
             if (!ok) break;
             tc_fence_after();
             tmem_ld32(tl + kColDP + 32 * cq, dp);

@@ -43,6 +43,8 @@ struct DevCtx {
   unsigned long long settle_ns;   // bound of the teardown waits for copies / MMAs already in flight
   unsigned int epoch;             // this call's epoch (never 0)
   int drop_load;                  // diagnostic: the ring load each producer skips (-1: none)
+  int late_warp;                  // diagnostic of debug builds: this warp comes late to its waits (-1: none),
+  unsigned int late_ns;           // by so many nanoseconds
 };
 
 // Host side: per-device status word address, wait bound, error message.
@@ -168,14 +170,33 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, unsign
   }
 }
 
+// Debug builds: the warp that uaa_debug_late_warp() named comes late to a wait.  Nothing in the other builds.
+__device__ __forceinline__ void dbg_late(const DevCtx& ctx) {
+#ifdef UAA_DEBUG
+  if ((int)(threadIdx.x >> 5) == ctx.late_warp) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < ctx.late_ns) __nanosleep(200);
+  }
+#else
+  (void)ctx;
+#endif
+}
+
 // Bounded wait of a kernel role on barrier phase `parity`.  Returns false --
 // and the role then leaves its loops -- when the phase did not complete within
 // ctx.timeout_ns (the device status records a timeout and this call's epoch is
 // published so that every CTA of the call stops waiting), when another role of
 // this CTA has already given up (ctl->abort), or when another CTA of the same
 // call has (status[1] == epoch).
+//
+// A wait knows its phase by parity alone.  So the phase after the awaited one
+// must not be able to complete before the waiting thread has passed: it has to
+// depend on something that this thread does later (its arrival at a barrier, the
+// product it issues, the copy it starts).  Where it does not, a late thread finds
+// the parity of the phase after next and waits for what never comes.
 template <typename Ctl>
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, const DevCtx& ctx, Ctl* ctl) {
+  dbg_late(ctx);
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (true) {
