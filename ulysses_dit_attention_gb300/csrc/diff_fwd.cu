@@ -798,6 +798,9 @@ __global__ void __launch_bounds__(kRowThreads) diff_fwd_rows_kernel(
         }
       }
     }
+    float base[NQ];  // 0 while every score was -inf, so that ex2(-inf - base) is 0
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) base[n] = mx[n] == -INFINITY ? 0.f : mx[n];
 #pragma unroll
     for (int u = 0; u < kRowUnroll; ++u) {
       const uint32_t w[4] = {vr[u].x, vr[u].y, vr[u].z, vr[u].w};
@@ -806,7 +809,7 @@ __global__ void __launch_bounds__(kRowThreads) diff_fwd_rows_kernel(
       for (int e = 0; e < 4; ++e) vf[e] = bf2(w[e]);
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
-        const float p = on[u] ? ex2(s[n][u] - mx[n]) : 0.f;
+        const float p = ex2(s[n][u] - base[n]);  // a key outside the mask has a score of -inf
         const float o = __shfl_xor_sync(0xffffffffu, p, G / 2);
         sum[n] += p;
 #pragma unroll
