@@ -402,6 +402,9 @@ int uaa_attn_bwd_act8(const int8_t* const* codes, const float* const* steps, con
  *                  out = out2 = 0, lse = -inf and no gradient
  *   out2         : what the backward needs next to out; NULL when no gradient is wanted
  *   lse          : device, fp32 (B, H, 2, Sq)
+ * A key with a score of -inf has no weight (a row of such keys only is one without an attended key).  A row with a
+ * score of NaN or +inf gets lse = NaN or +inf, a row of NaN in out (in out2: from map 2), and gradients of NaN wherever
+ * it enters.
  * scale is usually 1/sqrt(D/2).  Returns UAA_OK or a negative uaa_status. */
 int uaa_diff_attn_fwd(const void* q, const void* k, const void* v, const void* lambda, int lambda_dtype,
                       const uint8_t* key_mask, void* out, void* out2, float* lse, int B, int Sq, int Sk, int H, int D,

@@ -167,7 +167,8 @@ __global__ void __launch_bounds__(kRowThreads) diff_rows_kernel(
       float x = sub == 2 ? fmaf(lm, d2, d1) : d2;
       if (sub < 2) {
         const float l = i < Sq ? lse[(bh * 2 + sub) * Sq + i] : -INFINITY;
-        x = l == -INFINITY ? -INFINITY : -l * kLog2e;  // rows past Sq, or without a key: P = 0
+        // rows past Sq, or without a key: P = 0; where a score was NaN or +inf (LSE = NaN or +inf): P = NaN
+        x = l == -INFINITY ? -INFINITY : l < INFINITY ? -l * kLog2e : NAN;
         if (sub == 1 && l != -INFINITY) x += log2f(fabsf(lm));
       }
       rows[rows_at(bh, Sq, i) + sub * kTile] = x;

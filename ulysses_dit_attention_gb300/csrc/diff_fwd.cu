@@ -34,6 +34,7 @@
 // Keys outside the mask get P = 0; their rows of V are zeroed in shared memory
 // before the product reads them, so an infinity or a NaN there leaves no trace.
 #include <cooperative_groups.h>
+#include <float.h>
 
 #include "diff_shared.cuh"
 
@@ -516,7 +517,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int q = 0; q < 8; ++q) m8[q] = max3(m8[q], s[c + q], s[c + q + 8]);
         const float mt = fmaxf(max3(m8[0], m8[1], m8[2]), max3(max3(m8[3], m8[4], m8[5]), m8[6], m8[7]));
-        const float mt2 = mt * scale_log2;  // -inf if every key of the tile is masked
+        // -inf if every key of the tile is masked.  The offset stays finite: a score of +inf then gives P = l = +inf, so
+        // LSE = +inf and, times 1/l = 0, a row of NaN; a NaN score, which a maximum passes over, gives P = l = NaN.
+        const float mt2 = fminf(mt * scale_log2, FLT_MAX);
         float alpha = 1.f;
         if (mt2 > mu + kRescaleThreshold) {
           alpha = ex2(mu - mt2);  // 0 when mu = -inf
@@ -561,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, okw);
       }
       // both maps' products are done, which the previous item's readers of these sums allowed (bar_o_free)
-      sSum[m * kTile + row] = l_run > 0.f ? 1.f / l_run : 0.f;
+      sSum[m * kTile + row] = l_run == 0.f ? 0.f : 1.f / l_run;
       named_sync(kBarL, 256);
       const uint32_t qs = ne & 1;
       g += nt;
@@ -614,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       named_arrive(kBarO, kBarOut);
       tc_fence_before();
       mbar_arrive(&ctl->bar_o_free);
-      if (ostore) lse[lo] = l_run > 0.f ? mu * kLn2 + logf(l_run) : -INFINITY;
+      if (ostore) lse[lo] = l_run == 0.f ? -INFINITY : mu * kLn2 + logf(l_run);
     }
   }
 
@@ -786,7 +789,7 @@ __global__ void __launch_bounds__(kRowThreads) diff_fwd_rows_kernel(
 #pragma unroll
       for (int u = 1; u < kRowUnroll; ++u) top = fmaxf(top, s[n][u]);
       if (__any_sync(0xffffffffu, top > mx[n])) {
-        const float now = fmaxf(mx[n], top);
+        const float now = fminf(fmaxf(mx[n], top), FLT_MAX);  // finite, as in the tiles
         const float alpha = mx[n] == now ? 1.f : ex2(mx[n] - now);  // 0 from -inf
         mx[n] = now;
         sum[n] *= alpha;
@@ -907,7 +910,7 @@ __global__ void __launch_bounds__(kRowThreads) diff_fwd_rows_kernel(
         o[mm].x += a.x * f;
         o[mm].y += a.y * f;
       }
-      const float inv = lsum[mm] > 0.f ? 1.f / lsum[mm] : 0.f;
+      const float inv = lsum[mm] == 0.f ? 0.f : 1.f / lsum[mm];
       o[mm].x *= inv;
       o[mm].y *= inv;
     }
@@ -916,7 +919,7 @@ __global__ void __launch_bounds__(kRowThreads) diff_fwd_rows_kernel(
     if (out2) *reinterpret_cast<uint32_t*>(out2 + oo) = pack_bf16(o[1].x, o[1].y);
     if (c < 4) {  // columns 0 and 2 stand for the two maps
       const int mm = c / 2;
-      lse[(((size_t)b * H + h) * 2 + mm) * Sq + i0 + n] = lsum[mm] > 0.f ? top[mm] * kLn2 + logf(lsum[mm]) : -INFINITY;
+      lse[(((size_t)b * H + h) * 2 + mm) * Sq + i0 + n] = lsum[mm] == 0.f ? -INFINITY : top[mm] * kLn2 + logf(lsum[mm]);
     }
   }
   cl.sync();  // no CTA leaves while another reads its shared memory
