@@ -334,8 +334,10 @@ def attn_bwd_groups(q, k, v, out, dout, lse, key_mask=None, scale=None, dq=None,
     return dq, dk, dv
 
 
-def _save(ctx, saved, tensors, *others):
-    """Keeps ``tensors`` for the backward pass, as they are or (``saved="int8"``) as an 8-bit checkpoint."""
+def _save(ctx, saved, tensors, *others, key_mask):
+    """Keeps ``tensors`` for the backward pass, as they are or (``saved="int8"``) as an 8-bit checkpoint, and the key
+    mask among the saved tensors, so that a change to it between the passes raises.  (A mask made in inference mode has
+    no versions and cannot be saved: it stays on ``ctx``.)"""
     if saved not in (None, "int8"):
         raise ValueError(f"saved must be None or 'int8', got {saved!r}")
     ctx.packed = None
@@ -343,15 +345,22 @@ def _save(ctx, saved, tensors, *others):
         packed = act8_pack(tensors)
         ctx.packed = packed._meta()
         tensors = (packed.data,)
-    ctx.save_for_backward(*tensors, *others)
+    ctx.held_mask = key_mask if key_mask is not None and key_mask.is_inference() else None
+    ctx.save_for_backward(*tensors, *others, None if ctx.held_mask is not None else key_mask)
+
+
+def _kept(ctx):
+    """What :func:`_save` kept: the tensors or their checkpoint's buffer, the others, and the key mask."""
+    *kept, key_mask = ctx.saved_tensors
+    return kept, key_mask if ctx.held_mask is None else ctx.held_mask
 
 
 def _saved(ctx, n):
-    """The ``n`` tensors that :func:`_save` kept, and the others."""
-    kept = ctx.saved_tensors
+    """The ``n`` tensors that :func:`_save` kept, the others, and the key mask."""
+    kept, key_mask = _kept(ctx)
     if ctx.packed is None:
-        return list(kept[:n]), kept[n:]
-    return act8_unpack(Act8(kept[0], *ctx.packed)), kept[1:]
+        return kept[:n], kept[n:], key_mask
+    return act8_unpack(Act8(kept[0], *ctx.packed)), kept[1:], key_mask
 
 
 class Attention(torch.autograd.Function):
@@ -363,8 +372,7 @@ class Attention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, key_mask=None, scale=None, saved=None):
         out, lse = attn_fwd(q, k, v, key_mask, scale)
-        _save(ctx, saved, (q, k, v, out), lse)
-        ctx.key_mask = key_mask
+        _save(ctx, saved, (q, k, v, out), lse, key_mask=key_mask)
         ctx.scale = scale
         ctx.mark_non_differentiable(lse)
         ctx.set_materialize_grads(False)  # no zeros for lse
@@ -374,12 +382,13 @@ class Attention(torch.autograd.Function):
     def backward(ctx, dout, _dlse):
         if dout is None:
             return None, None, None, None, None, None
+        kept, key_mask = _kept(ctx)
         if ctx.packed is not None:
-            data, lse = ctx.saved_tensors
-            grads = attn_bwd_act8(Act8(data, *ctx.packed), dout.contiguous(), lse, ctx.key_mask, ctx.scale)
+            data, lse = kept
+            grads = attn_bwd_act8(Act8(data, *ctx.packed), dout.contiguous(), lse, key_mask, ctx.scale)
         else:
-            q, k, v, out, lse = ctx.saved_tensors
-            grads = attn_bwd(q, k, v, out, dout.contiguous(), lse, ctx.key_mask, ctx.scale)
+            q, k, v, out, lse = kept
+            grads = attn_bwd(q, k, v, out, dout.contiguous(), lse, key_mask, ctx.scale)
         return *grads, None, None, None
 
 
@@ -758,8 +767,7 @@ class DiffAttention(torch.autograd.Function):
         grad = any(ctx.needs_input_grad)
         out, out2, lse = diff_attn_fwd(q, k, v, lam, key_mask, scale, need_out2=grad)
         if grad:
-            _save(ctx, saved, (q, k, v, out, out2), lam, lse)
-        ctx.key_mask = key_mask
+            _save(ctx, saved, (q, k, v, out, out2), lam, lse, key_mask=key_mask)
         ctx.scale = scale
         ctx.mark_non_differentiable(lse)
         ctx.set_materialize_grads(False)  # no zeros for lse
@@ -770,8 +778,8 @@ class DiffAttention(torch.autograd.Function):
     def backward(ctx, dout, _dlse):
         if dout is None:
             return None, None, None, None, None, None, None
-        (q, k, v, out, out2), (lam, lse) = _saved(ctx, 5)
-        dq, dk, dv, dlam = diff_attn_bwd(q, k, v, lam, out, out2, dout.contiguous(), lse, ctx.key_mask, ctx.scale)
+        (q, k, v, out, out2), (lam, lse), key_mask = _saved(ctx, 5)
+        dq, dk, dv, dlam = diff_attn_bwd(q, k, v, lam, out, out2, dout.contiguous(), lse, key_mask, ctx.scale)
         return dq, dk, dv, dlam, None, None, None
 
 
@@ -917,16 +925,16 @@ class UlyssesAttention(torch.autograd.Function):
         # emulated ranks
         o, lse = attn_fwd_groups(yq, yk, yv, key_mask, scale)
         o_sh = head_to_seq(o, shard_lens, cap, H)
-        _save(ctx, saved, (yq, yk, yv, o), lse)
-        ctx.shard_lens, ctx.key_mask, ctx.scale, ctx.cap, ctx.H = tuple(shard_lens), key_mask, scale, cap, H
+        _save(ctx, saved, (yq, yk, yv, o), lse, key_mask=key_mask)
+        ctx.shard_lens, ctx.scale, ctx.cap, ctx.H = tuple(shard_lens), scale, cap, H
         ctx.mark_non_differentiable(lse)
         return o_sh, lse
 
     @staticmethod
     def backward(ctx, do_sh, _dlse):
-        (yq, yk, yv, o), (lse,) = _saved(ctx, 4)
+        (yq, yk, yv, o), (lse,), key_mask = _saved(ctx, 4)
         ydo = seq_to_head(do_sh.contiguous(), ctx.shard_lens)
-        dq, dk, dv = attn_bwd_groups(yq, yk, yv, o, ydo, lse, ctx.key_mask, ctx.scale)
+        dq, dk, dv = attn_bwd_groups(yq, yk, yv, o, ydo, lse, key_mask, ctx.scale)
         return (head_to_seq(dq, ctx.shard_lens, ctx.cap, ctx.H), head_to_seq(dk, ctx.shard_lens, ctx.cap, ctx.H),
                 head_to_seq(dv, ctx.shard_lens, ctx.cap, ctx.H), None, None, None, None)
 
@@ -1019,15 +1027,15 @@ class FusedUlyssesAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q_sh, k_sh, v_sh, shard_lens, key_mask=None, scale=None, saved=None):
         out, lse = ulysses_attn_fwd(q_sh, k_sh, v_sh, shard_lens, key_mask, scale)
-        _save(ctx, saved, (q_sh, k_sh, v_sh, out), lse)
-        ctx.shard_lens, ctx.key_mask, ctx.scale = tuple(shard_lens), key_mask, scale
+        _save(ctx, saved, (q_sh, k_sh, v_sh, out), lse, key_mask=key_mask)
+        ctx.shard_lens, ctx.scale = tuple(shard_lens), scale
         ctx.mark_non_differentiable(lse)
         return out, lse
 
     @staticmethod
     def backward(ctx, dout, _dlse):
-        (q_sh, k_sh, v_sh, out), (lse,) = _saved(ctx, 4)
-        dq, dk, dv = ulysses_attn_bwd(q_sh, k_sh, v_sh, out, dout.contiguous(), lse, ctx.shard_lens, ctx.key_mask,
+        (q_sh, k_sh, v_sh, out), (lse,), key_mask = _saved(ctx, 4)
+        dq, dk, dv = ulysses_attn_bwd(q_sh, k_sh, v_sh, out, dout.contiguous(), lse, ctx.shard_lens, key_mask,
                                       ctx.scale)
         return dq, dk, dv, None, None, None, None
 
