@@ -52,3 +52,15 @@ def test_a_mask_made_in_inference_mode(which, saved):
         out = call(*leaves)[0]
         grads.append(torch.autograd.grad(out, leaves, torch.ones_like(out)))
     assert all(torch.equal(a, b) for a, b in zip(*grads))
+
+
+def test_saved_is_checked_whether_a_gradient_is_wanted_or_not():
+    q, lam = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16), torch.zeros(2)
+    sh = torch.zeros(1, 1, 4, 2, 64, dtype=torch.bfloat16)
+    for grad in (False, True):
+        q.requires_grad_(grad)
+        for call in (lambda: uaa.attention(q, q, q, saved="int4"), lambda: uaa.diff_attention(q, q, q, lam, saved="int4"),
+                     lambda: uaa.ulysses_attention(sh, sh, sh, (4,), saved="int4"),
+                     lambda: uaa.ulysses_attention_fused(sh, sh, sh, (4,), saved="int4")):
+            with pytest.raises(ValueError, match="saved must be"):
+                call()

@@ -334,12 +334,15 @@ def attn_bwd_groups(q, k, v, out, dout, lse, key_mask=None, scale=None, dq=None,
     return dq, dk, dv
 
 
+def _check_saved(saved):
+    if saved not in (None, "int8"):
+        raise ValueError(f"saved must be None or 'int8', got {saved!r}")
+
+
 def _save(ctx, saved, tensors, *others, key_mask):
     """Keeps ``tensors`` for the backward pass, as they are or (``saved="int8"``) as an 8-bit checkpoint, and the key
     mask among the saved tensors, so that a change to it between the passes raises.  (A mask made in inference mode has
     no versions and cannot be saved: it stays on ``ctx``.)"""
-    if saved not in (None, "int8"):
-        raise ValueError(f"saved must be None or 'int8', got {saved!r}")
     ctx.packed = None
     if saved == "int8" and any(ctx.needs_input_grad):
         packed = act8_pack(tensors)
@@ -371,6 +374,7 @@ class Attention(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, key_mask=None, scale=None, saved=None):
+        _check_saved(saved)
         out, lse = attn_fwd(q, k, v, key_mask, scale)
         _save(ctx, saved, (q, k, v, out), lse, key_mask=key_mask)
         ctx.scale = scale
@@ -764,6 +768,7 @@ class DiffAttention(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, lam, key_mask=None, scale=None, saved=None):
+        _check_saved(saved)
         grad = any(ctx.needs_input_grad)
         out, out2, lse = diff_attn_fwd(q, k, v, lam, key_mask, scale, need_out2=grad)
         if grad:
@@ -918,6 +923,7 @@ class UlyssesAttention(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q_sh, k_sh, v_sh, shard_lens, key_mask=None, scale=None, saved=None):
+        _check_saved(saved)
         cap, H = q_sh.shape[2], q_sh.shape[3]
         yq, yk, yv = (seq_to_head(t, shard_lens) for t in (q_sh, k_sh, v_sh))
         P = yq.shape[0]
@@ -1026,6 +1032,7 @@ class FusedUlyssesAttention(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q_sh, k_sh, v_sh, shard_lens, key_mask=None, scale=None, saved=None):
+        _check_saved(saved)
         out, lse = ulysses_attn_fwd(q_sh, k_sh, v_sh, shard_lens, key_mask, scale)
         _save(ctx, saved, (q_sh, k_sh, v_sh, out), lse, key_mask=key_mask)
         ctx.shard_lens, ctx.scale = tuple(shard_lens), scale
