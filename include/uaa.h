@@ -418,7 +418,8 @@ size_t uaa_diff_attn_bwd_workspace_bytes(int B, int Sq, int Sk, int H, int D);
 /* Gradients of uaa_diff_attn_fwd; deterministic (no atomics).
  *   dq, dk, dv : bf16, written, in the layouts of q, k, v; dlambda: (H) in lambda's type
  *   workspace  : device, at least uaa_diff_attn_bwd_workspace_bytes() bytes, 256-byte aligned
- * Sq and Sk must both be positive (or B*H = 0).  Returns UAA_OK or a negative uaa_status. */
+ * Sq and Sk must both be positive; without a row (B = 0, or Sq = Sk = 0) dlambda is set to 0 and the other
+ * pointers are not read.  Returns UAA_OK or a negative uaa_status. */
 int uaa_diff_attn_bwd(const void* q, const void* k, const void* v, const void* lambda, int lambda_dtype,
                       const void* out, const void* out2, const void* dout, const float* lse, const uint8_t* key_mask,
                       void* dq, void* dk, void* dv, void* dlambda, int B, int Sq, int Sk, int H, int D, float scale,

@@ -1169,7 +1169,14 @@ extern "C" int uaa_diff_attn_bwd(const void* q, const void* k, const void* v, co
   const char* fn = "uaa_diff_attn_bwd";
   int st = validate_attn_sizes(fn, B, Sq, Sk, H, D, scale);
   if (st) return st;
-  if ((uint64_t)B * H == 0 || (uint64_t)Sq + Sk == 0) return UAA_OK;
+  if (H == 0) return UAA_OK;
+  if (B == 0 || (uint64_t)Sq + Sk == 0) {  // no row: the sum over them is 0
+    if ((st = check_lambda(fn, dlambda, lambda_dtype))) return st;
+    const cudaError_t e = cudaMemsetAsync(dlambda, 0, (size_t)H * (lambda_dtype == UAA_BF16 ? 2 : 4),
+                                          static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return set_error(UAA_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+    return UAA_OK;
+  }
   if (Sq == 0) return set_error(UAA_ERR_INVALID_ARG, "%s: keys without queries (Sq = 0)", fn);
   if ((st = check_dev_ptr(fn, "q", q)) || (st = check_dev_ptr(fn, "k", k)) || (st = check_dev_ptr(fn, "v", v)) ||
       (st = check_dev_ptr(fn, "out", out)) || (st = check_dev_ptr(fn, "out2", out2)) ||
