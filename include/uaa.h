@@ -345,7 +345,9 @@ int uaa_rotary_plan_init(uaa_rotary_plan* plan, int layout, int axes, const int*
                          int scaling, double factor, double original, double alpha, double beta);
 
 /* A (B, S, H, D) operand and its result: device pointers and strides in elements; the D columns of a
- * head are contiguous.  y may be x (with x's strides); otherwise the two must not overlap. */
+ * head are contiguous.  y may be x, with x's strides; it must not overlap x in another way, nor the other operand or
+ * its result.  Such calls are refused where the strides are alike, as those of slices of one packed tensor are, or
+ * two tensors begin at one place. */
 typedef struct {
   const void* x;
   void* y;

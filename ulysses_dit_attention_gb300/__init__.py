@@ -542,7 +542,7 @@ def rotary_fwd(q, k, plan, positions=None, start=0, out_q=None, out_k=None):
     ``q``, ``k``: ``(B, S, H, D)`` bf16, fp16 or fp32 with contiguous columns -- slices of a packed
     projection are fine.  ``positions``: int32 or int64 ``(S,)`` or ``(B, S)``, with a last dimension of
     ``plan.axes`` when the plan has several; None stands for ``start, start + 1, ...``.  ``out_q=q`` rotates
-    in place.
+    in place; otherwise a result must not overlap an operand or the other result.
     """
     return _rotate(q, k, plan, positions, start, 0, out_q, out_k)
 

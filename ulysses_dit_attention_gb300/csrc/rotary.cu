@@ -313,6 +313,69 @@ int check_tensor(const char* fn, const char* name, const RotTensor& t, const Rot
   return UAA_OK;
 }
 
+// Do the rows at p (strides b, s, h over nb, ns, nh) and at q, of D elements each, share an element?  Decided exactly where
+// the strides are alike, as those of slices of one packed tensor are: then the distance of the two bases has to be a sum
+// of strides, within a row.  Rows of other strides are only known to meet where they begin at one place.
+struct Rows {
+  const void* at;
+  long long b, s, h;
+  int nh;
+};
+bool rows_meet(const Rows& p, const Rows& q, int B, int S, int D, int elem) {
+  const long long bytes = static_cast<const char*>(p.at) - static_cast<const char*>(q.at);
+  if (bytes == 0) return true;
+  struct Dim {
+    long long stride;
+    int n, m;
+  } d[3] = {{p.b, B, B}, {p.s, S, S}, {p.h, p.nh, q.nh}};
+  const long long other[3] = {q.b, q.s, q.h};
+  auto span = [&](const Rows& r) { return ((B - 1) * r.b + (S - 1) * r.s + (r.nh - 1) * r.h + D) * elem; };
+  if (bytes >= span(q) || -bytes >= span(p)) return false;
+  for (int i = 0; i < 3; ++i) {
+    if (d[i].n < 2) d[i].stride = other[i];
+    if (d[i].n < 2 && d[i].m < 2) d[i].stride = 0;
+    if (d[i].stride != other[i] && d[i].m > 1) return false;
+  }
+  std::sort(d, d + 3, [](const Dim& u, const Dim& v) { return u.stride > v.stride; });
+  // the steps of each stride from the largest down: what is left is less than one of them, on either side
+  for (int choice = 0; choice < 8; ++choice) {
+    long long left = bytes;
+    bool fits = true;
+    for (int i = 0; i < 3 && fits; ++i) {
+      if (d[i].stride == 0) continue;
+      const long long st = d[i].stride * elem;
+      long long k = left / st - (left % st < 0);  // rounded down
+      k += choice >> i & 1;
+      left -= k * st;
+      fits = -k < d[i].n && k < d[i].m;  // row i of p lies where row i + k of q does
+    }
+    if (fits && left > -(long long)D * elem && left < (long long)D * elem) return true;
+  }
+  return false;
+}
+
+// An output may lie on its own input, row on row; on nothing else.
+int check_overlap(const char* fn, const RotArgs& a, int elem) {
+  const char* names[2] = {"q", "k"};
+  auto in = [&](const RotTensor& t) { return Rows{t.x, t.xb, t.xs, t.xh, t.H}; };
+  auto out = [&](const RotTensor& t) { return Rows{t.y, t.yb, t.ys, t.yh, t.H}; };
+  for (int i = 0; i < 2; ++i) {
+    const RotTensor& t = a.t[i];
+    if (t.H == 0) continue;
+    const bool in_place = t.x == t.y && (a.B < 2 || t.xb == t.yb) && (a.S < 2 || t.xs == t.ys) &&
+                          (t.H < 2 || t.xh == t.yh);
+    if (!in_place && rows_meet(out(t), in(t), a.B, a.S, a.D, elem))
+      return set_error(UAA_ERR_INVALID_ARG, "%s: %s's output overlaps its input", fn, names[i]);
+    const RotTensor& o = a.t[1 - i];
+    if (o.H == 0) continue;
+    if (rows_meet(out(t), in(o), a.B, a.S, a.D, elem))
+      return set_error(UAA_ERR_INVALID_ARG, "%s: %s's output overlaps %s", fn, names[i], names[1 - i]);
+    if (rows_meet(out(t), out(o), a.B, a.S, a.D, elem))
+      return set_error(UAA_ERR_INVALID_ARG, "%s: the outputs of q and k overlap", fn);
+  }
+  return UAA_OK;
+}
+
 int check_plan(const char* fn, const uaa_rotary_plan* p, int D) {
   if (!p) return set_error(UAA_ERR_INVALID_ARG, "%s: the plan is NULL", fn);
   if (p->rot < 0 || p->rot % 2 || p->rot > 2 * kMaxPairs || p->rot > D)
@@ -410,6 +473,7 @@ extern "C" int uaa_rotary(const uaa_rotary_plan* plan, const uaa_rotary_tensor* 
   a.plan = *plan;
   const int elem = dtype == UAA_FP32 ? 4 : 2;
   if ((st = check_tensor(fn, "q", a.t[0], a, elem)) || (st = check_tensor(fn, "k", a.t[1], a, elem))) return st;
+  if (a.tokens && (st = check_overlap(fn, a, elem))) return st;
   if (positions && (reinterpret_cast<uintptr_t>(positions) & (pos64 ? 7 : 3)))
     return set_error(UAA_ERR_INVALID_ARG, "%s: positions are not aligned to their element", fn);
   if (a.tokens == 0 || a.t[0].H + a.t[1].H == 0) return UAA_OK;
