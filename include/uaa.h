@@ -482,10 +482,10 @@ const char* uaa_version(void);
 /* 1 for the debug build of the library (libuaa_debug.so, compiled with
  * -DUAA_DEBUG), 0 otherwise.  The debug build checks, before each access, that
  * every tensor-core operand lies inside the issuing CTA's shared memory and
- * TMEM allocation and that every output store of the attention kernels lies
- * inside its tensor; a failed check skips the access and is reported by
- * uaa_check_device_status() as UAA_ERR_DEBUG_CHECK.  Same entry points and
- * results; slower. */
+ * TMEM allocation and that every output store of the attention, rotation and
+ * 8-bit checkpoint kernels lies inside its tensor; a failed check skips the
+ * access and is reported by uaa_check_device_status() as UAA_ERR_DEBUG_CHECK.
+ * Same entry points and results; slower. */
 int uaa_debug_build(void);
 
 #ifdef __cplusplus

@@ -57,6 +57,7 @@ struct ActArgs {
   float* steps[UAA_ACT8_MAX_TENSORS];
   long long first[UAA_ACT8_MAX_TENSORS + 1];  // first row of each tensor, among all
   int n, D;
+  DevCtx ctx;
 };
 
 // A lane's values: kRuns runs of kRun consecutive ones (16 bytes), run i at element i * (D / kRuns) + lane * kRun.
@@ -196,13 +197,15 @@ __global__ void __launch_bounds__(kThreads, std::is_same<T, __nv_bfloat16>::valu
     if (here) {
 #pragma unroll
       for (int i = 0; i < kRuns; ++i) {
+        if (!guard_store(a.ctx, at + i * part, kRun, (a.first[t + 1] - a.first[t]) * a.D)) continue;
         int8_t* c = a.codes[t] + at + i * part;
         if constexpr (kRun == 8)
           __stcs(reinterpret_cast<uint2*>(c), make_uint2(packed[2 * i], packed[2 * i + 1]));
         else
           __stcs(reinterpret_cast<uint32_t*>(c), packed[i]);
       }
-      if (lane == 0) a.steps[t][row] = !finite ? __uint_as_float(0x7fc00000u) : some ? step_of(top) : 0.f;
+      if (lane == 0 && guard_store(a.ctx, row, 1, a.first[t + 1] - a.first[t]))
+        a.steps[t][row] = !finite ? __uint_as_float(0x7fc00000u) : some ? step_of(top) : 0.f;
     }
   }
 }
@@ -234,7 +237,9 @@ __global__ void __launch_bounds__(kThreads) act8_unpack_kernel(const __grid_cons
     for (int i = 0; i < kPer; ++i)
       v[i] = static_cast<float>(static_cast<int8_t>(w[i / 4] >> (8 * (i % 4)))) * step;
 #pragma unroll
-    for (int i = 0; i < kRuns; ++i) write_run(static_cast<T*>(a.y[t]) + at + i * part, v + i * kRun);
+    for (int i = 0; i < kRuns; ++i)
+      if (guard_store(a.ctx, at + i * part, kRun, (a.first[t + 1] - a.first[t]) * a.D))
+        write_run(static_cast<T*>(a.y[t]) + at + i * part, v + i * kRun);
   }
 }
 
@@ -298,6 +303,7 @@ int act8(const char* fn, bool pack, int n, const void* const* x, int8_t* const* 
     ++a.n;
   }
   if (a.n == 0) return UAA_OK;
+  if (int st = get_check_ctx(&a.ctx)) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == UAA_BF16) return launch_t<__nv_bfloat16>(a, pack, s);
   if (dtype == UAA_FP16) return launch_t<__half>(a, pack, s);

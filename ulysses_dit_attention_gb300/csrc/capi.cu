@@ -83,6 +83,15 @@ int get_dev_ctx(DevCtx* ctx) {
   return UAA_OK;
 }
 
+int get_check_ctx(DevCtx* ctx) {
+  *ctx = DevCtx{};
+#ifdef UAA_DEBUG
+  return get_dev_ctx(ctx);
+#else
+  return UAA_OK;
+#endif
+}
+
 // The driver's tensor-map encoder, resolved once through the runtime.
 static PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   std::call_once(g_encode_once, [] {

@@ -35,6 +35,9 @@ constexpr uint32_t kIdescNegateA = 1u << 13;  // instruction descriptor: the A o
 
 // Row vectors, (B, H, tiles, 4, 128): -LSE_1 log2(e), -LSE_2 log2(e) + log2 |lambda|, Delta_1, Delta_2 of a tile's
 // queries
+__host__ __device__ __forceinline__ size_t row_floats(int B, int Sq, int H) {
+  return (size_t)B * H * tiles_of(Sq) * 4 * kTile;
+}
 __host__ __device__ __forceinline__ size_t rows_at(size_t bh, int Sq, int i) {
   return (bh * tiles_of(Sq) + i / kTile) * (4 * kTile) + i % kTile;
 }
@@ -127,7 +130,7 @@ template <int D>
 __global__ void __launch_bounds__(kRowThreads) diff_rows_kernel(
     const __nv_bfloat16* __restrict__ out, const __nv_bfloat16* __restrict__ out2,
     const __nv_bfloat16* __restrict__ dout, const float* __restrict__ lse, const void* __restrict__ lam, int lam_bf16,
-    float* __restrict__ rows, float* __restrict__ part, int B, int Sq, int H) {
+    float* __restrict__ rows, float* __restrict__ part, int B, int Sq, int H, DevCtx ctx) {
   constexpr int G = D / 8;
   constexpr int kGroups = kRowThreads / G;
   __shared__ float sums[kGroups];
@@ -171,7 +174,8 @@ __global__ void __launch_bounds__(kRowThreads) diff_rows_kernel(
         x = l == -INFINITY ? -INFINITY : l < INFINITY ? -l * kLog2e : NAN;
         if (sub == 1 && l != -INFINITY) x += log2f(fabsf(lm));
       }
-      rows[rows_at(bh, Sq, i) + sub * kTile] = x;
+      const size_t to = rows_at(bh, Sq, i) + sub * kTile;
+      if (guard_store(ctx, to, 1, row_floats(B, Sq, H))) rows[to] = x;
     }
   }
   if (sub == 0) sums[group] = sum;
@@ -179,7 +183,8 @@ __global__ void __launch_bounds__(kRowThreads) diff_rows_kernel(
   if (threadIdx.x == 0) {
     float s = 0.f;
     for (int x = 0; x < kGroups; ++x) s += sums[x];
-    part[(size_t)h * B * steps + (size_t)b * steps + t] = s;
+    const size_t to = (size_t)h * B * steps + (size_t)b * steps + t;
+    if (guard_store(ctx, to, 1, (size_t)B * H * steps)) part[to] = s;
   }
 }
 
@@ -501,10 +506,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // this thread writes a quarter of the row's columns
       const size_t off = (((size_t)w.b * Sk + (exists ? j : 0)) * H + w.h) * D + cq * (D / 4);
       const bool store = exists && guard_store(ctx, off, D / 4, k_extent);
-      float* const rest_at = rest + ((size_t)w.h * B + w.b) * nkt + w.t;
+      const size_t rest_at = ((size_t)w.h * B + w.b) * nkt + w.t;
+      const bool rest_store = threadIdx.x == 0 && guard_store(ctx, rest_at, 1, (size_t)B * H * nkt);
       if (kMask && !tile_any(key_mask, w.b, w.t, Sk)) {
         // no attended key in this tile: dK = dV = 0
-        if (threadIdx.x == 0) *rest_at = 0.f;
+        if (rest_store) rest[rest_at] = 0.f;
         if (store) {
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
@@ -584,12 +590,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int o = 16; o > 0; o /= 2) total += __shfl_xor_sync(0xffffffffu, total, o);
       if (lane == 0) ctl->sums[warp] = total;
       named_sync(kBarSum, kCompute);
-      if (threadIdx.x == 0) {
+      if (rest_store) {
         // where lambda is 0, or so small that dS_2 may be, the row kernel's sum stands
         const float l = fabsf(load_lambda(lam, lam_bf16, w.h));
         total = 0.f;
         for (int x = 0; x < kCompute / 32; ++x) total += ctl->sums[x];
-        *rest_at = l >= 0x1p-60f ? total / l : 0.f;
+        rest[rest_at] = l >= 0x1p-60f ? total / l : 0.f;
       }
       // epilogue: dV, and dK = scale * (dS^T Q).  A key outside the mask gets zeros, whatever its rows hold.
       if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(&ctl->bar_acc_done, it & 1, ctx, ctl));
@@ -1074,8 +1080,6 @@ int prepare(K kern, int smem) {
   return UAA_OK;
 }
 
-size_t row_floats(int B, int Sq, int H) { return (size_t)B * H * tiles_of(Sq) * 4 * kTile; }
-
 // Launches a kernel that may start as soon as all blocks of the one before it on the stream allow it.
 template <typename K, typename... Args>
 int launch_next(const char* what, K kern, int grid, int smem, cudaStream_t s, Args... args) {
@@ -1116,7 +1120,7 @@ int launch_bwd(const void* q, const void* k, const void* v, const void* lam, int
     return st;
   diff_rows_kernel<D><<<(int)row_blocks, kRowThreads, 0, s>>>(static_cast<const bf*>(out), static_cast<const bf*>(out2),
                                                              static_cast<const bf*>(dout), lse, lam, lam_bf16, rows,
-                                                             part, B, Sq, H);
+                                                             part, B, Sq, H, ctx);
   if ((st = check_launch("uaa_diff_attn_bwd (rows)"))) return st;
   const int sms = device_sms();
   // with a key mask the heads go innermost while one batch's Q and dO fit in half of L2, so that the empty key

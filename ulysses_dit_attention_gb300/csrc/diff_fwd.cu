@@ -423,7 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (m == 0) {
         named_sync(kBarO, kBarOut);
-        if (lane == 0 && ok && !*reinterpret_cast<volatile int*>(&ctl->abort)) {
+        if (lane == 0 && ok && !*reinterpret_cast<volatile int*>(&ctl->abort) &&
+            guard_store(ctx, (((size_t)w.b * Sq + w.t * kTile) * H + w.h) * D, D, o_extent)) {
 #pragma unroll
           for (int c = 0; c < kChunks; ++c)
             tma_store_4d(smem + L::kQ + (ne & 1) * L::kTileBytes + c * kChunkBytes, &tmO, c * 64, w.h, w.t * kTile,
@@ -701,7 +702,7 @@ __global__ void __launch_bounds__(kRowThreads) diff_fwd_rows_kernel(
     const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
     const void* __restrict__ lam, int lam_bf16, const uint8_t* __restrict__ mask, __nv_bfloat16* __restrict__ out,
     __nv_bfloat16* __restrict__ out2, float* __restrict__ lse, int B, int Sq, int Sk, int H, int cluster,
-    float scale_log2) {
+    float scale_log2, DevCtx ctx) {
   constexpr int G = D / 8;       // lanes of a row
   constexpr int KW = 32 / G;     // keys of a warp's load
   constexpr int kRowUnroll = row_unroll(NQ);
@@ -914,12 +915,15 @@ __global__ void __launch_bounds__(kRowThreads) diff_fwd_rows_kernel(
       o[mm].x *= inv;
       o[mm].y *= inv;
     }
-    const size_t oo = (((size_t)b * Sq + i0 + n) * H + h) * D + c;
+    const size_t oo = (((size_t)b * Sq + i0 + n) * H + h) * D + c, o_extent = (size_t)B * Sq * H * D;
+    if (!guard_store(ctx, oo, 2, o_extent)) continue;
     *reinterpret_cast<uint32_t*>(out + oo) = pack_bf16(o[0].x - lm * o[1].x, o[0].y - lm * o[1].y);
     if (out2) *reinterpret_cast<uint32_t*>(out2 + oo) = pack_bf16(o[1].x, o[1].y);
     if (c < 4) {  // columns 0 and 2 stand for the two maps
       const int mm = c / 2;
-      lse[(((size_t)b * H + h) * 2 + mm) * Sq + i0 + n] = lsum[mm] == 0.f ? -INFINITY : top[mm] * kLn2 + logf(lsum[mm]);
+      const size_t lo = (((size_t)b * H + h) * 2 + mm) * Sq + i0 + n;
+      if (guard_store(ctx, lo, 1, (size_t)B * H * 2 * Sq))
+        lse[lo] = lsum[mm] == 0.f ? -INFINITY : top[mm] * kLn2 + logf(lsum[mm]);
     }
   }
   cl.sync();  // no CTA leaves while another reads its shared memory
@@ -929,6 +933,8 @@ template <int D, int NQ, bool kMask>
 int launch_rows(const void* q, const void* k, const void* v, const void* lam, int lam_bf16, const uint8_t* mask,
                 void* out, void* out2, float* lse, int B, int Sq, int Sk, int H, float scale, cudaStream_t s) {
   const char* fn = "uaa_diff_attn_fwd";
+  DevCtx ctx;
+  if (int st = get_check_ctx(&ctx)) return st;
   auto kern = diff_fwd_rows_kernel<D, NQ, kMask>;
   const int smem = kRowWarps * (int)sizeof(RowPart<D, NQ>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -954,7 +960,7 @@ int launch_rows(const void* q, const void* k, const void* v, const void* lam, in
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
                          static_cast<const __nv_bfloat16*>(v), lam, lam_bf16, mask, static_cast<__nv_bfloat16*>(out),
-                         static_cast<__nv_bfloat16*>(out2), lse, B, Sq, Sk, H, cluster, scale * kLog2e);
+                         static_cast<__nv_bfloat16*>(out2), lse, B, Sq, Sk, H, cluster, scale * kLog2e, ctx);
   if (e != cudaSuccess) return set_error(UAA_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
   return check_launch(fn);
 }

@@ -39,6 +39,7 @@ struct RotTensor {
   void* y;
   long long xb, xs, xh, yb, ys, yh;  // batch, token and head strides in elements; columns are contiguous
   int H;
+  long long extent;  // elements from the first of y to its last
 };
 
 struct RotArgs {
@@ -49,6 +50,7 @@ struct RotArgs {
   int B, S, D, inverse;
   uint32_t tokens, tokens_per_block, units, pair_units;  // units of a head row; the first pair_units hold pairs
   uaa_rotary_plan plan;
+  DevCtx ctx;
 };
 
 template <typename T>
@@ -104,13 +106,20 @@ __device__ __forceinline__ void angles(const RotArgs& a, uint32_t t0, uint32_t n
 
 // Row h of token tok: the tensor that holds it, its input and its output
 template <typename T>
-__device__ __forceinline__ void locate(const RotArgs& a, uint32_t tok, uint32_t h, const T** x, T** y) {
+__device__ __forceinline__ const RotTensor& locate(const RotArgs& a, uint32_t tok, uint32_t h, const T** x, T** y) {
   const uint32_t b = tok / a.S, s = tok - b * a.S;
   const bool second = h >= static_cast<uint32_t>(a.t[0].H);
   const RotTensor& t = a.t[second ? 1 : 0];
   if (second) h -= a.t[0].H;
   *x = static_cast<const T*>(t.x) + (b * t.xb + s * t.xs + h * t.xh);
   *y = static_cast<T*>(t.y) + (b * t.yb + s * t.ys + h * t.yh);
+  return t;
+}
+
+// A store of a vector, range-checked in debug builds.
+template <typename T, int V>
+__device__ __forceinline__ void store(const RotArgs& a, const RotTensor& t, T* at, const Vec<T, V>& v) {
+  if (guard_store(a.ctx, at - static_cast<T*>(t.y), V, t.extent)) *reinterpret_cast<Vec<T, V>*>(at) = v;
 }
 
 // One thread takes units: of V pairs in two runs of V columns (halves, or V = 1), of V / 2 interleaved pairs in one run,
@@ -130,7 +139,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
       const uint32_t lt = row / heads;
       const T* x;
       T* y;
-      locate(a, t0 + lt, row - lt * heads, &x, &y);
+      const RotTensor& t = locate(a, t0 + lt, row - lt * heads, &x, &y);
       using VT = Vec<T, V>;
       if (u < a.pair_units) {
         if constexpr (kHalf || V == 1) {
@@ -139,18 +148,18 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
           const float2* w = cs + lt * pairs + u * V;
 #pragma unroll
           for (int e = 0; e < V; ++e) turn_pair(w[e], v0.e[e], v1.e[e]);
-          *reinterpret_cast<VT*>(y + c0) = v0;
-          *reinterpret_cast<VT*>(y + c1) = v1;
+          store(a, t, y + c0, v0);
+          store(a, t, y + c1, v1);
         } else {
           VT v = *reinterpret_cast<const VT*>(x + u * V);
           const float2* w = cs + lt * pairs + u * (V / 2);
 #pragma unroll
           for (int e = 0; e < V / 2; ++e) turn_pair(w[e], v.e[2 * e], v.e[2 * e + 1]);
-          *reinterpret_cast<VT*>(y + u * V) = v;
+          store(a, t, y + u * V, v);
         }
       } else {
         const int c = a.plan.rot + (u - a.pair_units) * V;
-        *reinterpret_cast<VT*>(y + c) = *reinterpret_cast<const VT*>(x + c);
+        store(a, t, y + c, *reinterpret_cast<const VT*>(x + c));
       }
     }
     __syncthreads();  // the next tokens' angles replace these
@@ -180,8 +189,9 @@ __global__ void __launch_bounds__(kThreads) rotary_rows_kernel(const __grid_cons
       const T* x;
       T* y = nullptr;
       Vec<T, E> v;
+      const RotTensor* t = nullptr;
       if (active) {
-        locate(a, t0 + lt, row - lt * heads, &x, &y);
+        t = &locate(a, t0 + lt, row - lt * heads, &x, &y);
         v = *reinterpret_cast<const Vec<T, E>*>(x + j * E);
       }
       if constexpr (kHalf) {
@@ -207,7 +217,7 @@ __global__ void __launch_bounds__(kThreads) rotary_rows_kernel(const __grid_cons
           turn_pair(cs[lt * pairs + p], v.e[2 * e], v.e[2 * e + 1]);
         }
       }
-      if (active) *reinterpret_cast<Vec<T, E>*>(y + j * E) = v;
+      if (active) store(a, *t, y + j * E, v);
     }
     __syncthreads();  // the next tokens' angles replace these
   }
@@ -455,8 +465,9 @@ extern "C" int uaa_rotary(const uaa_rotary_plan* plan, const uaa_rotary_tensor* 
   if (st) return st;
   if ((long long)B * S >= (1LL << 31)) return set_error(UAA_ERR_UNSUPPORTED, "%s: B*S must be below 2^31", fn);
   RotArgs a{};
-  auto take = [](const uaa_rotary_tensor& t) {
-    return RotTensor{t.x, t.y, t.x_batch, t.x_token, t.x_head, t.y_batch, t.y_token, t.y_head, t.H};
+  auto take = [&](const uaa_rotary_tensor& t) {
+    return RotTensor{t.x, t.y, t.x_batch, t.x_token, t.x_head, t.y_batch, t.y_token, t.y_head, t.H,
+                     (B - 1) * t.y_batch + (S - 1) * t.y_token + (t.H - 1) * t.y_head + D};
   };
   a.t[0] = take(*q);
   if (k) a.t[1] = take(*k);
@@ -480,6 +491,7 @@ extern "C" int uaa_rotary(const uaa_rotary_plan* plan, const uaa_rotary_tensor* 
   // a unit index of a block is 32 bits
   if ((long long)(a.t[0].H + a.t[1].H) * D * kMaxTokens >= (1LL << 31))
     return set_error(UAA_ERR_UNSUPPORTED, "%s: a token's heads hold too many columns", fn);
+  if ((st = get_check_ctx(&a.ctx))) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == UAA_BF16) return launch_t<__nv_bfloat16>(a, s);
   if (dtype == UAA_FP16) return launch_t<__half>(a, s);

@@ -49,6 +49,7 @@ struct DevCtx {
 
 // Host side: per-device status word address, wait bound, error message.
 int get_dev_ctx(DevCtx* ctx);           // returns UAA_OK or UAA_ERR_CUDA (message set)
+int get_check_ctx(DevCtx* ctx);         // for kernels without bounded waits: the same in debug builds, else nothing
 int set_error(int status, const char* fmt, ...);
 int check_launch(const char* what);     // cudaGetLastError -> UAA_ERR_CUDA
 
@@ -329,8 +330,8 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
 // Every MMA's operands are checked before it is issued -- shared-memory
 // descriptors must start inside this CTA's dynamic shared memory with room for a
 // 1 KB swizzle atom, accumulators and TMEM A operands must lie inside the CTA's
-// TMEM columns -- and every output store of the attention kernels against the end
-// of its tensor.  A failed check skips the access and sets kStatusDebugCheck (the
+// TMEM columns -- and every output store of the attention, rotation and 8-bit
+// checkpoint kernels against the end of its tensor.  A failed check skips the access and sets kStatusDebugCheck (the
 // first failure also records what and where, see kDbg*).  Release builds compile
 // the checks away: the guard structs are empty and every guard is `true`.
 // ----------------------------------------------------------------------------
@@ -420,7 +421,7 @@ __device__ __forceinline__ void mma_ts_checked(const MmaGuard& g, uint32_t d_tme
 // An output store of `n` elements at element offset `off` of a tensor of `extent` elements.
 __device__ __forceinline__ bool guard_store(const DevCtx& ctx, size_t off, size_t n, size_t extent) {
 #ifdef UAA_DEBUG
-  if (off + n > extent) {
+  if (off > extent || n > extent - off) {
     dbg_fail(ctx.status, kDbgGlobalStore, (uint32_t)(off > 0xFFFFFFFFull ? 0xFFFFFFFFull : off));
     return false;
   }
