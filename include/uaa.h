@@ -358,7 +358,8 @@ typedef struct {
 /* Rotates q and, if it is not NULL, k (which may have another head count) in one launch.
  *   plan      : host, read during the call
  *   positions : device, int32 (pos64 = 0) or int64, axis x of token (b, s) at
- *               b * pos_batch_stride + s * pos_token_stride + x; NULL: position start + s on every axis
+ *               b * pos_batch_stride + s * pos_token_stride + x; NULL: position start + s on every axis.  The
+ *               angle of position p is off by up to |p| * 2^-55 turns, the error of a 64-bit frequency
  *   dtype     : UAA_BF16, UAA_FP16 or UAA_FP32; computed in 32 bits, rounded once
  *   inverse   : nonzero applies the transposed map: the gradients of q and k from those of the results
  * Returns UAA_OK or a negative uaa_status. */

@@ -8,12 +8,14 @@
 // and columns R..D-1 are copied.  The transpose has -sin a.
 //
 // turns_i (turns per position) is kept as a 64-bit fixed-point fraction of a
-// turn, so the 64-bit product with the position drops whole turns by itself:
-// the fraction is off by at most |position| * 2^-65 turns and costs one integer
-// multiplication, where a 32-bit angle of a position near 2^18 would be off by
-// 2^-6 radians and a 64-bit floating-point one would use the FP64 pipe, 1/64 of
-// the FP32 rate here.  The upper 32 bits of the product, as a signed number of
-// half turns, go to sincospif.
+// turn, so the 64-bit product with the position drops whole turns by itself and
+// costs one integer multiplication, where a 32-bit angle of a position near 2^18
+// would be off by 2^-6 radians and a 64-bit floating-point one would use the FP64
+// pipe, 1/64 of the FP32 rate here.  turns_i itself is computed in 64-bit floating
+// point, at most 2^-2.6 turns with 53 bits: its error, up to 2^-55 turns (against
+// 200 bits; widths 2 to 256, bases 100 to 10^6, all scalings), is multiplied by the
+// position, 2^-24 turns at 2^31.  The upper 32 bits of the product, as a signed
+// number of half turns and rounded to 24 bits (2^-26 turns), go to sincospif.
 //
 // Bound: HBM.  Every element is read once and written once; the angles are
 // computed once per token by the block (R/2 of them, in shared memory) and used
