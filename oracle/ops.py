@@ -2,14 +2,14 @@
 checkpoints and differential attention, with the error each result may carry.
 
 Plain NumPy, no code shared with the library.  The error bounds count the roundings that the
-kernels make: a value rounded to bf16 is off by at most 2^-8 of itself (``BF16``), the exponentials
-on the FMA pipe by 8e-5 (``EXP``); 32-bit sums and products are covered by ``F32`` times the sum of
-the terms' magnitudes.
+kernels make: a value rounded to bf16 is off by at most 2^-8 of itself (``BF16``), an exponential of the
+special-function unit by 2^-22 (``EXP``), to which the error of its argument comes; 32-bit sums and
+products are covered by ``F32`` times the sum of the terms' magnitudes, a sum over all keys by ``norm_error``.
 """
 import numpy as np
 
 BF16 = 2.0 ** -8
-EXP = 8e-5
+EXP = 2.0 ** -22
 F32 = 2.0 ** -20
 
 
@@ -54,6 +54,16 @@ def act8_codes(x):
 
 
 # --------------------------------------------------------------------------- differential attention
+def norm_error(Sk):
+    """Relative error of a softmax's sum of Sk probabilities in 32 bits, beside that of the probabilities.
+
+    In steps of 2^-24.  Tiles of 80 or 128 keys: 64 additions within one at most, then a product, an addition and an
+    exponential (2^-22: four steps) to join it to the others: 64 + 6 (Sk / 80 + 1).  The few-row kernel adds every 16th key
+    and joins after 6 of them at least, with a product and an exponential: Sk / 16 + 5 Sk / 96; then groups of lanes, warps
+    and blocks, 16 + 3 additions and three times those five."""
+    return (96 + Sk / 8.0) * 2.0 ** -24
+
+
 def _maps(q, k, mask, scale):
     """Softmax maps and LSE of one batch element: q (Sq, H, D), k (Sk, H, D) -> (2, H, Sq, Sk), (2, H, Sq)."""
     w = q.shape[-1] // 2
@@ -76,7 +86,7 @@ def diff_attn(q, k, v, lam, mask=None, scale=None, dout=None):
     B, Sq, H, D = q.shape
     Sk, w = k.shape[1], D // 2
     scale = w ** -0.5 if scale is None else scale
-    P = BF16 + EXP  # a probability that a matrix product reads
+    norm = norm_error(Sk)
     names = ["out", "out2", "lse"] + ([] if dout is None else ["dq", "dk", "dv", "dlam"])
     shapes = {"out": q.shape, "out2": q.shape, "lse": (B, H, 2, Sq), "dq": q.shape, "dk": k.shape, "dv": k.shape,
               "dlam": (H,)}
@@ -94,14 +104,16 @@ def diff_attn(q, k, v, lam, mask=None, scale=None, dout=None):
         o2 = np.einsum("hij,jhd->ihd", a[1], vb)
         size = np.einsum("hij,jhd->ihd", both, np.abs(vb))
         size2 = np.einsum("hij,jhd->ihd", a[1], np.abs(vb))
+        # 32-bit scores: their terms' magnitudes
+        es = F32 * scale * np.stack([np.einsum("ihd,jhd->hij", np.abs(q[b][..., m * w:m * w + w]),
+                                               np.abs(k[b][..., m * w:m * w + w])).max(-1) for m in range(2)])
+        # a probability that a matrix product reads, and the sum that it is divided by
+        P = (BF16 + 2 * (EXP + es.max(0)) + norm).T[..., None]
         eo, eo2 = (P + F32) * size + BF16 * np.abs(o), (P + F32) * size2 + BF16 * np.abs(o2)
         put("out", b, o, eo)
         put("out2", b, o2, eo2)
-        # 32-bit scores: their terms' magnitudes, and the exponentials' own error
-        es = F32 * scale * np.stack([np.einsum("ihd,jhd->hij", np.abs(q[b][..., m * w:m * w + w]),
-                                               np.abs(k[b][..., m * w:m * w + w])).max(-1) for m in range(2)])
-        put("lse", b, np.moveaxis(lse, 0, 1), np.moveaxis(es + EXP + F32 * np.where(np.isinf(lse), 0, np.abs(lse)),
-                                                          0, 1))
+        elog = es + EXP + norm + F32 * np.where(np.isinf(lse), 0, np.abs(lse))
+        put("lse", b, np.moveaxis(lse, 0, 1), np.moveaxis(elog, 0, 1))
         if dout is None:
             continue
         g = dout[b]
@@ -113,12 +125,14 @@ def diff_attn(q, k, v, lam, mask=None, scale=None, dout=None):
                  + np.abs(lam)[:, None] * erow2)
         weight = np.stack([np.ones_like(L), -L])
         ds = weight * a * (da - rows[..., None])
+        # a probability formed again from the LSE: its score, the LSE and the exponential
+        ea = (es + elog + EXP)[..., None]
         # an entry of dS: its probability, its rounding to bf16, and the row dots' error
-        eds = (np.abs(ds) * (P + EXP + 2 * es[..., None] + F32)
+        eds = (np.abs(ds) * (BF16 + ea + F32)
                + np.abs(weight) * a * (eda + np.stack([erow1, erow2])[..., None]))
         pv = a[0] - L * a[1]
         # each map's probability is rounded to bf16 by itself: |A1 2^-8| + |lambda A2 2^-8|
-        epv = both * (BF16 + EXP + F32 + es.max(0)[..., None])
+        epv = both * (BF16 + F32 + ea.max(0))
         dv = np.einsum("hij,ihd->jhd", pv, g)
         edv = np.einsum("hij,ihd->jhd", epv + F32 * np.abs(pv), np.abs(g))
         put("dv", b, dv, edv + BF16 * np.abs(dv))
@@ -132,7 +146,14 @@ def diff_attn(q, k, v, lam, mask=None, scale=None, dout=None):
             put("dk", (b, slice(None), slice(None), c), dk,
                 scale * np.einsum("hij,ihd->jhd", e, np.abs(q[b][..., c])) + BF16 * np.abs(dk))
         res["dlam"][0][:] -= rows[1].sum(-1)
-        res["dlam"][1][:] += erow2.sum(-1) + F32 * np.abs(rows[1]).sum(-1)
+        # Delta_2 of the rounded O_2, and what sum_j A_2 (dA - Delta_2) of 32 bits says is missing from it: with A_2 and dA
+        # as they are computed, sum_j A_2 dA + (1 - sum_j A_2) Delta_2.  Where lambda is too small for dS_2, Delta_2 alone.
+        size_da = np.einsum("hij,hij->hi", a[1], np.abs(da))
+        near = ea[1, ..., 0] * (2 * size_da + erow2) + np.einsum("hij,hij->hi", a[1], eda)
+        # added up in 32 bits: a key's rows one after the other, then tiles, keys and rows in parts of at most 64
+        near = near + (Sq + 256) * 2.0 ** -24 * 2 * size_da
+        erow = np.where(np.abs(lam)[:, None] >= 2.0 ** -60, near, erow2 + F32 * np.abs(rows[1]))
+        res["dlam"][1][:] += erow.sum(-1)
     if dout is not None:
         res["dlam"][1][:] += BF16 * np.abs(res["dlam"][0])  # lambda in bf16
     return res
