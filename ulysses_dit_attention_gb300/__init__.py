@@ -467,8 +467,18 @@ class RotaryPlan:
         _check(lib().uaa_rotary_plan_init(ctypes.byref(self._c), self.LAYOUTS[layout], len(widths),
                                           (ctypes.c_int * len(widths))(*widths), float(base), self.SCALINGS[scaling],
                                           float(factor), float(original), float(alpha), float(beta)))
+        self._bind()
+
+    def _bind(self):
         self._ref = ctypes.byref(self._c)
         self.axes, self.rot, self.magnitude = self._c.axes, self._c.rot, self._c.magnitude
+
+    def __getstate__(self):  # for copies and pickles
+        return bytes(self._c)
+
+    def __setstate__(self, state):
+        self._c = _RotaryPlan.from_buffer_copy(state)
+        self._bind()
 
     @property
     def turns(self):
