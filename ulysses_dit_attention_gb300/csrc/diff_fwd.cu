@@ -684,7 +684,8 @@ constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kMaxCluster = 8;
 // Keys in flight per lane: as many as leave two CTAs on an SM (B = 4, Sk = 16389, H = 24, D = 128: one row 158 us with 4,
-// 134 with 8, 222 with 12; two rows 172 us with 4, 136 with 6, 390 with 8: 6.0 TB/s).
+// 134 with 8, 222 with 12; two rows 172 us with 4, 136 with 6, 390 with 8; these two now 118 and 127: 6.8 and
+// 6.3 TB/s).
 __host__ __device__ constexpr int row_unroll(int nq) { return nq == 1 ? 8 : 6; }
 
 template <int D, int NQ>
