@@ -68,8 +68,12 @@ typedef enum {
   UAA_ERR_CUDA = -4,          /* a CUDA runtime / driver call failed */
   UAA_ERR_TIMEOUT = -5,       /* a bounded device-side wait ran out (reported by
                                  uaa_check_device_status) */
-  UAA_ERR_DEBUG_CHECK = -6    /* debug builds only: a device-side range check failed
+  UAA_ERR_DEBUG_CHECK = -6,   /* debug builds only: a device-side range check failed
                                  and its access was skipped (uaa_check_device_status) */
+  UAA_ERR_NO_PAGES = -7,      /* the cache has fewer free pages than asked for; nothing changed */
+  UAA_ERR_BAD_PAGE = -8       /* a page, a table row or a length in device memory lies outside the
+                                 cache; the keys or rows it stands for were skipped
+                                 (uaa_check_device_status) */
 } uaa_status;
 
 /* Attention forward.
@@ -428,9 +432,119 @@ int uaa_diff_attn_bwd(const void* q, const void* k, const void* v, const void* l
                       void* dq, void* dk, void* dv, void* dlambda, int B, int Sq, int Sk, int H, int D, float scale,
                       void* workspace, size_t workspace_bytes, uaa_stream_t stream);
 
+/* ------------------------------------------------------------------ sequences of their own lengths
+ * Attention of B sequences, each with its own number of queries and keys, without padding.  Sequence b has the n
+ * query tokens starts[b] .. starts[b+1] - 1 and m keys; its last query stands at its last key.  With `causal` query i
+ * reads keys 0 .. m - n + i, without it all m.  Hq / Hk query heads in a row share a key head.  A query that reads no
+ * key gets out = 0, lse = -inf and no gradient.  Tokens behind starts[B] are left as they were.
+ *   packed : the keys are the tokens starts_k[b] .. starts_k[b+1] - 1 of k and v (starts_k NULL: as the queries)
+ *   paged  : key j is row j % page of page table[r, j / page] of the pools k and v, r = seqs[b] (seqs NULL: b), and
+ *            m = lens[r] counts the new tokens, whose keys are in the cache already
+ * starts, starts_k, seqs, table and lens are in device memory and are not seen by the host: starts must not decrease,
+ * and what lies outside the tensors is cut off (a starts entry is held between 0 and T; a page, table row or length
+ * outside the cache is skipped and reported by uaa_check_device_status as UAA_ERR_BAD_PAGE); nothing outside the
+ * tensors is read or written.
+ * A score of -inf is no weight; a row with a score of NaN or +inf gets lse = NaN or +inf and a row of NaN in out.  What
+ * keys, values, pages and queries hold that a row does not read leaves no trace in it, infinities and NaN too. */
+typedef struct {
+  const void *q, *k, *v;    /* device, 16-byte aligned; D contiguous elements a head.  q (T, Hq, D);
+                               k, v packed (Tk, Hk, D), paged (pages, page, Hk, D) */
+  void* out;                /* device, contiguous (T, Hq, D); must not overlap the inputs */
+  float* lse;               /* device, (Hq, T): natural log of the sum of exp(scale q.k) */
+  const int32_t* starts;    /* device, (B + 1) */
+  const int32_t* starts_k;  /* packed: device, (B + 1), or NULL */
+  const int32_t* table;     /* paged: device, contiguous (table_rows, width) */
+  const int32_t* lens;      /* paged: device, (table_rows) */
+  const int32_t* seqs;      /* paged: device, (B), or NULL */
+  long long q_row, q_head, k_row, k_head, v_row, v_head, k_page, v_page; /* strides in elements, multiples of 8 */
+  int B, T, Tk, Hq, Hk, D;  /* D = 64 or 128; Hq a multiple of Hk, 128 times at most */
+  int dtype;                /* UAA_BF16 or UAA_FP16 (the backward: UAA_BF16) */
+  int causal;
+  int pages, page, table_rows, width; /* paged: a page is 16, 32, 64 or a multiple of 128 tokens */
+  float scale;
+} uaa_seqs;
+
+/* Bytes of device workspace of the two forward calls (partial results of sequences whose keys are split over SMs).
+ * Returns 0 for invalid sizes. */
+size_t uaa_attn_seqs_workspace_bytes(int T, int Hq, int Hk, int D);
+
+/* Forward over packed sequences, and over the pages of a cache (a chunk of new tokens, or one).
+ *   args      : host, read during the call
+ *   workspace : device, at least uaa_attn_seqs_workspace_bytes() bytes, 256-byte aligned; contents on entry are
+ *               ignored.  Calls that may overlap need workspaces of their own.
+ * Returns UAA_OK or a negative uaa_status. */
+int uaa_attn_packed_fwd(const uaa_seqs* args, void* workspace, size_t workspace_bytes, uaa_stream_t stream);
+int uaa_attn_paged_fwd(const uaa_seqs* args, void* workspace, size_t workspace_bytes, uaa_stream_t stream);
+
+/* Gradients of uaa_attn_packed_fwd (bf16), deterministic (no atomics).
+ *   args           : the forward's, with its out and lse
+ *   dout           : device, contiguous (T, Hq, D)
+ *   dq; dk, dv     : device, contiguous (T, Hq, D); (Tk, Hk, D), written for the tokens of the sequences
+ *   workspace      : device, at least uaa_attn_packed_bwd_workspace_bytes() bytes, 256-byte aligned
+ * Returns UAA_OK or a negative uaa_status. */
+size_t uaa_attn_packed_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int D);
+int uaa_attn_packed_bwd(const uaa_seqs* args, const void* dout, void* dq, void* dk, void* dv, void* workspace,
+                        size_t workspace_bytes, uaa_stream_t stream);
+
+/* ------------------------------------------------------------------ pages of a cache
+ * A cache keeps the keys and values of `seqs` sequences in pages of `page` tokens.  Which page holds what is kept on
+ * the host, by this object, and copied to the device: table (seqs, width), -1 behind a sequence's pages, and lens.
+ * Pages may be shared (a fork); the lowest free page is always taken first.  The calls check everything before they
+ * change anything; then they enqueue the device's changes on `stream`, a few small launches.  They are made outside
+ * of graph captures (a captured one would be replayed without the host's part); the attention and write calls, which
+ * read table and lens on the device, may be captured.  One thread at a time per object is not required: calls lock. */
+typedef struct uaa_pages uaa_pages;
+
+/* The device's side; `pools` NULL in the calls below: the host's side alone. */
+typedef struct {
+  void *k, *v;            /* device, 16-byte aligned, contiguous (layers, pages, page, row_bytes) */
+  int32_t *table, *lens;  /* device, (seqs, width) and (seqs) */
+  int layers;
+  int row_bytes;          /* bytes of a token's keys of one layer, a multiple of 16 */
+} uaa_pools;
+
+int uaa_pages_create(uaa_pages** out, int pages, int page, int seqs, int width);
+void uaa_pages_destroy(uaa_pages* p);
+
+/* Adds counts[i] tokens to sequence seqs[i] (no sequence twice): takes the pages, and gives a sequence whose partly
+ * filled last page is shared a page of its own with the filled rows copied.  The new tokens' rows are then written by
+ * uaa_cache_write.
+ *   starts, seqs_dev : device, (n + 1) and (n): the sums of counts and seqs, for uaa_cache_write and
+ *                      uaa_attn_paged_fwd; or NULL
+ * Returns UAA_OK, UAA_ERR_NO_PAGES or another negative uaa_status. */
+int uaa_pages_append(uaa_pages* p, const uaa_pools* pools, int n, const int* seqs, const int* counts, int32_t* starts,
+                     int32_t* seqs_dev, uaa_stream_t stream);
+/* Makes children[i], an empty sequence, a copy of parents[i] that shares its pages. */
+int uaa_pages_fork(uaa_pages* p, const uaa_pools* pools, int n, const int* parents, const int* children,
+                   uaa_stream_t stream);
+/* Cuts sequence seqs[i] to its first lens[i] tokens and frees pages that no one holds any more; 0 frees it. */
+int uaa_pages_truncate(uaa_pages* p, const uaa_pools* pools, int n, const int* seqs, const int* lens,
+                       uaa_stream_t stream);
+/* Moves pages into the lowest places, so that the pages in use are 0 .. used - 1. */
+int uaa_pages_compact(uaa_pages* p, const uaa_pools* pools, uaa_stream_t stream);
+/* Tokens of a sequence, and its first `most` pages into `out` (NULL: none); a negative uaa_status for a bad seq. */
+int uaa_pages_row(uaa_pages* p, int seq, int* out, int most);
+/* Pages that are free. */
+int uaa_pages_free(uaa_pages* p);
+
+/* Writes the keys and values of new tokens of one layer into their pages: token starts[b] + i of k and v is row
+ * lens[r] - n + i of sequence r = seqs[b] (seqs NULL: b), n = starts[b+1] - starts[b].
+ *   k, v     : device, (T, Hk, D) of 2-byte elements, strides k_row, k_head, v_row, v_head, heads contiguous
+ *   k_pages, v_pages : device, the layer's pools (pages, page, Hk, D) with strides *_page, *_row, *_head of the pools
+ * Rows of a page that lies outside the cache, and of positions below 0, are skipped (UAA_ERR_BAD_PAGE). */
+typedef struct {
+  const void *k, *v;
+  void *k_pages, *v_pages;
+  const int32_t *starts, *seqs, *table, *lens;
+  long long k_row, k_head, v_row, v_head;                                   /* elements, multiples of 8 */
+  long long kp_page, kp_row, kp_head, vp_page, vp_row, vp_head;             /* elements, multiples of 8 */
+  int B, T, Hk, D, pages, page, table_rows, width;
+} uaa_cache_rows;
+int uaa_cache_write(const uaa_cache_rows* args, uaa_stream_t stream);
+
 /* Synchronises `stream`, then reads and clears the library's device status
  * words.  Returns UAA_OK, UAA_ERR_TIMEOUT (a bounded device wait ran out in
- * some kernel since the last check), UAA_ERR_DEBUG_CHECK (debug builds: a
+ * some kernel since the last check), UAA_ERR_BAD_PAGE, UAA_ERR_DEBUG_CHECK (debug builds: a
  * device-side range check failed; uaa_last_error() names the first one) or
  * UAA_ERR_CUDA. */
 int uaa_check_device_status(uaa_stream_t stream);

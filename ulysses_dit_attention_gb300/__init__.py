@@ -33,10 +33,13 @@ __all__ = [
     "RotaryPlan", "rotary_fwd", "rotary_bwd", "Rotary", "rotary", "shard_positions", "Act8", "act8_pack", "act8_unpack",
     "attn_bwd_act8",
     "diff_attn_fwd", "diff_attn_bwd", "diff_attn_bwd_workspace_bytes", "DiffAttention", "diff_attention",
+    "attn_packed_fwd", "attn_packed_bwd", "attn_packed_bwd_workspace_bytes", "attn_seqs_workspace_bytes",
+    "PackedAttention", "packed_attention", "attn_paged_fwd", "cache_write", "PagedCache",
 ]
 
 STATUS = {0: "UAA_OK", -1: "UAA_ERR_INVALID_ARG", -2: "UAA_ERR_UNSUPPORTED", -3: "UAA_ERR_PER_HEAD_MASK",
-          -4: "UAA_ERR_CUDA", -5: "UAA_ERR_TIMEOUT", -6: "UAA_ERR_DEBUG_CHECK"}
+          -4: "UAA_ERR_CUDA", -5: "UAA_ERR_TIMEOUT", -6: "UAA_ERR_DEBUG_CHECK", -7: "UAA_ERR_NO_PAGES",
+          -8: "UAA_ERR_BAD_PAGE"}
 
 
 class UAAError(RuntimeError):
@@ -61,7 +64,26 @@ class _RotaryPlan(ctypes.Structure):  # uaa_rotary_plan
 # uaa_rotary_tensor, as bytes: x, y, their batch, token and head strides, H
 _ROTARY_TENSOR = struct.Struct("@PP6qi0q")
 
+# uaa_seqs, uaa_pools and uaa_cache_rows, as bytes
+_SEQS = struct.Struct("@10P8q12if0q")
+_POOLS = struct.Struct("@4P2i0q")
+_CACHE_ROWS = struct.Struct("@8P10q8i0q")
+
 _SIGS = {
+    "uaa_attn_seqs_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I]),
+    "uaa_attn_packed_fwd": (_I, [_P, _P, ctypes.c_size_t, _P]),
+    "uaa_attn_paged_fwd": (_I, [_P, _P, ctypes.c_size_t, _P]),
+    "uaa_attn_packed_bwd_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I]),
+    "uaa_attn_packed_bwd": (_I, [_P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "uaa_pages_create": (_I, [ctypes.POINTER(_P), _I, _I, _I, _I]),
+    "uaa_pages_destroy": (None, [_P]),
+    "uaa_pages_append": (_I, [_P, _P, _I, _P, _P, _P, _P, _P]),
+    "uaa_pages_fork": (_I, [_P, _P, _I, _P, _P, _P]),
+    "uaa_pages_truncate": (_I, [_P, _P, _I, _P, _P, _P]),
+    "uaa_pages_compact": (_I, [_P, _P, _P]),
+    "uaa_pages_row": (_I, [_P, _I, _P, _I]),
+    "uaa_pages_free": (_I, [_P]),
+    "uaa_cache_write": (_I, [_P, _P]),
     "uaa_rotary_plan_init": (_I, [ctypes.POINTER(_RotaryPlan), _I, _I, _P, ctypes.c_double, _I, ctypes.c_double,
                                   ctypes.c_double, ctypes.c_double, ctypes.c_double]),
     "uaa_rotary": (_I, [ctypes.POINTER(_RotaryPlan), _P, _P, _P,
@@ -804,6 +826,310 @@ def diff_attention(q, k, v, lam, key_mask=None, scale=None, saved=None):
     To capture a step with its gradients in a CUDA graph, warm up on another stream and let no eager autograd graph
     of the same leaves live: PyTorch ties a leaf's gradients to the stream of the first graph that holds it."""
     return DiffAttention.apply(q, k, v, lam, key_mask, scale, saved)
+
+
+# --------------------------------------------------------------------------- sequences of their own lengths
+def _rows16(name, t, dims, D=None):
+    """Checks a 16-bit operand (..., heads, D); returns its strides, those of dimensions of one entry as if contiguous."""
+    shape = t.shape
+    if len(shape) != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {tuple(shape)}")
+    if D is not None and shape[-1] != D:
+        raise ValueError(f"{name} has heads of {shape[-1]} columns, not {D}")
+    strides, dense = list(t.stride()), 1
+    for i in range(dims - 1, -1, -1):
+        if shape[i] <= 1:
+            strides[i] = dense
+        dense *= max(shape[i], 1)
+    if strides[-1] != 1:
+        raise ValueError(f"the columns of {name} must be contiguous")
+    return strides
+
+
+def _starts(name, t, B=None):
+    if t.dim() != 1 or t.dtype != torch.int32 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 vector, got {t.dtype} {tuple(t.shape)}")
+    if t.shape[0] < 1 or (B is not None and t.shape[0] != B + 1):
+        raise ValueError(f"{name} must have one entry more than there are sequences, got {t.shape[0]}")
+
+
+def _seqs_common(q, k, v, starts, scale, out, lse, half=True):
+    """What packed and paged attention check alike; returns the type's number, the scale and the results."""
+    if q.dtype not in (torch.bfloat16, torch.float16) or (q.dtype != torch.bfloat16 and not half):
+        raise TypeError("q must be bfloat16 or float16" if half else "gradients are built for bfloat16")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError("q, k and v must have one type")
+    T, Hq, D = q.shape
+    if k.shape != v.shape:
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} must have one shape")
+    _starts("starts", starts)
+    dev = q.device
+    return (_DTYPES[q.dtype], float(1.0 / math.sqrt(D) if scale is None else scale),
+            _result("out", out, (T, Hq, D), q.dtype, dev), _result("lse", lse, (Hq, T), torch.float32, dev))
+
+
+def attn_seqs_workspace_bytes(T, Hq, Hk, D) -> int:
+    return int(lib().uaa_attn_seqs_workspace_bytes(T, Hq, Hk, D))
+
+
+def _seqs_workspace(workspace, T, Hq, Hk, D, dev):
+    if workspace is None:
+        workspace = torch.empty(attn_seqs_workspace_bytes(T, Hq, Hk, D), dtype=torch.uint8, device=dev)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _packed_args(q, k, v, starts, starts_k, causal, scale, out, lse, half=True):
+    (q0, q1, _), (k0, k1, _), (v0, v1, _) = _rows16("q", q, 3), _rows16("k", k, 3, q.shape[-1]), _rows16("v", v, 3)
+    dtype, scale, out, lse = _seqs_common(q, k, v, starts, scale, out, lse, half)
+    B = starts.shape[0] - 1
+    if starts_k is not None:
+        _starts("starts_k", starts_k, B)
+    elif k.shape[0] != q.shape[0]:
+        raise ValueError(f"{q.shape[0]} query and {k.shape[0]} key tokens: starts_k is needed")
+    T, Hq, D = q.shape
+    packed = _SEQS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), starts.data_ptr(),
+                        0 if starts_k is None else starts_k.data_ptr(), 0, 0, 0, q0, q1, k0, k1, v0, v1, 0, 0, B, T,
+                        k.shape[0], Hq, k.shape[1], D, dtype, 1 if causal else 0, 0, 0, 0, 0, scale)
+    return packed, out, lse
+
+
+def attn_packed_fwd(q, k, v, starts, starts_k=None, causal=True, scale=None, out=None, lse=None, workspace=None):
+    """``uaa_attn_packed_fwd``: attention of sequences packed one behind the other; returns ``(out, lse)``.
+
+    ``q`` ``(T, Hq, D)``, ``k``, ``v`` ``(Tk, Hk, D)``: bf16 or fp16 with contiguous columns -- slices of a packed
+    projection are fine.  ``Hq`` is a multiple of ``Hk``: query head h reads key head ``h // (Hq // Hk)``.
+    ``starts``: int32 ``(B + 1)`` on the device, the first token of each sequence and the end of the last;
+    ``starts_k`` the keys' where they are others than the queries'.  With ``causal`` a sequence's last query stands at
+    its last key and each reads the keys up to its own place.  Returns ``out`` ``(T, Hq, D)`` and ``lse`` fp32
+    ``(Hq, T)``; tokens behind ``starts[-1]`` are left as they were (in new results: undefined).
+    """
+    dev = _same_device(q, k, v, starts, starts_k, out, lse, workspace)
+    args, out, lse = _packed_args(q, k, v, starts, starts_k, causal, scale, out, lse)
+    T, Hq, D = q.shape
+    _call(dev, "uaa_attn_packed_fwd", args, *_seqs_workspace(workspace, T, Hq, k.shape[1], D, dev))
+    return out, lse
+
+
+def attn_packed_bwd_workspace_bytes(B, T, Hq, Hk, D) -> int:
+    return int(lib().uaa_attn_packed_bwd_workspace_bytes(B, T, Hq, Hk, D))
+
+
+def attn_packed_bwd(q, k, v, out, dout, lse, starts, starts_k=None, causal=True, scale=None, dq=None, dk=None, dv=None,
+                    workspace=None):
+    """``uaa_attn_packed_bwd``: the gradients ``(dq, dk, dv)`` of :func:`attn_packed_fwd` (bf16)."""
+    dev = _same_device(q, k, v, out, dout, lse, starts, starts_k, workspace)
+    if out is None or lse is None:
+        raise ValueError("out and lse are the forward's results")
+    args, out, lse = _packed_args(q, k, v, starts, starts_k, causal, scale, out, lse, half=False)
+    dout = _result("dout", dout, q.shape, q.dtype, dev)
+    dq = _result("dq", dq, q.shape, q.dtype, dev)
+    dk = _result("dk", dk, k.shape, q.dtype, dev)
+    dv = _result("dv", dv, k.shape, q.dtype, dev)
+    T, Hq, D = q.shape
+    if workspace is None:
+        nbytes = attn_packed_bwd_workspace_bytes(starts.shape[0] - 1, T, Hq, k.shape[1], D)
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+    _call(dev, "uaa_attn_packed_bwd", args, dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+          workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return dq, dk, dv
+
+
+class PackedAttention(torch.autograd.Function):
+    """Autograd pairing of ``attn_packed_fwd`` / ``attn_packed_bwd``; ``lse`` is non-differentiable.
+
+    ``saved="int8"`` keeps Q, K, V and O for the backward pass as an 8-bit checkpoint.  Tokens behind ``starts[-1]``
+    belong to no sequence: ``out`` and the gradients are zero there."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, starts, starts_k=None, causal=True, scale=None, saved=None):
+        _check_saved(saved)
+        if q.dtype != torch.bfloat16 and any(ctx.needs_input_grad):
+            raise TypeError("gradients are built for bfloat16")
+        out, lse = attn_packed_fwd(q, k, v, starts, starts_k, causal, scale, out=torch.zeros_like(q, memory_format=torch.contiguous_format))
+        if saved == "int8":  # the checkpoint takes contiguous rows
+            q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+        ctx.starts = (starts if starts.is_inference() else None, starts_k if starts_k is not None and starts_k.is_inference() else None)
+        _save(ctx, saved, (q, k, v, out), lse, None if ctx.starts[0] is not None else starts,
+              None if ctx.starts[1] is not None else starts_k, key_mask=None)
+        ctx.causal, ctx.scale = causal, scale
+        ctx.mark_non_differentiable(lse)
+        ctx.set_materialize_grads(False)  # no zeros for lse
+        return out, lse
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout, _dlse):
+        if dout is None:
+            return (None,) * 8
+        (q, k, v, out), (lse, starts, starts_k), _ = _saved(ctx, 4)
+        starts, starts_k = (a if b is None else b for a, b in zip((starts, starts_k), ctx.starts))
+        zeros = [torch.zeros(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v)]
+        dq, dk, dv = attn_packed_bwd(q, k, v, out, dout.contiguous(), lse, starts, starts_k, ctx.causal, ctx.scale,
+                                     *zeros)
+        return dq, dk, dv, None, None, None, None, None
+
+
+def packed_attention(q, k, v, starts, starts_k=None, causal=True, scale=None, saved=None):
+    """Differentiable :func:`attn_packed_fwd`: returns ``(out, lse)``."""
+    return PackedAttention.apply(q, k, v, starts, starts_k, causal, scale, saved)
+
+
+def _table(table, lens, seqs, B):
+    if table.dim() != 2 or table.dtype != torch.int32 or not table.is_contiguous():
+        raise ValueError(f"table must be contiguous int32 (sequences, pages), got {table.dtype} {tuple(table.shape)}")
+    if lens.dtype != torch.int32 or lens.shape != table.shape[:1] or not lens.is_contiguous():
+        raise ValueError(f"lens must be contiguous int32 ({table.shape[0]},), got {lens.dtype} {tuple(lens.shape)}")
+    if seqs is not None and (seqs.dtype != torch.int32 or seqs.shape != (B,) or not seqs.is_contiguous()):
+        raise ValueError(f"seqs must be contiguous int32 ({B},), got {seqs.dtype} {tuple(seqs.shape)}")
+
+
+def attn_paged_fwd(q, k_pages, v_pages, starts, table, lens, seqs=None, causal=True, scale=None, out=None, lse=None,
+                   workspace=None):
+    """``uaa_attn_paged_fwd``: new tokens attend to the pages of a cache; returns ``(out, lse)``.
+
+    ``q`` ``(T, Hq, D)``: the new tokens of B sequences packed one behind the other (``starts`` int32 ``(B + 1)``), one
+    or many of each.  ``k_pages``, ``v_pages`` ``(pages, page, Hk, D)``: a layer's pools, which hold the new tokens'
+    keys and values already (:func:`cache_write`).  ``table`` int32 ``(rows, width)`` and ``lens`` int32 ``(rows,)``, the
+    new tokens counted, are a :class:`PagedCache`'s; sequence b is row ``seqs[b]`` (None: b).  Everything is read on the
+    device when the call runs: it may be captured in a graph and replayed with other lengths and pages.
+    """
+    dev = _same_device(q, k_pages, v_pages, starts, table, lens, seqs, out, lse, workspace)
+    q0, q1, _ = _rows16("q", q, 3)
+    (k0, k1, k2, _), (v0, v1, v2, _) = _rows16("k_pages", k_pages, 4, q.shape[-1]), _rows16("v_pages", v_pages, 4)
+    dtype, scale, out, lse = _seqs_common(q, k_pages, v_pages, starts, scale, out, lse)
+    B = starts.shape[0] - 1
+    _table(table, lens, seqs, B)
+    (T, Hq, D), (N, page, Hk, _), (rows, width) = q.shape, k_pages.shape, table.shape
+    args = _SEQS.pack(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                      starts.data_ptr(), 0, table.data_ptr(), lens.data_ptr(), 0 if seqs is None else seqs.data_ptr(),
+                      q0, q1, k1, k2, v1, v2, k0, v0, B, T, 0, Hq, Hk, D, dtype, 1 if causal else 0, N, page, rows,
+                      width, scale)
+    _call(dev, "uaa_attn_paged_fwd", args, *_seqs_workspace(workspace, T, Hq, Hk, D, dev))
+    return out, lse
+
+
+def cache_write(k, v, k_pages, v_pages, starts, table, lens, seqs=None):
+    """``uaa_cache_write``: puts the keys and values ``(T, Hk, D)`` of new tokens into the pages of one layer.
+
+    Token ``starts[b] + i`` goes to row ``lens[r] - n + i`` of sequence ``r = seqs[b]`` (None: b), n being the
+    sequence's new tokens, which ``lens`` counts.  Any 2-byte type.
+    """
+    dev = _same_device(k, v, k_pages, v_pages, starts, table, lens, seqs)
+    if k.element_size() != 2 or any(t.dtype != k.dtype for t in (v, k_pages, v_pages)):
+        raise TypeError("k, v and the pages must have one 2-byte type")
+    if k.shape != v.shape or k_pages.shape != v_pages.shape or k.dim() != 3 or k_pages.dim() != 4 or k.shape[1:] != k_pages.shape[2:]:
+        raise ValueError(f"k {tuple(k.shape)}, v {tuple(v.shape)} and pages {tuple(k_pages.shape)}, "
+                         f"{tuple(v_pages.shape)} do not fit")
+    (k0, k1, _), (v0, v1, _) = _rows16("k", k, 3), _rows16("v", v, 3)
+    (a0, a1, a2, _), (b0, b1, b2, _) = _rows16("k_pages", k_pages, 4), _rows16("v_pages", v_pages, 4)
+    _starts("starts", starts)
+    B = starts.shape[0] - 1
+    _table(table, lens, seqs, B)
+    (T, Hk, D), (N, page, _, _), (rows, width) = k.shape, k_pages.shape, table.shape
+    _call(dev, "uaa_cache_write",
+          _CACHE_ROWS.pack(k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), starts.data_ptr(),
+                           0 if seqs is None else seqs.data_ptr(), table.data_ptr(), lens.data_ptr(), k0, k1, v0, v1,
+                           a0, a1, a2, b0, b1, b2, B, T, Hk, D, N, page, rows, width))
+
+
+class PagedCache:
+    """The keys and values of sequences, of all layers, in pages that sequences may share (``uaa_pages``).
+
+    ``k``, ``v`` ``(layers, pages, page, heads, dim)``; ``table`` int32 ``(seqs, width)`` and ``lens`` int32 ``(seqs,)``
+    on the device, for :func:`attn_paged_fwd`.  A sequence is a number below ``seqs`` and has ``width`` pages at most.
+    The lowest free pages are taken first.  A call that cannot be done raises before anything changes
+    (``UAA_ERR_NO_PAGES`` where pages are short).  The device's side is changed on the current stream, by small
+    launches that hold their data; these calls are made outside of graph captures, between replays.
+
+    A step of a model::
+
+        starts, seqs = cache.append(ids, [1] * len(ids))
+        for layer in range(layers):
+            cache.write(layer, k, v, starts, seqs)
+            out, _ = cache.attend(layer, q, starts, seqs)
+    """
+
+    def __init__(self, layers, pages, page, heads, dim, seqs, width, dtype=torch.bfloat16, device="cuda"):
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError("dtype must be bfloat16 or float16")
+        if min(layers, heads) < 1 or dim not in (64, 128):
+            raise ValueError(f"layers={layers} and heads={heads} must be positive, dim={dim} 64 or 128")
+        self._h = _P()
+        _check(lib().uaa_pages_create(ctypes.byref(self._h), pages, page, seqs, width))
+        self.page, self.seqs = page, seqs
+        self.k, self.v = (torch.empty((layers, pages, page, heads, dim), dtype=dtype, device=device) for _ in range(2))
+        self.table = torch.full((seqs, width), -1, dtype=torch.int32, device=device)
+        self.lens = torch.zeros(seqs, dtype=torch.int32, device=device)
+        self._pools = _POOLS.pack(self.k.data_ptr(), self.v.data_ptr(), self.table.data_ptr(), self.lens.data_ptr(),
+                                  layers, heads * dim * 2)
+
+    def __del__(self):
+        if getattr(self, "_h", None) and _lib is not None:
+            _lib.uaa_pages_destroy(self._h)
+            self._h = None
+
+    @property
+    def free_pages(self):
+        return int(lib().uaa_pages_free(self._h))
+
+    def length(self, seq):
+        """Tokens of a sequence, as the host knows them."""
+        n = int(lib().uaa_pages_row(self._h, seq, None, 0))
+        if n < 0:
+            _check(n)
+        return n
+
+    def pages_of(self, seq):
+        """The pages that a sequence holds, in order."""
+        n = -(-self.length(seq) // self.page)
+        row = (_I * max(n, 1))()
+        lib().uaa_pages_row(self._h, seq, row, n)
+        return list(row)[:n]
+
+    def _pair(self, name, a, b):
+        a, b = list(a), list(b)
+        if len(a) != len(b):
+            raise ValueError(f"{len(a)} and {len(b)} entries")
+        n = len(a)
+        _call(self.k.device, name, self._h, self._pools, n, (_I * n)(*a), (_I * n)(*b))
+
+    def append(self, seqs, counts):
+        """Makes room for ``counts[i]`` more tokens of sequence ``seqs[i]``; a shared, partly filled last page is
+        copied first.  Returns ``(starts, seqs)`` on the device, for :meth:`write` and :meth:`attend`."""
+        a, b = list(seqs), list(counts)
+        if len(a) != len(b):
+            raise ValueError(f"{len(a)} sequences and {len(b)} counts")
+        n, dev = len(a), self.k.device
+        both = torch.empty(2 * n + 1, dtype=torch.int32, device=dev)
+        starts, ids = both[: n + 1], both[n + 1:]
+        at = both.data_ptr()
+        _call(dev, "uaa_pages_append", self._h, self._pools, n, (_I * n)(*a), (_I * n)(*b), at, at + 4 * (n + 1))
+        return starts, ids
+
+    def fork(self, parents, children):
+        """Makes ``children[i]``, an empty sequence, a copy of ``parents[i]``: it shares the pages, none is copied."""
+        self._pair("uaa_pages_fork", parents, children)
+
+    def truncate(self, seqs, lens):
+        """Cuts sequence ``seqs[i]`` to its first ``lens[i]`` tokens."""
+        self._pair("uaa_pages_truncate", seqs, lens)
+
+    def free(self, seqs):
+        """Empties sequences; pages that no other sequence shares are free again."""
+        seqs = list(seqs)
+        self.truncate(seqs, [0] * len(seqs))
+
+    def compact(self):
+        """Moves pages so that those in use are the lowest ones."""
+        _call(self.k.device, "uaa_pages_compact", self._h, self._pools)
+
+    def write(self, layer, k, v, starts, seqs=None):
+        """:func:`cache_write` into a layer."""
+        cache_write(k, v, self.k[layer], self.v[layer], starts, self.table, self.lens, seqs)
+
+    def attend(self, layer, q, starts, seqs=None, causal=True, scale=None):
+        """:func:`attn_paged_fwd` over a layer."""
+        return attn_paged_fwd(q, self.k[layer], self.v[layer], starts, self.table, self.lens, seqs, causal, scale)
 
 
 # --------------------------------------------------------------------------- Ulysses re-layout

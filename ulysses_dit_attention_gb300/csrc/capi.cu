@@ -243,6 +243,8 @@ int uaa_check_device_status(uaa_stream_t stream) {
     return set_error(UAA_ERR_TIMEOUT, "a bounded device-side wait ran out (status word 0x%x)", word);
   if (word & kStatusBadLaunch)
     return set_error(UAA_ERR_CUDA, "a kernel refused its launch configuration (status word 0x%x)", word);
+  if (word & kStatusBadPage)
+    return set_error(UAA_ERR_BAD_PAGE, "a page, table row or length outside the cache was skipped (status word 0x%x)", word);
   if (word & kStatusDebugCheck) {
     static const char* what[4] = {"?", "MMA shared-memory operand outside the CTA's shared memory",
                                   "MMA TMEM address outside the CTA's allocation", "output store past the tensor end"};

@@ -22,6 +22,7 @@ enum : uint32_t {
   kStatusTimeout = 1u,      // a bounded wait ran out
   kStatusBadLaunch = 2u,    // a kernel refused its launch configuration (e.g. misaligned shared memory)
   kStatusDebugCheck = 4u,   // debug builds (UAA_DEBUG): a device-side range check failed, the access was skipped
+  kStatusBadPage = 8u,      // a page, table row or length outside the cache: what it stands for was skipped
 };
 // Debug builds leave the first failed check in status[2] (kDbg* below) and its
 // offending value in status[3].
