@@ -466,7 +466,7 @@ typedef struct {
 
 /* Bytes of device workspace of the two forward calls (partial results of sequences whose keys are split over SMs).
  * Returns 0 for invalid sizes. */
-size_t uaa_attn_seqs_workspace_bytes(int T, int Hq, int Hk, int D);
+size_t uaa_attn_seqs_workspace_bytes(int B, int T, int Hq, int Hk, int D);
 
 /* Forward over packed sequences, and over the pages of a cache (a chunk of new tokens, or one).
  *   args      : host, read during the call

@@ -98,7 +98,7 @@ def test_refusals_of_the_call():
     assert bwd(ws=P((1 << 24) + 16)) == -1 and "256-byte" in err()
     assert bwd(B=0, q=0) == 0 and bwd(T=0, Tk=0, q=0) == 0
     assert uaa.attn_packed_bwd_workspace_bytes(-1, 4, 4, 2, 64) == 0 and uaa.attn_packed_bwd_workspace_bytes(1, 4, 4, 2, 96) == 0
-    assert uaa.attn_seqs_workspace_bytes(-1, 4, 2, 64) == 0
+    assert uaa.attn_seqs_workspace_bytes(1, -1, 4, 2, 64) == 0
 
 
 def test_refusals_of_the_binding():
@@ -442,7 +442,7 @@ def test_starts_that_are_wrong_stay_inside():
         dk, dv = (g.empty(y["k"].shape, torch.bfloat16) for _ in range(2))
         lse = g.empty((4, 300), torch.float32)
         ws = g.empty((uaa.attn_packed_bwd_workspace_bytes(3, 300, 4, 2, 64),), torch.uint8)
-        ws2 = g.empty((uaa.attn_seqs_workspace_bytes(300, 4, 2, 64),), torch.uint8)
+        ws2 = g.empty((uaa.attn_seqs_workspace_bytes(3, 300, 4, 2, 64),), torch.uint8)
         for t in (out, dq, dk, dv, lse):
             t.zero_()
         uaa.attn_packed_fwd(y["q"], y["k"], y["v"], st, out=out, lse=lse, workspace=ws2)

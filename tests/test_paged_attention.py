@@ -286,7 +286,7 @@ def test_writes_stay_inside():
         y = {n: t.to(DEV) for n, t in x.items()}
         g, T = Guarded(), sum(news)
         out, lse = g.empty((T, 6, 128), torch.bfloat16), g.empty((6, T), torch.float32)
-        ws = g.empty((uaa.attn_seqs_workspace_bytes(T, 6, 2, 128),), torch.uint8)
+        ws = g.empty((uaa.attn_seqs_workspace_bytes(len(lens), T, 6, 2, 128),), torch.uint8)
         uaa.attn_paged_fwd(y["q"], y["k"], y["v"], y["starts"], y["table"], y["lens"], out=out, lse=lse, workspace=ws)
         uaa.check_device_status()
         g.check()

@@ -70,7 +70,7 @@ _POOLS = struct.Struct("@4P2i0q")
 _CACHE_ROWS = struct.Struct("@8P10q8i0q")
 
 _SIGS = {
-    "uaa_attn_seqs_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I]),
+    "uaa_attn_seqs_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I]),
     "uaa_attn_packed_fwd": (_I, [_P, _P, ctypes.c_size_t, _P]),
     "uaa_attn_paged_fwd": (_I, [_P, _P, ctypes.c_size_t, _P]),
     "uaa_attn_packed_bwd_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I]),
@@ -868,13 +868,13 @@ def _seqs_common(q, k, v, starts, scale, out, lse, half=True):
             _result("out", out, (T, Hq, D), q.dtype, dev), _result("lse", lse, (Hq, T), torch.float32, dev))
 
 
-def attn_seqs_workspace_bytes(T, Hq, Hk, D) -> int:
-    return int(lib().uaa_attn_seqs_workspace_bytes(T, Hq, Hk, D))
+def attn_seqs_workspace_bytes(B, T, Hq, Hk, D) -> int:
+    return int(lib().uaa_attn_seqs_workspace_bytes(B, T, Hq, Hk, D))
 
 
-def _seqs_workspace(workspace, T, Hq, Hk, D, dev):
+def _seqs_workspace(workspace, B, T, Hq, Hk, D, dev):
     if workspace is None:
-        workspace = torch.empty(attn_seqs_workspace_bytes(T, Hq, Hk, D), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(attn_seqs_workspace_bytes(B, T, Hq, Hk, D), dtype=torch.uint8, device=dev)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -906,7 +906,7 @@ def attn_packed_fwd(q, k, v, starts, starts_k=None, causal=True, scale=None, out
     dev = _same_device(q, k, v, starts, starts_k, out, lse, workspace)
     args, out, lse = _packed_args(q, k, v, starts, starts_k, causal, scale, out, lse)
     T, Hq, D = q.shape
-    _call(dev, "uaa_attn_packed_fwd", args, *_seqs_workspace(workspace, T, Hq, k.shape[1], D, dev))
+    _call(dev, "uaa_attn_packed_fwd", args, *_seqs_workspace(workspace, starts.shape[0] - 1, T, Hq, k.shape[1], D, dev))
     return out, lse
 
 
@@ -1004,7 +1004,7 @@ def attn_paged_fwd(q, k_pages, v_pages, starts, table, lens, seqs=None, causal=T
                       starts.data_ptr(), 0, table.data_ptr(), lens.data_ptr(), 0 if seqs is None else seqs.data_ptr(),
                       q0, q1, k1, k2, v1, v2, k0, v0, B, T, 0, Hq, Hk, D, dtype, 1 if causal else 0, N, page, rows,
                       width, scale)
-    _call(dev, "uaa_attn_paged_fwd", args, *_seqs_workspace(workspace, T, Hq, Hk, D, dev))
+    _call(dev, "uaa_attn_paged_fwd", args, *_seqs_workspace(workspace, B, T, Hq, Hk, D, dev))
     return out, lse
 
 

@@ -171,6 +171,30 @@ int encode_seq_maps(SegMaps* maps, const void* ptr, const SeqDesc& d, int B, int
   return UAA_OK;
 }
 
+int encode_map(CUtensorMap* map, const char* fn, const void* ptr, const long long (&dims)[4],
+               const long long (&strides)[3], const int (&box)[4]) {
+  if (!encoder()) return set_error(UAA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  cuuint64_t d[4], t[3];
+  cuuint32_t b[4], one[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 4; ++i) {
+    d[i] = (cuuint64_t)dims[i];
+    b[i] = (cuuint32_t)box[i];
+    if (i < 3) t[i] = (cuuint64_t)strides[i] * 2;
+  }
+  auto encode = [&] {
+    return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), d, t, b, one,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = encode();
+  if (r == CUDA_ERROR_INVALID_CONTEXT) {  // as above
+    int dev = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = encode();
+  }
+  if (r != CUDA_SUCCESS) return set_error(UAA_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (CUresult %d)", fn, (int)r);
+  return UAA_OK;
+}
+
 // exp2_fma2 (the forward's FMA-pipe exponential) over x[0 .. 2*npairs), pair by pair.
 __global__ void exp2_fma2_kernel(const float2* __restrict__ x, float2* __restrict__ y, long long npairs) {
   for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < npairs;

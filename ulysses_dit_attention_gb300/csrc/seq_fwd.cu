@@ -1,6 +1,33 @@
 // Attention over packed sequences and over the pages of a cache, forward (the
-// formulas stand in seq_shared.cuh).  One warp per (token, query head): the keys
-// one after the other, a running maximum and sum.
+// formulas stand in seq_shared.cuh).
+//
+// Rows.  The g query heads that share a key head are rows of one tile: row r of a
+// tile of a sequence is head r % g of token r / g, so a tile of 128 rows holds
+// TT = 128 / g tokens and K and V are read once for all of them.  An item is two
+// tiles (a pair) of one sequence and key head, against tiles of 128 keys.
+//
+// Work.  A persistent CTA per SM; the items of all sequences in a row, weighed by
+// the keys that they read plus kItemWork, are cut into equal shares, one a CTA, in
+// the middle of an item where it falls so: long prompts, many short ones and one
+// token over a long past fill the card alike, and the lengths stay on the device
+// (every CTA adds up the weights itself when it starts).  The parts of an item that
+// was cut go to the workspace, unnormalised, and a second kernel joins them in order.
+//   warp 8     TMA producer: the item's Q tiles, then K_j, V_j through a ring
+//   warp 9     tcgen05 issuer (one elected lane)
+//   warps 0-3  softmax of slot 0, warps 4-7 of slot 1: thread r owns row r (a TMEM
+//              lane); running maximum and sum, O rescaled only when the maximum grew
+//              by more than 2^8; P goes over S as the next product's operand
+// An item's two tiles take the two slots and read the same keys.  Where the second
+// tile is empty (few new tokens) both slots work on the first one, slot 0 on the even
+// key tiles and slot 1 on the odd ones, and are joined in the epilogue: without that
+// the chain S, softmax, P V of one tile takes longer than its keys take to arrive.
+//
+// TMEM: S / P of the slots in columns 0 and 128, O in 256 and 256 + D.
+//
+// Keys outside a row's border get P = 0.  P V multiplies that 0 by what V holds, so in
+// the tiles that the border crosses the warps look at V first: rows that no row of
+// the item reads become zeros, and an infinity or a NaN in a row that only some read
+// becomes a zero that the epilogue adds to those rows again.
 #include <float.h>
 
 #include "seq_shared.cuh"
@@ -8,67 +35,930 @@
 namespace uaa {
 namespace {
 
-template <int D, bool kPaged>
-__global__ void __launch_bounds__(256) seq_fwd_rows_kernel(const __grid_constant__ SeqArgs a, DevCtx ctx) {
+constexpr int kBN = 128;                // keys of a tile
+constexpr int kChunkBytes = 128 * 128;  // 128 rows x 128 bytes: 64 columns of a tile, 128-byte swizzled
+constexpr int kThreads = 320;
+constexpr int kProducerWarp = 8;
+constexpr int kMmaWarp = 9;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
+// Named barriers: kBarP + t, "P of slot t is in TMEM" (its warps arrive, the issuer syncs); kBarL, the slots' sums.
+constexpr uint32_t kBarP = 1, kBarPCount = 128 + 32, kBarL = 3;
+// Weight of an item beside its keys (its filling and draining), the least share of a CTA, and the least tiles of a part.
+constexpr int kItemWork = 256, kLeastShare = 512, kLeastTiles = 2;
+
+constexpr int kKeptSeqs = 64;  // sequences of a share that are kept in shared memory (more: in the workspace)
+
+template <int D>
+struct FwdLayout {
+  static constexpr int kRing = D == 128 ? 5 : 10;
+  static constexpr int kTileBytes = 128 * D * 2;
+  static constexpr int kQ = 0;  // two Q tiles
+  static constexpr int kRingOff = kQ + 2 * kTileBytes;
+  static constexpr int kCtl = kRingOff + kRing * kTileBytes;
+  static constexpr int kStat = kCtl + 512;  // maximum and sum of slot 1's rows
+  static constexpr int kKept = kStat + 2 * 128 * 4;  // the share's sequences
+  static constexpr int kSmem = kKept + kKeptSeqs * 16;
+  static_assert(kSmem <= 232448, "shared memory exceeds the per-CTA limit");
+};
+
+// A place in the row of all items' key tiles: tile j of pair p of sequence b, key head h.
+struct Cut {
+  int b, h, p, j;
+};
+__device__ __forceinline__ bool same_item(const Cut& x, const Cut& y) { return x.b == y.b && x.h == y.h && x.p == y.p; }
+__device__ __forceinline__ bool before(const Cut& x, const Cut& y) {  // x's item lies before y's
+  return x.b != y.b ? x.b < y.b : x.h != y.h ? x.h < y.h : x.p < y.p;
+}
+
+struct FwdCtl {
+  uint64_t bar_q_full, bar_q_empty;
+  uint64_t bar_kv_full[10], bar_kv_empty[10];
+  uint64_t bar_s_full[2], bar_pv_done[2];
+  uint64_t bar_o_free, bar_final;
+  uint32_t tmem_base;
+  int abort;
+  uint32_t dirty;                          // the last item with an infinity or a NaN taken out of V
+  alignas(16) Cut cut[2];                  // this CTA's share
+  alignas(16) uint32_t words[10][4];       // paged, per ring slot: keys whose page is there (filled with V)
+};
+static_assert(sizeof(FwdCtl) <= 512, "control block");
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool kHalf>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (kHalf) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+// 16-bit floats, two a word: whether one of them is an infinity or a NaN; and the word without them
+template <bool kHalf>
+__device__ __forceinline__ bool not_finite(uint32_t w) {
+  constexpr uint32_t e = kHalf ? 0x7c00u : 0x7f80u;
+  return (w & e) == e || (w >> 16 & e) == e;
+}
+template <bool kHalf>
+__device__ __forceinline__ uint32_t finite_part(uint32_t w) {
+  constexpr uint32_t e = kHalf ? 0x7c00u : 0x7f80u;
+  return ((w & e) == e ? 0u : w & 0xffffu) | ((w >> 16 & e) == e ? 0u : w & 0xffff0000u);
+}
+
+// ---------------------------------------------------------------------------
+// The row of items
+__device__ __forceinline__ int pairs_of(const SeqArgs& a, int n) { return (n + 2 * a.TT - 1) / (2 * a.TT); }
+
+// Weight of the first p pairs of a sequence and key head; the last pair counts as if it were full.
+__device__ __forceinline__ long long weight(const SeqArgs& a, const Seq& q, int p) {
+  const long long P = p, W = 2 * a.TT;
+  if (!a.s.causal) return P * (kItemWork + q.m);
+  const long long off = q.m - q.n, none = off < 0 ? -off / W : 0;  // pairs that read no key
+  const long long x = P > none ? (P - none) * off + W * (P * (P + 1) - none * (none + 1)) / 2 : 0;
+  return P * kItemWork + x;
+}
+
+__device__ __forceinline__ int tiles_of(const SeqArgs& a, const Seq& q, int p) {
+  return (keys_of(a.s, q, min(q.n, 2 * (p + 1) * a.TT) - 1) + kBN - 1) / kBN;
+}
+
+// The place at weight w of sequence b.
+__device__ Cut cut_at(const SeqArgs& a, const Seq& q, int b, long long w) {
+  const int np = pairs_of(a, q.n);
+  const long long head = weight(a, q, np);
+  Cut c{b, (int)(w / head), 0, 0};
+  w -= c.h * head;
+  int lo = 0, hi = np - 1;  // the last p with weight(p) <= w
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (weight(a, q, mid) <= w) lo = mid;
+    else hi = mid - 1;
+  }
+  c.p = lo;
+  const long long first = weight(a, q, lo), all = weight(a, q, lo + 1) - first;
+  const int nt = tiles_of(a, q, lo);
+  c.j = (int)(((w - first) * nt + all / 2) / all);
+  if (c.j < kLeastTiles) {
+    c.j = 0;
+  } else if (nt - c.j < kLeastTiles) {
+    c.j = 0;
+    if (++c.p == np) {
+      c.p = 0;
+      if (++c.h == a.s.Hk) {
+        c.h = 0;
+        ++c.b;
+      }
+    }
+  }
+  return c;
+}
+
+// Walks the items of a share.  Every role walks it for itself, over the sequences as the CTA found them when it
+// started, so all agree on every item: after a failure, and if someone writes into the lengths meanwhile.
+struct Item {
+  int j0, j1;    // key tiles of this part
+  bool part;     // of an item that was cut
+  bool split;    // the second tile is empty: the slots take the key tiles in turn
+  int n[2];      // key tiles of the slots
+  int lo, hi;    // keys that the first row reads, and the last one
+};
+struct Walk {
+  Cut at, end;
+  const Seq* kept;  // of sequence `base` and the next ones
+  int base, begin_j;
+  Seq q;
+  int np;
+  bool first;
+  __device__ __forceinline__ Walk(const Cut& from, const Cut& to, const Seq* seqs)
+      : at(from), end(to), kept(seqs), base(from.b), begin_j(from.j), np(-1), first(true) {
+    at.j = 0;
+  }
+  __device__ __forceinline__ bool next(const SeqArgs& a, Item& it) {
+    if (!first) {
+      ++at.p;
+      begin_j = 0;
+    }
+    first = false;
+    while (true) {
+      if (at.b >= a.s.B || at.b > end.b) return false;
+      if (np < 0) {
+        q = kept[at.b - base];
+        np = pairs_of(a, q.n);
+      }
+      if (at.p >= np) {
+        at.p = 0;
+        ++at.h;
+      }
+      if (np > 0 && at.h < a.s.Hk) break;
+      at.h = at.p = 0;
+      ++at.b;
+      np = -1;
+    }
+    const bool last = same_item(at, end);
+    if (!before(at, end) && !(last && end.j > 0)) return false;
+    const int TT = a.TT, t0 = 2 * at.p * TT;
+    it.hi = keys_of(a.s, q, min(q.n, t0 + 2 * TT) - 1);
+    it.lo = keys_of(a.s, q, t0);
+    const int nt = (it.hi + kBN - 1) / kBN;
+    it.j0 = begin_j;
+    it.j1 = last ? end.j : nt;
+    it.part = it.j0 > 0 || it.j1 < nt;
+    it.split = q.n <= t0 + TT;
+    const int c = max(it.j1 - it.j0, 0);
+    if (it.split) {
+      it.n[0] = (c + 1) / 2;
+      it.n[1] = c / 2;
+    } else {
+      const int n0 = (keys_of(a.s, q, t0 + TT - 1) + kBN - 1) / kBN;
+      it.n[0] = min(max(n0 - it.j0, 0), c);
+      it.n[1] = c;
+    }
+    return true;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// The workspace: the CTAs' first places, then 2 parts a CTA: O (D, rows) and (maximum, sum) of every row.
+struct Parts {
+  Cut* first;
+  Seq* seqs;  // of the shares, where they are too many for shared memory: CTA c's from its first sequence + c on
+  float* o;
+  float2* stat;
+  int rows;  // of a part: 128 or 256
+};
+__host__ __device__ __forceinline__ int part_rows(long long rows) { return rows <= 128 ? 128 : 256; }
+
+template <int D>
+__device__ __forceinline__ float* part_o(const Parts& w, int slot) { return w.o + (size_t)slot * D * w.rows; }
+__device__ __forceinline__ float2* part_stat(const Parts& w, int slot) { return w.stat + (size_t)slot * w.rows; }
+
+// Row j of V of key head h, or NULL where its page is not there.
+template <bool kPaged>
+__device__ __forceinline__ const uint16_t* value_row(const SeqArgs& a, const Seq& q, int h, int j) {
   const uaa_seqs& s = a.s;
-  constexpr int P = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long rows = (long long)s.T * s.Hq;
-  const int fp16 = s.dtype == UAA_FP16;
-  for (long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += (long long)gridDim.x * 8) {
-    const int t = (int)(r / s.Hq), h = (int)(r % s.Hq), hk = h / a.g;
-    const int b = seq_of_token(s.starts, s.B, t);
-    if (b < 0) continue;  // behind the last sequence: left as it was
-    const Seq q = load_seq<kPaged>(s, b);
-    if (q.bad && lane == 0) atomicOr(ctx.status, kStatusBadPage);
-    const int keys = keys_of(s, q, t - q.q0);
-    float x[P], acc[P], top = -INFINITY, sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      x[i] = load16(s.q, (size_t)t * s.q_row + (size_t)h * s.q_head + lane * P + i, fp16) * (s.scale * kLog2e);
-      acc[i] = 0.f;
-    }
-    for (int j = 0; j < keys; ++j) {
-      size_t ka, va;
-      if constexpr (kPaged) {
-        const int page = s.table[(size_t)q.k0 * s.width + j / s.page], at = j % s.page;
-        if (page < 0 || page >= s.pages) {
-          if (lane == 0) atomicOr(ctx.status, kStatusBadPage);
-          continue;
-        }
-        ka = (size_t)page * s.k_page + (size_t)at * s.k_row;
-        va = (size_t)page * s.v_page + (size_t)at * s.v_row;
-      } else {
-        ka = (size_t)(q.k0 + j) * s.k_row;
-        va = (size_t)(q.k0 + j) * s.v_row;
-      }
-      float d = 0.f;
-#pragma unroll
-      for (int i = 0; i < P; ++i) d += x[i] * load16(s.k, ka + (size_t)hk * s.k_head + lane * P + i, fp16);
-#pragma unroll
-      for (int o = 16; o > 0; o /= 2) d += __shfl_xor_sync(0xffffffffu, d, o);
-      if (d > top) {
-        const float now = fminf(d, FLT_MAX);  // finite: a score of +inf then gives p = sum = +inf and NaN behind it
-        const float f = exp2f(top - now);
-        sum *= f;
-#pragma unroll
-        for (int i = 0; i < P; ++i) acc[i] *= f;
-        top = now;
-      }
-      const float p = d == -INFINITY ? 0.f : exp2f(d - top);
-      sum += p;
-#pragma unroll
-      for (int i = 0; i < P; ++i) acc[i] += p * load16(s.v, va + (size_t)hk * s.v_head + lane * P + i, fp16);
-    }
-#pragma unroll
-    for (int i = 0; i < P; ++i) store16(s.out, (size_t)r * D + lane * P + i, sum == 0.f ? 0.f : acc[i] / sum, fp16);
-    if (lane == 0) s.lse[(size_t)h * s.T + t] = sum == 0.f ? -INFINITY : (top + log2f(sum)) / kLog2e;
+  const uint16_t* v = static_cast<const uint16_t*>(s.v) + (size_t)h * s.v_head;
+  if constexpr (kPaged) {
+    const int page = s.table[(size_t)q.k0 * s.width + j / s.page];
+    if (page < 0 || page >= s.pages) return nullptr;
+    return v + (size_t)page * s.v_page + (size_t)(j % s.page) * s.v_row;
+  } else {
+    return v + (size_t)(q.k0 + j) * s.v_row;
   }
 }
 
-size_t workspace_bytes(int T, int g, int D) {
-  (void)T, (void)g, (void)D;
-  return 256;
+template <int D, bool kPaged, bool kHalf>
+__global__ void __launch_bounds__(kThreads, 1)
+    seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ SeqArgs a, const Parts parts,
+                   float scale_log2, DevCtx ctx) {
+  using L = FwdLayout<D>;
+  constexpr int kChunks = D / 64;
+  constexpr int R = L::kRing;
+  constexpr uint32_t kIdescS = idesc_f16_f32(128, kBN, false, false, kHalf);
+  constexpr uint32_t kIdescPV = idesc_f16_f32(128, D, false, true, kHalf);
+  constexpr float kLn2 = 0.6931471805599453f;
+
+  extern __shared__ __align__(1024) uint8_t smem[];
+  FwdCtl* ctl = reinterpret_cast<FwdCtl*>(smem + L::kCtl);
+  float* sStat = reinterpret_cast<float*>(smem + L::kStat);
+  const uint32_t sbase = smem_u32(smem);
+  if (sbase & 1023u) {
+    // the swizzled operand tiles need 1024-byte alignment; never expected to trigger
+    if (threadIdx.x == 0) atomicOr(ctx.status, kStatusBadLaunch);
+    return;
+  }
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int cta = blockIdx.x, ctas = gridDim.x;
+  const uaa_seqs& s = a.s;
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  if (threadIdx.x == 0) {
+    mbar_init(&ctl->bar_q_full, 1);
+    mbar_init(&ctl->bar_q_empty, 1);
+    for (int i = 0; i < R; ++i) {
+      mbar_init(&ctl->bar_kv_full[i], 1);
+      mbar_init(&ctl->bar_kv_empty[i], 1);
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&ctl->bar_s_full[w], 1);
+      mbar_init(&ctl->bar_pv_done[w], 1);
+    }
+    mbar_init(&ctl->bar_o_free, 256);
+    mbar_init(&ctl->bar_final, 1);
+    ctl->abort = 0;
+    ctl->dirty = 0;
+    ctl->cut[0] = Cut{s.B, 0, 0, 0};
+    ctl->cut[1] = Cut{s.B, 0, 0, 0};
+    fence_mbar_init();
+  }
+  if (warp == kProducerWarp && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&ctl->tmem_base, 512);
+    tmem_relinquish();
+  }
+  Seq q{};  // of sequence threadIdx.x, if there are no more than threads
+  // This CTA's share: the sequences' weights, added up by all threads, 320 sequences at a time
+  {
+    long long* sums = reinterpret_cast<long long*>(sStat);  // a partial sum a warp
+    auto scan = [&](long long x, long long& all) {         // sum of the threads before this one; `all`: of all
+      long long run = x;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const long long y = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += y;
+      }
+      __syncthreads();
+      if (lane == 31) sums[warp] = run;
+      __syncthreads();
+      long long before = 0;
+      all = 0;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += sums[w];
+        all += sums[w];
+      }
+      return before + run - x;
+    };
+    auto of = [&](int b, Seq& q) {
+      q.n = 0;
+      if (b >= s.B) return 0LL;
+      bool bad;
+      q = load_seq<kPaged>(s, b, &bad);
+      if (bad && cta == 0) atomicOr(ctx.status, kStatusBadPage);
+      return q.n > 0 ? s.Hk * weight(a, q, pairs_of(a, q.n)) : 0LL;
+    };
+    long long total = 0, all;
+    long long w = 0;
+    for (int b0 = 0; b0 < s.B; b0 += kThreads) {
+      w = of(b0 + threadIdx.x, q);
+      scan(w, all);
+      total += all;
+    }
+    const long long most = total / kLeastShare;
+    const int shares = most < 1 ? 1 : most < ctas ? (int)most : ctas;
+    if (cta < shares && total > 0) {
+      const long long w0 = total / shares * cta + total % shares * cta / shares;
+      const long long w1 = total / shares * (cta + 1) + total % shares * (cta + 1) / shares;
+      long long done = 0;
+      for (int b0 = 0; b0 < s.B; b0 += kThreads) {
+        const int b = b0 + threadIdx.x;
+        if (s.B > kThreads) w = of(b, q);
+        const long long at = done + scan(w, all);
+        if (w > 0 && w0 >= at && w0 < at + w) ctl->cut[0] = cut_at(a, q, b, w0 - at);
+        if (w > 0 && w1 >= at && w1 < at + w) ctl->cut[1] = cut_at(a, q, b, w1 - at);
+        done += all;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const Cut from = ctl->cut[0], to = ctl->cut[1];
+  if (threadIdx.x == 0) parts.first[cta] = from;
+  const int held = min(to.b, s.B - 1) - from.b + 1;  // its sequences (none: from.b = B)
+  Seq* kept = held <= kKeptSeqs ? reinterpret_cast<Seq*>(smem + L::kKept) : parts.seqs + from.b + cta;
+  for (int b = from.b + threadIdx.x; b < from.b + held && s.B > kThreads; b += kThreads)
+    kept[b - from.b] = load_seq<kPaged>(s, b);
+  if (s.B <= kThreads && (int)threadIdx.x >= from.b && (int)threadIdx.x < from.b + held) kept[threadIdx.x - from.b] = q;
+  __syncthreads();
+  const uint32_t tmem = ctl->tmem_base;
+  const MmaGuard mg = mma_guard(ctx, sbase, L::kSmem, tmem, 512);  // debug builds' operand checks
+  const size_t o_extent = (size_t)s.T * s.Hq * D, lse_extent = (size_t)s.Hq * s.T;
+
+  uint32_t kv_armed[R] = {}, q_armed = 0;  // uses armed per barrier, for the teardown
+  bool mma_issued = false;                 // set in the issuing lane once it has issued an MMA
+
+  if (warp == kProducerWarp) {
+    // ------------------------------------------------------------ producer
+    bool ok = true;
+    uint32_t n = 0;   // K/V ring counter across items
+    uint32_t ne = 0;  // items with at least one key tile
+    Walk w(from, to, kept);
+    Item it;
+    while (ok && w.next(a, it)) {
+      if (it.j1 <= it.j0) continue;
+      const int h = w.at.h;
+      if (lane == 0) {
+        if (ne > 0) ok = wait_or_abort(&ctl->bar_q_empty, (ne - 1) & 1, ctx, ctl);
+        if (ok) {
+          const int tiles = it.split ? 1 : 2;
+          mbar_arrive_expect_tx(&ctl->bar_q_full, tiles * kChunks * a.TT * a.g * 128);
+          for (int t = 0; t < tiles; ++t)
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c)
+              tma_load_4d(smem + L::kQ + t * L::kTileBytes + c * kChunkBytes, &tmQ, &ctl->bar_q_full, c * 64, 0, h,
+                          w.q.q0 + (2 * w.at.p + t) * a.TT);
+          q_armed = ne + 1;
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      ++ne;
+      // Paged: the table's entries, a lane's of a window of 32 and of the next one, read long before they are needed
+      const int per = kPaged ? (s.page < kBN ? kBN / s.page : 1) : 1;  // pages of a tile
+      const int held = kPaged ? (w.q.m + s.page - 1) / s.page : 0;
+      int base = 0, cur = -1, nxt = -1;
+      auto entry = [&](int e) {
+        const int i = e + lane;
+        return i < held ? s.table[(size_t)w.q.k0 * s.width + i] : -1;
+      };
+      auto first_page = [&](int j) { return s.page < kBN ? j * per : (int)((long long)j * kBN / s.page); };
+      if constexpr (kPaged) {
+        base = first_page(it.j0);
+        cur = entry(base);
+        nxt = entry(base + 32);
+      }
+      for (int j = it.j0; ok && j < it.j1; ++j) {
+        uint32_t words[4] = {~0u, ~0u, ~0u, ~0u};
+        int pages[8];
+        int row = 0, rows = 0, loads = 1;  // paged: first row within the page, rows of a load, loads
+        if constexpr (kPaged) {
+          int e = first_page(j);
+          if (e + per > base + 32) {
+            base += 32;
+            cur = nxt;
+            nxt = entry(base + 32);
+          }
+          row = s.page < kBN ? 0 : (int)((long long)j * kBN % s.page);
+          rows = s.page < kBN ? s.page : kBN;
+          loads = per;
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            pages[x] = -1;
+            if (x < per) {
+              pages[x] = __shfl_sync(0xffffffffu, cur, e + x - base);
+              const bool there = pages[x] >= 0 && pages[x] < s.pages;
+              if (!there) {
+                pages[x] = -1;
+                // keys x * rows .. of the tile have no weight; behind the sequence's end no page is asked for
+                if (e + x < held) {
+                  if (lane == 0) atomicOr(ctx.status, kStatusBadPage);
+                  if (rows >= 32) {
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                      if (32 * y >= x * rows && 32 * y < (x + 1) * rows) words[y] = 0u;
+                  } else {
+                    words[x >> 1] &= x & 1 ? 0x0000ffffu : 0xffff0000u;
+                  }
+                }
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int kind = 0; kind < 2; ++kind, ++n) {  // 0 = K_j, 1 = V_j
+          const int slot = n % R;
+          const uint32_t use = n / R;
+          if (lane == 0 && use > 0) ok = wait_or_abort(&ctl->bar_kv_empty[slot], (use - 1) & 1, ctx, ctl);
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          if (lane == 0) {
+            uint8_t* dst = smem + L::kRingOff + slot * L::kTileBytes;
+            const CUtensorMap* map = kind == 0 ? &tmK : &tmV;
+            if constexpr (kPaged) {
+              if (kind == 1) *reinterpret_cast<uint4*>(ctl->words[slot]) = make_uint4(words[0], words[1], words[2], words[3]);
+              uint32_t bytes = 0;
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                if (x < loads && pages[x] >= 0) bytes += rows * 128 * kChunks;
+              if ((int)n != ctx.drop_load) {
+                if (bytes) mbar_arrive_expect_tx(&ctl->bar_kv_full[slot], bytes);
+                else mbar_arrive(&ctl->bar_kv_full[slot]);
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                  if (x < loads && pages[x] >= 0)
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c)
+                      tma_load_4d(dst + c * kChunkBytes + x * rows * 128, map, &ctl->bar_kv_full[slot], c * 64, h, row,
+                                  pages[x]);
+                kv_armed[slot] = use + 1;
+              }
+            } else if ((int)n != ctx.drop_load) {
+              mbar_arrive_expect_tx(&ctl->bar_kv_full[slot], L::kTileBytes);
+#pragma unroll
+              for (int c = 0; c < kChunks; ++c)
+                tma_load_4d(dst + c * kChunkBytes, map, &ctl->bar_kv_full[slot], c * 64, h, w.q.k0 + j * kBN, 0);
+              kv_armed[slot] = use + 1;
+            }
+          }
+        }
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issuer
+    // The whole warp runs the schedule and computes the descriptors, one elected lane waits and issues.
+    uint32_t el_lane;
+    const bool el = elect_one_sync(&el_lane);
+    bool ok = true;
+    uint32_t base = 0;  // ring counter of the item's first K
+    uint32_t ne = 0;    // items with at least one key tile
+    auto ring_addr = [&](uint32_t n) { return sbase + L::kRingOff + (n % R) * L::kTileBytes; };
+    auto wait_el = [&](uint64_t* bar, uint32_t parity) {
+      bool r = true;
+      if (el) r = wait_or_abort(bar, parity, ctx, ctl);
+      return __shfl_sync(0xffffffffu, r ? 1 : 0, el_lane) != 0;
+    };
+    auto wait_kv = [&](uint32_t n) { return wait_el(&ctl->bar_kv_full[n % R], (n / R) & 1); };
+    auto release = [&](uint32_t n) {
+      if (el) mma_commit(&ctl->bar_kv_empty[n % R]);
+    };
+    auto issue_s = [&](int t, int qt, uint32_t nk) {
+      const uint64_t a0 = sdesc_sw128(sbase + L::kQ + qt * L::kTileBytes, 16, 1024);
+      const uint64_t b0 = sdesc_sw128(ring_addr(nk), 16, 1024);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk >> 2) * kChunkBytes + (kk & 3) * 32;
+        const uint64_t x = desc_add(a0, off), y = desc_add(b0, off);
+        if (el) mma_ss_checked(mg, tmem + (uint32_t)(t * kBN), x, y, kIdescS, kk > 0, kBN);
+      }
+      if (el) mma_commit(&ctl->bar_s_full[t]);
+    };
+    auto issue_pv = [&](int t, uint32_t nv, bool acc) {
+      const uint64_t b0 = sdesc_sw128(ring_addr(nv), kChunkBytes, 1024);
+#pragma unroll
+      for (int kk = 0; kk < kBN / 16; ++kk) {
+        const uint64_t y = desc_add(b0, kk * 2048);
+        if (el)
+          mma_ts_checked(mg, tmem + 256 + (uint32_t)(t * D), tmem + (uint32_t)(t * kBN) + kk * 8, y, kIdescPV,
+                         (acc || kk > 0) ? 1u : 0u, D);
+      }
+      if (el) mma_commit(&ctl->bar_pv_done[t]);
+    };
+    Walk w(from, to, kept);
+    Item it;
+    while (w.next(a, it)) {
+      const int c = it.j1 - it.j0;
+      if (c <= 0) continue;
+      // After a failure anywhere in the CTA this warp stops issuing but still meets the softmax warps at every
+      // named barrier of the schedule.
+      if (ok && *reinterpret_cast<volatile int*>(&ctl->abort)) ok = false;
+      const int stride = it.split ? 2 : 1;
+      auto off = [&](int t, int i) { return (uint32_t)(it.split ? 2 * i + t : i); };  // key tile of slot t's step i
+      if (ok) ok = wait_el(&ctl->bar_q_full, ne & 1);
+      if (ok) ok = wait_kv(base);
+      if (ok) {
+        tc_fence_after();
+        if (it.n[0] > 0) issue_s(0, 0, base);
+        if (it.split) release(base);
+        if (el) mma_issued = true;
+      }
+      if (it.n[1] > 0) {
+        if (ok && it.split) ok = wait_kv(base + 2);
+        if (ok) {
+          tc_fence_after();
+          issue_s(1, it.split ? 0 : 1, base + 2 * off(1, 0));
+          release(base + 2 * off(1, 0));
+        }
+      }
+      const int steps = max(it.n[0], it.n[1]);
+      for (int i = 0; i < steps; ++i) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (i >= it.n[t]) continue;
+          const uint32_t nk = base + 2 * off(t, i), nv = nk + 1, nk1 = nk + 2 * stride;
+          // V has landed, and, where the slots share their keys, so has the next K: the softmax warps waited
+          named_sync(kBarP + t, kBarPCount);
+          if (ok && i == 0 && ne > 0)  // the previous item's epilogue must have read O before the first P V overwrites it
+            ok = wait_el(&ctl->bar_o_free, (ne - 1) & 1);
+          if (ok) {
+            tc_fence_after();
+            issue_pv(t, nv, i > 0);
+            if (it.split || t == 1) release(nv);
+          }
+          if (i + 1 < it.n[t]) {
+            if (ok && it.split) ok = wait_kv(nk1);
+            if (ok) {
+              if (it.split) tc_fence_after();
+              issue_s(t, it.split ? 0 : t, nk1);
+              if (it.split || t == 1) release(nk1);
+            }
+          }
+          __syncwarp();
+        }
+      }
+      // the Q tiles are free once this item's products are done
+      if (ok && el) mma_commit(&ctl->bar_q_empty);
+      __syncwarp();
+      base += 2 * c;
+      ++ne;
+    }
+  } else {
+    // ------------------------------------------------------------ softmax warps
+    const int t = warp >> 2;                 // slot
+    const int row = (warp & 3) * 32 + lane;  // TMEM lane = row of the tile
+    const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t colS = (uint32_t)(t * kBN);
+    const int rt = row / a.g, rh = row - rt * a.g;  // token within the tile and head of the group
+    const bool in_tile = rt < a.TT;
+    bool ok = true;
+    uint32_t base = 0, g[2] = {0, 0}, ne = 0;  // ring counter; steps of the slots; items
+    Walk w(from, to, kept);
+    Item it;
+    while (w.next(a, it)) {
+      const int c = it.j1 - it.j0;
+      const Seq& q = w.q;
+      const int hq = w.at.h * a.g + rh;
+      const int tok = (2 * w.at.p + (it.split ? 0 : t)) * a.TT + rt;  // token within the sequence
+      const bool valid = in_tile && tok < q.n;
+      const int lim = valid ? keys_of(s, q, tok) : 0;
+      const size_t oo = ((size_t)(q.q0 + (valid ? tok : 0)) * s.Hq + hq) * D;
+      const size_t lo = (size_t)hq * s.T + q.q0 + (valid ? tok : 0);
+      const bool mine = valid && !(it.split && t == 1);  // this thread writes the row
+      const bool store = mine && guard_store(ctx, oo, D, o_extent) && guard_store(ctx, lo, 1, lse_extent);
+      if (c <= 0) {  // no key: O = 0 and LSE = -inf, without products or barriers
+        if (store) {
+#pragma unroll
+          for (int x = 0; x < D / 8; ++x)
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(s.out) + oo + 8 * x) = make_uint4(0u, 0u, 0u, 0u);
+          s.lse[lo] = -INFINITY;
+        }
+        continue;
+      }
+      const int nt = it.n[t];
+      const bool busy = __any_sync(0xffffffffu, valid);  // warps without a row only keep the barriers
+      float mu = -INFINITY;  // log2-domain offset in use (scaled maximum, possibly stale by < 2^8)
+      float l_run = 0.f;
+      for (int i = 0; i < nt; ++i) {
+        const uint32_t o = it.split ? 2 * i + t : i;
+        const int j = it.j0 + (int)o;
+        const uint32_t nv = base + 2 * o + 1, nk1 = nv + 1;
+        if (ok) {
+          bool okw = wait_or_abort(&ctl->bar_kv_full[nv % R], (nv / R) & 1, ctx, ctl);
+          if (okw && !it.split && i + 1 < nt)
+            okw = wait_or_abort(&ctl->bar_kv_full[nk1 % R], (nk1 / R) & 1, ctx, ctl);
+          if (okw) okw = wait_or_abort(&ctl->bar_s_full[t], (g[t] + i) & 1, ctx, ctl);
+          ok = __all_sync(0xffffffffu, okw);
+        }
+        if (!ok) {
+          // after a failure: keep meeting the issuer at every step; a rendezvous, so this warp never runs ahead of it
+          named_sync(kBarP + t, kBarPCount);
+          continue;
+        }
+        tc_fence_after();
+        uint4 words = make_uint4(~0u, ~0u, ~0u, ~0u);
+        if constexpr (kPaged) words = *reinterpret_cast<const uint4*>(ctl->words[nv % R]);
+        const bool whole = !kPaged || (words.x & words.y & words.z & words.w) == ~0u;
+        const bool edge = (j + 1) * kBN > it.lo;
+        // V's rows that P must not meet (this slot's product of this V comes first)
+        if ((edge || !whole) && (it.split || t == 0 || i >= it.n[0])) {
+          const int key = j * kBN + row;
+          const uint32_t mw = row < 64 ? (row < 32 ? words.x : words.y) : (row < 96 ? words.z : words.w);
+          uint8_t* v = smem + L::kRingOff + (nv % R) * L::kTileBytes + row * 128;
+          if (key >= it.hi || !((mw >> lane) & 1u)) {
+#pragma unroll
+            for (int x = 0; x < kChunks * 8; ++x)
+              *reinterpret_cast<uint4*>(v + (x >> 3) * kChunkBytes + (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          } else if (key >= it.lo) {
+            bool bad = false;
+#pragma unroll
+            for (int x = 0; x < kChunks * 8; ++x) {
+              uint4* p = reinterpret_cast<uint4*>(v + (x >> 3) * kChunkBytes + (x & 7) * 16);
+              const uint4 y = *p;
+              if (not_finite<kHalf>(y.x) || not_finite<kHalf>(y.y) || not_finite<kHalf>(y.z) || not_finite<kHalf>(y.w)) {
+                bad = true;
+                *p = make_uint4(finite_part<kHalf>(y.x), finite_part<kHalf>(y.y), finite_part<kHalf>(y.z),
+                                finite_part<kHalf>(y.w));
+              }
+            }
+            if (bad) *reinterpret_cast<volatile uint32_t*>(&ctl->dirty) = ne + 1;
+          }
+          fence_proxy_async_smem();
+        }
+        if (busy) {
+          float x[kBN];
+          tmem_ld32x2(tl + colS, tl + colS + 32, *reinterpret_cast<float(*)[64]>(&x[0]));
+          tmem_ld32x2(tl + colS + 64, tl + colS + 96, *reinterpret_cast<float(*)[64]>(&x[64]));
+          if (edge) {
+            const int left = lim - j * kBN;
+#pragma unroll
+            for (int e = 0; e < kBN; ++e)
+              if (e >= left) x[e] = -INFINITY;
+          }
+          if (!whole) {
+            const uint32_t mw[4] = {words.x, words.y, words.z, words.w};
+#pragma unroll
+            for (int e = 0; e < kBN; ++e)
+              if (!((mw[e >> 5] >> (e & 31)) & 1u)) x[e] = -INFINITY;
+          }
+          float m8[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m8[e] = fmaxf(x[e], x[e + 8]);
+#pragma unroll
+          for (int f = 16; f < kBN; f += 16)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m8[e] = max3(m8[e], x[f + e], x[f + e + 8]);
+          const float mt = fmaxf(max3(m8[0], m8[1], m8[2]), max3(max3(m8[3], m8[4], m8[5]), m8[6], m8[7]));
+          // -inf if the row reads no key of the tile.  The offset stays finite: a score of +inf then gives P = l = +inf,
+          // so LSE = +inf and, times 1/l = 0, a row of NaN; a NaN score, which a maximum passes over, gives P = l = NaN.
+          const float mt2 = fminf(mt * scale_log2, FLT_MAX);
+          float alpha = 1.f;
+          if (mt2 > mu + kRescaleThreshold) {
+            alpha = ex2(mu - mt2);  // 0 when mu = -inf
+            mu = mt2;
+          }
+          const float mu_use = (mu == -INFINITY) ? 0.f : mu;
+          const float2 c2 = make_float2(scale_log2, scale_log2);
+          const float2 nm2 = make_float2(-mu_use, -mu_use);
+          float2 rs2 = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float2 y = fma2(make_float2(x[64 * hh + 2 * e], x[64 * hh + 2 * e + 1]), c2, nm2);
+              const float2 z = make_float2(ex2(y.x), ex2(y.y));
+              rs2 = add2(rs2, z);
+              pk[e] = pack2<kHalf>(z.x, z.y);
+            }
+            tmem_st32_bits(tl + colS + 32 * hh, pk);  // P over the first 64 columns of S
+          }
+          l_run = l_run * alpha + (rs2.x + rs2.y);
+          // P V of the step before, which reads the columns just overwritten and adds to O, is done: it was issued
+          // before S, and the commit behind s_full covers every earlier product
+          if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+            for (int e = 0; e < D / 32; ++e) {
+              float y[32];
+              tmem_ld32(tl + 256 + t * D + 32 * e, y);
+#pragma unroll
+              for (int f = 0; f < 32; ++f) y[f] *= alpha;
+              tmem_st32(tl + 256 + t * D + 32 * e, y);
+            }
+          }
+        }
+        tc_fence_before();
+        named_arrive(kBarP + t, kBarPCount);
+      }
+      if (ok && nt > 0)
+        ok = __all_sync(0xffffffffu, wait_or_abort(&ctl->bar_pv_done[t], (g[t] + nt - 1) & 1, ctx, ctl));
+      const bool join = it.split && it.n[1] > 0;
+      float f0 = 1.f, f1 = 0.f;
+      // slot 1's rows go to the threads of slot 0, which own the same TMEM lanes; the readers of the sums before these
+      // are through, since this item's first P V waited for them
+      if (join && t == 1) {
+        sStat[row] = mu;
+        sStat[128 + row] = l_run;
+      }
+      // a slot without a step waits here too: it must not run ahead, into phases of its barriers that look like others
+      if (join || it.n[0] == 0 || it.n[1] == 0) named_sync(kBarL, 256);
+      if (join) {
+        if (t == 0) {
+          if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(&ctl->bar_pv_done[1], (g[1] + it.n[1] - 1) & 1, ctx, ctl));
+          const float mu1 = sStat[row], top = fmaxf(mu, mu1);
+          f0 = mu == -INFINITY ? 0.f : ex2(mu - top);
+          f1 = mu1 == -INFINITY ? 0.f : ex2(mu1 - top);
+          // (a row of NaN scores has a sum of NaN beside any offset)
+          l_run = l_run * f0 + sStat[128 + row] * f1;
+          mu = top;
+        }
+      }
+      g[0] += it.n[0];
+      g[1] += it.n[1];
+      base += 2 * c;
+      ++ne;
+      if (!ok) continue;
+      tc_fence_after();
+      if (!(it.split && t == 1) && busy) {
+        const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+        const bool dirty = *reinterpret_cast<volatile uint32_t*>(&ctl->dirty) == ne;
+        const int slot = 2 * cta + (it.j0 > 0 ? 0 : 1);
+        const bool none = nt == 0;  // this tile reads no key of the part
+#pragma unroll 1
+        for (int e = 0; e < D / 32; ++e) {
+          float y[32];
+          if (!none) {
+            tmem_ld32(tl + 256 + t * D + 32 * e, y);
+          } else {
+#pragma unroll
+            for (int f = 0; f < 32; ++f) y[f] = 0.f;
+          }
+          if (join) {
+            float z[32];
+            tmem_ld32(tl + 256 + D + 32 * e, z);
+#pragma unroll
+            for (int f = 0; f < 32; ++f) y[f] = y[f] * f0 + z[f] * f1;
+          }
+          if (dirty && valid) {
+            for (int k = max(it.lo, it.j0 * kBN); k < min(lim, it.j1 * kBN); ++k) {
+              const uint16_t* v = value_row<kPaged>(a, q, w.at.h, k);
+              if (!v) continue;
+#pragma unroll
+              for (int f = 0; f < 32; ++f) {
+                const float z = load16(v, 32 * e + f, kHalf);
+                if (!isfinite(z)) y[f] += z;
+              }
+            }
+          }
+          if (it.part) {
+            float* po = part_o<D>(parts, slot) + t * 128 + row;
+            if (valid)
+#pragma unroll
+              for (int f = 0; f < 32; ++f) po[(size_t)(32 * e + f) * parts.rows] = y[f];
+          } else if (store) {
+            uint16_t* orow = static_cast<uint16_t*>(s.out) + oo + 32 * e;
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              uint4 v;
+              v.x = pack2<kHalf>(y[8 * f + 0] * inv, y[8 * f + 1] * inv);
+              v.y = pack2<kHalf>(y[8 * f + 2] * inv, y[8 * f + 3] * inv);
+              v.z = pack2<kHalf>(y[8 * f + 4] * inv, y[8 * f + 5] * inv);
+              v.w = pack2<kHalf>(y[8 * f + 6] * inv, y[8 * f + 7] * inv);
+              *reinterpret_cast<uint4*>(orow + 8 * f) = v;
+            }
+          }
+        }
+        if (it.part) {
+          if (valid) part_stat(parts, slot)[t * 128 + row] = make_float2(mu, l_run);
+        } else if (store) {
+          s.lse[lo] = l_run == 0.f ? -INFINITY : mu * kLn2 + logf(l_run);
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&ctl->bar_o_free);
+    }
+  }
+
+  // ------------------------------------------------------------ teardown
+  // Waits here ignore the abort flag (they must see in-flight work land) but stay bounded.
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp && mma_issued) {
+    mma_commit(&ctl->bar_final);
+    settle(&ctl->bar_final, 0, ctx);
+  }
+  if (warp == kProducerWarp && lane == 0) {
+    if (q_armed) settle(&ctl->bar_q_full, (q_armed - 1) & 1, ctx);
+    for (int i = 0; i < R; ++i)
+      if (kv_armed[i]) settle(&ctl->bar_kv_full[i], (kv_armed[i] - 1) & 1, ctx);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Joins the parts of the items that were cut.  Block (c - 1, x): the item that CTA c's share begins inside of, if no
+// earlier share does, rows 32 x .. 32 x + 31: a lane a row, a warp D / 8 columns.
+template <int D, bool kPaged, bool kHalf>
+__global__ void __launch_bounds__(256) seq_join_kernel(const __grid_constant__ SeqArgs a, const Parts parts, int ctas,
+                                                       DevCtx ctx) {
+  constexpr float kLn2 = 0.6931471805599453f;
+  constexpr int kCols = D / 8;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const uaa_seqs& s = a.s;
+  const int c = blockIdx.x + 1;
+  const Cut me = parts.first[c], prev = parts.first[c - 1];
+  if (me.b >= s.B || me.j == 0 || (same_item(me, prev) && prev.j > 0)) return;
+  const Seq q = load_seq<kPaged>(s, me.b);
+  const int lane = threadIdx.x & 31, r = blockIdx.y * 32 + lane, col = (threadIdx.x >> 5) * kCols;
+  const int t = r >> 7, rt = (r & 127) / a.g, rh = (r & 127) - rt * a.g;
+  const int tok = (2 * me.p + t) * a.TT + rt;
+  const bool valid = rt < a.TT && tok < q.n;
+  if (!__any_sync(0xffffffffu, valid)) return;
+  const int nt = tiles_of(a, q, me.p);
+  float top = -INFINITY, sum = 0.f, acc[kCols];
+#pragma unroll
+  for (int x = 0; x < kCols; ++x) acc[x] = 0.f;
+  // part k: the tail of CTA c - 1's share, then what the shares that begin inside the item have of it
+  auto each = [&](auto&& f) {
+    f(2 * (c - 1) + 1);
+    for (int k = c; k < ctas; ++k) {
+      const Cut x = parts.first[k];
+      if (!same_item(x, me)) break;
+      const int end = k + 1 < ctas && same_item(parts.first[k + 1], me) ? parts.first[k + 1].j : nt;
+      if (end > x.j) f(2 * k);
+    }
+  };
+  const int at = valid ? r : 0;
+  each([&](int k) { top = fmaxf(top, part_stat(parts, k)[at].x); });
+  each([&](int k) {
+    const float2 st = part_stat(parts, k)[at];
+    const float f = st.x == -INFINITY ? 0.f : ex2(st.x - top);
+    sum += st.y * f;
+    const float* o = part_o<D>(parts, k) + (size_t)col * parts.rows + at;
+#pragma unroll
+    for (int x = 0; x < kCols; ++x) acc[x] += o[(size_t)x * parts.rows] * f;
+  });
+  if (!valid) return;
+  const int hq = me.h * a.g + rh;
+  const size_t oo = ((size_t)(q.q0 + tok) * s.Hq + hq) * D + col, lo = (size_t)hq * s.T + q.q0 + tok;
+  if (!guard_store(ctx, oo, kCols, (size_t)s.T * s.Hq * D) || !guard_store(ctx, lo, 1, (size_t)s.Hq * s.T)) return;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint16_t* out = static_cast<uint16_t*>(s.out) + oo;
+#pragma unroll
+  for (int x = 0; x < kCols; x += 8)
+    *reinterpret_cast<uint4*>(out + x) =
+        make_uint4(pack2<kHalf>(acc[x] * inv, acc[x + 1] * inv), pack2<kHalf>(acc[x + 2] * inv, acc[x + 3] * inv),
+                   pack2<kHalf>(acc[x + 4] * inv, acc[x + 5] * inv), pack2<kHalf>(acc[x + 6] * inv, acc[x + 7] * inv));
+  if (col == 0) s.lse[lo] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
+}
+
+// ---------------------------------------------------------------------------
+// Host
+size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+size_t workspace_bytes(int B, int T, int g, int D, Parts* parts = nullptr, void* at = nullptr) {
+  const size_t ctas = device_sms(), rows = part_rows((long long)T * g);
+  const size_t first = round256(ctas * sizeof(Cut)), seqs = round256((B + ctas) * sizeof(Seq));
+  const size_t o = round256(2 * ctas * rows * D * 4);
+  if (parts) {
+    char* p = static_cast<char*>(at);
+    *parts = Parts{reinterpret_cast<Cut*>(p), reinterpret_cast<Seq*>(p + first),
+                   reinterpret_cast<float*>(p + first + seqs), reinterpret_cast<float2*>(p + first + seqs + o), (int)rows};
+  }
+  return first + seqs + o + round256(2 * ctas * rows * 8);
+}
+
+template <int D, bool kPaged, bool kHalf>
+int launch(const char* fn, const SeqArgs& a, const Parts& parts, cudaStream_t stream) {
+  const uaa_seqs& s = a.s;
+  CUtensorMap mq, mk, mv;
+  int st;
+  const int box = kPaged && s.page < kBN ? s.page : kBN;
+  // no key at all: maps of one row over q, which no tile reads
+  const bool keys = kPaged ? s.pages > 0 && s.width > 0 : s.Tk > 0;
+  const void *k = keys ? s.k : s.q, *v = keys ? s.v : s.q;
+  const long long rows = !keys ? 1 : kPaged ? s.page : s.Tk, pages = kPaged && keys ? s.pages : 1;
+  const long long kp = kPaged ? s.k_page : s.k_row, vp = kPaged ? s.v_page : s.v_row;
+  if ((st = encode_map(&mq, fn, s.q, {D, a.g, s.Hk, s.T}, {s.q_head, a.g * s.q_head, s.q_row}, {64, a.g, 1, a.TT})) ||
+      (st = encode_map(&mk, fn, k, {D, s.Hk, rows, pages}, {s.k_head, s.k_row, kp}, {64, 1, box, 1})) ||
+      (st = encode_map(&mv, fn, v, {D, s.Hk, rows, pages}, {s.v_head, s.v_row, vp}, {64, 1, box, 1})))
+    return st;
+  DevCtx ctx;
+  if ((st = get_dev_ctx(&ctx))) return st;
+  auto kern = seq_fwd_kernel<D, kPaged, kHalf>;
+  const int smem = FwdLayout<D>::kSmem, ctas = device_sms();
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return set_error(UAA_ERR_CUDA, "%s: smem attribute: %s", fn, cudaGetErrorString(e));
+  kern<<<ctas, kThreads, smem, stream>>>(mq, mk, mv, a, parts, s.scale * kLog2e, ctx);
+  if ((st = check_launch(fn))) return st;
+  // items of so few key tiles are not cut
+  const long long most = kPaged ? (long long)s.width * s.page : s.Tk;
+  if (most <= (2 * kLeastTiles - 1) * kBN) return UAA_OK;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(ctas - 1), (unsigned)(parts.rows / 32));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, seq_join_kernel<D, kPaged, kHalf>, a, parts, ctas, ctx);
+  if (e != cudaSuccess) return set_error(UAA_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+  return check_launch(fn);
 }
 
 template <bool kPaged>
@@ -78,24 +968,22 @@ int seq_fwd(const char* fn, const uaa_seqs* s, void* workspace, size_t bytes, cu
   if (s->T == 0 || s->B == 0) return UAA_OK;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return set_error(UAA_ERR_INVALID_ARG, "%s: workspace is NULL or not 256-byte aligned", fn);
-  const size_t need = workspace_bytes(s->T, s->Hq / s->Hk, s->D);
-  if (bytes < need) return set_error(UAA_ERR_INVALID_ARG, "%s: workspace has %zu bytes, %zu needed", fn, bytes, need);
-  DevCtx ctx;
-  if ((st = get_dev_ctx(&ctx))) return st;
   const SeqArgs a = seq_args(*s);
-  const long long blocks = ((long long)s->T * s->Hq + 7) / 8;
-  const int grid = (int)(blocks < 152 * 8 ? blocks : 152 * 8);
-  if (s->D == 64) seq_fwd_rows_kernel<64, kPaged><<<grid, 256, 0, stream>>>(a, ctx);
-  else seq_fwd_rows_kernel<128, kPaged><<<grid, 256, 0, stream>>>(a, ctx);
-  return check_launch(fn);
+  Parts parts;
+  const size_t need = workspace_bytes(s->B, s->T, a.g, s->D, &parts, workspace);
+  if (bytes < need) return set_error(UAA_ERR_INVALID_ARG, "%s: workspace has %zu bytes, %zu needed", fn, bytes, need);
+  const bool half = s->dtype == UAA_FP16;
+  auto go = s->D == 64 ? (half ? launch<64, kPaged, true> : launch<64, kPaged, false>)
+                       : (half ? launch<128, kPaged, true> : launch<128, kPaged, false>);
+  return go(fn, a, parts, stream);
 }
 
 }  // namespace
 }  // namespace uaa
 
-extern "C" size_t uaa_attn_seqs_workspace_bytes(int T, int Hq, int Hk, int D) {
-  if (T < 0 || Hk < 1 || Hq < 1 || Hq % Hk || (D != 64 && D != 128)) return 0;
-  return uaa::workspace_bytes(T, Hq / Hk, D);
+extern "C" size_t uaa_attn_seqs_workspace_bytes(int B, int T, int Hq, int Hk, int D) {
+  if (B < 0 || T < 0 || Hk < 1 || Hq < 1 || Hq % Hk || (D != 64 && D != 128)) return 0;
+  return uaa::workspace_bytes(B, T, Hq / Hk, D);
 }
 
 extern "C" int uaa_attn_packed_fwd(const uaa_seqs* args, void* workspace, size_t workspace_bytes, uaa_stream_t stream) {

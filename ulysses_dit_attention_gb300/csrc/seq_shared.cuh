@@ -29,40 +29,39 @@ struct SeqArgs {
   int TT;  // tokens of a tile of 128 rows, a row being one head of one token
 };
 
+__device__ __forceinline__ int held_in(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
+
 // One sequence: its first query token, its queries, its first key token (packed) or table row (paged), its keys.
-// (bad: its table row or its length lies outside the cache.)
-struct Seq {
+struct alignas(16) Seq {
   int q0, n, k0, m;
-  bool bad;
 };
 
-__device__ __forceinline__ int cut(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
-
+// `bad`: its table row or its length lies outside the cache.
 template <bool kPaged>
-__device__ __forceinline__ Seq load_seq(const uaa_seqs& s, int b) {
+__device__ __forceinline__ Seq load_seq(const uaa_seqs& s, int b, bool* bad = nullptr) {
   Seq r;
-  r.q0 = cut(s.starts[b], 0, s.T);
-  r.n = cut(s.starts[b + 1], r.q0, s.T) - r.q0;
+  r.q0 = held_in(s.starts[b], 0, s.T);
+  r.n = held_in(s.starts[b + 1], r.q0, s.T) - r.q0;
   if constexpr (kPaged) {
     r.k0 = s.seqs ? s.seqs[b] : b;
     const bool there = r.k0 >= 0 && r.k0 < s.table_rows;
     r.k0 = there ? r.k0 : 0;
     const int m = there ? s.lens[r.k0] : -1;
     const long long most = (long long)s.width * s.page;
-    r.bad = m < 0 || m > most;
+    if (bad) *bad = m < 0 || m > most;
     r.m = m < 0 ? 0 : (int)min((long long)m, most);
   } else {
     const int* st = s.starts_k ? s.starts_k : s.starts;
-    r.k0 = cut(st[b], 0, s.Tk);
-    r.m = cut(st[b + 1], r.k0, s.Tk) - r.k0;
-    r.bad = false;
+    r.k0 = held_in(st[b], 0, s.Tk);
+    r.m = held_in(st[b + 1], r.k0, s.Tk) - r.k0;
+    if (bad) *bad = false;
   }
   return r;
 }
 
 // Keys that query i of the sequence reads.
 __device__ __forceinline__ int keys_of(const uaa_seqs& s, const Seq& q, int i) {
-  return s.causal ? cut(q.m - q.n + i + 1, 0, q.m) : q.m;
+  return s.causal ? held_in(q.m - q.n + i + 1, 0, q.m) : q.m;
 }
 
 // The sequence that token t belongs to, or -1 behind the last one (binary search; starts must not decrease).
@@ -135,6 +134,14 @@ int check_seqs(const char* fn, const uaa_seqs* s, bool paged, bool bwd = false) 
       return set_error(UAA_ERR_INVALID_ARG, "%s: %d sequences over a table of %d rows", fn, s->B, s->table_rows);
   }
   return UAA_OK;
+}
+
+int device_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) !=
+                                                cudaSuccess || n <= 0)
+    return 148;
+  return n;
 }
 
 SeqArgs seq_args(const uaa_seqs& s) {

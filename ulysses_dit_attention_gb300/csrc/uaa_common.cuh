@@ -91,6 +91,9 @@ SeqDesc seq_plain(int S);
 // Host: P segments of the given lengths in slabs of cap rows; UAA_ERR_* on bad input.
 int seq_sharded(SeqDesc* d, int P, const int* lens, int cap, const char* fn);
 int encode_seq_maps(SegMaps* maps, const void* ptr, const SeqDesc& d, int B, int H, int D, int box_rows);
+// Host: a tensor map of a 16-bit tensor, 128-byte swizzled: four dimensions, the strides of the last three in elements.
+int encode_map(CUtensorMap* map, const char* fn, const void* ptr, const long long (&dims)[4],
+               const long long (&strides)[3], const int (&box)[4]);
 // Host: write zeros to the padding rows [len[p], cap) of every slab of a (nseg*B, cap, H, D) bf16 buffer.
 int zero_pad_rows(void* x, const SeqDesc& d, int B, int H, int D, cudaStream_t stream);
 
@@ -640,6 +643,11 @@ __device__ __forceinline__ uint64_t desc_add(uint64_t d, uint32_t byte_off) {
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn_major, bool b_mn_major) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// The same with bf16 or (half) fp16 operands: formats 1 and 0.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool a_mn_major, bool b_mn_major, bool half) {
+  return idesc_bf16_f32(M, N, a_mn_major, b_mn_major) & ~(half ? (1u << 7) | (1u << 10) : 0u);
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
