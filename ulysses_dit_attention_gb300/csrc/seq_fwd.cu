@@ -17,6 +17,7 @@
 //   warps 0-3  softmax of slot 0, warps 4-7 of slot 1: thread r owns row r (a TMEM
 //              lane); running maximum and sum, O rescaled only when the maximum grew
 //              by more than 2^8; P goes over S as the next product's operand
+//   warps 10, 11  wait, look at V and send the rows out on behalf of slots 0 and 1
 // An item's two tiles take the two slots and read the same keys.  Where the second
 // tile is empty (few new tokens) both slots work on the first one, slot 0 on the even
 // key tiles and slot 1 on the odd ones, and are joined in the epilogue: without that
@@ -25,9 +26,8 @@
 // TMEM: S / P of the slots in columns 0 and 128, O in 256 and 256 + D.
 //
 // Keys outside a row's border get P = 0.  P V multiplies that 0 by what V holds, so in
-// the tiles that the border crosses the warps look at V first: rows that no row of
-// the item reads become zeros, and an infinity or a NaN in a row that only some read
-// becomes a zero that the epilogue adds to those rows again.
+// the tiles that the border crosses the relay warps look at V first: an infinity or a
+// NaN there becomes a zero, and the epilogue adds it to the rows that do read it.
 #include <float.h>
 
 #include "seq_shared.cuh"
@@ -37,12 +37,18 @@ namespace {
 
 constexpr int kBN = 128;                // keys of a tile
 constexpr int kChunkBytes = 128 * 128;  // 128 rows x 128 bytes: 64 columns of a tile, 128-byte swizzled
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;
+constexpr int kRelayWarp = 10;  // + slot
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-// Named barriers: kBarP + t, "P of slot t is in TMEM" (its warps arrive, the issuer syncs); kBarL, the slots' sums.
-constexpr uint32_t kBarP = 1, kBarPCount = 128 + 32, kBarL = 3;
+// Named barriers.  kBarP + t, "P of slot t is in TMEM, and the next K has landed": its softmax warps and its relay warp
+// arrive, the issuer syncs.  Between the softmax warps and the relay warp of a slot: kBarF + t, "S is complete and V has
+// landed", behind the last step "O is complete"; kBarI + t, the next item; kBarOut + t, the rows lie in shared memory.
+// kBarL, the slots' sums.
+constexpr uint32_t kBarP = 1, kBarPCount = 128 + 32 + 32;
+constexpr uint32_t kBarF = 3, kBarI = 5, kBarOut = 7, kBarRelay = 128 + 32;
+constexpr uint32_t kBarL = 9;
 // Weight of an item beside its keys (its filling and draining), the least share of a CTA, and the least tiles of a part.
 constexpr int kItemWork = 256, kLeastShare = 512, kLeastTiles = 2;
 
@@ -57,7 +63,8 @@ struct FwdLayout {
   static constexpr int kCtl = kRingOff + kRing * kTileBytes;
   static constexpr int kStat = kCtl + 512;  // maximum and sum of slot 1's rows
   static constexpr int kKept = kStat + 2 * 128 * 4;  // the share's sequences
-  static constexpr int kSmem = kKept + kKeptSeqs * 16;
+  static constexpr int kJobs = kKept + kKeptSeqs * 16;  // two a slot
+  static constexpr int kSmem = kJobs + 4 * 64;
   static_assert(kSmem <= 232448, "shared memory exceeds the per-CTA limit");
 };
 
@@ -89,6 +96,16 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// 4-D tiled tensor store from shared memory (bulk-group completion).
+__device__ __forceinline__ void tma_store_4d(const void* smem_src, const CUtensorMap* map, int c0, int c1, int c2,
+                                             int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(smem_u32(smem_src)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
 template <bool kHalf>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   if constexpr (kHalf) {
@@ -106,6 +123,12 @@ __device__ __forceinline__ bool not_finite(uint32_t w) {
   return (w & e) == e || (w >> 16 & e) == e;
 }
 template <bool kHalf>
+__device__ __forceinline__ uint32_t times0_plus(uint32_t w, uint32_t c) {
+  if constexpr (kHalf) asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(c) : "r"(w), "r"(0u));
+  else asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(c) : "r"(w), "r"(0u));
+  return c;
+}
+template <bool kHalf>
 __device__ __forceinline__ uint32_t finite_part(uint32_t w) {
   constexpr uint32_t e = kHalf ? 0x7c00u : 0x7f80u;
   return ((w & e) == e ? 0u : w & 0xffffu) | ((w >> 16 & e) == e ? 0u : w & 0xffff0000u);
@@ -115,35 +138,58 @@ __device__ __forceinline__ uint32_t finite_part(uint32_t w) {
 // The row of items
 __device__ __forceinline__ int pairs_of(const SeqArgs& a, int n) { return (n + 2 * a.TT - 1) / (2 * a.TT); }
 
-// Weight of the first p pairs of a sequence and key head; the last pair counts as if it were full.
-__device__ __forceinline__ long long weight(const SeqArgs& a, const Seq& q, int p) {
-  const long long P = p, W = 2 * a.TT;
-  if (!a.s.causal) return P * (kItemWork + q.m);
-  const long long off = q.m - q.n, none = off < 0 ? -off / W : 0;  // pairs that read no key
-  const long long x = P > none ? (P - none) * off + W * (P * (P + 1) - none * (none + 1)) / 2 : 0;
-  return P * kItemWork + x;
-}
+// Weights: a pair weighs kItemWork and the keys that its last query reads (the last pair as if it were full).  Of a
+// causal sequence with m keys for n queries the first `none` pairs read no key; pair none + i reads base + W (i + 1).
+struct Weigh {
+  int none;
+  long long flat, slope;  // weight of the first p pairs: kItemWork none + (P = p - none) flat + slope P (P + 1) / 2
+  __device__ __forceinline__ Weigh(const SeqArgs& a, const Seq& q) {
+    const int W = 2 * a.TT, off = q.m - q.n;
+    none = a.s.causal && off < 0 ? -off / W : 0;
+    flat = kItemWork + (a.s.causal ? (long long)off + (long long)none * W : q.m);
+    slope = a.s.causal ? W : 0;
+  }
+  __device__ __forceinline__ long long of(int p) const {
+    const long long P = p - none;
+    return P <= 0 ? (long long)kItemWork * p : (long long)kItemWork * none + P * flat + slope * (P * (P + 1) / 2);
+  }
+  // the last p < np with of(p) <= w: a guess in 32 bits, put right
+  __device__ __forceinline__ int at(long long w, int np) const {
+    const float x = (float)(w - (long long)kItemWork * none);
+    float g = x <= 0.f ? (float)w / kItemWork : none + x / (float)flat;
+    if (x > 0.f && slope) {
+      const float h = 0.5f * (float)slope, f = (float)flat + h;
+      g = none + 2.f * x / (f + sqrtf(f * f + 4.f * h * x));
+    }
+    int p = held_in((int)g, 0, np - 1);
+    while (p > 0 && of(p) > w) --p;
+    while (p + 1 < np && of(p + 1) <= w) ++p;
+    return p;
+  }
+};
 
 __device__ __forceinline__ int tiles_of(const SeqArgs& a, const Seq& q, int p) {
   return (keys_of(a.s, q, min(q.n, 2 * (p + 1) * a.TT) - 1) + kBN - 1) / kBN;
 }
 
-// The place at weight w of sequence b.
-__device__ Cut cut_at(const SeqArgs& a, const Seq& q, int b, long long w) {
+struct Found {  // weight w of sequence b
+  Seq q;
+  long long w;
+  int b;
+};
+// The place at weight w of sequence b.  (One copy of the code: a share's end has to be the next one's beginning.)
+__device__ __noinline__ Cut cut_at(const SeqArgs& a, const Seq& q, int b, long long w) {
   const int np = pairs_of(a, q.n);
-  const long long head = weight(a, q, np);
-  Cut c{b, (int)(w / head), 0, 0};
+  const Weigh weigh(a, q);
+  const long long head = weigh.of(np);
+  Cut c{b, min((int)((float)w / (float)head), a.s.Hk - 1), 0, 0};
+  while (c.h > 0 && c.h * head > w) --c.h;
+  while ((c.h + 1) * head <= w) ++c.h;
   w -= c.h * head;
-  int lo = 0, hi = np - 1;  // the last p with weight(p) <= w
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (weight(a, q, mid) <= w) lo = mid;
-    else hi = mid - 1;
-  }
-  c.p = lo;
-  const long long first = weight(a, q, lo), all = weight(a, q, lo + 1) - first;
-  const int nt = tiles_of(a, q, lo);
-  c.j = (int)(((w - first) * nt + all / 2) / all);
+  c.p = weigh.at(w, np);
+  const long long first = weigh.of(c.p);
+  const int nt = tiles_of(a, q, c.p);
+  c.j = min((int)((float)(w - first) / (float)(weigh.of(c.p + 1) - first) * nt + 0.5f), nt);
   if (c.j < kLeastTiles) {
     c.j = 0;
   } else if (nt - c.j < kLeastTiles) {
@@ -168,6 +214,11 @@ struct Item {
   int n[2];      // key tiles of the slots
   int lo, hi;    // keys that the first row reads, and the last one
 };
+// The key tile whose K slot slot 0 takes its rows out through: every S that reads it comes before slot 0's last P V (before
+// slot 1's, where slot 0 works on the same tile or on none, and waits for slot 1).
+__device__ __forceinline__ int stage_k(const Item& it) {
+  return (it.split || it.n[0] == 0 ? it.j1 - it.j0 : it.n[0]) - 1;
+}
 struct Walk {
   Cut at, end;
   const Seq* kept;  // of sequence `base` and the next ones
@@ -223,6 +274,19 @@ struct Walk {
   }
 };
 
+// What the softmax warps of a slot have to know of an item.
+enum { kSplit = 1, kPart = 2, kJoin = 4, kFull = 8 };  // kFull: every token of the slot's tile is there
+struct alignas(16) Job {
+  int c, n;  // key tiles of the part (-1: no more items) and of the slot
+  int j0, lo, hi, flags;
+  uint32_t base;   // ring counter of the first K
+  uint32_t stage;  // ring slot for the way out
+  Seq q;
+  int tok0, h;  // first token of the tile within the sequence, key head
+  uint32_t ne;
+};
+static_assert(sizeof(Job) == 64, "jobs");
+
 // ---------------------------------------------------------------------------
 // The workspace: the CTAs' first places, then 2 parts a CTA: O (D, rows) and (maximum, sum) of every row.
 struct Parts {
@@ -255,7 +319,8 @@ __device__ __forceinline__ const uint16_t* value_row(const SeqArgs& a, const Seq
 template <int D, bool kPaged, bool kHalf>
 __global__ void __launch_bounds__(kThreads, 1)
     seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ SeqArgs a, const Parts parts,
+                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                   const __grid_constant__ SeqArgs a, const Parts parts,
                    float scale_log2, DevCtx ctx) {
   using L = FwdLayout<D>;
   constexpr int kChunks = D / 64;
@@ -267,6 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   FwdCtl* ctl = reinterpret_cast<FwdCtl*>(smem + L::kCtl);
   float* sStat = reinterpret_cast<float*>(smem + L::kStat);
+  Job* jobs = reinterpret_cast<Job*>(smem + L::kJobs);
   const uint32_t sbase = smem_u32(smem);
   if (sbase & 1023u) {
     // the swizzled operand tiles need 1024-byte alignment; never expected to trigger
@@ -311,6 +377,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // This CTA's share: the sequences' weights, added up by all threads, 320 sequences at a time
   {
     long long* sums = reinterpret_cast<long long*>(sStat);  // a partial sum a warp
+    Found* found = reinterpret_cast<Found*>(sStat + 64);
+    if (threadIdx.x == 0) found[0].b = found[1].b = -1;
     auto scan = [&](long long x, long long& all) {         // sum of the threads before this one; `all`: of all
       long long run = x;
 #pragma unroll
@@ -335,30 +403,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool bad;
       q = load_seq<kPaged>(s, b, &bad);
       if (bad && cta == 0) atomicOr(ctx.status, kStatusBadPage);
-      return q.n > 0 ? s.Hk * weight(a, q, pairs_of(a, q.n)) : 0LL;
+      return q.n > 0 ? s.Hk * Weigh(a, q).of(pairs_of(a, q.n)) : 0LL;
     };
-    long long total = 0, all;
-    long long w = 0;
-    for (int b0 = 0; b0 < s.B; b0 += kThreads) {
-      w = of(b0 + threadIdx.x, q);
-      scan(w, all);
-      total += all;
-    }
-    const long long most = total / kLeastShare;
-    const int shares = most < 1 ? 1 : most < ctas ? (int)most : ctas;
-    if (cta < shares && total > 0) {
-      const long long w0 = total / shares * cta + total % shares * cta / shares;
-      const long long w1 = total / shares * (cta + 1) + total % shares * (cta + 1) / shares;
-      long long done = 0;
+    long long w = 0, w0 = 0, w1 = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {  // the total; then the sequences that the share begins and ends in
+      long long done = 0, all;
+#pragma unroll 1
       for (int b0 = 0; b0 < s.B; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
-        if (s.B > kThreads) w = of(b, q);
+        if (pass == 0 || s.B > kThreads) w = of(b, q);
         const long long at = done + scan(w, all);
-        if (w > 0 && w0 >= at && w0 < at + w) ctl->cut[0] = cut_at(a, q, b, w0 - at);
-        if (w > 0 && w1 >= at && w1 < at + w) ctl->cut[1] = cut_at(a, q, b, w1 - at);
+        if (pass == 1 && w > 0) {
+          if (w0 >= at && w0 < at + w) found[0] = Found{q, w0 - at, b};
+          if (w1 >= at && w1 < at + w) found[1] = Found{q, w1 - at, b};
+        }
         done += all;
       }
+      if (pass == 0) {
+        const long long most = done / kLeastShare;
+        const int shares = most < 1 ? 1 : most < ctas ? (int)most : ctas;
+        if (cta >= shares) break;
+        const long long each = done / shares;
+        const int rest = (int)(done - each * shares);
+        w0 = each * cta + rest * cta / shares;
+        w1 = each * (cta + 1) + rest * (cta + 1) / shares;
+      }
     }
+    __syncthreads();
+    if (lane == 0 && warp < 2 && found[warp].b >= 0) ctl->cut[warp] = cut_at(a, found[warp].q, found[warp].b, found[warp].w);
   }
   tc_fence_before();
   __syncthreads();
@@ -383,6 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     uint32_t n = 0;   // K/V ring counter across items
     uint32_t ne = 0;  // items with at least one key tile
+    const int my_part = lane & 7, my_chunk = lane >> 3;  // paged: this lane's copy of a tile
     Walk w(from, to, kept);
     Item it;
     while (ok && w.next(a, it)) {
@@ -419,10 +493,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int j = it.j0; ok && j < it.j1; ++j) {
         uint32_t words[4] = {~0u, ~0u, ~0u, ~0u};
-        int pages[8];
-        int row = 0, rows = 0, loads = 1;  // paged: first row within the page, rows of a load, loads
+        // paged: first row within the page, rows of a copy, copies of a chunk that are made; this lane's copy
+        int row = 0, rows = 0, there = 0, my_page = -1;
         if constexpr (kPaged) {
-          int e = first_page(j);
+          const int e = first_page(j);
           if (e + per > base + 32) {
             base += 32;
             cur = nxt;
@@ -430,28 +504,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           row = s.page < kBN ? 0 : (int)((long long)j * kBN % s.page);
           rows = s.page < kBN ? s.page : kBN;
-          loads = per;
+          my_page = __shfl_sync(0xffffffffu, cur, (e + my_part - base) & 31);
+          const bool asked = my_part < per && e + my_part < held;  // behind the sequence's end no page is asked for
+          const bool good = asked && my_page >= 0 && my_page < s.pages;
+          if (!good || my_chunk >= kChunks) my_page = -1;
+          there = __popc(__ballot_sync(0xffffffffu, good && my_chunk == 0));
+          const uint32_t gone = __ballot_sync(0xffffffffu, asked && !good && my_chunk == 0);  // bit x: part x
+          if (gone) {  // their keys have no weight
+            if (lane == 0) atomicOr(ctx.status, kStatusBadPage);
+            for (int x = 0; x < per; ++x)
+              if ((gone >> x) & 1u) {
+                if (rows >= 32) {
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            pages[x] = -1;
-            if (x < per) {
-              pages[x] = __shfl_sync(0xffffffffu, cur, e + x - base);
-              const bool there = pages[x] >= 0 && pages[x] < s.pages;
-              if (!there) {
-                pages[x] = -1;
-                // keys x * rows .. of the tile have no weight; behind the sequence's end no page is asked for
-                if (e + x < held) {
-                  if (lane == 0) atomicOr(ctx.status, kStatusBadPage);
-                  if (rows >= 32) {
+                  for (int y = 0; y < 4; ++y)
+                    if (32 * y >= x * rows && 32 * y < (x + 1) * rows) words[y] = 0u;
+                } else {
 #pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                      if (32 * y >= x * rows && 32 * y < (x + 1) * rows) words[y] = 0u;
-                  } else {
-                    words[x >> 1] &= x & 1 ? 0x0000ffffu : 0xffff0000u;
-                  }
+                  for (int y = 0; y < 4; ++y)
+                    if (y == x >> 1) words[y] &= x & 1 ? 0x0000ffffu : 0xffff0000u;
                 }
               }
-            }
           }
         }
 #pragma unroll
@@ -461,34 +533,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0 && use > 0) ok = wait_or_abort(&ctl->bar_kv_empty[slot], (use - 1) & 1, ctx, ctl);
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
-          if (lane == 0) {
-            uint8_t* dst = smem + L::kRingOff + slot * L::kTileBytes;
-            const CUtensorMap* map = kind == 0 ? &tmK : &tmV;
-            if constexpr (kPaged) {
+          uint8_t* dst = smem + L::kRingOff + slot * L::kTileBytes;
+          const CUtensorMap* map = kind == 0 ? &tmK : &tmV;
+          const bool drop = (int)n == ctx.drop_load;
+          if constexpr (kPaged) {
+            if (lane == 0) {
               if (kind == 1) *reinterpret_cast<uint4*>(ctl->words[slot]) = make_uint4(words[0], words[1], words[2], words[3]);
-              uint32_t bytes = 0;
-#pragma unroll
-              for (int x = 0; x < 8; ++x)
-                if (x < loads && pages[x] >= 0) bytes += rows * 128 * kChunks;
-              if ((int)n != ctx.drop_load) {
-                if (bytes) mbar_arrive_expect_tx(&ctl->bar_kv_full[slot], bytes);
+              if (!drop) {
+                if (there) mbar_arrive_expect_tx(&ctl->bar_kv_full[slot], there * rows * 128 * kChunks);
                 else mbar_arrive(&ctl->bar_kv_full[slot]);
-#pragma unroll
-                for (int x = 0; x < 8; ++x)
-                  if (x < loads && pages[x] >= 0)
-#pragma unroll
-                    for (int c = 0; c < kChunks; ++c)
-                      tma_load_4d(dst + c * kChunkBytes + x * rows * 128, map, &ctl->bar_kv_full[slot], c * 64, h, row,
-                                  pages[x]);
-                kv_armed[slot] = use + 1;
               }
-            } else if ((int)n != ctx.drop_load) {
-              mbar_arrive_expect_tx(&ctl->bar_kv_full[slot], L::kTileBytes);
-#pragma unroll
-              for (int c = 0; c < kChunks; ++c)
-                tma_load_4d(dst + c * kChunkBytes, map, &ctl->bar_kv_full[slot], c * 64, h, w.q.k0 + j * kBN, 0);
-              kv_armed[slot] = use + 1;
             }
+            __syncwarp();
+            // a lane a copy
+            if (!drop && my_page >= 0)
+              tma_load_4d(dst + my_chunk * kChunkBytes + my_part * rows * 128, map, &ctl->bar_kv_full[slot], my_chunk * 64,
+                          h, row, my_page);
+            if (!drop) kv_armed[slot] = use + 1;
+          } else if (lane == 0 && !drop) {
+            mbar_arrive_expect_tx(&ctl->bar_kv_full[slot], L::kTileBytes);
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c)
+              tma_load_4d(dst + c * kChunkBytes, map, &ctl->bar_kv_full[slot], c * 64, h, w.q.k0 + j * kBN, 0);
+            kv_armed[slot] = use + 1;
           }
         }
       }
@@ -508,8 +575,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       return __shfl_sync(0xffffffffu, r ? 1 : 0, el_lane) != 0;
     };
     auto wait_kv = [&](uint32_t n) { return wait_el(&ctl->bar_kv_full[n % R], (n / R) & 1); };
+    uint32_t kept_k = 0, kept_v = 0;  // the item's last K and V: their slots are the epilogue's, which releases them
     auto release = [&](uint32_t n) {
-      if (el) mma_commit(&ctl->bar_kv_empty[n % R]);
+      if (el && n != kept_k && n != kept_v) mma_commit(&ctl->bar_kv_empty[n % R]);
     };
     auto issue_s = [&](int t, int qt, uint32_t nk) {
       const uint64_t a0 = sdesc_sw128(sbase + L::kQ + qt * L::kTileBytes, 16, 1024);
@@ -542,12 +610,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       // named barrier of the schedule.
       if (ok && *reinterpret_cast<volatile int*>(&ctl->abort)) ok = false;
       const int stride = it.split ? 2 : 1;
+      kept_k = base + 2 * stage_k(it);
+      kept_v = it.split ? kept_k : base + 2 * c - 1;
+      int left = it.n[0] + it.n[1];  // products S of this item that are still to come; behind the last the Q tiles are free
+      auto last_s = [&] {
+        if (--left == 0 && el) mma_commit(&ctl->bar_q_empty);
+      };
       auto off = [&](int t, int i) { return (uint32_t)(it.split ? 2 * i + t : i); };  // key tile of slot t's step i
       if (ok) ok = wait_el(&ctl->bar_q_full, ne & 1);
       if (ok) ok = wait_kv(base);
       if (ok) {
         tc_fence_after();
-        if (it.n[0] > 0) issue_s(0, 0, base);
+        if (it.n[0] > 0) {
+          issue_s(0, 0, base);
+          last_s();
+        }
         if (it.split) release(base);
         if (el) mma_issued = true;
       }
@@ -556,6 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) {
           tc_fence_after();
           issue_s(1, it.split ? 0 : 1, base + 2 * off(1, 0));
+          last_s();
           release(base + 2 * off(1, 0));
         }
       }
@@ -565,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < 2; ++t) {
           if (i >= it.n[t]) continue;
           const uint32_t nk = base + 2 * off(t, i), nv = nk + 1, nk1 = nk + 2 * stride;
-          // V has landed, and, where the slots share their keys, so has the next K: the softmax warps waited
+          // V has landed, and, where the slots share their keys, so has the next K: the relay warp waited
           named_sync(kBarP + t, kBarPCount);
           if (ok && i == 0 && ne > 0)  // the previous item's epilogue must have read O before the first P V overwrites it
             ok = wait_el(&ctl->bar_o_free, (ne - 1) & 1);
@@ -579,17 +657,162 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok) {
               if (it.split) tc_fence_after();
               issue_s(t, it.split ? 0 : t, nk1);
+              last_s();
               if (it.split || t == 1) release(nk1);
             }
           }
           __syncwarp();
         }
       }
-      // the Q tiles are free once this item's products are done
-      if (ok && el) mma_commit(&ctl->bar_q_empty);
-      __syncwarp();
       base += 2 * c;
       ++ne;
+    }
+  } else if (warp >= kRelayWarp) {
+    // ------------------------------------------------------------ relay warps
+    // All waits for copies and products on behalf of slot t's softmax warps, which wait on named barriers only: a test of
+    // an mbarrier takes 150 to 300 cycles beside the matrix instructions' shared-memory reads, even when it passes, and a
+    // named barrier about 30.  This warp also looks at V where P V could meet what it must not, tells the softmax warps
+    // what the next item is, and sends their rows out.  After a failure it keeps meeting the others.
+    const int t = warp - kRelayWarp;
+    bool ok = true;
+    uint32_t base = 0, g[2] = {0, 0}, ne = 0;  // ring counter; steps of the slots; items with a key tile
+    auto wait = [&](uint64_t* bar, uint32_t phase) {
+      if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bar, phase & 1, ctx, ctl));
+    };
+    Walk w(from, to, kept);
+    Item it{};
+    int par = 0;
+    auto post = [&](bool more) {
+      Job* job = jobs + 2 * t + par;
+      if (lane == 0) {
+        if (!more) {
+          job->c = -1;
+        } else {
+          const int tok0 = (2 * w.at.p + (it.split ? 0 : t)) * a.TT;
+          job->c = max(it.j1 - it.j0, 0);
+          job->n = it.n[t];
+          job->j0 = it.j0;
+          job->lo = it.lo;
+          job->hi = it.hi;
+          job->flags = (it.split ? kSplit : 0) | (it.part ? kPart : 0) | (it.split && it.n[1] > 0 ? kJoin : 0) |
+                       (tok0 + a.TT <= w.q.n ? kFull : 0);
+          job->base = base;
+          job->stage = (t == 0 ? base + 2 * stage_k(it) : base + 2 * (it.j1 - it.j0) - 1) % R;
+          job->tok0 = tok0;
+          job->h = w.at.h;
+          job->q = w.q;
+          job->ne = ne + 1;
+        }
+      }
+      __syncwarp();
+      par ^= 1;
+    };
+    bool more = w.next(a, it);
+    post(more);
+    named_sync(kBarI + t, kBarRelay);
+    while (more) {
+      const int c = it.j1 - it.j0;
+      if (c > 0) {
+        // V of step i: an infinity or a NaN in a row of V that not every row of the item reads becomes a zero, and the
+        // epilogue adds it to the rows that read it (dirty).  Slot 0 does it where the slots share V, since its product comes first.
+        auto look = [&](int i) {
+          const uint32_t o = it.split ? 2 * i + t : i, nv = base + 2 * o + 1;
+          const int j = it.j0 + (int)o;
+          if (!ok || (!it.split && t == 1 && i < it.n[0])) return;
+          uint4 words = make_uint4(~0u, ~0u, ~0u, ~0u);
+          if constexpr (kPaged) words = *reinterpret_cast<const uint4*>(ctl->words[nv % R]);
+          const bool whole = !kPaged || (words.x & words.y & words.z & words.w) == ~0u;
+          if (whole && (j + 1) * kBN <= it.lo) return;
+          bool bad = false;
+#pragma unroll 1
+          for (int wr = whole ? max(0, it.lo - j * kBN) & ~31 : 0; wr < kBN; wr += 32) {
+            uint4* v = reinterpret_cast<uint4*>(smem + L::kRingOff + (nv % R) * L::kTileBytes + wr * 128) + lane;
+            uint4 y[8 * kChunks];
+#pragma unroll
+            for (int x = 0; x < 8 * kChunks; ++x) y[x] = v[(x / 8) * (kChunkBytes / 16) + (x % 8) * 32];
+            uint32_t sum = 0;  // 0 as long as all are finite: an infinity or a NaN times 0 is a NaN
+#pragma unroll
+            for (int x = 0; x < 8 * kChunks; ++x)
+              sum = times0_plus<kHalf>(y[x].x, times0_plus<kHalf>(y[x].y, times0_plus<kHalf>(y[x].z, times0_plus<kHalf>(y[x].w, sum))));
+            if (!__any_sync(0xffffffffu, not_finite<kHalf>(sum))) continue;
+            const uint32_t mw = wr < 64 ? (wr < 32 ? words.x : words.y) : (wr < 96 ? words.z : words.w);
+#pragma unroll 1
+            for (int x = 0; x < 8 * kChunks; ++x) {
+              const int r = 4 * (x % 8) + (lane >> 3), key = j * kBN + wr + r;
+              uint4* p = v + (x / 8) * (kChunkBytes / 16) + (x % 8) * 32;
+              const uint4 z = *p;
+              if (key < it.lo && ((mw >> r) & 1u)) continue;  // every row reads it
+              if (!(not_finite<kHalf>(z.x) || not_finite<kHalf>(z.y) || not_finite<kHalf>(z.z) || not_finite<kHalf>(z.w)))
+                continue;
+              bad = true;
+              *p = make_uint4(finite_part<kHalf>(z.x), finite_part<kHalf>(z.y), finite_part<kHalf>(z.z),
+                              finite_part<kHalf>(z.w));
+            }
+          }
+          if (bad) *reinterpret_cast<volatile uint32_t*>(&ctl->dirty) = ne + 1;
+          fence_proxy_async_smem();
+          __syncwarp();
+        };
+        auto nv_of = [&](int i) { return base + 2 * (uint32_t)(it.split ? 2 * i + t : i) + 1; };
+        int looked = -1;
+        for (int i = 0; i < it.n[t]; ++i) {
+          const uint32_t nv = nv_of(i);
+          if (looked < i) {
+            wait(&ctl->bar_kv_full[nv % R], nv / R);
+            look(i);
+          }
+          wait(&ctl->bar_s_full[t], g[t] + i);
+          named_arrive(kBarF + t, kBarRelay);
+          looked = i;
+          if (i + 1 < it.n[t]) {
+            // the next V while the softmax warps are at work, if it is there; and the next K, where the slots share their
+            // keys (else the issuer waits for it: this V is not to wait for that K)
+            const uint32_t nv1 = nv_of(i + 1);
+            if (ok && __all_sync(0xffffffffu, mbar_test(&ctl->bar_kv_full[nv1 % R], (nv1 / R) & 1))) {
+              look(i + 1);
+              looked = i + 1;
+            }
+            if (!it.split) wait(&ctl->bar_kv_full[(nv + 1) % R], (nv + 1) / R);
+          }
+          // A rendezvous: so the softmax warps, whose next step waits for this warp, cannot come to this barrier again
+          // before the issuer has passed it, whatever failed.
+          named_sync(kBarP + t, kBarPCount);
+        }
+        // O is complete.  A slot without a step waits for the other's: it must not run ahead, into phases of its barriers
+        // that look like others.
+        if (it.n[t] > 0) wait(&ctl->bar_pv_done[t], g[t] + it.n[t] - 1);
+        if (it.n[t] == 0 || (t == 0 && it.split && it.n[1] > 0)) wait(&ctl->bar_pv_done[1 - t], g[1 - t] + it.n[1 - t] - 1);
+        named_arrive(kBarF + t, kBarRelay);
+      }
+      // where this item's rows go, for the copy below
+      const bool out = c > 0 && (t == 0 || !it.split);
+      const uint32_t stage = (t == 0 ? base + 2 * stage_k(it) : base + 2 * c - 1) % R;
+      const int tok0 = (2 * w.at.p + (it.split ? 0 : t)) * a.TT, h = w.at.h, token = w.q.q0 + tok0;
+      const bool full = !it.part && tok0 + a.TT <= w.q.n;
+      if (c > 0) {
+        g[0] += it.n[0];
+        g[1] += it.n[1];
+        base += 2 * c;
+        ++ne;
+      }
+      more = w.next(a, it);
+      post(more);
+      if (out) {
+        named_sync(kBarOut + t, kBarRelay);
+        if (lane == 0 && ok && full && guard_store(ctx, ((size_t)token * s.Hq + h * a.g) * D, D, o_extent)) {
+#pragma unroll
+          for (int x = 0; x < kChunks; ++x)
+            tma_store_4d(smem + L::kRingOff + stage * L::kTileBytes + x * kChunkBytes, &tmO, x * 64, 0, h, token);
+          bulk_commit_group();
+        }
+        __syncwarp();
+      }
+      named_sync(kBarI + t, kBarRelay);
+      if (out && lane == 0) {
+        bulk_wait_read_all();
+        if (ok) mbar_arrive(&ctl->bar_kv_empty[stage]);
+      }
+      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ softmax warps
@@ -599,91 +822,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t colS = (uint32_t)(t * kBN);
     const int rt = row / a.g, rh = row - rt * a.g;  // token within the tile and head of the group
     const bool in_tile = rt < a.TT;
-    bool ok = true;
-    uint32_t base = 0, g[2] = {0, 0}, ne = 0;  // ring counter; steps of the slots; items
-    Walk w(from, to, kept);
-    Item it;
-    while (w.next(a, it)) {
-      const int c = it.j1 - it.j0;
-      const Seq& q = w.q;
-      const int hq = w.at.h * a.g + rh;
-      const int tok = (2 * w.at.p + (it.split ? 0 : t)) * a.TT + rt;  // token within the sequence
-      const bool valid = in_tile && tok < q.n;
-      const int lim = valid ? keys_of(s, q, tok) : 0;
-      const size_t oo = ((size_t)(q.q0 + (valid ? tok : 0)) * s.Hq + hq) * D;
-      const size_t lo = (size_t)hq * s.T + q.q0 + (valid ? tok : 0);
-      const bool mine = valid && !(it.split && t == 1);  // this thread writes the row
-      const bool store = mine && guard_store(ctx, oo, D, o_extent) && guard_store(ctx, lo, 1, lse_extent);
-      if (c <= 0) {  // no key: O = 0 and LSE = -inf, without products or barriers
+    for (int par = 0;; par ^= 1) {
+      named_sync(kBarI + t, kBarRelay);
+      const Job job = jobs[2 * t + par];
+      if (job.c < 0) break;
+      const bool split = job.flags & kSplit, part = job.flags & kPart, join = job.flags & kJoin;
+      const int hq = job.h * a.g + rh, tok = job.tok0 + rt;
+      const bool valid = in_tile && tok < job.q.n;
+      const int lim = valid ? keys_of(s, job.q, tok) : 0;
+      const uint32_t orow = (uint32_t)(job.q.q0 + (valid ? tok : 0)) * s.Hq + hq;  // row of out
+      const size_t lo = (size_t)hq * s.T + job.q.q0 + (valid ? tok : 0);
+      const bool mine = valid && !(split && t == 1);  // this thread writes the row
+      const bool store = mine && guard_store(ctx, (size_t)orow * D, D, o_extent) && guard_store(ctx, lo, 1, lse_extent);
+      if (job.c == 0) {  // no key: O = 0 and LSE = -inf, without products or barriers
         if (store) {
-#pragma unroll
+#pragma unroll 1
           for (int x = 0; x < D / 8; ++x)
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(s.out) + oo + 8 * x) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(s.out) + (size_t)orow * D + 8 * x) = make_uint4(0u, 0u, 0u, 0u);
           s.lse[lo] = -INFINITY;
         }
         continue;
       }
-      const int nt = it.n[t];
+      const int nt = job.n;
       const bool busy = __any_sync(0xffffffffu, valid);  // warps without a row only keep the barriers
       float mu = -INFINITY;  // log2-domain offset in use (scaled maximum, possibly stale by < 2^8)
       float l_run = 0.f;
       for (int i = 0; i < nt; ++i) {
-        const uint32_t o = it.split ? 2 * i + t : i;
-        const int j = it.j0 + (int)o;
-        const uint32_t nv = base + 2 * o + 1, nk1 = nv + 1;
-        if (ok) {
-          bool okw = wait_or_abort(&ctl->bar_kv_full[nv % R], (nv / R) & 1, ctx, ctl);
-          if (okw && !it.split && i + 1 < nt)
-            okw = wait_or_abort(&ctl->bar_kv_full[nk1 % R], (nk1 / R) & 1, ctx, ctl);
-          if (okw) okw = wait_or_abort(&ctl->bar_s_full[t], (g[t] + i) & 1, ctx, ctl);
-          ok = __all_sync(0xffffffffu, okw);
-        }
-        if (!ok) {
-          // after a failure: keep meeting the issuer at every step; a rendezvous, so this warp never runs ahead of it
-          named_sync(kBarP + t, kBarPCount);
-          continue;
-        }
+        const int o = split ? 2 * i + t : i, k0 = (job.j0 + o) * kBN;
+        named_sync(kBarF + t, kBarRelay);  // S is complete and V has landed
         tc_fence_after();
-        uint4 words = make_uint4(~0u, ~0u, ~0u, ~0u);
-        if constexpr (kPaged) words = *reinterpret_cast<const uint4*>(ctl->words[nv % R]);
-        const bool whole = !kPaged || (words.x & words.y & words.z & words.w) == ~0u;
-        const bool edge = (j + 1) * kBN > it.lo;
-        // V's rows that P must not meet (this slot's product of this V comes first)
-        if ((edge || !whole) && (it.split || t == 0 || i >= it.n[0])) {
-          const int key = j * kBN + row;
-          const uint32_t mw = row < 64 ? (row < 32 ? words.x : words.y) : (row < 96 ? words.z : words.w);
-          uint8_t* v = smem + L::kRingOff + (nv % R) * L::kTileBytes + row * 128;
-          if (key >= it.hi || !((mw >> lane) & 1u)) {
-#pragma unroll
-            for (int x = 0; x < kChunks * 8; ++x)
-              *reinterpret_cast<uint4*>(v + (x >> 3) * kChunkBytes + (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-          } else if (key >= it.lo) {
-            bool bad = false;
-#pragma unroll
-            for (int x = 0; x < kChunks * 8; ++x) {
-              uint4* p = reinterpret_cast<uint4*>(v + (x >> 3) * kChunkBytes + (x & 7) * 16);
-              const uint4 y = *p;
-              if (not_finite<kHalf>(y.x) || not_finite<kHalf>(y.y) || not_finite<kHalf>(y.z) || not_finite<kHalf>(y.w)) {
-                bad = true;
-                *p = make_uint4(finite_part<kHalf>(y.x), finite_part<kHalf>(y.y), finite_part<kHalf>(y.z),
-                                finite_part<kHalf>(y.w));
-              }
-            }
-            if (bad) *reinterpret_cast<volatile uint32_t*>(&ctl->dirty) = ne + 1;
-          }
-          fence_proxy_async_smem();
-        }
         if (busy) {
+          uint4 words = make_uint4(~0u, ~0u, ~0u, ~0u);
+          if constexpr (kPaged) words = *reinterpret_cast<const uint4*>(ctl->words[(job.base + 2 * o + 1) % R]);
           float x[kBN];
           tmem_ld32x2(tl + colS, tl + colS + 32, *reinterpret_cast<float(*)[64]>(&x[0]));
           tmem_ld32x2(tl + colS + 64, tl + colS + 96, *reinterpret_cast<float(*)[64]>(&x[64]));
-          if (edge) {
-            const int left = lim - j * kBN;
+          const int left = lim - k0;  // lane 0's row, the warp's first, reads the fewest keys
+          if (__shfl_sync(0xffffffffu, left, 0) < kBN) {
 #pragma unroll
             for (int e = 0; e < kBN; ++e)
               if (e >= left) x[e] = -INFINITY;
           }
-          if (!whole) {
+          if (kPaged && (words.x & words.y & words.z & words.w) != ~0u) {
             const uint32_t mw[4] = {words.x, words.y, words.z, words.w};
 #pragma unroll
             for (int e = 0; e < kBN; ++e)
@@ -738,21 +918,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         named_arrive(kBarP + t, kBarPCount);
       }
-      if (ok && nt > 0)
-        ok = __all_sync(0xffffffffu, wait_or_abort(&ctl->bar_pv_done[t], (g[t] + nt - 1) & 1, ctx, ctl));
-      const bool join = it.split && it.n[1] > 0;
       float f0 = 1.f, f1 = 0.f;
-      // slot 1's rows go to the threads of slot 0, which own the same TMEM lanes; the readers of the sums before these
-      // are through, since this item's first P V waited for them
-      if (join && t == 1) {
-        sStat[row] = mu;
-        sStat[128 + row] = l_run;
-      }
-      // a slot without a step waits here too: it must not run ahead, into phases of its barriers that look like others
-      if (join || it.n[0] == 0 || it.n[1] == 0) named_sync(kBarL, 256);
+      named_sync(kBarF + t, kBarRelay);  // O is complete: this slot's, and for slot 0 of a joined item both
       if (join) {
+        // slot 1's rows go to the threads of slot 0, which own the same TMEM lanes; the readers of the sums before these
+        // are through, since this item's first P V waited for them
+        if (t == 1) {
+          sStat[row] = mu;
+          sStat[128 + row] = l_run;
+        }
+        named_sync(kBarL, 256);
         if (t == 0) {
-          if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(&ctl->bar_pv_done[1], (g[1] + it.n[1] - 1) & 1, ctx, ctl));
           const float mu1 = sStat[row], top = fmaxf(mu, mu1);
           f0 = mu == -INFINITY ? 0.f : ex2(mu - top);
           f1 = mu1 == -INFINITY ? 0.f : ex2(mu1 - top);
@@ -761,23 +937,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           mu = top;
         }
       }
-      g[0] += it.n[0];
-      g[1] += it.n[1];
-      base += 2 * c;
-      ++ne;
-      if (!ok) continue;
       tc_fence_after();
-      if (!(it.split && t == 1) && busy) {
+      if (split && t == 1) {
+        tc_fence_before();
+        mbar_arrive(&ctl->bar_o_free);
+        continue;
+      }
+      // The way out: 16-bit rows in the slot's free ring slot, 16-byte pieces swizzled as a tensor copy takes them.  A
+      // tile of full rows leaves by one; of others this warp stores its 32 rows, D / 8 lanes a row.
+      constexpr int kPieces = D / 8;
+      uint8_t* out_rows = smem + L::kRingOff + job.stage * L::kTileBytes + (warp & 3) * 32 * 128;
+      auto piece = [&](int r, int i) {
+        return reinterpret_cast<uint4*>(out_rows + (i >> 3) * kChunkBytes + r * 128 + ((i ^ r) & 7) * 16);
+      };
+      if (busy) {
         const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
-        const bool dirty = *reinterpret_cast<volatile uint32_t*>(&ctl->dirty) == ne;
-        const int slot = 2 * cta + (it.j0 > 0 ? 0 : 1);
-        const bool none = nt == 0;  // this tile reads no key of the part
+        const bool dirty = *reinterpret_cast<volatile uint32_t*>(&ctl->dirty) == job.ne;
+        const int slot = 2 * cta + (job.j0 > 0 ? 0 : 1);
 #pragma unroll 1
         for (int e = 0; e < D / 32; ++e) {
           float y[32];
-          if (!none) {
-            tmem_ld32(tl + 256 + t * D + 32 * e, y);
-          } else {
+          tmem_ld32(tl + 256 + t * D + 32 * e, y);
+          if (nt == 0) {  // this tile reads no key of the part
 #pragma unroll
             for (int f = 0; f < 32; ++f) y[f] = 0.f;
           }
@@ -788,8 +969,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int f = 0; f < 32; ++f) y[f] = y[f] * f0 + z[f] * f1;
           }
           if (dirty && valid) {
-            for (int k = max(it.lo, it.j0 * kBN); k < min(lim, it.j1 * kBN); ++k) {
-              const uint16_t* v = value_row<kPaged>(a, q, w.at.h, k);
+#pragma unroll 1
+            for (int k = max(job.lo, job.j0 * kBN); k < min(lim, (job.j0 + job.c) * kBN); ++k) {
+              const uint16_t* v = value_row<kPaged>(a, job.q, job.h, k);
               if (!v) continue;
 #pragma unroll
               for (int f = 0; f < 32; ++f) {
@@ -798,32 +980,42 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          if (it.part) {
+          if (part) {
             float* po = part_o<D>(parts, slot) + t * 128 + row;
             if (valid)
 #pragma unroll
               for (int f = 0; f < 32; ++f) po[(size_t)(32 * e + f) * parts.rows] = y[f];
-          } else if (store) {
-            uint16_t* orow = static_cast<uint16_t*>(s.out) + oo + 32 * e;
+          } else {
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
-              uint4 v;
-              v.x = pack2<kHalf>(y[8 * f + 0] * inv, y[8 * f + 1] * inv);
-              v.y = pack2<kHalf>(y[8 * f + 2] * inv, y[8 * f + 3] * inv);
-              v.z = pack2<kHalf>(y[8 * f + 4] * inv, y[8 * f + 5] * inv);
-              v.w = pack2<kHalf>(y[8 * f + 6] * inv, y[8 * f + 7] * inv);
-              *reinterpret_cast<uint4*>(orow + 8 * f) = v;
-            }
+            for (int f = 0; f < 4; ++f)
+              *piece(lane, 4 * e + f) =
+                  make_uint4(pack2<kHalf>(y[8 * f + 0] * inv, y[8 * f + 1] * inv), pack2<kHalf>(y[8 * f + 2] * inv, y[8 * f + 3] * inv),
+                             pack2<kHalf>(y[8 * f + 4] * inv, y[8 * f + 5] * inv), pack2<kHalf>(y[8 * f + 6] * inv, y[8 * f + 7] * inv));
           }
         }
-        if (it.part) {
-          if (valid) part_stat(parts, slot)[t * 128 + row] = make_float2(mu, l_run);
-        } else if (store) {
-          s.lse[lo] = l_run == 0.f ? -INFINITY : mu * kLn2 + logf(l_run);
+        if (!part && !(job.flags & kFull)) {
+          __syncwarp();
+          const int some = __popc(__ballot_sync(0xffffffffu, valid));  // rows of tokens that are there come first
+#pragma unroll 2
+          for (int x = 0; x * (32 / kPieces) < some; ++x) {
+            const int r = x * (32 / kPieces) + lane / kPieces;
+            const bool to = __shfl_sync(0xffffffffu, store ? 1 : 0, r);
+            const uint32_t at = __shfl_sync(0xffffffffu, orow, r);
+            if (to)
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(s.out) + (size_t)at * D + 8 * (lane % kPieces)) =
+                  *piece(r, lane % kPieces);
+          }
         }
       }
+      fence_proxy_async_smem();
+      named_arrive(kBarOut + t, kBarRelay);
       tc_fence_before();
       mbar_arrive(&ctl->bar_o_free);
+      if (part) {
+        if (valid) part_stat(parts, 2 * cta + (job.j0 > 0 ? 0 : 1))[t * 128 + row] = make_float2(mu, l_run);
+      } else if (store) {
+        s.lse[lo] = l_run == 0.f ? -INFINITY : mu * kLn2 + logf(l_run);
+      }
     }
   }
 
@@ -924,7 +1116,7 @@ size_t workspace_bytes(int B, int T, int g, int D, Parts* parts = nullptr, void*
 template <int D, bool kPaged, bool kHalf>
 int launch(const char* fn, const SeqArgs& a, const Parts& parts, cudaStream_t stream) {
   const uaa_seqs& s = a.s;
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, mo;
   int st;
   const int box = kPaged && s.page < kBN ? s.page : kBN;
   // no key at all: maps of one row over q, which no tile reads
@@ -933,6 +1125,7 @@ int launch(const char* fn, const SeqArgs& a, const Parts& parts, cudaStream_t st
   const long long rows = !keys ? 1 : kPaged ? s.page : s.Tk, pages = kPaged && keys ? s.pages : 1;
   const long long kp = kPaged ? s.k_page : s.k_row, vp = kPaged ? s.v_page : s.v_row;
   if ((st = encode_map(&mq, fn, s.q, {D, a.g, s.Hk, s.T}, {s.q_head, a.g * s.q_head, s.q_row}, {64, a.g, 1, a.TT})) ||
+      (st = encode_map(&mo, fn, s.out, {D, a.g, s.Hk, s.T}, {D, a.g * D, (long long)s.Hq * D}, {64, a.g, 1, a.TT})) ||
       (st = encode_map(&mk, fn, k, {D, s.Hk, rows, pages}, {s.k_head, s.k_row, kp}, {64, 1, box, 1})) ||
       (st = encode_map(&mv, fn, v, {D, s.Hk, rows, pages}, {s.v_head, s.v_row, vp}, {64, 1, box, 1})))
     return st;
@@ -942,7 +1135,7 @@ int launch(const char* fn, const SeqArgs& a, const Parts& parts, cudaStream_t st
   const int smem = FwdLayout<D>::kSmem, ctas = device_sms();
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return set_error(UAA_ERR_CUDA, "%s: smem attribute: %s", fn, cudaGetErrorString(e));
-  kern<<<ctas, kThreads, smem, stream>>>(mq, mk, mv, a, parts, s.scale * kLog2e, ctx);
+  kern<<<ctas, kThreads, smem, stream>>>(mq, mk, mv, mo, a, parts, s.scale * kLog2e, ctx);
   if ((st = check_launch(fn))) return st;
   // items of so few key tiles are not cut
   const long long most = kPaged ? (long long)s.width * s.page : s.Tk;

@@ -98,6 +98,8 @@ int check_seqs(const char* fn, const uaa_seqs* s, bool paged, bool bwd = false) 
   if (s->Hq / s->Hk > 128)
     return set_error(UAA_ERR_UNSUPPORTED, "%s: %d query heads a key head (128 at most)", fn, s->Hq / s->Hk);
   if (s->B > 65535 || s->Hq > 65535) return set_error(UAA_ERR_UNSUPPORTED, "%s: B and Hq must be <= 65535", fn);
+  if ((long long)s->T * s->Hq >= (1LL << 32) - 1 || (long long)s->Tk * s->Hk >= (1LL << 32) - 1)
+    return set_error(UAA_ERR_UNSUPPORTED, "%s: 2^32 rows of one head or more", fn);
   if (!(s->scale > 0.f) || !isfinite(s->scale))
     return set_error(UAA_ERR_INVALID_ARG, "%s: scale must be positive and finite", fn);
   if (s->B == 0 || (s->T == 0 && !(bwd && s->Tk > 0))) return UAA_OK;
