@@ -35,7 +35,6 @@
 namespace uaa {
 namespace {
 
-constexpr int kBN = 128;                // keys of a tile
 constexpr int kChunkBytes = 128 * 128;  // 128 rows x 128 bytes: 64 columns of a tile, 128-byte swizzled
 constexpr int kThreads = 384;
 constexpr int kProducerWarp = 8;
@@ -49,11 +48,6 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr uint32_t kBarP = 1, kBarPCount = 128 + 32 + 32;
 constexpr uint32_t kBarF = 3, kBarI = 5, kBarOut = 7, kBarRelay = 128 + 32;
 constexpr uint32_t kBarL = 9;
-// Weight of an item beside its keys (its filling and draining), the least share of a CTA, and the least tiles of a part.
-constexpr int kItemWork = 256, kLeastShare = 512, kLeastTiles = 2;
-
-constexpr int kKeptSeqs = 64;  // sequences of a share that are kept in shared memory (more: in the workspace)
-
 template <int D>
 struct FwdLayout {
   static constexpr int kRing = D == 128 ? 5 : 10;
@@ -68,15 +62,6 @@ struct FwdLayout {
   static_assert(kSmem <= 232448, "shared memory exceeds the per-CTA limit");
 };
 
-// A place in the row of all items' key tiles: tile j of pair p of sequence b, key head h.
-struct Cut {
-  int b, h, p, j;
-};
-__device__ __forceinline__ bool same_item(const Cut& x, const Cut& y) { return x.b == y.b && x.h == y.h && x.p == y.p; }
-__device__ __forceinline__ bool before(const Cut& x, const Cut& y) {  // x's item lies before y's
-  return x.b != y.b ? x.b < y.b : x.h != y.h ? x.h < y.h : x.p < y.p;
-}
-
 struct FwdCtl {
   uint64_t bar_q_full, bar_q_empty;
   uint64_t bar_kv_full[10], bar_kv_empty[10];
@@ -85,7 +70,6 @@ struct FwdCtl {
   uint32_t tmem_base;
   int abort;
   uint32_t dirty;                          // the last item with an infinity or a NaN taken out of V
-  alignas(16) Cut cut[2];                  // this CTA's share
   alignas(16) uint32_t words[10][4];       // paged, per ring slot: keys whose page is there (filled with V)
 };
 static_assert(sizeof(FwdCtl) <= 512, "control block");
@@ -135,144 +119,32 @@ __device__ __forceinline__ uint32_t finite_part(uint32_t w) {
 }
 
 // ---------------------------------------------------------------------------
-// The row of items
-__device__ __forceinline__ int pairs_of(const SeqArgs& a, int n) { return (n + 2 * a.TT - 1) / (2 * a.TT); }
-
-// Weights: a pair weighs kItemWork and the keys that its last query reads (the last pair as if it were full).  Of a
-// causal sequence with m keys for n queries the first `none` pairs read no key; pair none + i reads base + W (i + 1).
-struct Weigh {
-  int none;
-  long long flat, slope;  // weight of the first p pairs: kItemWork none + (P = p - none) flat + slope P (P + 1) / 2
-  __device__ __forceinline__ Weigh(const SeqArgs& a, const Seq& q) {
-    const int W = 2 * a.TT, off = q.m - q.n;
-    none = a.s.causal && off < 0 ? -off / W : 0;
-    flat = kItemWork + (a.s.causal ? (long long)off + (long long)none * W : q.m);
-    slope = a.s.causal ? W : 0;
-  }
-  __device__ __forceinline__ long long of(int p) const {
-    const long long P = p - none;
-    return P <= 0 ? (long long)kItemWork * p : (long long)kItemWork * none + P * flat + slope * (P * (P + 1) / 2);
-  }
-  // the last p < np with of(p) <= w: a guess in 32 bits, put right
-  __device__ __forceinline__ int at(long long w, int np) const {
-    const float x = (float)(w - (long long)kItemWork * none);
-    float g = x <= 0.f ? (float)w / kItemWork : none + x / (float)flat;
-    if (x > 0.f && slope) {
-      const float h = 0.5f * (float)slope, f = (float)flat + h;
-      g = none + 2.f * x / (f + sqrtf(f * f + 4.f * h * x));
-    }
-    int p = held_in((int)g, 0, np - 1);
-    while (p > 0 && of(p) > w) --p;
-    while (p + 1 < np && of(p + 1) <= w) ++p;
-    return p;
-  }
-};
-
-__device__ __forceinline__ int tiles_of(const SeqArgs& a, const Seq& q, int p) {
-  return (keys_of(a.s, q, min(q.n, 2 * (p + 1) * a.TT) - 1) + kBN - 1) / kBN;
-}
-
-struct Found {  // weight w of sequence b
-  Seq q;
-  long long w;
-  int b;
-};
-// The place at weight w of sequence b.  (One copy of the code: a share's end has to be the next one's beginning.)
-__device__ __noinline__ Cut cut_at(const SeqArgs& a, const Seq& q, int b, long long w) {
-  const int np = pairs_of(a, q.n);
-  const Weigh weigh(a, q);
-  const long long head = weigh.of(np);
-  Cut c{b, min((int)((float)w / (float)head), a.s.Hk - 1), 0, 0};
-  while (c.h > 0 && c.h * head > w) --c.h;
-  while ((c.h + 1) * head <= w) ++c.h;
-  w -= c.h * head;
-  c.p = weigh.at(w, np);
-  const long long first = weigh.of(c.p);
-  const int nt = tiles_of(a, q, c.p);
-  c.j = min((int)((float)(w - first) / (float)(weigh.of(c.p + 1) - first) * nt + 0.5f), nt);
-  if (c.j < kLeastTiles) {
-    c.j = 0;
-  } else if (nt - c.j < kLeastTiles) {
-    c.j = 0;
-    if (++c.p == np) {
-      c.p = 0;
-      if (++c.h == a.s.Hk) {
-        c.h = 0;
-        ++c.b;
-      }
-    }
-  }
-  return c;
-}
-
-// Walks the items of a share.  Every role walks it for itself, over the sequences as the CTA found them when it
-// started, so all agree on every item: after a failure, and if someone writes into the lengths meanwhile.
+// Items: pairs of tiles
+using Pairs = QueryRow<2>;
 struct Item {
-  int j0, j1;    // key tiles of this part
-  bool part;     // of an item that was cut
   bool split;    // the second tile is empty: the slots take the key tiles in turn
-  int n[2];      // key tiles of the slots
+  int c, n[2];   // key tiles of the part, and of the slots
   int lo, hi;    // keys that the first row reads, and the last one
 };
+__device__ __forceinline__ Item item_of(const SeqArgs& a, const Walk<Pairs>& w) {
+  Item it;
+  const int TT = a.TT, t0 = 2 * w.at.p * TT;
+  it.hi = keys_of(a.s, w.q, min(w.q.n, t0 + 2 * TT) - 1);
+  it.lo = keys_of(a.s, w.q, t0);
+  it.split = w.q.n <= t0 + TT;
+  it.c = max(w.j1 - w.j0, 0);
+  if (it.split) {
+    it.n[0] = (it.c + 1) / 2;
+    it.n[1] = it.c / 2;
+  } else {
+    it.n[0] = held_in(tiles_in(keys_of(a.s, w.q, t0 + TT - 1), kBN) - w.j0, 0, it.c);
+    it.n[1] = it.c;
+  }
+  return it;
+}
 // The key tile whose K slot slot 0 takes its rows out through: every S that reads it comes before slot 0's last P V (before
 // slot 1's, where slot 0 works on the same tile or on none, and waits for slot 1).
-__device__ __forceinline__ int stage_k(const Item& it) {
-  return (it.split || it.n[0] == 0 ? it.j1 - it.j0 : it.n[0]) - 1;
-}
-struct Walk {
-  Cut at, end;
-  const Seq* kept;  // of sequence `base` and the next ones
-  int base, begin_j;
-  Seq q;
-  int np;
-  bool first;
-  __device__ __forceinline__ Walk(const Cut& from, const Cut& to, const Seq* seqs)
-      : at(from), end(to), kept(seqs), base(from.b), begin_j(from.j), np(-1), first(true) {
-    at.j = 0;
-  }
-  __device__ __forceinline__ bool next(const SeqArgs& a, Item& it) {
-    if (!first) {
-      ++at.p;
-      begin_j = 0;
-    }
-    first = false;
-    while (true) {
-      if (at.b >= a.s.B || at.b > end.b) return false;
-      if (np < 0) {
-        q = kept[at.b - base];
-        np = pairs_of(a, q.n);
-      }
-      if (at.p >= np) {
-        at.p = 0;
-        ++at.h;
-      }
-      if (np > 0 && at.h < a.s.Hk) break;
-      at.h = at.p = 0;
-      ++at.b;
-      np = -1;
-    }
-    const bool last = same_item(at, end);
-    if (!before(at, end) && !(last && end.j > 0)) return false;
-    const int TT = a.TT, t0 = 2 * at.p * TT;
-    it.hi = keys_of(a.s, q, min(q.n, t0 + 2 * TT) - 1);
-    it.lo = keys_of(a.s, q, t0);
-    const int nt = (it.hi + kBN - 1) / kBN;
-    it.j0 = begin_j;
-    it.j1 = last ? end.j : nt;
-    it.part = it.j0 > 0 || it.j1 < nt;
-    it.split = q.n <= t0 + TT;
-    const int c = max(it.j1 - it.j0, 0);
-    if (it.split) {
-      it.n[0] = (c + 1) / 2;
-      it.n[1] = c / 2;
-    } else {
-      const int n0 = (keys_of(a.s, q, t0 + TT - 1) + kBN - 1) / kBN;
-      it.n[0] = min(max(n0 - it.j0, 0), c);
-      it.n[1] = c;
-    }
-    return true;
-  }
-};
+__device__ __forceinline__ int stage_k(const Item& it) { return (it.split || it.n[0] == 0 ? it.c : it.n[0]) - 1; }
 
 // What the softmax warps of a slot have to know of an item.
 enum { kSplit = 1, kPart = 2, kJoin = 4, kFull = 8 };  // kFull: every token of the slot's tile is there
@@ -360,8 +232,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&ctl->bar_final, 1);
     ctl->abort = 0;
     ctl->dirty = 0;
-    ctl->cut[0] = Cut{s.B, 0, 0, 0};
-    ctl->cut[1] = Cut{s.B, 0, 0, 0};
     fence_mbar_init();
   }
   if (warp == kProducerWarp && lane == 0) {
@@ -373,77 +243,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&ctl->tmem_base, 512);
     tmem_relinquish();
   }
-  Seq q{};  // of sequence threadIdx.x, if there are no more than threads
-  // This CTA's share: the sequences' weights, added up by all threads, 320 sequences at a time
-  {
-    long long* sums = reinterpret_cast<long long*>(sStat);  // a partial sum a warp
-    Found* found = reinterpret_cast<Found*>(sStat + 64);
-    if (threadIdx.x == 0) found[0].b = found[1].b = -1;
-    auto scan = [&](long long x, long long& all) {         // sum of the threads before this one; `all`: of all
-      long long run = x;
-#pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const long long y = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += y;
-      }
-      __syncthreads();
-      if (lane == 31) sums[warp] = run;
-      __syncthreads();
-      long long before = 0;
-      all = 0;
-      for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += sums[w];
-        all += sums[w];
-      }
-      return before + run - x;
-    };
-    auto of = [&](int b, Seq& q) {
-      q.n = 0;
-      if (b >= s.B) return 0LL;
-      bool bad;
-      q = load_seq<kPaged>(s, b, &bad);
-      if (bad && cta == 0) atomicOr(ctx.status, kStatusBadPage);
-      return q.n > 0 ? s.Hk * Weigh(a, q).of(pairs_of(a, q.n)) : 0LL;
-    };
-    long long w = 0, w0 = 0, w1 = 0;
-#pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {  // the total; then the sequences that the share begins and ends in
-      long long done = 0, all;
-#pragma unroll 1
-      for (int b0 = 0; b0 < s.B; b0 += kThreads) {
-        const int b = b0 + threadIdx.x;
-        if (pass == 0 || s.B > kThreads) w = of(b, q);
-        const long long at = done + scan(w, all);
-        if (pass == 1 && w > 0) {
-          if (w0 >= at && w0 < at + w) found[0] = Found{q, w0 - at, b};
-          if (w1 >= at && w1 < at + w) found[1] = Found{q, w1 - at, b};
-        }
-        done += all;
-      }
-      if (pass == 0) {
-        const long long most = done / kLeastShare;
-        const int shares = most < 1 ? 1 : most < ctas ? (int)most : ctas;
-        if (cta >= shares) break;
-        const long long each = done / shares;
-        const int rest = (int)(done - each * shares);
-        w0 = each * cta + rest * cta / shares;
-        w1 = each * (cta + 1) + rest * (cta + 1) / shares;
-      }
-    }
-    __syncthreads();
-    if (lane == 0 && warp < 2 && found[warp].b >= 0) ctl->cut[warp] = cut_at(a, found[warp].q, found[warp].b, found[warp].w);
-  }
+  const Share share = find_share<Pairs, kPaged, kThreads>(a, smem + L::kStat, smem + L::kKept, parts.seqs,
+                                                          ctx.status);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const Cut from = ctl->cut[0], to = ctl->cut[1];
-  if (threadIdx.x == 0) parts.first[cta] = from;
-  const int held = min(to.b, s.B - 1) - from.b + 1;  // its sequences (none: from.b = B)
-  Seq* kept = held <= kKeptSeqs ? reinterpret_cast<Seq*>(smem + L::kKept) : parts.seqs + from.b + cta;
-  for (int b = from.b + threadIdx.x; b < from.b + held && s.B > kThreads; b += kThreads)
-    kept[b - from.b] = load_seq<kPaged>(s, b);
-  if (s.B <= kThreads && (int)threadIdx.x >= from.b && (int)threadIdx.x < from.b + held) kept[threadIdx.x - from.b] = q;
-  __syncthreads();
+  if (threadIdx.x == 0) parts.first[cta] = share.from;
   const uint32_t tmem = ctl->tmem_base;
   const MmaGuard mg = mma_guard(ctx, sbase, L::kSmem, tmem, 512);  // debug builds' operand checks
   const size_t o_extent = (size_t)s.T * s.Hq * D, lse_extent = (size_t)s.Hq * s.T;
@@ -457,10 +262,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t n = 0;   // K/V ring counter across items
     uint32_t ne = 0;  // items with at least one key tile
     const int my_part = lane & 7, my_chunk = lane >> 3;  // paged: this lane's copy of a tile
-    Walk w(from, to, kept);
-    Item it;
-    while (ok && w.next(a, it)) {
-      if (it.j1 <= it.j0) continue;
+    Walk<Pairs> w(share);
+    while (ok && w.next(a)) {
+      const Item it = item_of(a, w);
+      if (it.c == 0) continue;
       const int h = w.at.h;
       if (lane == 0) {
         if (ne > 0) ok = wait_or_abort(&ctl->bar_q_empty, (ne - 1) & 1, ctx, ctl);
@@ -487,11 +292,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto first_page = [&](int j) { return s.page < kBN ? j * per : (int)((long long)j * kBN / s.page); };
       if constexpr (kPaged) {
-        base = first_page(it.j0);
+        base = first_page(w.j0);
         cur = entry(base);
         nxt = entry(base + 32);
       }
-      for (int j = it.j0; ok && j < it.j1; ++j) {
+      for (int j = w.j0; ok && j < w.j1; ++j) {
         uint32_t words[4] = {~0u, ~0u, ~0u, ~0u};
         // paged: first row within the page, rows of a copy, copies of a chunk that are made; this lane's copy
         int row = 0, rows = 0, there = 0, my_page = -1;
@@ -601,11 +406,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (el) mma_commit(&ctl->bar_pv_done[t]);
     };
-    Walk w(from, to, kept);
-    Item it;
-    while (w.next(a, it)) {
-      const int c = it.j1 - it.j0;
-      if (c <= 0) continue;
+    Walk<Pairs> w(share);
+    while (w.next(a)) {
+      const Item it = item_of(a, w);
+      const int c = it.c;
+      if (c == 0) continue;
       // After a failure anywhere in the CTA this warp stops issuing but still meets the softmax warps at every
       // named barrier of the schedule.
       if (ok && *reinterpret_cast<volatile int*>(&ctl->abort)) ok = false;
@@ -679,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait = [&](uint64_t* bar, uint32_t phase) {
       if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bar, phase & 1, ctx, ctl));
     };
-    Walk w(from, to, kept);
+    Walk<Pairs> w(share);
     Item it{};
     int par = 0;
     auto post = [&](bool more) {
@@ -689,15 +494,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           job->c = -1;
         } else {
           const int tok0 = (2 * w.at.p + (it.split ? 0 : t)) * a.TT;
-          job->c = max(it.j1 - it.j0, 0);
+          job->c = it.c;
           job->n = it.n[t];
-          job->j0 = it.j0;
+          job->j0 = w.j0;
           job->lo = it.lo;
           job->hi = it.hi;
-          job->flags = (it.split ? kSplit : 0) | (it.part ? kPart : 0) | (it.split && it.n[1] > 0 ? kJoin : 0) |
+          job->flags = (it.split ? kSplit : 0) | (w.part ? kPart : 0) | (it.split && it.n[1] > 0 ? kJoin : 0) |
                        (tok0 + a.TT <= w.q.n ? kFull : 0);
           job->base = base;
-          job->stage = (t == 0 ? base + 2 * stage_k(it) : base + 2 * (it.j1 - it.j0) - 1) % R;
+          job->stage = (t == 0 ? base + 2 * stage_k(it) : base + 2 * it.c - 1) % R;
           job->tok0 = tok0;
           job->h = w.at.h;
           job->q = w.q;
@@ -707,17 +512,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       par ^= 1;
     };
-    bool more = w.next(a, it);
+    bool more = w.next(a);
+    if (more) it = item_of(a, w);
     post(more);
     named_sync(kBarI + t, kBarRelay);
     while (more) {
-      const int c = it.j1 - it.j0;
+      const int c = it.c;
       if (c > 0) {
         // V of step i: an infinity or a NaN in a row of V that not every row of the item reads becomes a zero, and the
         // epilogue adds it to the rows that read it (dirty).  Slot 0 does it where the slots share V, since its product comes first.
         auto look = [&](int i) {
           const uint32_t o = it.split ? 2 * i + t : i, nv = base + 2 * o + 1;
-          const int j = it.j0 + (int)o;
+          const int j = w.j0 + (int)o;
           if (!ok || (!it.split && t == 1 && i < it.n[0])) return;
           uint4 words = make_uint4(~0u, ~0u, ~0u, ~0u);
           if constexpr (kPaged) words = *reinterpret_cast<const uint4*>(ctl->words[nv % R]);
@@ -788,14 +594,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool out = c > 0 && (t == 0 || !it.split);
       const uint32_t stage = (t == 0 ? base + 2 * stage_k(it) : base + 2 * c - 1) % R;
       const int tok0 = (2 * w.at.p + (it.split ? 0 : t)) * a.TT, h = w.at.h, token = w.q.q0 + tok0;
-      const bool full = !it.part && tok0 + a.TT <= w.q.n;
+      const bool full = !w.part && tok0 + a.TT <= w.q.n;
       if (c > 0) {
         g[0] += it.n[0];
         g[1] += it.n[1];
         base += 2 * c;
         ++ne;
       }
-      more = w.next(a, it);
+      more = w.next(a);
+      if (more) it = item_of(a, w);
       post(more);
       if (out) {
         named_sync(kBarOut + t, kBarRelay);
@@ -953,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (busy) {
         const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
         const bool dirty = *reinterpret_cast<volatile uint32_t*>(&ctl->dirty) == job.ne;
-        const int slot = 2 * cta + (job.j0 > 0 ? 0 : 1);
+        const int slot = part_of(cta, job.j0);
 #pragma unroll 1
         for (int e = 0; e < D / 32; ++e) {
           float y[32];
@@ -1012,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       mbar_arrive(&ctl->bar_o_free);
       if (part) {
-        if (valid) part_stat(parts, 2 * cta + (job.j0 > 0 ? 0 : 1))[t * 128 + row] = make_float2(mu, l_run);
+        if (valid) part_stat(parts, part_of(cta, job.j0))[t * 128 + row] = make_float2(mu, l_run);
       } else if (store) {
         s.lse[lo] = l_run == 0.f ? -INFINITY : mu * kLn2 + logf(l_run);
       }
@@ -1051,31 +858,21 @@ __global__ void __launch_bounds__(256) seq_join_kernel(const __grid_constant__ S
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const uaa_seqs& s = a.s;
   const int c = blockIdx.x + 1;
-  const Cut me = parts.first[c], prev = parts.first[c - 1];
-  if (me.b >= s.B || me.j == 0 || (same_item(me, prev) && prev.j > 0)) return;
+  if (!leads(parts.first, c, s.B)) return;
+  const Cut me = parts.first[c];
   const Seq q = load_seq<kPaged>(s, me.b);
   const int lane = threadIdx.x & 31, r = blockIdx.y * 32 + lane, col = (threadIdx.x >> 5) * kCols;
   const int t = r >> 7, rt = (r & 127) / a.g, rh = (r & 127) - rt * a.g;
   const int tok = (2 * me.p + t) * a.TT + rt;
   const bool valid = rt < a.TT && tok < q.n;
   if (!__any_sync(0xffffffffu, valid)) return;
-  const int nt = tiles_of(a, q, me.p);
+  const int nt = Pairs::inner(a, q, me.p);
   float top = -INFINITY, sum = 0.f, acc[kCols];
 #pragma unroll
   for (int x = 0; x < kCols; ++x) acc[x] = 0.f;
-  // part k: the tail of CTA c - 1's share, then what the shares that begin inside the item have of it
-  auto each = [&](auto&& f) {
-    f(2 * (c - 1) + 1);
-    for (int k = c; k < ctas; ++k) {
-      const Cut x = parts.first[k];
-      if (!same_item(x, me)) break;
-      const int end = k + 1 < ctas && same_item(parts.first[k + 1], me) ? parts.first[k + 1].j : nt;
-      if (end > x.j) f(2 * k);
-    }
-  };
   const int at = valid ? r : 0;
-  each([&](int k) { top = fmaxf(top, part_stat(parts, k)[at].x); });
-  each([&](int k) {
+  each_part(parts.first, c, ctas, nt, [&](int k) { top = fmaxf(top, part_stat(parts, k)[at].x); });
+  each_part(parts.first, c, ctas, nt, [&](int k) {
     const float2 st = part_stat(parts, k)[at];
     const float f = st.x == -INFINITY ? 0.f : ex2(st.x - top);
     sum += st.y * f;

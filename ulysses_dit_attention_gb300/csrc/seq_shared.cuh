@@ -83,6 +83,273 @@ __device__ __forceinline__ void store16(void* p, size_t at, float x, int fp16) {
   else static_cast<__nv_bfloat16*>(p)[at] = __float2bfloat16_rn(x);
 }
 
+// ---------------------------------------------------------------------------
+// A row of items and its shares.  Each kernel works on tiles (of queries or of keys) of every sequence and key head, and
+// an item's inner loop runs over tiles of the other kind; the items of all sequences stand in a row, (sequence, head,
+// tile), weighed by the tokens that the inner loop meets plus kItemWork, and the row is cut into equal shares, one a CTA,
+// in the middle of an item where it falls so.  A kind of row says how many tiles a sequence has, how many inner tiles a
+// tile has and what the first p tiles weigh.
+constexpr int kBN = 128;  // keys of a tile
+// Weight of an item beside its tokens (its filling and draining), the least share of a CTA, and the least inner tiles of
+// a part.
+constexpr int kItemWork = 256, kLeastShare = 512, kLeastTiles = 2;
+
+__device__ __forceinline__ int tiles_in(int x, int per) { return (x + per - 1) / per; }
+
+// Tiles of W query tokens, inner tiles of keys: tile p's last query reads the most keys (the last tile weighs as if it
+// were full).  Of a causal sequence with fewer keys than queries the first `none` tiles read no key.
+template <int kTilesOf2>  // tiles of 128 rows: 1 or 2 (a pair)
+struct QueryRow {
+  static __device__ __forceinline__ int width(const SeqArgs& a) { return kTilesOf2 * a.TT; }
+  static __device__ __forceinline__ int tiles(const SeqArgs& a, const Seq& q) { return tiles_in(q.n, width(a)); }
+  static __device__ __forceinline__ int inner(const SeqArgs& a, const Seq& q, int p) {
+    return tiles_in(keys_of(a.s, q, min(q.n, (p + 1) * width(a)) - 1), kBN);
+  }
+  int none;
+  long long flat, slope;  // kItemWork none + (P = p - none) flat + slope P (P + 1) / 2
+  __device__ __forceinline__ QueryRow(const SeqArgs& a, const Seq& q) {
+    const int W = width(a), off = q.m - q.n;
+    none = a.s.causal && off < 0 ? -off / W : 0;
+    flat = kItemWork + (a.s.causal ? (long long)off + (long long)none * W : q.m);
+    slope = a.s.causal ? W : 0;
+  }
+  __device__ __forceinline__ long long of(int p) const {
+    const long long P = p - none;
+    return P <= 0 ? (long long)kItemWork * p : (long long)kItemWork * none + P * flat + slope * (P * (P + 1) / 2);
+  }
+  __device__ __forceinline__ int guess(long long w) const {
+    const float x = (float)(w - (long long)kItemWork * none);
+    if (x <= 0.f) return (int)((float)w / kItemWork);
+    if (!slope) return (int)(none + x / (float)flat);
+    const float h = 0.5f * (float)slope, f = (float)flat + h;
+    return (int)(none + 2.f * x / (f + sqrtf(f * f + 4.f * h * x)));
+  }
+};
+
+// Tiles of 128 keys, inner tiles of TT query tokens: min(n, m - 128 p) queries read keys of tile p.
+struct KeyRow {
+  static __device__ __forceinline__ int tiles(const SeqArgs&, const Seq& q) { return tiles_in(q.m, kBN); }
+  static __device__ __forceinline__ int first(const SeqArgs& a, const Seq& q, int p) {  // the first inner tile
+    return a.s.causal ? max(0, p * kBN - (q.m - q.n)) / a.TT : 0;
+  }
+  static __device__ __forceinline__ int inner(const SeqArgs& a, const Seq& q, int p) {
+    return max(0, tiles_in(q.n, a.TT) - first(a, q, p));
+  }
+  int full;  // the first tiles, which all queries read
+  long long n, m;
+  __device__ __forceinline__ KeyRow(const SeqArgs& a, const Seq& q) : n(q.n), m(q.m) {
+    full = !a.s.causal ? INT32_MAX : q.m >= q.n ? (q.m - q.n) / kBN + 1 : 0;
+  }
+  __device__ __forceinline__ long long of(int p) const {
+    const long long f = min(p, full), P = p;
+    return P * kItemWork + f * n + (P - f) * m - kBN / 2 * (P * (P - 1) - f * (f - 1));
+  }
+  __device__ __forceinline__ int guess(long long w) const {
+    const long long f = (long long)full * (kItemWork + n);
+    const float flat = (float)(kItemWork + n);
+    if (w <= f) return (int)((float)w / flat);
+    // behind the full tiles: x = b P - 64 P (P - 1) with P = p - full
+    const float x = (float)(w - f), b = (float)(kItemWork + m - (long long)kBN * full) + kBN / 2;
+    return full + (int)(2.f * x / (b + sqrtf(fmaxf(b * b - 2.f * kBN * x, 0.f))));
+  }
+};
+
+// A place in the row: inner tile j of tile p of sequence b, key head h.
+struct Cut {
+  int b, h, p, j;
+};
+__device__ __forceinline__ bool same_item(const Cut& x, const Cut& y) { return x.b == y.b && x.h == y.h && x.p == y.p; }
+__device__ __forceinline__ bool before(const Cut& x, const Cut& y) {  // x's item lies before y's
+  return x.b != y.b ? x.b < y.b : x.h != y.h ? x.h < y.h : x.p < y.p;
+}
+struct Found {  // weight w of sequence b
+  Seq q;
+  long long w;
+  int b;
+};
+
+// The place at weight w of a sequence.  (One copy of the code: a share's end has to be the next one's beginning.)
+template <class Row>
+__device__ __noinline__ Cut cut_at(const SeqArgs& a, const Found& f) {
+  const Seq q = f.q;
+  long long w = f.w;
+  const int np = Row::tiles(a, q);
+  const Row row(a, q);
+  const long long head = row.of(np);
+  Cut c{f.b, min((int)((float)w / (float)head), a.s.Hk - 1), 0, 0};
+  while (c.h > 0 && c.h * head > w) --c.h;
+  while ((c.h + 1) * head <= w) ++c.h;
+  w -= c.h * head;
+  c.p = held_in(row.guess(w), 0, np - 1);  // the last p with of(p) <= w: guessed in 32 bits, put right
+  while (c.p > 0 && row.of(c.p) > w) --c.p;
+  while (c.p + 1 < np && row.of(c.p + 1) <= w) ++c.p;
+  const long long first = row.of(c.p);
+  const int nt = Row::inner(a, q, c.p);
+  c.j = min((int)((float)(w - first) / (float)(row.of(c.p + 1) - first) * nt + 0.5f), nt);
+  if (c.j < kLeastTiles) {
+    c.j = 0;
+  } else if (nt - c.j < kLeastTiles) {
+    c.j = 0;
+    if (++c.p == np) {
+      c.p = 0;
+      if (++c.h == a.s.Hk) {
+        c.h = 0;
+        ++c.b;
+      }
+    }
+  }
+  return c;
+}
+
+// The share of a CTA, with its sequences as they are now: all roles of the CTA walk it over this copy, so that they agree
+// on every item, after a failure and if someone writes into the lengths meanwhile.
+constexpr int kKeptSeqs = 64;      // sequences of a share that shared memory usually has room for (more: the workspace)
+constexpr int kShareBytes = 512;   // shared scratch of find_share
+struct Share {
+  Cut from, to;
+  const Seq* kept;  // of sequence from.b and the next ones
+};
+// All threads of the block.  `spill`: kept sequences of all shares, CTA c's from its first sequence + c on.
+template <class Row, bool kPaged, int kThreads, int kKept = kKeptSeqs>
+__device__ __forceinline__ Share find_share(const SeqArgs& a, uint8_t* scratch, uint8_t* kept_smem, Seq* spill,
+                                            unsigned int* status) {
+  const uaa_seqs& s = a.s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x, ctas = gridDim.x;
+  long long* sums = reinterpret_cast<long long*>(scratch);  // a sum a warp
+  Found* found = reinterpret_cast<Found*>(scratch + 256);
+  Cut* cuts = reinterpret_cast<Cut*>(scratch + 384);
+  if (threadIdx.x < 2) {
+    found[threadIdx.x].b = -1;
+    cuts[threadIdx.x] = Cut{s.B, 0, 0, 0};
+  }
+  auto scan = [&](long long x, long long& all) {  // sum of the threads before this one; `all`: of all
+    long long run = x;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const long long y = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += y;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = run;
+    __syncthreads();
+    long long ahead = 0;
+    all = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) ahead += sums[w];
+      all += sums[w];
+    }
+    return ahead + run - x;
+  };
+  Seq q{};  // of sequence threadIdx.x, if there are no more than threads
+  long long w = 0, w0 = 0, w1 = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {  // the total; then the sequences that the share begins and ends in
+    long long done = 0, all;
+#pragma unroll 1
+    for (int b0 = 0; b0 < s.B; b0 += kThreads) {
+      const int b = b0 + threadIdx.x;
+      if (pass == 0 || s.B > kThreads) {
+        w = 0;
+        if (b < s.B) {
+          bool bad;
+          q = load_seq<kPaged>(s, b, &bad);
+          if (bad && cta == 0) atomicOr(status, kStatusBadPage);
+          const int np = Row::tiles(a, q);
+          if (np > 0) w = s.Hk * Row(a, q).of(np);
+        }
+      }
+      const long long at = done + scan(w, all);
+      if (pass == 1 && w > 0) {
+        if (w0 >= at && w0 < at + w) found[0] = Found{q, w0 - at, b};
+        if (w1 >= at && w1 < at + w) found[1] = Found{q, w1 - at, b};
+      }
+      done += all;
+    }
+    if (pass == 0) {
+      const long long most = done / kLeastShare;
+      const int shares = most < 1 ? 1 : most < ctas ? (int)most : ctas;
+      if (cta >= shares) break;
+      const long long each = done / shares;
+      const int rest = (int)(done - each * shares);
+      w0 = each * cta + rest * cta / shares;
+      w1 = each * (cta + 1) + rest * (cta + 1) / shares;
+    }
+  }
+  __syncthreads();
+  if (lane == 0 && warp < 2 && found[warp].b >= 0) cuts[warp] = cut_at<Row>(a, found[warp]);
+  __syncthreads();
+  Share r{cuts[0], cuts[1], nullptr};
+  const int held = min(r.to.b, s.B - 1) - r.from.b + 1;  // its sequences (none: from.b = B)
+  Seq* kept = held <= kKept ? reinterpret_cast<Seq*>(kept_smem) : spill + r.from.b + cta;
+  for (int b = r.from.b + threadIdx.x; b < r.from.b + held && s.B > kThreads; b += kThreads)
+    kept[b - r.from.b] = load_seq<kPaged>(s, b);
+  if (s.B <= kThreads && (int)threadIdx.x >= r.from.b && (int)threadIdx.x < r.from.b + held)
+    kept[threadIdx.x - r.from.b] = q;
+  r.kept = kept;
+  return r;  // the caller's barrier makes `kept` visible
+}
+
+// Walks the items of a share.
+template <class Row>
+struct Walk {
+  Cut at, end;
+  const Seq* kept;
+  int base, j0, j1, np;  // inner tiles j0 .. j1 - 1 of this part
+  Seq q;
+  bool part, first;  // part: of an item that was cut
+  __device__ __forceinline__ explicit Walk(const Share& s)
+      : at(s.from), end(s.to), kept(s.kept), base(s.from.b), j0(s.from.j), j1(0), np(-1), part(false), first(true) {
+    at.j = 0;
+  }
+  __device__ __forceinline__ bool next(const SeqArgs& a) {
+    if (!first) {
+      ++at.p;
+      j0 = 0;
+    }
+    first = false;
+    while (true) {
+      if (at.b >= a.s.B || at.b > end.b) return false;
+      if (np < 0) {
+        q = kept[at.b - base];
+        np = Row::tiles(a, q);
+      }
+      if (at.p >= np) {
+        at.p = 0;
+        ++at.h;
+      }
+      if (np > 0 && at.h < a.s.Hk) break;
+      at.h = at.p = 0;
+      ++at.b;
+      np = -1;
+    }
+    const bool last = same_item(at, end);
+    if (!before(at, end) && !(last && end.j > 0)) return false;
+    const int nt = Row::inner(a, q, at.p);
+    j1 = last ? end.j : nt;
+    part = j0 > 0 || j1 < nt;
+    return true;
+  }
+};
+
+// The parts of an item that was cut, for the kernel that joins them: block c - 1 takes the item that CTA c's share begins
+// inside of, if no earlier share does.  Part 2 k + 1 is the tail of CTA k's share, 2 k its head; f(part) in order.
+__device__ __forceinline__ bool leads(const Cut* first, int c, int B) {
+  return first[c].b < B && first[c].j > 0 && !(same_item(first[c], first[c - 1]) && first[c - 1].j > 0);
+}
+template <typename F>
+__device__ __forceinline__ void each_part(const Cut* first, int c, int ctas, int nt, F&& f) {
+  const Cut me = first[c];
+  f(2 * (c - 1) + 1);
+  for (int k = c; k < ctas; ++k) {
+    const Cut x = first[k];
+    if (!same_item(x, me)) break;
+    const int end = k + 1 < ctas && same_item(first[k + 1], me) ? first[k + 1].j : nt;
+    if (end > x.j) f(2 * k);
+  }
+}
+__device__ __forceinline__ int part_of(int cta, int j0) { return 2 * cta + (j0 > 0 ? 0 : 1); }
+
+// ---------------------------------------------------------------------------
 // Host: the checks that the calls share.
 int check_seqs(const char* fn, const uaa_seqs* s, bool paged, bool bwd = false) {
   if (!s) return set_error(UAA_ERR_INVALID_ARG, "%s: the arguments are NULL", fn);
