@@ -50,6 +50,45 @@ __device__ __forceinline__ void store_packed64(uint32_t taddr, const float (&x)[
 // TMEM column of the A operand for K step kk when each half of the 128 columns lies packed at its own half's start.
 __device__ __forceinline__ uint32_t packed_a_col(int kk) { return kk < 4 ? kk * 8 : 64 + (kk - 4) * 8; }
 
+// 4-D tiled tensor store from shared memory (bulk-group completion).
+__device__ __forceinline__ void tma_store_4d(const void* smem_src, const CUtensorMap* map, int c0, int c1, int c2,
+                                             int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(smem_u32(smem_src)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+// The way out of a gradient tile: this thread's half row (columns hf D / 2 ..) in 16-bit pieces, swizzled as a tensor copy
+// takes them.  A tile whose rows all exist leaves by one; of others each warp stores its 32 half rows, a row by D / 16 lanes.
+template <int D>
+__device__ __forceinline__ uint4* out_piece(uint8_t* tile, int row, int hf, int i) {
+  const int p = hf * (D / 16) + i;
+  return reinterpret_cast<uint4*>(tile + (p >> 3) * kChunkBytes + row * 128 + (((p ^ row) & 7) << 4));
+}
+template <int D>
+__device__ __forceinline__ void put_columns(uint8_t* tile, int row, int hf, int i0, const float (&v)[32], float f) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    *out_piece<D>(tile, row, hf, i0 + e) =
+        make_uint4(pack_bf16(v[8 * e + 0] * f, v[8 * e + 1] * f), pack_bf16(v[8 * e + 2] * f, v[8 * e + 3] * f),
+                   pack_bf16(v[8 * e + 4] * f, v[8 * e + 5] * f), pack_bf16(v[8 * e + 6] * f, v[8 * e + 7] * f));
+}
+// to: the offset of this thread's half row in `out`, or ~0 where it is not stored
+template <int D>
+__device__ __forceinline__ void store_rows(uint8_t* tile, int row0, int hf, __nv_bfloat16* out, size_t to) {
+  constexpr int G = D / 16, kRows = 32 / G;  // lanes of a half row, half rows of a store
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+#pragma unroll 2
+  for (int x = 0; x < G; ++x) {
+    const int r = x * kRows + lane / G;
+    const size_t at = __shfl_sync(0xffffffffu, to, r);
+    if (at != ~(size_t)0) *reinterpret_cast<uint4*>(out + at + 8 * (lane % G)) = *out_piece<D>(tile, row0 + r, hf, lane % G);
+  }
+}
+
 __device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -151,7 +190,7 @@ struct DkdvCtl {
   uint64_t bar_q_full[3], bar_q_empty[3];
   uint64_t bar_do_full[2], bar_do_empty[2];
   uint64_t bar_s_full, bar_dp_full, bar_p_ready, bar_ds_ready;
-  uint64_t bar_acc_done, bar_acc_free, bar_final, bar_tail;
+  uint64_t bar_acc_done, bar_acc_free, bar_final, bar_tail, bar_out;
   uint32_t tmem_base;
   int abort;
 };
@@ -172,6 +211,7 @@ template <int D>
 __global__ void __launch_bounds__(kDkdvThreads, 1)
     seq_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
+                    const __grid_constant__ CUtensorMap tmDK, const __grid_constant__ CUtensorMap tmDV,
                     const __grid_constant__ BwdArgs x, float scale_log2, DevCtx ctx) {
   using L = DkdvLayout<D>;
   constexpr int kChunks = D / 64;
@@ -215,6 +255,7 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
     mbar_init(&ctl->bar_acc_free, kComputeThreads);
     mbar_init(&ctl->bar_final, 1);
     mbar_init(&ctl->bar_tail, 1);
+    mbar_init(&ctl->bar_out, kComputeThreads);
     ctl->abort = 0;
     fence_mbar_init();
   }
@@ -345,7 +386,8 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
       }
     };
     // dV += P^T dO_g (c = 0) or dK += dS^T Q_g (c = 1)
-    auto issue_acc = [&](int c, uint32_t g, bool first) {
+    // (the last Q and dO of an item stay: their stages are the epilogue's, which releases them)
+    auto issue_acc = [&](int c, uint32_t g, bool first, bool last) {
       const uint64_t b0 = sdesc_sw128(c == 0 ? sdo(g) : sq(g), kChunkBytes, 1024);
       const uint32_t d = tmem + (c == 0 ? kColDV : kColDK);
       const uint32_t p = tmem + (c == 0 ? kColS : kColDP);
@@ -354,7 +396,11 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
         const uint64_t z = desc_add(b0, kk * 2048);
         if (el) mma_ts_checked(mg, d, p + packed_a_col(kk), z, kIdescKM, (!first || kk > 0) ? 1u : 0u, D);
       }
-      if (el) mma_commit(c == 0 ? &ctl->bar_do_empty[g % L::kDStages] : &ctl->bar_q_empty[g % L::kQStages]);
+      if (el && !last) mma_commit(c == 0 ? &ctl->bar_do_empty[g % L::kDStages] : &ctl->bar_q_empty[g % L::kQStages]);
+    };
+    // behind the last product that reads K or V
+    auto release_kv = [&] {
+      if (el) mma_commit(&ctl->bar_kv_empty);
     };
     Walk<KeyRow> w(share);
     while (ok && w.next(a)) {
@@ -367,6 +413,7 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
         tc_fence_after();
         issue_kk(0, nq);
         issue_kk(1, nq);
+        if (nt == 1) release_kv();
         if (el) mma_issued = true;
       }
       for (int i = 0; ok && i < nt; ++i) {
@@ -378,17 +425,17 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
           if (!(ok = wait_el(&ctl->bar_acc_free, (it - 1) & 1))) break;
         }
         tc_fence_after();
-        issue_acc(0, g, i == 0);
+        issue_acc(0, g, i == 0, !more);
         if (more) issue_kk(0, g + 1);
         if (!(ok = wait_el(&ctl->bar_ds_ready, g & 1))) break;
         tc_fence_after();
-        issue_acc(1, g, i == 0);
+        issue_acc(1, g, i == 0, !more);
         if (more) issue_kk(1, g + 1);
+        if (i + 2 == nt) release_kv();
       }
       if (el) {
         if (ok) {
           mma_commit(&ctl->bar_acc_done);
-          mma_commit(&ctl->bar_kv_empty);
         } else {
           *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
         }
@@ -493,6 +540,9 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
       if (!ok) break;
       tc_fence_after();
       float* part = x.w.part_kv + (size_t)part_of(blockIdx.x, w.j0) * (2 * D * 128) + jrow;
+      const uint32_t gl = nq + nt - 1;  // dK leaves through the last Q's stage, dV through the last dO's
+      uint8_t* out[2] = {smem + L::kDO + (gl % L::kDStages) * L::kTileBytes, smem + L::kQ + (gl % L::kQStages) * L::kTileBytes};
+      const bool whole = !w.part && (w.at.p + 1) * kBN <= w.q.m;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {  // 32 columns of dV and of dK in turn
         const int col = hf * (D / 2) + 32 * (c >> 1), which = c & 1;
@@ -501,18 +551,37 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
         if (w.part) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) part[(size_t)(which * D + col + e) * 128] = v[e];
-        } else if (store) {
-          const float f = which ? s.scale : 1.f;
-          __nv_bfloat16* to = (which ? x.dk : x.dv) + off + 32 * (c >> 1);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4*>(to + 8 * e) =
-                make_uint4(pack_bf16(v[8 * e + 0] * f, v[8 * e + 1] * f), pack_bf16(v[8 * e + 2] * f, v[8 * e + 3] * f),
-                           pack_bf16(v[8 * e + 4] * f, v[8 * e + 5] * f), pack_bf16(v[8 * e + 6] * f, v[8 * e + 7] * f));
+        } else {
+          put_columns<D>(out[which], jrow, hf, 4 * (c >> 1), v, which ? s.scale : 1.f);
         }
       }
       tc_fence_before();
       mbar_arrive(&ctl->bar_acc_free);
+      if (!w.part && !whole) {
+        const size_t to = store ? off : ~(size_t)0;
+        store_rows<D>(out[0], quad * 32, hf, x.dv, to);
+        store_rows<D>(out[1], quad * 32, hf, x.dk, to);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&ctl->bar_out);
+      if (warp == 0) {
+        ok = __all_sync(0xffffffffu, wait_or_abort(&ctl->bar_out, it & 1, ctx, ctl));
+        if (!ok) break;
+        if (lane == 0) {
+          if (whole && store) {
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+              tma_store_4d(out[0] + c * kChunkBytes, &tmDV, c * 64, w.at.h, w.q.k0 + w.at.p * kBN, 0);
+              tma_store_4d(out[1] + c * kChunkBytes, &tmDK, c * 64, w.at.h, w.q.k0 + w.at.p * kBN, 0);
+            }
+            bulk_commit_group();
+            bulk_wait_read_all();
+          }
+          mbar_arrive(&ctl->bar_do_empty[gl % L::kDStages]);
+          mbar_arrive(&ctl->bar_q_empty[gl % L::kQStages]);
+        }
+        __syncwarp();
+      }
       nq += nt;
       ++it;
     }
@@ -546,12 +615,15 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
 // 3. dQ
 template <int D>
 struct DqLayout {
-  // K and V in rings of their own: a K slot is freed only by dQ, late in a key tile's processing, a V slot already by dP
-  static constexpr int kKRing = (D == 128) ? 4 : 7;
-  static constexpr int kVRing = (D == 128) ? 3 : 6;
+  // K and V in rings of their own: a K slot is freed only by dQ, late in a key tile's processing, a V slot already by dP.
+  // Behind them an item's Q and dO, on their way into TMEM.
+  static constexpr int kKRing = (D == 128) ? 3 : 6;
+  static constexpr int kVRing = (D == 128) ? 2 : 5;
   static constexpr int kRing = kKRing + kVRing;
   static constexpr int kTileBytes = 128 * D * 2;
-  static constexpr int kCtl = kRing * kTileBytes;  // Q and dO live in TMEM
+  static constexpr int kQ = kRing * kTileBytes;
+  static constexpr int kDO = kQ + kTileBytes;
+  static constexpr int kCtl = kDO + kTileBytes;
   static constexpr int kKept = kCtl + 512;
   static constexpr int kScratch = kKept + kKeptSeqs * 16;
   static constexpr int kSmem = kScratch + kShareBytes;
@@ -562,7 +634,7 @@ struct DqCtl {
   uint64_t bar_qdo_ready;
   uint64_t bar_kv_full[16], bar_kv_empty[16];
   uint64_t bar_s_full, bar_s_read, bar_dp_full, bar_ds_ready;
-  uint64_t bar_dq_done, bar_dq_free, bar_final[2], bar_dq_step, bar_tail;
+  uint64_t bar_dq_done, bar_dq_free, bar_final[2], bar_dq_step, bar_tail, bar_out, bar_qd_full, bar_qd_free;
   uint32_t tmem_base;
   int abort;
 };
@@ -572,8 +644,9 @@ using Rows = QueryRow<1>;
 
 template <int D>
 __global__ void __launch_bounds__(kDqThreads, 1)
-    seq_dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                  const __grid_constant__ BwdArgs x, float scale_log2, DevCtx ctx) {
+    seq_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
+                  const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                  const __grid_constant__ CUtensorMap tmDQ, const __grid_constant__ BwdArgs x, float scale_log2, DevCtx ctx) {
   using L = DqLayout<D>;
   constexpr int kChunks = D / 64;
   constexpr int R = L::kRing;
@@ -614,6 +687,9 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     mbar_init(&ctl->bar_dq_free, kComputeThreads);
     mbar_init(&ctl->bar_dq_step, 1);
     mbar_init(&ctl->bar_tail, 1);
+    mbar_init(&ctl->bar_out, kComputeThreads);
+    mbar_init(&ctl->bar_qd_full, 1);
+    mbar_init(&ctl->bar_qd_free, kComputeThreads);
     mbar_init(&ctl->bar_final[0], 1);
     mbar_init(&ctl->bar_final[1], 1);
     ctl->abort = 0;
@@ -622,6 +698,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   if (warp == kProducerWarp && lane == 0) {
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmDO);
   }
   if (warp == kMmaWarp) {
     tmem_alloc(&ctl->tmem_base, 512);
@@ -638,15 +716,31 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   const MmaGuard mg = mma_guard(ctx, sbase, L::kSmem, tmem, 512);  // debug builds' operand checks
   const size_t q_extent = (size_t)s.T * s.Hq * D;
 
-  uint32_t kv_armed[R] = {}, tails = 0;
+  uint32_t kv_armed[R] = {}, tails = 0, qd_armed = 0;
   bool mma_issued = false;
 
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer
     bool ok = true;
-    uint32_t n = 0, gp = 0;  // n: loads, gp: key tiles loaded
+    uint32_t n = 0, gp = 0, it = 0;  // n: loads, gp: key tiles loaded
     Walk<Rows> w(share);
     while (ok && w.next(a)) {
+      if (w.j1 <= w.j0) continue;
+      if (lane == 0) {
+        if (it > 0) ok = wait_or_abort(&ctl->bar_qd_free, (it - 1) & 1, ctx, ctl);
+        if (ok) {
+          const int at = w.q.q0 + w.at.p * a.TT;
+          mbar_arrive_expect_tx(&ctl->bar_qd_full, 2 * a.TT * a.g * 128 * kChunks);
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            tma_load_4d(smem + L::kQ + c * kChunkBytes, &tmQ, &ctl->bar_qd_full, c * 64, 0, w.at.h, at);
+            tma_load_4d(smem + L::kDO + c * kChunkBytes, &tmDO, &ctl->bar_qd_full, c * 64, 0, w.at.h, at);
+          }
+          qd_armed = it + 1;
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      ++it;
       for (int j = w.j0; ok && j < w.j1; ++j, ++gp) {
         const int left = held_in(w.q.m - j * kBN, 0, kBN);  // the tile's keys that belong to the sequence
 #pragma unroll
@@ -717,13 +811,14 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       mma_commit(&ctl->bar_dp_full);
       mma_commit(&ctl->bar_kv_empty[vslot(gg)]);
     };
-    auto issue_dq = [&](uint32_t gg, bool first) {
+    // (the last K of an item stays: its slot is the epilogue's, which releases it)
+    auto issue_dq = [&](uint32_t gg, bool first, bool last) {
       const uint64_t b0 = sdesc_sw128(slot_addr(kslot(gg)), kChunkBytes, 1024);
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk)
         mma_ts_checked(mg, tmem + kColDQ, tmem + kColDP + packed_a_col(kk), desc_add(b0, kk * 2048), kIdescKM,
                        (!first || kk > 0) ? 1u : 0u, D);
-      mma_commit(&ctl->bar_kv_empty[kslot(gg)]);
+      if (!last) mma_commit(&ctl->bar_kv_empty[kslot(gg)]);
     };
     Walk<Rows> w(share);
     while (ok && w.next(a)) {
@@ -759,7 +854,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
             if (ok && i == 0 && it > 0) ok = wait_or_abort(&ctl->bar_dq_free, (it - 1) & 1, ctx, ctl);
             if (ok) {
               tc_fence_after();
-              issue_dq(g, i == 0);
+              issue_dq(g, i == 0, !more);
               if (more) {
                 mma_commit(&ctl->bar_dq_step);
                 ok = wait_or_abort(&ctl->bar_dq_step, dq_step & 1, ctx, ctl);
@@ -808,25 +903,25 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         continue;
       }
       {
-        // the previous item's products have all completed (its dq_done was waited for)
-        const uint4* src = reinterpret_cast<const uint4*>(
-            hf == 0 ? static_cast<const __nv_bfloat16*>(s.q) + (size_t)(w.q.q0 + (valid ? tok : 0)) * s.q_row +
-                          (size_t)(valid ? hq : 0) * s.q_head
-                    : x.dout + qoff);
+        // Q (hf = 0) or dO from shared memory into TMEM: the previous item's products have all completed (its dq_done was
+        // waited for).  Rows of no token become zeros.
+        ok = __all_sync(0xffffffffu, wait_or_abort(&ctl->bar_qd_full, it & 1, ctx, ctl));
+        if (!ok) break;
+        const uint8_t* src = smem + (hf == 0 ? L::kQ : L::kDO) + row * 128;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
           uint32_t wv[32];
 #pragma unroll
           for (int t = 0; t < 8; ++t) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (valid) v = __ldg(src + 8 * c + t);
-            wv[4 * t + 0] = v.x;
-            wv[4 * t + 1] = v.y;
-            wv[4 * t + 2] = v.z;
-            wv[4 * t + 3] = v.w;
+            const uint4 v = *reinterpret_cast<const uint4*>(src + c * kChunkBytes + (((t ^ row) & 7) << 4));
+            wv[4 * t + 0] = valid ? v.x : 0u;
+            wv[4 * t + 1] = valid ? v.y : 0u;
+            wv[4 * t + 2] = valid ? v.z : 0u;
+            wv[4 * t + 3] = valid ? v.w : 0u;
           }
           tmem_st32_bits(tl + (hf == 0 ? kColQ : kColDO) + 32 * c, wv);
         }
+        mbar_arrive(&ctl->bar_qd_free);
         tc_fence_before();
         mbar_arrive(&ctl->bar_qdo_ready);
       }
@@ -892,6 +987,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       if (!ok) break;
       tc_fence_after();
       float* part = x.w.part_q + (size_t)part_of(blockIdx.x, w.j0) * (D * 128) + row;
+      uint8_t* out = smem + kslot(g - 1) * L::kTileBytes;  // dQ leaves through the last K's slot
+      const bool whole = !w.part && (w.at.p + 1) * a.TT <= w.q.n;
 #pragma unroll 1
       for (int c = 0; c < D / 64; ++c) {
         const int col = hf * (D / 2) + 32 * c;
@@ -900,17 +997,30 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         if (w.part) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) part[(size_t)(col + e) * 128] = v[e];
-        } else if (store) {
-          const float f = s.scale;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4*>(x.dq + qoff + col + 8 * e) =
-                make_uint4(pack_bf16(v[8 * e + 0] * f, v[8 * e + 1] * f), pack_bf16(v[8 * e + 2] * f, v[8 * e + 3] * f),
-                           pack_bf16(v[8 * e + 4] * f, v[8 * e + 5] * f), pack_bf16(v[8 * e + 6] * f, v[8 * e + 7] * f));
+        } else {
+          put_columns<D>(out, row, hf, 4 * c, v, s.scale);
         }
       }
       tc_fence_before();
       mbar_arrive(&ctl->bar_dq_free);
+      if (!w.part && !whole) store_rows<D>(out, quad * 32, hf, x.dq, store ? qoff + hf * (D / 2) : ~(size_t)0);
+      fence_proxy_async_smem();
+      mbar_arrive(&ctl->bar_out);
+      if (warp == 0) {
+        ok = __all_sync(0xffffffffu, wait_or_abort(&ctl->bar_out, it & 1, ctx, ctl));
+        if (!ok) break;
+        if (lane == 0) {
+          if (whole && store) {
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c)
+              tma_store_4d(out + c * kChunkBytes, &tmDQ, c * 64, 0, w.at.h, w.q.q0 + w.at.p * a.TT);
+            bulk_commit_group();
+            bulk_wait_read_all();
+          }
+          mbar_arrive(&ctl->bar_kv_empty[kslot(g - 1)]);
+        }
+        __syncwarp();
+      }
       ++it;
     }
   }
@@ -924,6 +1034,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   }
   if (warp == kProducerWarp && lane == 0) {
     if (tails) settle(&ctl->bar_tail, (tails - 1) & 1, ctx);
+    if (qd_armed) settle(&ctl->bar_qd_full, (qd_armed - 1) & 1, ctx);
     for (int i = 0; i < R; ++i)
       if (kv_armed[i]) settle(&ctl->bar_kv_full[i], (kv_armed[i] - 1) & 1, ctx);
   }
@@ -1030,7 +1141,7 @@ template <int D>
 int launch_bwd(const char* fn, const BwdArgs& x, cudaStream_t stream) {
   const uaa_seqs& s = x.a.s;
   const SeqArgs& a = x.a;
-  CUtensorMap mq, mk, mv, md;
+  CUtensorMap mq, mk, mv, md, oq, ok, ov;
   int st;
   // without queries, or without keys, the maps lie over the other's tensor and no tile reads them
   const bool some = s.T > 0, keys = s.Tk > 0;
@@ -1038,6 +1149,9 @@ int launch_bwd(const char* fn, const BwdArgs& x, cudaStream_t stream) {
   const long long T = some ? s.T : 1, Tk = keys ? s.Tk : 1;
   if ((st = encode_map(&mq, fn, q, {D, a.g, s.Hk, T}, {s.q_head, a.g * s.q_head, s.q_row}, {64, a.g, 1, a.TT})) ||
       (st = encode_map(&md, fn, d, {D, a.g, s.Hk, T}, {D, a.g * D, (long long)s.Hq * D}, {64, a.g, 1, a.TT})) ||
+      (st = encode_map(&oq, fn, some ? x.dq : x.dk, {D, a.g, s.Hk, T}, {D, a.g * D, (long long)s.Hq * D}, {64, a.g, 1, a.TT})) ||
+      (st = encode_map(&ok, fn, keys ? x.dk : x.dq, {D, s.Hk, Tk, 1}, {D, s.Hk * D, s.Hk * D}, {64, 1, kBN, 1})) ||
+      (st = encode_map(&ov, fn, keys ? x.dv : x.dq, {D, s.Hk, Tk, 1}, {D, s.Hk * D, s.Hk * D}, {64, 1, kBN, 1})) ||
       (st = encode_map(&mk, fn, k, {D, s.Hk, Tk, 1}, {s.k_head, s.k_row, s.k_row}, {64, 1, kBN, 1})) ||
       (st = encode_map(&mv, fn, v, {D, s.Hk, Tk, 1}, {s.v_head, s.v_row, s.v_row}, {64, 1, kBN, 1})))
     return st;
@@ -1047,9 +1161,9 @@ int launch_bwd(const char* fn, const BwdArgs& x, cudaStream_t stream) {
   const float c = s.scale * kLog2e;
   seq_stats_kernel<D><<<dim3(x.w.slots, s.Hk), 256, 0, stream>>>(x);
   if ((st = check_launch(fn))) return st;
-  if ((st = launch_after(fn, seq_dkdv_kernel<D>, dim3(ctas), kDkdvThreads, DkdvLayout<D>::kSmem, stream, mq, mk, mv, md, x, c, ctx)))
+  if ((st = launch_after(fn, seq_dkdv_kernel<D>, dim3(ctas), kDkdvThreads, DkdvLayout<D>::kSmem, stream, mq, mk, mv, md, ok, ov, x, c, ctx)))
     return st;
-  if (some && (st = launch_after(fn, seq_dq_kernel<D>, dim3(ctas), kDqThreads, DqLayout<D>::kSmem, stream, mk, mv, x, c, ctx)))
+  if (some && (st = launch_after(fn, seq_dq_kernel<D>, dim3(ctas), kDqThreads, DqLayout<D>::kSmem, stream, mq, md, mk, mv, oq, x, c, ctx)))
     return st;
   if (!some) return UAA_OK;  // nothing was cut: no tile has an inner one
   return launch_after(fn, seq_bwd_join_kernel<D>, dim3(ctas - 1, 4, 2), 256, 0, stream, x, ctas, ctx);
