@@ -436,7 +436,8 @@ int uaa_diff_attn_bwd(const void* q, const void* k, const void* v, const void* l
  * Attention of B sequences, each with its own number of queries and keys, without padding.  Sequence b has the n
  * query tokens starts[b] .. starts[b+1] - 1 and m keys; its last query stands at its last key.  With `causal` query i
  * reads keys 0 .. m - n + i, without it all m.  Hq / Hk query heads in a row share a key head.  A query that reads no
- * key gets out = 0, lse = -inf and no gradient.  Tokens behind starts[B] are left as they were.
+ * key gets out = 0, lse = -inf and no gradient.  Tokens of no sequence (before starts[0], behind starts[B]) are left as
+ * they were, unless `rest` asks for zeros.
  *   packed : the keys are the tokens starts_k[b] .. starts_k[b+1] - 1 of k and v (starts_k NULL: as the queries)
  *   paged  : key j is row j % page of page table[r, j / page] of the pools k and v, r = seqs[b] (seqs NULL: b), and
  *            m = lens[r] counts the new tokens, whose keys are in the cache already
@@ -461,6 +462,7 @@ typedef struct {
   int dtype;                /* UAA_BF16 or UAA_FP16 (the backward: UAA_BF16) */
   int causal;
   int pages, page, table_rows, width; /* paged: a page is 16, 32, 64 or a multiple of 128 tokens */
+  int rest;                 /* nonzero: tokens of no sequence get out = 0 and lse = -inf, their gradients are 0 */
   float scale;
 } uaa_seqs;
 

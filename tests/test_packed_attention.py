@@ -48,7 +48,7 @@ def args(**kw):
     f = 1 << 20
     x = dict(q=f, k=f, v=f, out=f, lse=f, starts=f, starts_k=0, table=0, lens=0, seqs=0, q_row=256, q_head=64, k_row=128,
              k_head=64, v_row=128, v_head=64, k_page=0, v_page=0, B=2, T=10, Tk=10, Hq=4, Hk=2, D=64, dtype=0, causal=1,
-             pages=0, page=0, table_rows=0, width=0, scale=0.1)
+             pages=0, page=0, table_rows=0, width=0, rest=0, scale=0.1)
     x.update(kw)
     return uaa._SEQS.pack(*x.values())
 
@@ -362,14 +362,28 @@ def test_autograd(saved):
 
 
 @pytest.mark.gpu
-def test_tokens_of_no_sequence_have_no_gradient():
-    x = draw([50], [50], 2, 1, 64, seed=17, tail=14)
+@pytest.mark.parametrize("first,last", [(0, 50), (7, 50), (20, 64), (64, 64), (0, 0)])
+def test_tokens_of_no_sequence_have_no_gradient(first, last):
+    """Before the first sequence and behind the last one: zeros, where raw calls leave what was there."""
+    x = draw([64], [64], 2, 1, 64, seed=17)
+    x["starts"] = x["starts_k"] = torch.tensor([first, last], dtype=torch.int32)
     y = {n: t.to(DEV) for n, t in x.items()}
+    for n in ("q", "k", "v", "do"):
+        y[n][:first] = y[n][last:] = float("nan")
     q, k, v = (y[n].requires_grad_() for n in ("q", "k", "v"))
-    out, _ = uaa.packed_attention(q, k, v, y["starts"])
-    assert not out[50:].any()
-    for t in torch.autograd.grad(out, (q, k, v), y["do"]):
-        assert not t[50:].any() and t[:50].any()
+    for _ in range(2):  # the second time over memory that is not fresh
+        out, lse = uaa.packed_attention(q, k, v, y["starts"])
+        grads = torch.autograd.grad(out, (q, k, v), y["do"])
+        got = dict(zip(ALL, (out, lse) + grads))
+        want = against(x)
+        check(got, want, ALL)
+        for n, t in got.items():
+            t = t.T if n == "lse" else t
+            for rest in (t[:first], t[last:]):
+                assert torch.isneginf(rest).all() if n == "lse" else not rest.any(), n
+        del out, lse, grads, got, t
+        torch.full((1 << 22,), float("nan"), device=DEV)
+    uaa.check_device_status()
 
 
 @pytest.mark.gpu

@@ -14,6 +14,7 @@ for P emulated ranks on one device.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import math
 import os
@@ -65,7 +66,7 @@ class _RotaryPlan(ctypes.Structure):  # uaa_rotary_plan
 _ROTARY_TENSOR = struct.Struct("@PP6qi0q")
 
 # uaa_seqs, uaa_pools and uaa_cache_rows, as bytes
-_SEQS = struct.Struct("@10P8q12if0q")
+_SEQS = struct.Struct("@10P8q13if0q")
 _POOLS = struct.Struct("@4P2i0q")
 _CACHE_ROWS = struct.Struct("@8P10q8i0q")
 
@@ -831,16 +832,17 @@ def diff_attention(q, k, v, lam, key_mask=None, scale=None, saved=None):
 # --------------------------------------------------------------------------- sequences of their own lengths
 def _rows16(name, t, dims, D=None):
     """Checks a 16-bit operand (..., heads, D); returns its strides, those of dimensions of one entry as if contiguous."""
-    shape = t.shape
+    shape, strides = t.shape, t.stride()
     if len(shape) != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got {tuple(shape)}")
     if D is not None and shape[-1] != D:
         raise ValueError(f"{name} has heads of {shape[-1]} columns, not {D}")
-    strides, dense = list(t.stride()), 1
-    for i in range(dims - 1, -1, -1):
-        if shape[i] <= 1:
-            strides[i] = dense
-        dense *= max(shape[i], 1)
+    if 1 in shape or 0 in shape:
+        strides, dense = list(strides), 1
+        for i in range(dims - 1, -1, -1):
+            if shape[i] <= 1:
+                strides[i] = dense
+            dense *= max(shape[i], 1)
     if strides[-1] != 1:
         raise ValueError(f"the columns of {name} must be contiguous")
     return strides
@@ -878,7 +880,7 @@ def _seqs_workspace(workspace, B, T, Hq, Hk, D, dev):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _packed_args(q, k, v, starts, starts_k, causal, scale, out, lse, half=True):
+def _packed_args(q, k, v, starts, starts_k, causal, scale, out, lse, half=True, rest=0):
     (q0, q1, _), (k0, k1, _), (v0, v1, _) = _rows16("q", q, 3), _rows16("k", k, 3, q.shape[-1]), _rows16("v", v, 3)
     dtype, scale, out, lse = _seqs_common(q, k, v, starts, scale, out, lse, half)
     B = starts.shape[0] - 1
@@ -889,7 +891,7 @@ def _packed_args(q, k, v, starts, starts_k, causal, scale, out, lse, half=True):
     T, Hq, D = q.shape
     packed = _SEQS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), starts.data_ptr(),
                         0 if starts_k is None else starts_k.data_ptr(), 0, 0, 0, q0, q1, k0, k1, v0, v1, 0, 0, B, T,
-                        k.shape[0], Hq, k.shape[1], D, dtype, 1 if causal else 0, 0, 0, 0, 0, scale)
+                        k.shape[0], Hq, k.shape[1], D, dtype, 1 if causal else 0, 0, 0, 0, 0, rest, scale)
     return packed, out, lse
 
 
@@ -903,8 +905,12 @@ def attn_packed_fwd(q, k, v, starts, starts_k=None, causal=True, scale=None, out
     its last key and each reads the keys up to its own place.  Returns ``out`` ``(T, Hq, D)`` and ``lse`` fp32
     ``(Hq, T)``; tokens behind ``starts[-1]`` are left as they were (in new results: undefined).
     """
+    return _packed_fwd(q, k, v, starts, starts_k, causal, scale, out, lse, workspace, 0)
+
+
+def _packed_fwd(q, k, v, starts, starts_k, causal, scale, out, lse, workspace, rest):
     dev = _same_device(q, k, v, starts, starts_k, out, lse, workspace)
-    args, out, lse = _packed_args(q, k, v, starts, starts_k, causal, scale, out, lse)
+    args, out, lse = _packed_args(q, k, v, starts, starts_k, causal, scale, out, lse, rest=rest)
     T, Hq, D = q.shape
     _call(dev, "uaa_attn_packed_fwd", args, *_seqs_workspace(workspace, starts.shape[0] - 1, T, Hq, k.shape[1], D, dev))
     return out, lse
@@ -917,10 +923,14 @@ def attn_packed_bwd_workspace_bytes(B, T, Hq, Hk, D) -> int:
 def attn_packed_bwd(q, k, v, out, dout, lse, starts, starts_k=None, causal=True, scale=None, dq=None, dk=None, dv=None,
                     workspace=None):
     """``uaa_attn_packed_bwd``: the gradients ``(dq, dk, dv)`` of :func:`attn_packed_fwd` (bf16)."""
-    dev = _same_device(q, k, v, out, dout, lse, starts, starts_k, workspace)
     if out is None or lse is None:
         raise ValueError("out and lse are the forward's results")
-    args, out, lse = _packed_args(q, k, v, starts, starts_k, causal, scale, out, lse, half=False)
+    return _packed_bwd(q, k, v, out, dout, lse, starts, starts_k, causal, scale, dq, dk, dv, workspace, 0)
+
+
+def _packed_bwd(q, k, v, out, dout, lse, starts, starts_k, causal, scale, dq, dk, dv, workspace, rest):
+    dev = _same_device(q, k, v, out, dout, lse, starts, starts_k, workspace)
+    args, out, lse = _packed_args(q, k, v, starts, starts_k, causal, scale, out, lse, half=False, rest=rest)
     dout = _result("dout", dout, q.shape, q.dtype, dev)
     dq = _result("dq", dq, q.shape, q.dtype, dev)
     dk = _result("dk", dk, k.shape, q.dtype, dev)
@@ -937,20 +947,21 @@ def attn_packed_bwd(q, k, v, out, dout, lse, starts, starts_k=None, causal=True,
 class PackedAttention(torch.autograd.Function):
     """Autograd pairing of ``attn_packed_fwd`` / ``attn_packed_bwd``; ``lse`` is non-differentiable.
 
-    ``saved="int8"`` keeps Q, K, V and O for the backward pass as an 8-bit checkpoint.  Tokens behind ``starts[-1]``
-    belong to no sequence: ``out`` and the gradients are zero there."""
+    ``saved="int8"`` keeps Q, K, V and O for the backward pass as an 8-bit checkpoint.  For tokens of no sequence (before
+    ``starts[0]``, behind ``starts[-1]``) ``out`` and the gradients are zero."""
 
     @staticmethod
     def forward(ctx, q, k, v, starts, starts_k=None, causal=True, scale=None, saved=None):
         _check_saved(saved)
         if q.dtype != torch.bfloat16 and any(ctx.needs_input_grad):
             raise TypeError("gradients are built for bfloat16")
-        out, lse = attn_packed_fwd(q, k, v, starts, starts_k, causal, scale, out=torch.zeros_like(q, memory_format=torch.contiguous_format))
+        out, lse = _packed_fwd(q, k, v, starts, starts_k, causal, scale, None, None, None, 1)
         if saved == "int8":  # the checkpoint takes contiguous rows
             q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
-        ctx.starts = (starts if starts.is_inference() else None, starts_k if starts_k is not None and starts_k.is_inference() else None)
-        _save(ctx, saved, (q, k, v, out), lse, None if ctx.starts[0] is not None else starts,
-              None if ctx.starts[1] is not None else starts_k, key_mask=None)
+        # (made in inference mode they have no versions and cannot be saved: they stay on ctx)
+        ctx.starts = [t if t is not None and t.is_inference() else None for t in (starts, starts_k)]
+        _save(ctx, saved, (q, k, v, out), lse, *(t if c is None else None for t, c in zip((starts, starts_k), ctx.starts)),
+              key_mask=None)
         ctx.causal, ctx.scale = causal, scale
         ctx.mark_non_differentiable(lse)
         ctx.set_materialize_grads(False)  # no zeros for lse
@@ -963,9 +974,8 @@ class PackedAttention(torch.autograd.Function):
             return (None,) * 8
         (q, k, v, out), (lse, starts, starts_k), _ = _saved(ctx, 4)
         starts, starts_k = (a if b is None else b for a, b in zip((starts, starts_k), ctx.starts))
-        zeros = [torch.zeros(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v)]
-        dq, dk, dv = attn_packed_bwd(q, k, v, out, dout.contiguous(), lse, starts, starts_k, ctx.causal, ctx.scale,
-                                     *zeros)
+        dq, dk, dv = _packed_bwd(q, k, v, out, dout.contiguous(), lse, starts, starts_k, ctx.causal, ctx.scale, None, None,
+                                 None, None, 1)
         return dq, dk, dv, None, None, None, None, None
 
 
@@ -1003,7 +1013,7 @@ def attn_paged_fwd(q, k_pages, v_pages, starts, table, lens, seqs=None, causal=T
     args = _SEQS.pack(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), lse.data_ptr(),
                       starts.data_ptr(), 0, table.data_ptr(), lens.data_ptr(), 0 if seqs is None else seqs.data_ptr(),
                       q0, q1, k1, k2, v1, v2, k0, v0, B, T, 0, Hq, Hk, D, dtype, 1 if causal else 0, N, page, rows,
-                      width, scale)
+                      width, 0, scale)
     _call(dev, "uaa_attn_paged_fwd", args, *_seqs_workspace(workspace, B, T, Hq, Hk, D, dev))
     return out, lse
 
@@ -1060,8 +1070,11 @@ class PagedCache:
         self.k, self.v = (torch.empty((layers, pages, page, heads, dim), dtype=dtype, device=device) for _ in range(2))
         self.table = torch.full((seqs, width), -1, dtype=torch.int32, device=device)
         self.lens = torch.zeros(seqs, dtype=torch.int32, device=device)
-        self._pools = _POOLS.pack(self.k.data_ptr(), self.v.data_ptr(), self.table.data_ptr(), self.lens.data_ptr(),
-                                  layers, heads * dim * 2)
+        self._at = tuple(t.data_ptr() for t in (self.k, self.v, self.table, self.lens))
+        self._pools = _POOLS.pack(*self._at, layers, heads * dim * 2)
+        self._strides = (page * heads * dim, heads * dim, dim) * 2
+        self._rows = (heads, dim, pages, page, seqs, width)
+        self._layer_bytes = pages * page * heads * dim * 2
 
     def __del__(self):
         if getattr(self, "_h", None) and _lib is not None:
@@ -1087,23 +1100,23 @@ class PagedCache:
         return list(row)[:n]
 
     def _pair(self, name, a, b):
-        a, b = list(a), list(b)
+        a, b = array.array("i", a), array.array("i", b)
         if len(a) != len(b):
             raise ValueError(f"{len(a)} and {len(b)} entries")
-        n = len(a)
-        _call(self.k.device, name, self._h, self._pools, n, (_I * n)(*a), (_I * n)(*b))
+        _call(self.k.device, name, self._h, self._pools, len(a), a.buffer_info()[0], b.buffer_info()[0])
 
     def append(self, seqs, counts):
         """Makes room for ``counts[i]`` more tokens of sequence ``seqs[i]``; a shared, partly filled last page is
         copied first.  Returns ``(starts, seqs)`` on the device, for :meth:`write` and :meth:`attend`."""
-        a, b = list(seqs), list(counts)
+        a, b = array.array("i", seqs), array.array("i", counts)
         if len(a) != len(b):
             raise ValueError(f"{len(a)} sequences and {len(b)} counts")
         n, dev = len(a), self.k.device
         both = torch.empty(2 * n + 1, dtype=torch.int32, device=dev)
         starts, ids = both[: n + 1], both[n + 1:]
         at = both.data_ptr()
-        _call(dev, "uaa_pages_append", self._h, self._pools, n, (_I * n)(*a), (_I * n)(*b), at, at + 4 * (n + 1))
+        _call(dev, "uaa_pages_append", self._h, self._pools, n, a.buffer_info()[0], b.buffer_info()[0], at,
+              at + 4 * (n + 1))
         return starts, ids
 
     def fork(self, parents, children):
@@ -1125,7 +1138,24 @@ class PagedCache:
 
     def write(self, layer, k, v, starts, seqs=None):
         """:func:`cache_write` into a layer."""
-        cache_write(k, v, self.k[layer], self.v[layer], starts, self.table, self.lens, seqs)
+        pools, shape = self.k, k.shape
+        if k.dtype != pools.dtype or v.dtype != pools.dtype:
+            raise TypeError(f"k and v must be {pools.dtype}")
+        if shape != v.shape or len(shape) != 3 or shape[1] != self._rows[0] or shape[2] != self._rows[1]:
+            raise ValueError(f"k {tuple(shape)} and v {tuple(v.shape)} must be (tokens, {self._rows[0]}, {self._rows[1]})")
+        if not 0 <= layer < pools.shape[0]:
+            raise IndexError(f"layer {layer} of {pools.shape[0]}")
+        dev = _same_device(pools, k, v, starts, seqs)
+        (k0, k1, _), (v0, v1, _) = _rows16("k", k, 3), _rows16("v", v, 3)
+        _starts("starts", starts)
+        B = starts.shape[0] - 1
+        if seqs is not None and (seqs.dtype != torch.int32 or seqs.shape != (B,) or not seqs.is_contiguous()):
+            raise ValueError(f"seqs must be contiguous int32 ({B},), got {seqs.dtype} {tuple(seqs.shape)}")
+        at = layer * self._layer_bytes
+        _call(dev, "uaa_cache_write",
+              _CACHE_ROWS.pack(k.data_ptr(), v.data_ptr(), self._at[0] + at, self._at[1] + at, starts.data_ptr(),
+                               0 if seqs is None else seqs.data_ptr(), self._at[2], self._at[3], k0, k1, v0, v1,
+                               *self._strides, B, shape[0], *self._rows))
 
     def attend(self, layer, q, starts, seqs=None, causal=True, scale=None):
         """:func:`attn_paged_fwd` over a layer."""

@@ -113,12 +113,26 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const __grid_constant_
     const char* v = static_cast<const char*>(a.v) + (size_t)t * a.v_row * 2;
     char* kp = static_cast<char*>(a.k_pages) + ((size_t)page * a.kp_page + (size_t)row * a.kp_row) * 2;
     char* vp = static_cast<char*>(a.v_pages) + ((size_t)page * a.vp_page + (size_t)row * a.vp_row) * 2;
-    for (int i = lane; i < all; i += 32) {
-      const int h = i / pieces, c = (i % pieces) * 16;
-      const uint4 x = *reinterpret_cast<const uint4*>(k + (size_t)h * a.k_head * 2 + c);
-      const uint4 y = *reinterpret_cast<const uint4*>(v + (size_t)h * a.v_head * 2 + c);
-      *reinterpret_cast<uint4*>(kp + (size_t)h * a.kp_head * 2 + c) = x;
-      *reinterpret_cast<uint4*>(vp + (size_t)h * a.vp_head * 2 + c) = y;
+    // kRows pieces of the keys and of the values in flight a lane
+    constexpr int kRows = 4;
+    for (int i0 = lane; i0 < all; i0 += 32 * kRows) {
+      uint4 x[kRows], y[kRows];
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        const int i = i0 + 32 * u, h = i / pieces, c = (i - h * pieces) * 16;
+        if (i < all) {
+          x[u] = __ldcs(reinterpret_cast<const uint4*>(k + (size_t)h * a.k_head * 2 + c));
+          y[u] = __ldcs(reinterpret_cast<const uint4*>(v + (size_t)h * a.v_head * 2 + c));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        const int i = i0 + 32 * u, h = i / pieces, c = (i - h * pieces) * 16;
+        if (i < all) {
+          *reinterpret_cast<uint4*>(kp + (size_t)h * a.kp_head * 2 + c) = x[u];
+          *reinterpret_cast<uint4*>(vp + (size_t)h * a.vp_head * 2 + c) = y[u];
+        }
+      }
     }
   }
 }

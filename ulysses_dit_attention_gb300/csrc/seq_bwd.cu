@@ -452,6 +452,11 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
     const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
     bool ok = true;
     uint32_t nq = 0, it = 0;
+    if (s.rest) {
+      const int* starts = s.starts_k ? s.starts_k : s.starts;
+      clear_rest(starts, s.B, s.Tk, x.dk, (long long)s.Hk * D, nullptr, 0, threadIdx.x, kComputeThreads);
+      clear_rest(starts, s.B, s.Tk, x.dv, (long long)s.Hk * D, nullptr, 0, threadIdx.x, kComputeThreads);
+    }
     Walk<KeyRow> w(share);
     while (ok && w.next(a)) {
       const int nt = w.j1 - w.j0, key = w.at.p * kBN + jrow;
@@ -885,6 +890,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     const int rt = row / a.g, rh = row - rt * a.g;
     bool ok = true;
     uint32_t g = 0, it = 0;
+    if (s.rest) clear_rest(s.starts, s.B, s.T, x.dq, (long long)s.Hq * D, nullptr, 0, threadIdx.x, kComputeThreads);
     await_previous();  // the rows' statistics, which the dK/dV kernel waited for before it let this one start
     Walk<Rows> w(share);
     while (ok && w.next(a)) {

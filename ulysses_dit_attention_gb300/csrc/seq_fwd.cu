@@ -629,6 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t colS = (uint32_t)(t * kBN);
     const int rt = row / a.g, rh = row - rt * a.g;  // token within the tile and head of the group
     const bool in_tile = rt < a.TT;
+    if (s.rest) clear_rest(s.starts, s.B, s.T, s.out, (long long)s.Hq * D, s.lse, s.Hq, threadIdx.x, 256);
     for (int par = 0;; par ^= 1) {
       named_sync(kBarI + t, kBarRelay);
       const Job job = jobs[2 * t + par];

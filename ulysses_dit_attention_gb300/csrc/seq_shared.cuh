@@ -75,6 +75,21 @@ __device__ __forceinline__ int seq_of_token(const int* starts, int B, int t) {
   return lo < B && starts[lo] <= t ? lo : -1;
 }
 
+// Zeros to the tokens of no sequence, before starts[0] and behind starts[B], of a (T, row) tensor of 16-bit elements: the
+// calling threads, `n` of them a block, take 16-byte pieces in turn.  lse: -inf beside them, of `heads` heads.
+__device__ __forceinline__ void clear_rest(const int* starts, int B, int T, void* x, long long row, float* lse, int heads,
+                                           int thread, int n) {
+  const int a = held_in(starts[0], 0, T), b = held_in(starts[B], a, T);
+  const long long head = (long long)a * row / 8, all = head + (long long)(T - b) * row / 8, skip = (long long)(b - a) * row / 8;
+  for (long long i = (long long)blockIdx.x * n + thread; i < all; i += (long long)gridDim.x * n)
+    static_cast<uint4*>(x)[i < head ? i : i + skip] = make_uint4(0u, 0u, 0u, 0u);
+  const long long none = T - (b - a);
+  for (long long i = (long long)blockIdx.x * n + thread; lse && i < none * heads; i += (long long)gridDim.x * n) {
+    const long long h = i / none, t = i - h * none;
+    lse[h * T + (t < a ? t : t + (b - a))] = -INFINITY;
+  }
+}
+
 __device__ __forceinline__ float load16(const void* p, size_t at, int fp16) {
   return fp16 ? __half2float(static_cast<const __half*>(p)[at]) : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]);
 }
@@ -86,13 +101,13 @@ __device__ __forceinline__ void store16(void* p, size_t at, float x, int fp16) {
 // ---------------------------------------------------------------------------
 // A row of items and its shares.  Each kernel works on tiles (of queries or of keys) of every sequence and key head, and
 // an item's inner loop runs over tiles of the other kind; the items of all sequences stand in a row, (sequence, head,
-// tile), weighed by the tokens that the inner loop meets plus kItemWork, and the row is cut into equal shares, one a CTA,
+// tile), weighed by the tokens that the inner loop meets plus those that its filling and draining
+// cost (`item`), and the row is cut into equal shares, one a CTA,
 // in the middle of an item where it falls so.  A kind of row says how many tiles a sequence has, how many inner tiles a
 // tile has and what the first p tiles weigh.
 constexpr int kBN = 128;  // keys of a tile
-// Weight of an item beside its tokens (its filling and draining), the least share of a CTA, and the least inner tiles of
-// a part.
-constexpr int kItemWork = 256, kLeastShare = 512, kLeastTiles = 2;
+// The least inner tiles of a share, and of a part.
+constexpr int kLeastShare = 4, kLeastTiles = 2;
 
 __device__ __forceinline__ int tiles_in(int x, int per) { return (x + per - 1) / per; }
 
@@ -105,21 +120,25 @@ struct QueryRow {
   static __device__ __forceinline__ int inner(const SeqArgs& a, const Seq& q, int p) {
     return tiles_in(keys_of(a.s, q, min(q.n, (p + 1) * width(a)) - 1), kBN);
   }
+  static __device__ __forceinline__ int unit(const SeqArgs&) { return kBN; }  // tokens of an inner tile
+  // A pair's costs 3 key tiles' time (4.4 us beside 1.44 us at D = 128) and the half tile that is rounded up; a single
+  // tile's (dQ) was measured: of 2, 3, 4 and 5 tiles 3 is the fastest or within 1 %.
+  static constexpr int item = kTilesOf2 == 2 ? 7 * kBN / 2 : 3 * kBN;
   int none;
-  long long flat, slope;  // kItemWork none + (P = p - none) flat + slope P (P + 1) / 2
+  long long flat, slope;  // item none + (P = p - none) flat + slope P (P + 1) / 2
   __device__ __forceinline__ QueryRow(const SeqArgs& a, const Seq& q) {
     const int W = width(a), off = q.m - q.n;
     none = a.s.causal && off < 0 ? -off / W : 0;
-    flat = kItemWork + (a.s.causal ? (long long)off + (long long)none * W : q.m);
+    flat = item + (a.s.causal ? (long long)off + (long long)none * W : q.m);
     slope = a.s.causal ? W : 0;
   }
   __device__ __forceinline__ long long of(int p) const {
     const long long P = p - none;
-    return P <= 0 ? (long long)kItemWork * p : (long long)kItemWork * none + P * flat + slope * (P * (P + 1) / 2);
+    return P <= 0 ? (long long)item * p : (long long)item * none + P * flat + slope * (P * (P + 1) / 2);
   }
   __device__ __forceinline__ int guess(long long w) const {
-    const float x = (float)(w - (long long)kItemWork * none);
-    if (x <= 0.f) return (int)((float)w / kItemWork);
+    const float x = (float)(w - (long long)item * none);
+    if (x <= 0.f) return (int)((float)w / item);
     if (!slope) return (int)(none + x / (float)flat);
     const float h = 0.5f * (float)slope, f = (float)flat + h;
     return (int)(none + 2.f * x / (f + sqrtf(f * f + 4.f * h * x)));
@@ -135,21 +154,23 @@ struct KeyRow {
   static __device__ __forceinline__ int inner(const SeqArgs& a, const Seq& q, int p) {
     return max(0, tiles_in(q.n, a.TT) - first(a, q, p));
   }
+  static __device__ __forceinline__ int unit(const SeqArgs& a) { return a.TT; }
+  int item;  // (of 1.5 to 8 inner tiles 4 to 7 are the fastest within 2 %)
   int full;  // the first tiles, which all queries read
   long long n, m;
-  __device__ __forceinline__ KeyRow(const SeqArgs& a, const Seq& q) : n(q.n), m(q.m) {
+  __device__ __forceinline__ KeyRow(const SeqArgs& a, const Seq& q) : item(11 * a.TT / 2), n(q.n), m(q.m) {
     full = !a.s.causal ? INT32_MAX : q.m >= q.n ? (q.m - q.n) / kBN + 1 : 0;
   }
   __device__ __forceinline__ long long of(int p) const {
     const long long f = min(p, full), P = p;
-    return P * kItemWork + f * n + (P - f) * m - kBN / 2 * (P * (P - 1) - f * (f - 1));
+    return P * item + f * n + (P - f) * m - kBN / 2 * (P * (P - 1) - f * (f - 1));
   }
   __device__ __forceinline__ int guess(long long w) const {
-    const long long f = (long long)full * (kItemWork + n);
-    const float flat = (float)(kItemWork + n);
+    const long long f = (long long)full * (item + n);
+    const float flat = (float)(item + n);
     if (w <= f) return (int)((float)w / flat);
     // behind the full tiles: x = b P - 64 P (P - 1) with P = p - full
-    const float x = (float)(w - f), b = (float)(kItemWork + m - (long long)kBN * full) + kBN / 2;
+    const float x = (float)(w - f), b = (float)(item + m - (long long)kBN * full) + kBN / 2;
     return full + (int)(2.f * x / (b + sqrtf(fmaxf(b * b - 2.f * kBN * x, 0.f))));
   }
 };
@@ -266,7 +287,7 @@ __device__ __forceinline__ Share find_share(const SeqArgs& a, uint8_t* scratch, 
       done += all;
     }
     if (pass == 0) {
-      const long long most = done / kLeastShare;
+      const long long most = done / (kLeastShare * Row::unit(a));
       const int shares = most < 1 ? 1 : most < ctas ? (int)most : ctas;
       if (cta >= shares) break;
       const long long each = done / shares;
