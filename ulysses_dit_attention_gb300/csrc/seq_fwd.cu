@@ -335,7 +335,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kind = 0; kind < 2; ++kind, ++n) {  // 0 = K_j, 1 = V_j
           const int slot = n % R;
           const uint32_t use = n / R;
-          if (lane == 0 && use > 0) ok = wait_or_abort(&ctl->bar_kv_empty[slot], (use - 1) & 1, ctx, ctl);
+          // (after a failure no further copy: the issuer goes on until it notices)
+          if (lane == 0)
+            ok = !*reinterpret_cast<volatile int*>(&ctl->abort) &&
+                 (use == 0 || wait_or_abort(&ctl->bar_kv_empty[slot], (use - 1) & 1, ctx, ctl));
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
           uint8_t* dst = smem + L::kRingOff + slot * L::kTileBytes;
