@@ -1084,10 +1084,16 @@ __global__ void __launch_bounds__(256) seq_bwd_join_kernel(const __grid_constant
 #pragma unroll 1
   for (int c0 = warp * cols; c0 < (warp + 1) * cols; c0 += 8) {
     float acc[8] = {};
-    each_part(first, c, ctas, nt, [&](int k) {
-      const float* p = part + (size_t)k * size + (size_t)c0 * 128;
+    each_part(first, c, ctas, nt, [&](const int (&ids)[kBatch]) {
+      float v[kBatch][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += p[e * 128];
+      for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[u][e] = ids[u] < 0 ? 0.f : part[(size_t)ids[u] * size + (size_t)(c0 + e) * 128];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] += v[u][e];
     });
     const bool dv = keys && c0 < D;
     const float f = dv ? 1.f : s.scale;

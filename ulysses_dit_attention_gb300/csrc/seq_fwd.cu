@@ -90,6 +90,14 @@ __device__ __forceinline__ void tma_store_4d(const void* smem_src, const CUtenso
       : "memory");
 }
 
+// The softmax warps take registers that the other four do not need: 256 x 200 + 128 x 96 of the 384 x 168 that the block is
+// launched with, which the host makes sure of (the softmax warps would wait for ever otherwise).  It keeps spills out of
+// their loop: 2048 tokens over 27280 keys 755 -> 729 us, 24 sequences in chunks 152 -> 145, 8192 tokens at D = 64 433 -> 425.
+constexpr int kLaunchRegs = 168;
+__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 96;"); }
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 200;"); }
+static_assert(256 * 200 + 128 * 96 <= 384 * kLaunchRegs, "registers of the block");
+
 template <bool kHalf>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   if constexpr (kHalf) {
@@ -213,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int cta = blockIdx.x, ctas = gridDim.x;
+  const int cta = blockIdx.x;
   const uaa_seqs& s = a.s;
   asm volatile("griddepcontrol.launch_dependents;");
 
@@ -256,375 +264,379 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t kv_armed[R] = {}, q_armed = 0;  // uses armed per barrier, for the teardown
   bool mma_issued = false;                 // set in the issuing lane once it has issued an MMA
 
-  if (warp == kProducerWarp) {
-    // ------------------------------------------------------------ producer
-    bool ok = true;
-    uint32_t n = 0;   // K/V ring counter across items
-    uint32_t ne = 0;  // items with at least one key tile
-    const int my_part = lane & 7, my_chunk = lane >> 3;  // paged: this lane's copy of a tile
-    Walk<Pairs> w(share);
-    while (ok && w.next(a)) {
-      const Item it = item_of(a, w);
-      if (it.c == 0) continue;
-      const int h = w.at.h;
-      if (lane == 0) {
-        if (ne > 0) ok = wait_or_abort(&ctl->bar_q_empty, (ne - 1) & 1, ctx, ctl);
-        if (ok) {
-          const int tiles = it.split ? 1 : 2;
-          mbar_arrive_expect_tx(&ctl->bar_q_full, tiles * kChunks * a.TT * a.g * 128);
-          for (int t = 0; t < tiles; ++t)
+  if (warp >= kProducerWarp) {
+    give_registers();
+    if (warp == kProducerWarp) {
+      // ------------------------------------------------------------ producer
+      bool ok = true;
+      uint32_t n = 0;   // K/V ring counter across items
+      uint32_t ne = 0;  // items with at least one key tile
+      const int my_part = lane & 7, my_chunk = lane >> 3;  // paged: this lane's copy of a tile
+      Walk<Pairs> w(share);
+      while (ok && w.next(a)) {
+        const Item it = item_of(a, w);
+        if (it.c == 0) continue;
+        const int h = w.at.h;
+        if (lane == 0) {
+          if (ne > 0) ok = wait_or_abort(&ctl->bar_q_empty, (ne - 1) & 1, ctx, ctl);
+          if (ok) {
+            const int tiles = it.split ? 1 : 2;
+            mbar_arrive_expect_tx(&ctl->bar_q_full, tiles * kChunks * a.TT * a.g * 128);
+            for (int t = 0; t < tiles; ++t)
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c)
-              tma_load_4d(smem + L::kQ + t * L::kTileBytes + c * kChunkBytes, &tmQ, &ctl->bar_q_full, c * 64, 0, h,
-                          w.q.q0 + (2 * w.at.p + t) * a.TT);
-          q_armed = ne + 1;
-        }
-      }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      ++ne;
-      // Paged: the table's entries, a lane's of a window of 32 and of the next one, read long before they are needed
-      const int per = kPaged ? (s.page < kBN ? kBN / s.page : 1) : 1;  // pages of a tile
-      const int held = kPaged ? (w.q.m + s.page - 1) / s.page : 0;
-      int base = 0, cur = -1, nxt = -1;
-      auto entry = [&](int e) {
-        const int i = e + lane;
-        return i < held ? s.table[(size_t)w.q.k0 * s.width + i] : -1;
-      };
-      auto first_page = [&](int j) { return s.page < kBN ? j * per : (int)((long long)j * kBN / s.page); };
-      if constexpr (kPaged) {
-        base = first_page(w.j0);
-        cur = entry(base);
-        nxt = entry(base + 32);
-      }
-      for (int j = w.j0; ok && j < w.j1; ++j) {
-        uint32_t words[4] = {~0u, ~0u, ~0u, ~0u};
-        // paged: first row within the page, rows of a copy, copies of a chunk that are made; this lane's copy
-        int row = 0, rows = 0, there = 0, my_page = -1;
-        if constexpr (kPaged) {
-          const int e = first_page(j);
-          if (e + per > base + 32) {
-            base += 32;
-            cur = nxt;
-            nxt = entry(base + 32);
+              for (int c = 0; c < kChunks; ++c)
+                tma_load_4d(smem + L::kQ + t * L::kTileBytes + c * kChunkBytes, &tmQ, &ctl->bar_q_full, c * 64, 0, h,
+                            w.q.q0 + (2 * w.at.p + t) * a.TT);
+            q_armed = ne + 1;
           }
-          row = s.page < kBN ? 0 : (int)((long long)j * kBN % s.page);
-          rows = s.page < kBN ? s.page : kBN;
-          my_page = __shfl_sync(0xffffffffu, cur, (e + my_part - base) & 31);
-          const bool asked = my_part < per && e + my_part < held;  // behind the sequence's end no page is asked for
-          const bool good = asked && my_page >= 0 && my_page < s.pages;
-          if (!good || my_chunk >= kChunks) my_page = -1;
-          there = __popc(__ballot_sync(0xffffffffu, good && my_chunk == 0));
-          const uint32_t gone = __ballot_sync(0xffffffffu, asked && !good && my_chunk == 0);  // bit x: part x
-          if (gone) {  // their keys have no weight
-            if (lane == 0) atomicOr(ctx.status, kStatusBadPage);
-            for (int x = 0; x < per; ++x)
-              if ((gone >> x) & 1u) {
-                if (rows >= 32) {
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ++ne;
+        // Paged: the table's entries, a lane's of a window of 32 and of the next one, read long before they are needed
+        const int per = kPaged ? (s.page < kBN ? kBN / s.page : 1) : 1;  // pages of a tile
+        const int held = kPaged ? (w.q.m + s.page - 1) / s.page : 0;
+        int base = 0, cur = -1, nxt = -1;
+        auto entry = [&](int e) {
+          const int i = e + lane;
+          return i < held ? s.table[(size_t)w.q.k0 * s.width + i] : -1;
+        };
+        auto first_page = [&](int j) { return s.page < kBN ? j * per : (int)((long long)j * kBN / s.page); };
+        if constexpr (kPaged) {
+          base = first_page(w.j0);
+          cur = entry(base);
+          nxt = entry(base + 32);
+        }
+        for (int j = w.j0; ok && j < w.j1; ++j) {
+          uint32_t words[4] = {~0u, ~0u, ~0u, ~0u};
+          // paged: first row within the page, rows of a copy, copies of a chunk that are made; this lane's copy
+          int row = 0, rows = 0, there = 0, my_page = -1;
+          if constexpr (kPaged) {
+            const int e = first_page(j);
+            if (e + per > base + 32) {
+              base += 32;
+              cur = nxt;
+              nxt = entry(base + 32);
+            }
+            row = s.page < kBN ? 0 : (int)((long long)j * kBN % s.page);
+            rows = s.page < kBN ? s.page : kBN;
+            my_page = __shfl_sync(0xffffffffu, cur, (e + my_part - base) & 31);
+            const bool asked = my_part < per && e + my_part < held;  // behind the sequence's end no page is asked for
+            const bool good = asked && my_page >= 0 && my_page < s.pages;
+            if (!good || my_chunk >= kChunks) my_page = -1;
+            there = __popc(__ballot_sync(0xffffffffu, good && my_chunk == 0));
+            const uint32_t gone = __ballot_sync(0xffffffffu, asked && !good && my_chunk == 0);  // bit x: part x
+            if (gone) {  // their keys have no weight
+              if (lane == 0) atomicOr(ctx.status, kStatusBadPage);
+              for (int x = 0; x < per; ++x)
+                if ((gone >> x) & 1u) {
+                  if (rows >= 32) {
 #pragma unroll
-                  for (int y = 0; y < 4; ++y)
-                    if (32 * y >= x * rows && 32 * y < (x + 1) * rows) words[y] = 0u;
-                } else {
+                    for (int y = 0; y < 4; ++y)
+                      if (32 * y >= x * rows && 32 * y < (x + 1) * rows) words[y] = 0u;
+                  } else {
 #pragma unroll
-                  for (int y = 0; y < 4; ++y)
-                    if (y == x >> 1) words[y] &= x & 1 ? 0x0000ffffu : 0xffff0000u;
+                    for (int y = 0; y < 4; ++y)
+                      if (y == x >> 1) words[y] &= x & 1 ? 0x0000ffffu : 0xffff0000u;
+                  }
+                }
+            }
+          }
+#pragma unroll
+          for (int kind = 0; kind < 2; ++kind, ++n) {  // 0 = K_j, 1 = V_j
+            const int slot = n % R;
+            const uint32_t use = n / R;
+            // (after a failure no further copy: the issuer goes on until it notices)
+            if (lane == 0)
+              ok = !*reinterpret_cast<volatile int*>(&ctl->abort) &&
+                   (use == 0 || wait_or_abort(&ctl->bar_kv_empty[slot], (use - 1) & 1, ctx, ctl));
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            uint8_t* dst = smem + L::kRingOff + slot * L::kTileBytes;
+            const CUtensorMap* map = kind == 0 ? &tmK : &tmV;
+            const bool drop = (int)n == ctx.drop_load;
+            if constexpr (kPaged) {
+              if (lane == 0) {
+                if (kind == 1) *reinterpret_cast<uint4*>(ctl->words[slot]) = make_uint4(words[0], words[1], words[2], words[3]);
+                if (!drop) {
+                  if (there) mbar_arrive_expect_tx(&ctl->bar_kv_full[slot], there * rows * 128 * kChunks);
+                  else mbar_arrive(&ctl->bar_kv_full[slot]);
                 }
               }
+              __syncwarp();
+              // a lane a copy
+              if (!drop && my_page >= 0)
+                tma_load_4d(dst + my_chunk * kChunkBytes + my_part * rows * 128, map, &ctl->bar_kv_full[slot], my_chunk * 64,
+                            h, row, my_page);
+              if (!drop) kv_armed[slot] = use + 1;
+            } else if (lane == 0 && !drop) {
+              mbar_arrive_expect_tx(&ctl->bar_kv_full[slot], L::kTileBytes);
+#pragma unroll
+              for (int c = 0; c < kChunks; ++c)
+                tma_load_4d(dst + c * kChunkBytes, map, &ctl->bar_kv_full[slot], c * 64, h, w.q.k0 + j * kBN, 0);
+              kv_armed[slot] = use + 1;
+            }
           }
         }
+      }
+    } else if (warp == kMmaWarp) {
+      // ------------------------------------------------------------ MMA issuer
+      // The whole warp runs the schedule and computes the descriptors, one elected lane waits and issues.
+      uint32_t el_lane;
+      const bool el = elect_one_sync(&el_lane);
+      bool ok = true;
+      uint32_t base = 0;  // ring counter of the item's first K
+      uint32_t ne = 0;    // items with at least one key tile
+      auto ring_addr = [&](uint32_t n) { return sbase + L::kRingOff + (n % R) * L::kTileBytes; };
+      auto wait_el = [&](uint64_t* bar, uint32_t parity) {
+        bool r = true;
+        if (el) r = wait_or_abort(bar, parity, ctx, ctl);
+        return __shfl_sync(0xffffffffu, r ? 1 : 0, el_lane) != 0;
+      };
+      auto wait_kv = [&](uint32_t n) { return wait_el(&ctl->bar_kv_full[n % R], (n / R) & 1); };
+      uint32_t kept_k = 0, kept_v = 0;  // the item's last K and V: their slots are the epilogue's, which releases them
+      auto release = [&](uint32_t n) {
+        if (el && n != kept_k && n != kept_v) mma_commit(&ctl->bar_kv_empty[n % R]);
+      };
+      auto issue_s = [&](int t, int qt, uint32_t nk) {
+        const uint64_t a0 = sdesc_sw128(sbase + L::kQ + qt * L::kTileBytes, 16, 1024);
+        const uint64_t b0 = sdesc_sw128(ring_addr(nk), 16, 1024);
 #pragma unroll
-        for (int kind = 0; kind < 2; ++kind, ++n) {  // 0 = K_j, 1 = V_j
-          const int slot = n % R;
-          const uint32_t use = n / R;
-          // (after a failure no further copy: the issuer goes on until it notices)
-          if (lane == 0)
-            ok = !*reinterpret_cast<volatile int*>(&ctl->abort) &&
-                 (use == 0 || wait_or_abort(&ctl->bar_kv_empty[slot], (use - 1) & 1, ctx, ctl));
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) break;
-          uint8_t* dst = smem + L::kRingOff + slot * L::kTileBytes;
-          const CUtensorMap* map = kind == 0 ? &tmK : &tmV;
-          const bool drop = (int)n == ctx.drop_load;
-          if constexpr (kPaged) {
-            if (lane == 0) {
-              if (kind == 1) *reinterpret_cast<uint4*>(ctl->words[slot]) = make_uint4(words[0], words[1], words[2], words[3]);
-              if (!drop) {
-                if (there) mbar_arrive_expect_tx(&ctl->bar_kv_full[slot], there * rows * 128 * kChunks);
-                else mbar_arrive(&ctl->bar_kv_full[slot]);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * kChunkBytes + (kk & 3) * 32;
+          const uint64_t x = desc_add(a0, off), y = desc_add(b0, off);
+          if (el) mma_ss_checked(mg, tmem + (uint32_t)(t * kBN), x, y, kIdescS, kk > 0, kBN);
+        }
+        if (el) mma_commit(&ctl->bar_s_full[t]);
+      };
+      auto issue_pv = [&](int t, uint32_t nv, bool acc) {
+        const uint64_t b0 = sdesc_sw128(ring_addr(nv), kChunkBytes, 1024);
+#pragma unroll
+        for (int kk = 0; kk < kBN / 16; ++kk) {
+          const uint64_t y = desc_add(b0, kk * 2048);
+          if (el)
+            mma_ts_checked(mg, tmem + 256 + (uint32_t)(t * D), tmem + (uint32_t)(t * kBN) + kk * 8, y, kIdescPV,
+                           (acc || kk > 0) ? 1u : 0u, D);
+        }
+        if (el) mma_commit(&ctl->bar_pv_done[t]);
+      };
+      Walk<Pairs> w(share);
+      while (w.next(a)) {
+        const Item it = item_of(a, w);
+        const int c = it.c;
+        if (c == 0) continue;
+        // After a failure anywhere in the CTA this warp stops issuing but still meets the softmax warps at every
+        // named barrier of the schedule.
+        if (ok && *reinterpret_cast<volatile int*>(&ctl->abort)) ok = false;
+        const int stride = it.split ? 2 : 1;
+        kept_k = base + 2 * stage_k(it);
+        kept_v = it.split ? kept_k : base + 2 * c - 1;
+        int left = it.n[0] + it.n[1];  // products S of this item that are still to come; behind the last the Q tiles are free
+        auto last_s = [&] {
+          if (--left == 0 && el) mma_commit(&ctl->bar_q_empty);
+        };
+        auto off = [&](int t, int i) { return (uint32_t)(it.split ? 2 * i + t : i); };  // key tile of slot t's step i
+        if (ok) ok = wait_el(&ctl->bar_q_full, ne & 1);
+        if (ok) ok = wait_kv(base);
+        if (ok) {
+          tc_fence_after();
+          if (it.n[0] > 0) {
+            issue_s(0, 0, base);
+            last_s();
+          }
+          if (it.split) release(base);
+          if (el) mma_issued = true;
+        }
+        if (it.n[1] > 0) {
+          if (ok && it.split) ok = wait_kv(base + 2);
+          if (ok) {
+            tc_fence_after();
+            issue_s(1, it.split ? 0 : 1, base + 2 * off(1, 0));
+            last_s();
+            release(base + 2 * off(1, 0));
+          }
+        }
+        const int steps = max(it.n[0], it.n[1]);
+        for (int i = 0; i < steps; ++i) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (i >= it.n[t]) continue;
+            const uint32_t nk = base + 2 * off(t, i), nv = nk + 1, nk1 = nk + 2 * stride;
+            // V has landed, and, where the slots share their keys, so has the next K: the relay warp waited
+            named_sync(kBarP + t, kBarPCount);
+            if (ok && i == 0 && ne > 0)  // the previous item's epilogue must have read O before the first P V overwrites it
+              ok = wait_el(&ctl->bar_o_free, (ne - 1) & 1);
+            if (ok) {
+              tc_fence_after();
+              issue_pv(t, nv, i > 0);
+              if (it.split || t == 1) release(nv);
+            }
+            if (i + 1 < it.n[t]) {
+              if (ok && it.split) ok = wait_kv(nk1);
+              if (ok) {
+                if (it.split) tc_fence_after();
+                issue_s(t, it.split ? 0 : t, nk1);
+                last_s();
+                if (it.split || t == 1) release(nk1);
               }
             }
             __syncwarp();
-            // a lane a copy
-            if (!drop && my_page >= 0)
-              tma_load_4d(dst + my_chunk * kChunkBytes + my_part * rows * 128, map, &ctl->bar_kv_full[slot], my_chunk * 64,
-                          h, row, my_page);
-            if (!drop) kv_armed[slot] = use + 1;
-          } else if (lane == 0 && !drop) {
-            mbar_arrive_expect_tx(&ctl->bar_kv_full[slot], L::kTileBytes);
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c)
-              tma_load_4d(dst + c * kChunkBytes, map, &ctl->bar_kv_full[slot], c * 64, h, w.q.k0 + j * kBN, 0);
-            kv_armed[slot] = use + 1;
           }
         }
-      }
-    }
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------ MMA issuer
-    // The whole warp runs the schedule and computes the descriptors, one elected lane waits and issues.
-    uint32_t el_lane;
-    const bool el = elect_one_sync(&el_lane);
-    bool ok = true;
-    uint32_t base = 0;  // ring counter of the item's first K
-    uint32_t ne = 0;    // items with at least one key tile
-    auto ring_addr = [&](uint32_t n) { return sbase + L::kRingOff + (n % R) * L::kTileBytes; };
-    auto wait_el = [&](uint64_t* bar, uint32_t parity) {
-      bool r = true;
-      if (el) r = wait_or_abort(bar, parity, ctx, ctl);
-      return __shfl_sync(0xffffffffu, r ? 1 : 0, el_lane) != 0;
-    };
-    auto wait_kv = [&](uint32_t n) { return wait_el(&ctl->bar_kv_full[n % R], (n / R) & 1); };
-    uint32_t kept_k = 0, kept_v = 0;  // the item's last K and V: their slots are the epilogue's, which releases them
-    auto release = [&](uint32_t n) {
-      if (el && n != kept_k && n != kept_v) mma_commit(&ctl->bar_kv_empty[n % R]);
-    };
-    auto issue_s = [&](int t, int qt, uint32_t nk) {
-      const uint64_t a0 = sdesc_sw128(sbase + L::kQ + qt * L::kTileBytes, 16, 1024);
-      const uint64_t b0 = sdesc_sw128(ring_addr(nk), 16, 1024);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = (kk >> 2) * kChunkBytes + (kk & 3) * 32;
-        const uint64_t x = desc_add(a0, off), y = desc_add(b0, off);
-        if (el) mma_ss_checked(mg, tmem + (uint32_t)(t * kBN), x, y, kIdescS, kk > 0, kBN);
-      }
-      if (el) mma_commit(&ctl->bar_s_full[t]);
-    };
-    auto issue_pv = [&](int t, uint32_t nv, bool acc) {
-      const uint64_t b0 = sdesc_sw128(ring_addr(nv), kChunkBytes, 1024);
-#pragma unroll
-      for (int kk = 0; kk < kBN / 16; ++kk) {
-        const uint64_t y = desc_add(b0, kk * 2048);
-        if (el)
-          mma_ts_checked(mg, tmem + 256 + (uint32_t)(t * D), tmem + (uint32_t)(t * kBN) + kk * 8, y, kIdescPV,
-                         (acc || kk > 0) ? 1u : 0u, D);
-      }
-      if (el) mma_commit(&ctl->bar_pv_done[t]);
-    };
-    Walk<Pairs> w(share);
-    while (w.next(a)) {
-      const Item it = item_of(a, w);
-      const int c = it.c;
-      if (c == 0) continue;
-      // After a failure anywhere in the CTA this warp stops issuing but still meets the softmax warps at every
-      // named barrier of the schedule.
-      if (ok && *reinterpret_cast<volatile int*>(&ctl->abort)) ok = false;
-      const int stride = it.split ? 2 : 1;
-      kept_k = base + 2 * stage_k(it);
-      kept_v = it.split ? kept_k : base + 2 * c - 1;
-      int left = it.n[0] + it.n[1];  // products S of this item that are still to come; behind the last the Q tiles are free
-      auto last_s = [&] {
-        if (--left == 0 && el) mma_commit(&ctl->bar_q_empty);
-      };
-      auto off = [&](int t, int i) { return (uint32_t)(it.split ? 2 * i + t : i); };  // key tile of slot t's step i
-      if (ok) ok = wait_el(&ctl->bar_q_full, ne & 1);
-      if (ok) ok = wait_kv(base);
-      if (ok) {
-        tc_fence_after();
-        if (it.n[0] > 0) {
-          issue_s(0, 0, base);
-          last_s();
-        }
-        if (it.split) release(base);
-        if (el) mma_issued = true;
-      }
-      if (it.n[1] > 0) {
-        if (ok && it.split) ok = wait_kv(base + 2);
-        if (ok) {
-          tc_fence_after();
-          issue_s(1, it.split ? 0 : 1, base + 2 * off(1, 0));
-          last_s();
-          release(base + 2 * off(1, 0));
-        }
-      }
-      const int steps = max(it.n[0], it.n[1]);
-      for (int i = 0; i < steps; ++i) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (i >= it.n[t]) continue;
-          const uint32_t nk = base + 2 * off(t, i), nv = nk + 1, nk1 = nk + 2 * stride;
-          // V has landed, and, where the slots share their keys, so has the next K: the relay warp waited
-          named_sync(kBarP + t, kBarPCount);
-          if (ok && i == 0 && ne > 0)  // the previous item's epilogue must have read O before the first P V overwrites it
-            ok = wait_el(&ctl->bar_o_free, (ne - 1) & 1);
-          if (ok) {
-            tc_fence_after();
-            issue_pv(t, nv, i > 0);
-            if (it.split || t == 1) release(nv);
-          }
-          if (i + 1 < it.n[t]) {
-            if (ok && it.split) ok = wait_kv(nk1);
-            if (ok) {
-              if (it.split) tc_fence_after();
-              issue_s(t, it.split ? 0 : t, nk1);
-              last_s();
-              if (it.split || t == 1) release(nk1);
-            }
-          }
-          __syncwarp();
-        }
-      }
-      base += 2 * c;
-      ++ne;
-    }
-  } else if (warp >= kRelayWarp) {
-    // ------------------------------------------------------------ relay warps
-    // All waits for copies and products on behalf of slot t's softmax warps, which wait on named barriers only: a test of
-    // an mbarrier takes 150 to 300 cycles beside the matrix instructions' shared-memory reads, even when it passes, and a
-    // named barrier about 30.  This warp also looks at V where P V could meet what it must not, tells the softmax warps
-    // what the next item is, and sends their rows out.  After a failure it keeps meeting the others.
-    const int t = warp - kRelayWarp;
-    bool ok = true;
-    uint32_t base = 0, g[2] = {0, 0}, ne = 0;  // ring counter; steps of the slots; items with a key tile
-    auto wait = [&](uint64_t* bar, uint32_t phase) {
-      if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bar, phase & 1, ctx, ctl));
-    };
-    Walk<Pairs> w(share);
-    Item it{};
-    int par = 0;
-    auto post = [&](bool more) {
-      Job* job = jobs + 2 * t + par;
-      if (lane == 0) {
-        if (!more) {
-          job->c = -1;
-        } else {
-          const int tok0 = (2 * w.at.p + (it.split ? 0 : t)) * a.TT;
-          job->c = it.c;
-          job->n = it.n[t];
-          job->j0 = w.j0;
-          job->lo = it.lo;
-          job->hi = it.hi;
-          job->flags = (it.split ? kSplit : 0) | (w.part ? kPart : 0) | (it.split && it.n[1] > 0 ? kJoin : 0) |
-                       (tok0 + a.TT <= w.q.n ? kFull : 0);
-          job->base = base;
-          job->stage = (t == 0 ? base + 2 * stage_k(it) : base + 2 * it.c - 1) % R;
-          job->tok0 = tok0;
-          job->h = w.at.h;
-          job->q = w.q;
-          job->ne = ne + 1;
-        }
-      }
-      __syncwarp();
-      par ^= 1;
-    };
-    bool more = w.next(a);
-    if (more) it = item_of(a, w);
-    post(more);
-    named_sync(kBarI + t, kBarRelay);
-    while (more) {
-      const int c = it.c;
-      if (c > 0) {
-        // V of step i: an infinity or a NaN in a row of V that not every row of the item reads becomes a zero, and the
-        // epilogue adds it to the rows that read it (dirty).  Slot 0 does it where the slots share V, since its product comes first.
-        auto look = [&](int i) {
-          const uint32_t o = it.split ? 2 * i + t : i, nv = base + 2 * o + 1;
-          const int j = w.j0 + (int)o;
-          if (!ok || (!it.split && t == 1 && i < it.n[0])) return;
-          uint4 words = make_uint4(~0u, ~0u, ~0u, ~0u);
-          if constexpr (kPaged) words = *reinterpret_cast<const uint4*>(ctl->words[nv % R]);
-          const bool whole = !kPaged || (words.x & words.y & words.z & words.w) == ~0u;
-          if (whole && (j + 1) * kBN <= it.lo) return;
-          bool bad = false;
-#pragma unroll 1
-          for (int wr = whole ? max(0, it.lo - j * kBN) & ~31 : 0; wr < kBN; wr += 32) {
-            uint4* v = reinterpret_cast<uint4*>(smem + L::kRingOff + (nv % R) * L::kTileBytes + wr * 128) + lane;
-            uint4 y[8 * kChunks];
-#pragma unroll
-            for (int x = 0; x < 8 * kChunks; ++x) y[x] = v[(x / 8) * (kChunkBytes / 16) + (x % 8) * 32];
-            uint32_t sum = 0;  // 0 as long as all are finite: an infinity or a NaN times 0 is a NaN
-#pragma unroll
-            for (int x = 0; x < 8 * kChunks; ++x)
-              sum = times0_plus<kHalf>(y[x].x, times0_plus<kHalf>(y[x].y, times0_plus<kHalf>(y[x].z, times0_plus<kHalf>(y[x].w, sum))));
-            if (!__any_sync(0xffffffffu, not_finite<kHalf>(sum))) continue;
-            const uint32_t mw = wr < 64 ? (wr < 32 ? words.x : words.y) : (wr < 96 ? words.z : words.w);
-#pragma unroll 1
-            for (int x = 0; x < 8 * kChunks; ++x) {
-              const int r = 4 * (x % 8) + (lane >> 3), key = j * kBN + wr + r;
-              uint4* p = v + (x / 8) * (kChunkBytes / 16) + (x % 8) * 32;
-              const uint4 z = *p;
-              if (key < it.lo && ((mw >> r) & 1u)) continue;  // every row reads it
-              if (!(not_finite<kHalf>(z.x) || not_finite<kHalf>(z.y) || not_finite<kHalf>(z.z) || not_finite<kHalf>(z.w)))
-                continue;
-              bad = true;
-              *p = make_uint4(finite_part<kHalf>(z.x), finite_part<kHalf>(z.y), finite_part<kHalf>(z.z),
-                              finite_part<kHalf>(z.w));
-            }
-          }
-          if (bad) *reinterpret_cast<volatile uint32_t*>(&ctl->dirty) = ne + 1;
-          fence_proxy_async_smem();
-          __syncwarp();
-        };
-        auto nv_of = [&](int i) { return base + 2 * (uint32_t)(it.split ? 2 * i + t : i) + 1; };
-        int looked = -1;
-        for (int i = 0; i < it.n[t]; ++i) {
-          const uint32_t nv = nv_of(i);
-          if (looked < i) {
-            wait(&ctl->bar_kv_full[nv % R], nv / R);
-            look(i);
-          }
-          wait(&ctl->bar_s_full[t], g[t] + i);
-          named_arrive(kBarF + t, kBarRelay);
-          looked = i;
-          if (i + 1 < it.n[t]) {
-            // the next V while the softmax warps are at work, if it is there; and the next K, where the slots share their
-            // keys (else the issuer waits for it: this V is not to wait for that K)
-            const uint32_t nv1 = nv_of(i + 1);
-            if (ok && __all_sync(0xffffffffu, mbar_test(&ctl->bar_kv_full[nv1 % R], (nv1 / R) & 1))) {
-              look(i + 1);
-              looked = i + 1;
-            }
-            if (!it.split) wait(&ctl->bar_kv_full[(nv + 1) % R], (nv + 1) / R);
-          }
-          // A rendezvous: so the softmax warps, whose next step waits for this warp, cannot come to this barrier again
-          // before the issuer has passed it, whatever failed.
-          named_sync(kBarP + t, kBarPCount);
-        }
-        // O is complete.  A slot without a step waits for the other's: it must not run ahead, into phases of its barriers
-        // that look like others.
-        if (it.n[t] > 0) wait(&ctl->bar_pv_done[t], g[t] + it.n[t] - 1);
-        if (it.n[t] == 0 || (t == 0 && it.split && it.n[1] > 0)) wait(&ctl->bar_pv_done[1 - t], g[1 - t] + it.n[1 - t] - 1);
-        named_arrive(kBarF + t, kBarRelay);
-      }
-      // where this item's rows go, for the copy below
-      const bool out = c > 0 && (t == 0 || !it.split);
-      const uint32_t stage = (t == 0 ? base + 2 * stage_k(it) : base + 2 * c - 1) % R;
-      const int tok0 = (2 * w.at.p + (it.split ? 0 : t)) * a.TT, h = w.at.h, token = w.q.q0 + tok0;
-      const bool full = !w.part && tok0 + a.TT <= w.q.n;
-      if (c > 0) {
-        g[0] += it.n[0];
-        g[1] += it.n[1];
         base += 2 * c;
         ++ne;
       }
-      more = w.next(a);
+    } else if (warp >= kRelayWarp) {
+      // ------------------------------------------------------------ relay warps
+      // All waits for copies and products on behalf of slot t's softmax warps, which wait on named barriers only: a test of
+      // an mbarrier takes 150 to 300 cycles beside the matrix instructions' shared-memory reads, even when it passes, and a
+      // named barrier about 30.  This warp also looks at V where P V could meet what it must not, tells the softmax warps
+      // what the next item is, and sends their rows out.  After a failure it keeps meeting the others.
+      const int t = warp - kRelayWarp;
+      bool ok = true;
+      uint32_t base = 0, g[2] = {0, 0}, ne = 0;  // ring counter; steps of the slots; items with a key tile
+      auto wait = [&](uint64_t* bar, uint32_t phase) {
+        if (ok) ok = __all_sync(0xffffffffu, wait_or_abort(bar, phase & 1, ctx, ctl));
+      };
+      Walk<Pairs> w(share);
+      Item it{};
+      int par = 0;
+      auto post = [&](bool more) {
+        Job* job = jobs + 2 * t + par;
+        if (lane == 0) {
+          if (!more) {
+            job->c = -1;
+          } else {
+            const int tok0 = (2 * w.at.p + (it.split ? 0 : t)) * a.TT;
+            job->c = it.c;
+            job->n = it.n[t];
+            job->j0 = w.j0;
+            job->lo = it.lo;
+            job->hi = it.hi;
+            job->flags = (it.split ? kSplit : 0) | (w.part ? kPart : 0) | (it.split && it.n[1] > 0 ? kJoin : 0) |
+                         (tok0 + a.TT <= w.q.n ? kFull : 0);
+            job->base = base;
+            job->stage = (t == 0 ? base + 2 * stage_k(it) : base + 2 * it.c - 1) % R;
+            job->tok0 = tok0;
+            job->h = w.at.h;
+            job->q = w.q;
+            job->ne = ne + 1;
+          }
+        }
+        __syncwarp();
+        par ^= 1;
+      };
+      bool more = w.next(a);
       if (more) it = item_of(a, w);
       post(more);
-      if (out) {
-        named_sync(kBarOut + t, kBarRelay);
-        if (lane == 0 && ok && full && guard_store(ctx, ((size_t)token * s.Hq + h * a.g) * D, D, o_extent)) {
+      named_sync(kBarI + t, kBarRelay);
+      while (more) {
+        const int c = it.c;
+        if (c > 0) {
+          // V of step i: an infinity or a NaN in a row of V that not every row of the item reads becomes a zero, and the
+          // epilogue adds it to the rows that read it (dirty).  Slot 0 does it where the slots share V, since its product comes first.
+          auto look = [&](int i) {
+            const uint32_t o = it.split ? 2 * i + t : i, nv = base + 2 * o + 1;
+            const int j = w.j0 + (int)o;
+            if (!ok || (!it.split && t == 1 && i < it.n[0])) return;
+            uint4 words = make_uint4(~0u, ~0u, ~0u, ~0u);
+            if constexpr (kPaged) words = *reinterpret_cast<const uint4*>(ctl->words[nv % R]);
+            const bool whole = !kPaged || (words.x & words.y & words.z & words.w) == ~0u;
+            if (whole && (j + 1) * kBN <= it.lo) return;
+            bool bad = false;
+#pragma unroll 1
+            for (int wr = whole ? max(0, it.lo - j * kBN) & ~31 : 0; wr < kBN; wr += 32) {
+              uint4* v = reinterpret_cast<uint4*>(smem + L::kRingOff + (nv % R) * L::kTileBytes + wr * 128) + lane;
+              uint4 y[8 * kChunks];
 #pragma unroll
-          for (int x = 0; x < kChunks; ++x)
-            tma_store_4d(smem + L::kRingOff + stage * L::kTileBytes + x * kChunkBytes, &tmO, x * 64, 0, h, token);
-          bulk_commit_group();
+              for (int x = 0; x < 8 * kChunks; ++x) y[x] = v[(x / 8) * (kChunkBytes / 16) + (x % 8) * 32];
+              uint32_t sum = 0;  // 0 as long as all are finite: an infinity or a NaN times 0 is a NaN
+#pragma unroll
+              for (int x = 0; x < 8 * kChunks; ++x)
+                sum = times0_plus<kHalf>(y[x].x, times0_plus<kHalf>(y[x].y, times0_plus<kHalf>(y[x].z, times0_plus<kHalf>(y[x].w, sum))));
+              if (!__any_sync(0xffffffffu, not_finite<kHalf>(sum))) continue;
+              const uint32_t mw = wr < 64 ? (wr < 32 ? words.x : words.y) : (wr < 96 ? words.z : words.w);
+#pragma unroll 1
+              for (int x = 0; x < 8 * kChunks; ++x) {
+                const int r = 4 * (x % 8) + (lane >> 3), key = j * kBN + wr + r;
+                uint4* p = v + (x / 8) * (kChunkBytes / 16) + (x % 8) * 32;
+                const uint4 z = *p;
+                if (key < it.lo && ((mw >> r) & 1u)) continue;  // every row reads it
+                if (!(not_finite<kHalf>(z.x) || not_finite<kHalf>(z.y) || not_finite<kHalf>(z.z) || not_finite<kHalf>(z.w)))
+                  continue;
+                bad = true;
+                *p = make_uint4(finite_part<kHalf>(z.x), finite_part<kHalf>(z.y), finite_part<kHalf>(z.z),
+                                finite_part<kHalf>(z.w));
+              }
+            }
+            if (bad) *reinterpret_cast<volatile uint32_t*>(&ctl->dirty) = ne + 1;
+            fence_proxy_async_smem();
+            __syncwarp();
+          };
+          auto nv_of = [&](int i) { return base + 2 * (uint32_t)(it.split ? 2 * i + t : i) + 1; };
+          int looked = -1;
+          for (int i = 0; i < it.n[t]; ++i) {
+            const uint32_t nv = nv_of(i);
+            if (looked < i) {
+              wait(&ctl->bar_kv_full[nv % R], nv / R);
+              look(i);
+            }
+            wait(&ctl->bar_s_full[t], g[t] + i);
+            named_arrive(kBarF + t, kBarRelay);
+            looked = i;
+            if (i + 1 < it.n[t]) {
+              // the next V while the softmax warps are at work, if it is there; and the next K, where the slots share their
+              // keys (else the issuer waits for it: this V is not to wait for that K)
+              const uint32_t nv1 = nv_of(i + 1);
+              if (ok && __all_sync(0xffffffffu, mbar_test(&ctl->bar_kv_full[nv1 % R], (nv1 / R) & 1))) {
+                look(i + 1);
+                looked = i + 1;
+              }
+              if (!it.split) wait(&ctl->bar_kv_full[(nv + 1) % R], (nv + 1) / R);
+            }
+            // A rendezvous: so the softmax warps, whose next step waits for this warp, cannot come to this barrier again
+            // before the issuer has passed it, whatever failed.
+            named_sync(kBarP + t, kBarPCount);
+          }
+          // O is complete.  A slot without a step waits for the other's: it must not run ahead, into phases of its barriers
+          // that look like others.
+          if (it.n[t] > 0) wait(&ctl->bar_pv_done[t], g[t] + it.n[t] - 1);
+          if (it.n[t] == 0 || (t == 0 && it.split && it.n[1] > 0)) wait(&ctl->bar_pv_done[1 - t], g[1 - t] + it.n[1 - t] - 1);
+          named_arrive(kBarF + t, kBarRelay);
+        }
+        // where this item's rows go, for the copy below
+        const bool out = c > 0 && (t == 0 || !it.split);
+        const uint32_t stage = (t == 0 ? base + 2 * stage_k(it) : base + 2 * c - 1) % R;
+        const int tok0 = (2 * w.at.p + (it.split ? 0 : t)) * a.TT, h = w.at.h, token = w.q.q0 + tok0;
+        const bool full = !w.part && tok0 + a.TT <= w.q.n;
+        if (c > 0) {
+          g[0] += it.n[0];
+          g[1] += it.n[1];
+          base += 2 * c;
+          ++ne;
+        }
+        more = w.next(a);
+        if (more) it = item_of(a, w);
+        post(more);
+        if (out) {
+          named_sync(kBarOut + t, kBarRelay);
+          if (lane == 0 && ok && full && guard_store(ctx, ((size_t)token * s.Hq + h * a.g) * D, D, o_extent)) {
+#pragma unroll
+            for (int x = 0; x < kChunks; ++x)
+              tma_store_4d(smem + L::kRingOff + stage * L::kTileBytes + x * kChunkBytes, &tmO, x * 64, 0, h, token);
+            bulk_commit_group();
+          }
+          __syncwarp();
+        }
+        named_sync(kBarI + t, kBarRelay);
+        if (out && lane == 0) {
+          bulk_wait_read_all();
+          if (ok) mbar_arrive(&ctl->bar_kv_empty[stage]);
         }
         __syncwarp();
       }
-      named_sync(kBarI + t, kBarRelay);
-      if (out && lane == 0) {
-        bulk_wait_read_all();
-        if (ok) mbar_arrive(&ctl->bar_kv_empty[stage]);
-      }
-      __syncwarp();
     }
   } else {
+    take_registers();
     // ------------------------------------------------------------ softmax warps
     const int t = warp >> 2;                 // slot
     const int row = (warp & 3) * 32 + lane;  // TMEM lane = row of the tile
@@ -765,6 +777,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
         const bool dirty = *reinterpret_cast<volatile uint32_t*>(&ctl->dirty) == job.ne;
         const int slot = part_of(cta, job.j0);
+        if (!join && !dirty && !part && nt > 0) {  // the usual way, 64 columns at a time
+#pragma unroll 1
+          for (int e = 0; e < D / 64; ++e) {
+            float y[64];
+            tmem_ld32x2(tl + 256 + t * D + 64 * e, tl + 256 + t * D + 64 * e + 32, y);
+#pragma unroll
+            for (int f = 0; f < 8; ++f)
+              *piece(lane, 8 * e + f) =
+                  make_uint4(pack2<kHalf>(y[8 * f + 0] * inv, y[8 * f + 1] * inv), pack2<kHalf>(y[8 * f + 2] * inv, y[8 * f + 3] * inv),
+                             pack2<kHalf>(y[8 * f + 4] * inv, y[8 * f + 5] * inv), pack2<kHalf>(y[8 * f + 6] * inv, y[8 * f + 7] * inv));
+          }
+        } else {
 #pragma unroll 1
         for (int e = 0; e < D / 32; ++e) {
           float y[32];
@@ -803,6 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   make_uint4(pack2<kHalf>(y[8 * f + 0] * inv, y[8 * f + 1] * inv), pack2<kHalf>(y[8 * f + 2] * inv, y[8 * f + 3] * inv),
                              pack2<kHalf>(y[8 * f + 4] * inv, y[8 * f + 5] * inv), pack2<kHalf>(y[8 * f + 6] * inv, y[8 * f + 7] * inv));
           }
+        }
         }
         if (!part && !(job.flags & kFull)) {
           __syncwarp();
@@ -852,20 +877,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// Joins the parts of the items that were cut.  Block (c - 1, x): the item that CTA c's share begins inside of, if no
-// earlier share does, rows 32 x .. 32 x + 31: a lane a row, a warp D / 8 columns.
+// Joins the parts of the items that were cut.  Block (c - 1, x, y): the item that CTA c's share begins inside of, if no
+// earlier share does, rows 32 x .. 32 x + 31, columns 64 y .. 64 y + 63: a lane a row, a warp 8 columns.
 template <int D, bool kPaged, bool kHalf>
-__global__ void __launch_bounds__(256) seq_join_kernel(const __grid_constant__ SeqArgs a, const Parts parts, int ctas,
-                                                       DevCtx ctx) {
+__global__ void __launch_bounds__(256, 4) seq_join_kernel(const __grid_constant__ SeqArgs a, const Parts parts, int ctas,
+                                                          DevCtx ctx) {
   constexpr float kLn2 = 0.6931471805599453f;
-  constexpr int kCols = D / 8;
+  constexpr int kCols = 8;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const uaa_seqs& s = a.s;
   const int c = blockIdx.x + 1;
   if (!leads(parts.first, c, s.B)) return;
   const Cut me = parts.first[c];
   const Seq q = load_seq<kPaged>(s, me.b);
-  const int lane = threadIdx.x & 31, r = blockIdx.y * 32 + lane, col = (threadIdx.x >> 5) * kCols;
+  const int lane = threadIdx.x & 31, r = blockIdx.y * 32 + lane, col = blockIdx.z * 64 + (threadIdx.x >> 5) * kCols;
   const int t = r >> 7, rt = (r & 127) / a.g, rh = (r & 127) - rt * a.g;
   const int tok = (2 * me.p + t) * a.TT + rt;
   const bool valid = rt < a.TT && tok < q.n;
@@ -875,14 +900,31 @@ __global__ void __launch_bounds__(256) seq_join_kernel(const __grid_constant__ S
 #pragma unroll
   for (int x = 0; x < kCols; ++x) acc[x] = 0.f;
   const int at = valid ? r : 0;
-  each_part(parts.first, c, ctas, nt, [&](int k) { top = fmaxf(top, part_stat(parts, k)[at].x); });
-  each_part(parts.first, c, ctas, nt, [&](int k) {
-    const float2 st = part_stat(parts, k)[at];
-    const float f = st.x == -INFINITY ? 0.f : ex2(st.x - top);
-    sum += st.y * f;
-    const float* o = part_o<D>(parts, k) + (size_t)col * parts.rows + at;
+  each_part(parts.first, c, ctas, nt, [&](const int (&ids)[kBatch]) {
+    float x[kBatch];
 #pragma unroll
-    for (int x = 0; x < kCols; ++x) acc[x] += o[(size_t)x * parts.rows] * f;
+    for (int u = 0; u < kBatch; ++u) x[u] = ids[u] < 0 ? -INFINITY : part_stat(parts, ids[u])[at].x;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) top = fmaxf(top, x[u]);
+  });
+  each_part(parts.first, c, ctas, nt, [&](const int (&ids)[kBatch]) {
+    float2 st[kBatch];
+    float o[kBatch][kCols];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (ids[u] < 0) continue;
+      st[u] = part_stat(parts, ids[u])[at];
+#pragma unroll
+      for (int x = 0; x < kCols; ++x) o[u][x] = part_o<D>(parts, ids[u])[(size_t)(col + x) * parts.rows + at];
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (ids[u] < 0) continue;
+      const float f = st[u].x == -INFINITY ? 0.f : ex2(st[u].x - top);
+      sum += st[u].y * f;
+#pragma unroll
+      for (int x = 0; x < kCols; ++x) acc[x] += o[u][x] * f;
+    }
   });
   if (!valid) return;
   const int hq = me.h * a.g + rh;
@@ -890,11 +932,9 @@ __global__ void __launch_bounds__(256) seq_join_kernel(const __grid_constant__ S
   if (!guard_store(ctx, oo, kCols, (size_t)s.T * s.Hq * D) || !guard_store(ctx, lo, 1, (size_t)s.Hq * s.T)) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   uint16_t* out = static_cast<uint16_t*>(s.out) + oo;
-#pragma unroll
-  for (int x = 0; x < kCols; x += 8)
-    *reinterpret_cast<uint4*>(out + x) =
-        make_uint4(pack2<kHalf>(acc[x] * inv, acc[x + 1] * inv), pack2<kHalf>(acc[x + 2] * inv, acc[x + 3] * inv),
-                   pack2<kHalf>(acc[x + 4] * inv, acc[x + 5] * inv), pack2<kHalf>(acc[x + 6] * inv, acc[x + 7] * inv));
+  *reinterpret_cast<uint4*>(out) =
+      make_uint4(pack2<kHalf>(acc[0] * inv, acc[1] * inv), pack2<kHalf>(acc[2] * inv, acc[3] * inv),
+                 pack2<kHalf>(acc[4] * inv, acc[5] * inv), pack2<kHalf>(acc[6] * inv, acc[7] * inv));
   if (col == 0) s.lse[lo] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
 }
 
@@ -934,6 +974,11 @@ int launch(const char* fn, const SeqArgs& a, const Parts& parts, cudaStream_t st
   if ((st = get_dev_ctx(&ctx))) return st;
   auto kern = seq_fwd_kernel<D, kPaged, kHalf>;
   const int smem = FwdLayout<D>::kSmem, ctas = device_sms();
+  static const int regs = [&] {
+    cudaFuncAttributes f{};
+    return cudaFuncGetAttributes(&f, kern) == cudaSuccess ? f.numRegs : 0;
+  }();
+  if (regs != kLaunchRegs) return set_error(UAA_ERR_CUDA, "%s: built with %d registers, not %d", fn, regs, kLaunchRegs);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return set_error(UAA_ERR_CUDA, "%s: smem attribute: %s", fn, cudaGetErrorString(e));
   kern<<<ctas, kThreads, smem, stream>>>(mq, mk, mv, mo, a, parts, s.scale * kLog2e, ctx);
@@ -945,7 +990,7 @@ int launch(const char* fn, const SeqArgs& a, const Parts& parts, cudaStream_t st
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(ctas - 1), (unsigned)(parts.rows / 32));
+  cfg.gridDim = dim3((unsigned)(ctas - 1), (unsigned)(parts.rows / 32), D / 64);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cfg.attrs = &attr;

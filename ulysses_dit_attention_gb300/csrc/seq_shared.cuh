@@ -77,7 +77,7 @@ __device__ __forceinline__ int seq_of_token(const int* starts, int B, int t) {
 
 // Zeros to the tokens of no sequence, before starts[0] and behind starts[B], of a (T, row) tensor of 16-bit elements: the
 // calling threads, `n` of them a block, take 16-byte pieces in turn.  lse: -inf beside them, of `heads` heads.
-__device__ __forceinline__ void clear_rest(const int* starts, int B, int T, void* x, long long row, float* lse, int heads,
+__device__ __noinline__ void clear_rest(const int* starts, int B, int T, void* x, long long row, float* lse, int heads,
                                            int thread, int n) {
   const int a = held_in(starts[0], 0, T), b = held_in(starts[B], a, T);
   const long long head = (long long)a * row / 8, all = head + (long long)(T - b) * row / 8, skip = (long long)(b - a) * row / 8;
@@ -236,6 +236,24 @@ __device__ __forceinline__ Share find_share(const SeqArgs& a, uint8_t* scratch, 
                                             unsigned int* status) {
   const uaa_seqs& s = a.s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x, ctas = gridDim.x;
+  auto weigh = [&](int b, Seq& q, bool tell) {
+    bool bad;
+    q = load_seq<kPaged>(s, b, &bad);
+    if (bad && tell && cta == 0) atomicOr(status, kStatusBadPage);
+    const int np = Row::tiles(a, q);
+    return np > 0 ? s.Hk * Row(a, q).of(np) : 0LL;
+  };
+  // The weights where this share begins and ends; false: there are fewer shares.
+  auto borders = [&](long long total, long long& w0, long long& w1) {
+    const long long most = total / (kLeastShare * Row::unit(a));
+    const int shares = most < 1 ? 1 : most < ctas ? (int)most : ctas;
+    if (cta >= shares) return false;
+    const long long each = total / shares;
+    const int rest = (int)(total - each * shares);
+    w0 = each * cta + rest * cta / shares;
+    w1 = each * (cta + 1) + rest * (cta + 1) / shares;
+    return true;
+  };
   long long* sums = reinterpret_cast<long long*>(scratch);  // a sum a warp
   Found* found = reinterpret_cast<Found*>(scratch + 256);
   Cut* cuts = reinterpret_cast<Cut*>(scratch + 384);
@@ -270,14 +288,7 @@ __device__ __forceinline__ Share find_share(const SeqArgs& a, uint8_t* scratch, 
     for (int b0 = 0; b0 < s.B; b0 += kThreads) {
       const int b = b0 + threadIdx.x;
       if (pass == 0 || s.B > kThreads) {
-        w = 0;
-        if (b < s.B) {
-          bool bad;
-          q = load_seq<kPaged>(s, b, &bad);
-          if (bad && cta == 0) atomicOr(status, kStatusBadPage);
-          const int np = Row::tiles(a, q);
-          if (np > 0) w = s.Hk * Row(a, q).of(np);
-        }
+        w = b < s.B ? weigh(b, q, true) : 0;
       }
       const long long at = done + scan(w, all);
       if (pass == 1 && w > 0) {
@@ -286,15 +297,7 @@ __device__ __forceinline__ Share find_share(const SeqArgs& a, uint8_t* scratch, 
       }
       done += all;
     }
-    if (pass == 0) {
-      const long long most = done / (kLeastShare * Row::unit(a));
-      const int shares = most < 1 ? 1 : most < ctas ? (int)most : ctas;
-      if (cta >= shares) break;
-      const long long each = done / shares;
-      const int rest = (int)(done - each * shares);
-      w0 = each * cta + rest * cta / shares;
-      w1 = each * (cta + 1) + rest * (cta + 1) / shares;
-    }
+    if (pass == 0 && !borders(done, w0, w1)) break;
   }
   __syncthreads();
   if (lane == 0 && warp < 2 && found[warp].b >= 0) cuts[warp] = cut_at<Row>(a, found[warp]);
@@ -357,16 +360,38 @@ struct Walk {
 __device__ __forceinline__ bool leads(const Cut* first, int c, int B) {
   return first[c].b < B && first[c].j > 0 && !(same_item(first[c], first[c - 1]) && first[c - 1].j > 0);
 }
+// (The whole warp calls; f gets kBatch parts at a time, so that their loads are in flight together, the last batch filled
+// up with -1.)
+constexpr int kBatch = 4;
 template <typename F>
 __device__ __forceinline__ void each_part(const Cut* first, int c, int ctas, int nt, F&& f) {
+  const int lane = threadIdx.x & 31;
   const Cut me = first[c];
-  f(2 * (c - 1) + 1);
-  for (int k = c; k < ctas; ++k) {
-    const Cut x = first[k];
-    if (!same_item(x, me)) break;
-    const int end = k + 1 < ctas && same_item(first[k + 1], me) ? first[k + 1].j : nt;
-    if (end > x.j) f(2 * k);
+  int ids[kBatch] = {2 * (c - 1) + 1, -1, -1, -1}, n = 1;
+  for (int k0 = c;; k0 += 32) {
+    const int k = k0 + lane;
+    bool same = false, some = false;
+    if (k < ctas) {
+      const Cut x = first[k], y = first[min(k + 1, ctas - 1)];
+      same = same_item(x, me);
+      some = same && (k + 1 < ctas && same_item(y, me) ? y.j : nt) > x.j;
+    }
+    const uint32_t all = __ballot_sync(0xffffffffu, same);
+    for (uint32_t left = __ballot_sync(0xffffffffu, some); left; left &= left - 1) {
+      if (n == kBatch) {
+        f(ids);
+        n = 0;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) ids[u] = -1;
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (u == n) ids[u] = 2 * (k0 + __ffs(left) - 1);
+      ++n;
+    }
+    if (all != 0xffffffffu) break;
   }
+  f(ids);
 }
 __device__ __forceinline__ int part_of(int cta, int j0) { return 2 * cta + (j0 > 0 ? 0 : 1); }
 
