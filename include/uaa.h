@@ -458,7 +458,8 @@ typedef struct {
   const int32_t* lens;      /* paged: device, (table_rows) */
   const int32_t* seqs;      /* paged: device, (B), or NULL */
   long long q_row, q_head, k_row, k_head, v_row, v_head, k_page, v_page; /* strides in elements, multiples of 8 */
-  int B, T, Tk, Hq, Hk, D;  /* D = 64 or 128; Hq a multiple of Hk, 128 times at most */
+  int B, T, Tk, Hq, Hk, D;  /* D = 64 or 128; Hq a multiple of Hk, 128 times at most; T, Tk and width * page at most
+                               2^30 */
   int dtype;                /* UAA_BF16 or UAA_FP16 (the backward: UAA_BF16) */
   int causal;
   int pages, page, table_rows, width; /* paged: a page is 16, 32, 64 or a multiple of 128 tokens */
@@ -481,8 +482,12 @@ int uaa_attn_paged_fwd(const uaa_seqs* args, void* workspace, size_t workspace_b
 /* Gradients of uaa_attn_packed_fwd (bf16), deterministic (no atomics).
  *   args           : the forward's, with its out and lse
  *   dout           : device, contiguous (T, Hq, D)
- *   dq; dk, dv     : device, contiguous (T, Hq, D); (Tk, Hk, D), written for the tokens of the sequences
- *   workspace      : device, at least uaa_attn_packed_bwd_workspace_bytes() bytes, 256-byte aligned
+ *   dq; dk, dv     : device, contiguous (T, Hq, D); (Tk, Hk, D), written for the tokens of the sequences; they must not
+ *                    overlap the inputs nor each other
+ *   workspace      : device, at least uaa_attn_packed_bwd_workspace_bytes() bytes, 256-byte aligned; contents on entry
+ *                    are ignored.  Calls that may overlap need workspaces of their own.
+ * An infinity or a NaN in what a token of a sequence has in q, k, v or dout may show in the gradients of any token of
+ * the same sequence, whether they read one another or not; in those of other sequences it leaves no trace.
  * Returns UAA_OK or a negative uaa_status. */
 size_t uaa_attn_packed_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int D);
 int uaa_attn_packed_bwd(const uaa_seqs* args, const void* dout, void* dq, void* dk, void* dv, void* workspace,
@@ -505,6 +510,7 @@ typedef struct {
   int row_bytes;          /* bytes of a token's keys of one layer, a multiple of 16 */
 } uaa_pools;
 
+/* width * page at most 2^30, seqs * width at most 2^28. */
 int uaa_pages_create(uaa_pages** out, int pages, int page, int seqs, int width);
 void uaa_pages_destroy(uaa_pages* p);
 
@@ -533,7 +539,9 @@ int uaa_pages_free(uaa_pages* p);
  * lens[r] - n + i of sequence r = seqs[b] (seqs NULL: b), n = starts[b+1] - starts[b].
  *   k, v     : device, (T, Hk, D) of 2-byte elements, strides k_row, k_head, v_row, v_head, heads contiguous
  *   k_pages, v_pages : device, the layer's pools (pages, page, Hk, D) with strides *_page, *_row, *_head of the pools
- * Rows of a page that lies outside the cache, and of positions below 0, are skipped (UAA_ERR_BAD_PAGE). */
+ * Rows of a page that lies outside the cache, and of positions below 0, are skipped (UAA_ERR_BAD_PAGE).  No row of the
+ * table is named twice in one call, nor do two of them hold the page that is written to (uaa_pages_append sees to it):
+ * which of two tokens stays in a row would be undefined. */
 typedef struct {
   const void *k, *v;
   void *k_pages, *v_pages;
@@ -573,7 +581,8 @@ void uaa_debug_drop_load(int n);
 
 /* Diagnostic of the debug build, for tests of the order of waits: while warp >= 0,
  * that warp of every block of the attention kernels launched afterwards comes `ns`
- * nanoseconds (1000000 at most) late to each of its waits for a copy or a product.
+ * nanoseconds (1000000 at most) late to each of its waits for a copy or a product
+ * (the softmax warps of packed and paged attention: to each way out of an item).
  * Results must not change.  warp < 0 turns it off.  Returns UAA_OK,
  * UAA_ERR_INVALID_ARG, or UAA_ERR_UNSUPPORTED from the other builds. */
 int uaa_debug_late_warp(int warp, unsigned int ns);

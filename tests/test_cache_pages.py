@@ -56,6 +56,19 @@ def err():
     return uaa.lib().uaa_last_error().decode()
 
 
+def test_refusal_of_too_many_tokens():
+    assert Host(4, 1024, 2, 2 ** 20).status == 0
+    assert Host(4, 1024, 2, 2 ** 20 + 1).status == -2 and "table" in err()
+
+
+def test_the_tensors_keep_their_places():
+    """The calls hold the tensors' addresses: no other tensor takes their places."""
+    c = uaa.PagedCache(1, 2, 16, 1, 64, 2, 2, device="cpu")
+    for name in ("k", "v", "table", "lens", "page", "seqs"):
+        with pytest.raises(AttributeError):
+            setattr(c, name, getattr(c, name))
+
+
 def test_refusals():
     L = uaa.lib()
     assert L.uaa_pages_create(None, 4, 16, 2, 2) == -1

@@ -208,6 +208,31 @@ def test_a_late_warp_changes_nothing(lens, Hq, Hk, D, causal):
             assert np.array_equal(bits(got[n]), bits(want[n])), (warp, n)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_values_that_are_not_finite_in_every_item(D):
+    """Items in a row with infinities and NaNs in the values that only some of their rows read, whichever warp comes late."""
+    n, Hq, m = 256, 24, 128
+    x = draw([n] * 40, [n] * 40, Hq, Hq, D, seed=53)
+    bad = torch.arange(m - 1, n, m)  # the last key of each tile of keys
+    v = x["v"].view(40, n, Hq, D)
+    v[:, bad, :, 3] = float("inf")
+    v[:, bad, :, 5] = float("nan")
+    reads = torch.arange(n)[None, :, None] >= bad[0]
+    late = range(8) if uaa.debug_build() else ()
+    for warp in (-1, *late):
+        if warp >= 0:
+            uaa.debug_late_warp(warp, 1000000)  # longer than a way out with such values takes
+        try:
+            out = step(x, grads=False)["out"].cpu().float().view(40, n, Hq, D)
+        finally:
+            if warp >= 0:
+                uaa.debug_late_warp()
+        assert torch.equal(torch.isinf(out[..., 3]), reads.expand(40, n, Hq)), warp
+        assert torch.equal(torch.isnan(out[..., 5]), reads.expand(40, n, Hq)), warp
+        out[..., 3] = out[..., 5] = 0
+        assert torch.isfinite(out).all(), warp
+
+
 @pytest.mark.parametrize("news,lens", [([1] * 30, [900] * 30), ([1, 200, 7, 1], [3000, 700, 129, 1])], ids=["tokens", "chunks"])
 def test_a_late_warp_changes_nothing_over_pages(news, lens):
     if not uaa.debug_build():
@@ -227,7 +252,7 @@ def test_a_late_warp_changes_nothing_over_pages(news, lens):
 # --------------------------------------------------------------------------- the debug build
 @pytest.mark.parametrize("selection,least", [
     (["tests/test_packed_attention.py", "tests/test_paged_attention.py", "tests/test_cache_pages.py"], 300),
-    (["tests/test_gpu_sequences.py", "-k", "late_warp or stores_stay or many"], 30)])
+    (["tests/test_gpu_sequences.py", "-k", "late_warp or stores_stay or many or every_item"], 30)])
 def test_under_the_debug_build(selection, least):
     """The operators' tests once more in a child process whose library checks every tensor-core operand and store."""
     if uaa.debug_build():

@@ -101,6 +101,16 @@ def test_refusals_of_the_call():
     assert uaa.attn_seqs_workspace_bytes(1, -1, 4, 2, 64) == 0
 
 
+@pytest.mark.parametrize("kw", [dict(T=2 ** 30 + 1, Hq=1, Hk=1), dict(Tk=2 ** 30 + 1, Hq=1, Hk=1)])
+def test_refusal_of_too_many_tokens(kw):
+    L, P = uaa.lib(), ctypes.c_void_p
+    assert L.uaa_attn_packed_fwd(args(**kw), P(1 << 24), 1 << 40, None) == -2
+    assert "2^30 tokens" in L.uaa_last_error().decode()
+    f = P(1 << 20)
+    assert L.uaa_attn_packed_bwd(args(**kw), f, f, f, f, P(1 << 24), 1 << 40, None) == -2
+    assert "2^30 tokens" in L.uaa_last_error().decode()
+
+
 def test_refusals_of_the_binding():
     x = torch.zeros(10, 4, 64, dtype=torch.bfloat16)
     kv = torch.zeros(10, 2, 64, dtype=torch.bfloat16)
@@ -463,3 +473,19 @@ def test_starts_that_are_wrong_stay_inside():
         uaa.attn_packed_bwd(y["q"], y["k"], y["v"], out, y["do"], lse, st, dq=dq, dk=dk, dv=dv, workspace=ws)
         uaa.check_device_status()
         g.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,D", [(1, 64), (70, 128)])
+def test_no_sequence_at_all(T, D):
+    """No sequence: every token belongs to none, on memory that is not fresh."""
+    q, k, v = (torch.randn(T, h, D, device=DEV, dtype=torch.bfloat16).requires_grad_() for h in (4, 2, 2))
+    starts = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for _ in range(2):
+        keep = [torch.full_like(t, float("nan")) for t in (q, q, k, v)] + [torch.full((4, T), float("nan"), device=DEV)]
+        torch.cuda.synchronize()
+        del keep
+        out, lse = uaa.packed_attention(q, k, v, starts)
+        grads = torch.autograd.grad(out, (q, k, v), torch.ones_like(out))
+        assert torch.isneginf(lse).all() and not any(t.any() for t in (out,) + grads)
+    uaa.check_device_status()

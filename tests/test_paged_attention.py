@@ -57,6 +57,13 @@ def test_refusals_of_the_call():
     assert write(T=0, k=0) == 0 and write(B=0, k=0) == 0
 
 
+def test_refusal_of_too_many_tokens():
+    L, P, f = uaa.lib(), ctypes.c_void_p, 1 << 20
+    x = dict(table=f, lens=f, k_page=2048, v_page=2048, pages=9, page=1024, table_rows=2, width=2 ** 20 + 1)
+    assert L.uaa_attn_paged_fwd(args(**x), P(1 << 24), 1 << 40, None) == -2
+    assert "2^30 tokens" in L.uaa_last_error().decode()
+
+
 def test_refusals_of_the_binding():
     q, kv = torch.zeros(3, 4, 64, dtype=torch.bfloat16), torch.zeros(5, 16, 2, 64, dtype=torch.bfloat16)
     starts, lens = torch.tensor([0, 3], dtype=torch.int32), torch.zeros(2, dtype=torch.int32)

@@ -922,7 +922,9 @@ def attn_packed_bwd_workspace_bytes(B, T, Hq, Hk, D) -> int:
 
 def attn_packed_bwd(q, k, v, out, dout, lse, starts, starts_k=None, causal=True, scale=None, dq=None, dk=None, dv=None,
                     workspace=None):
-    """``uaa_attn_packed_bwd``: the gradients ``(dq, dk, dv)`` of :func:`attn_packed_fwd` (bf16)."""
+    """``uaa_attn_packed_bwd``: the gradients ``(dq, dk, dv)`` of :func:`attn_packed_fwd` (bf16).
+
+    An infinity or a NaN of a token may show in the gradients of any token of its own sequence; other sequences' stay clean."""
     if out is None or lse is None:
         raise ValueError("out and lse are the forward's results")
     return _packed_bwd(q, k, v, out, dout, lse, starts, starts_k, causal, scale, dq, dk, dv, workspace, 0)
@@ -980,7 +982,11 @@ class PackedAttention(torch.autograd.Function):
 
 
 def packed_attention(q, k, v, starts, starts_k=None, causal=True, scale=None, saved=None):
-    """Differentiable :func:`attn_packed_fwd`: returns ``(out, lse)``."""
+    """Differentiable :func:`attn_packed_fwd`: returns ``(out, lse)``.  ``saved`` and tokens of no sequence:
+    :class:`PackedAttention`.
+
+    To capture a step with its gradients in a CUDA graph, warm up on another stream and let no eager autograd graph
+    of the same leaves live: PyTorch ties a leaf's gradients to the stream of the first graph that holds it."""
     return PackedAttention.apply(q, k, v, starts, starts_k, causal, scale, saved)
 
 
@@ -1066,15 +1072,22 @@ class PagedCache:
             raise ValueError(f"layers={layers} and heads={heads} must be positive, dim={dim} 64 or 128")
         self._h = _P()
         _check(lib().uaa_pages_create(ctypes.byref(self._h), pages, page, seqs, width))
-        self.page, self.seqs = page, seqs
-        self.k, self.v = (torch.empty((layers, pages, page, heads, dim), dtype=dtype, device=device) for _ in range(2))
-        self.table = torch.full((seqs, width), -1, dtype=torch.int32, device=device)
-        self.lens = torch.zeros(seqs, dtype=torch.int32, device=device)
-        self._at = tuple(t.data_ptr() for t in (self.k, self.v, self.table, self.lens))
+        self._k, self._v = (torch.empty((layers, pages, page, heads, dim), dtype=dtype, device=device) for _ in range(2))
+        self._table = torch.full((seqs, width), -1, dtype=torch.int32, device=device)
+        self._lens = torch.zeros(seqs, dtype=torch.int32, device=device)
+        self._at = tuple(t.data_ptr() for t in (self._k, self._v, self._table, self._lens))
         self._pools = _POOLS.pack(*self._at, layers, heads * dim * 2)
         self._strides = (page * heads * dim, heads * dim, dim) * 2
         self._rows = (heads, dim, pages, page, seqs, width)
         self._layer_bytes = pages * page * heads * dim * 2
+
+    # The calls hold the tensors' addresses, so other tensors cannot take their places.
+    k = property(lambda self: self._k)
+    v = property(lambda self: self._v)
+    table = property(lambda self: self._table)
+    lens = property(lambda self: self._lens)
+    page = property(lambda self: self._rows[3])
+    seqs = property(lambda self: self._rows[4])
 
     def __del__(self):
         if getattr(self, "_h", None) and _lib is not None:
@@ -1103,7 +1116,7 @@ class PagedCache:
         a, b = array.array("i", a), array.array("i", b)
         if len(a) != len(b):
             raise ValueError(f"{len(a)} and {len(b)} entries")
-        _call(self.k.device, name, self._h, self._pools, len(a), a.buffer_info()[0], b.buffer_info()[0])
+        _call(self._k.device, name, self._h, self._pools, len(a), a.buffer_info()[0], b.buffer_info()[0])
 
     def append(self, seqs, counts):
         """Makes room for ``counts[i]`` more tokens of sequence ``seqs[i]``; a shared, partly filled last page is
@@ -1111,7 +1124,7 @@ class PagedCache:
         a, b = array.array("i", seqs), array.array("i", counts)
         if len(a) != len(b):
             raise ValueError(f"{len(a)} sequences and {len(b)} counts")
-        n, dev = len(a), self.k.device
+        n, dev = len(a), self._k.device
         both = torch.empty(2 * n + 1, dtype=torch.int32, device=dev)
         starts, ids = both[: n + 1], both[n + 1:]
         at = both.data_ptr()
@@ -1134,11 +1147,11 @@ class PagedCache:
 
     def compact(self):
         """Moves pages so that those in use are the lowest ones."""
-        _call(self.k.device, "uaa_pages_compact", self._h, self._pools)
+        _call(self._k.device, "uaa_pages_compact", self._h, self._pools)
 
     def write(self, layer, k, v, starts, seqs=None):
         """:func:`cache_write` into a layer."""
-        pools, shape = self.k, k.shape
+        pools, shape = self._k, k.shape
         if k.dtype != pools.dtype or v.dtype != pools.dtype:
             raise TypeError(f"k and v must be {pools.dtype}")
         if shape != v.shape or len(shape) != 3 or shape[1] != self._rows[0] or shape[2] != self._rows[1]:

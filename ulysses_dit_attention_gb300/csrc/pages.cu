@@ -295,7 +295,7 @@ extern "C" int uaa_pages_create(uaa_pages** out, int pages, int page, int seqs, 
       return set_error(UAA_ERR_INVALID_ARG, "%s: pages=%d seqs=%d width=%d must be positive", fn, pages, seqs, width);
     if (page != 16 && page != 32 && page != 64 && (page < 128 || page % 128 || page > 65536))
       return set_error(UAA_ERR_UNSUPPORTED, "%s: pages of %d tokens (16, 32, 64 or a multiple of 128)", fn, page);
-    if ((long long)seqs * width > (1 << 28) || (long long)width * page > INT_MAX)
+    if ((long long)seqs * width > (1 << 28) || (long long)width * page > (1 << 30))
       return set_error(UAA_ERR_UNSUPPORTED, "%s: a table of %d x %d pages of %d tokens", fn, seqs, width, page);
     uaa_pages* p = new uaa_pages;
     try {

@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(256) seq_stats_kernel(const __grid_constant__ 
   const SeqArgs& a = x.a;
   const uaa_seqs& s = a.s;
   allow_next();
+  if (s.B == 0) return;
   const int slot = blockIdx.x, hk = blockIdx.y;
   int lo = 0, hi = s.B - 1;  // the last b whose first slot is not behind this one
   while (lo < hi) {
@@ -1197,7 +1198,7 @@ extern "C" int uaa_attn_packed_bwd(const uaa_seqs* s, const void* dout, void* dq
   int st = check_seqs(fn, s, false, true);
   if (st) return st;
   if (s->dtype != UAA_BF16) return set_error(UAA_ERR_UNSUPPORTED, "%s: the backward is built for bf16", fn);
-  if (s->B == 0 || (s->T == 0 && s->Tk == 0)) return UAA_OK;
+  if ((s->B == 0 && !s->rest) || (s->T == 0 && s->Tk == 0)) return UAA_OK;
   if (s->T > 0 && ((st = check_dev_ptr(fn, "dout", dout)) || (st = check_dev_ptr(fn, "dq", dq)))) return st;
   if (s->Tk > 0 && ((st = check_dev_ptr(fn, "dk", dk)) || (st = check_dev_ptr(fn, "dv", dv)))) return st;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))

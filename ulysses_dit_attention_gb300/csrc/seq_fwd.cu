@@ -30,6 +30,8 @@
 // NaN there becomes a zero, and the epilogue adds it to the rows that do read it.
 #include <float.h>
 
+#include <atomic>
+
 #include "seq_shared.cuh"
 
 namespace uaa {
@@ -69,7 +71,8 @@ struct FwdCtl {
   uint64_t bar_o_free, bar_final;
   uint32_t tmem_base;
   int abort;
-  uint32_t dirty;                          // the last item with an infinity or a NaN taken out of V
+  uint32_t dirty[2];  // the last even and odd item with an infinity or a NaN taken out of V (a relay warp can be at V of
+                      // the next item while the other slot is in this one's epilogue, but not at that of one further)
   alignas(16) uint32_t words[10][4];       // paged, per ring slot: keys whose page is there (filled with V)
 };
 static_assert(sizeof(FwdCtl) <= 512, "control block");
@@ -239,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&ctl->bar_o_free, 256);
     mbar_init(&ctl->bar_final, 1);
     ctl->abort = 0;
-    ctl->dirty = 0;
+    ctl->dirty[0] = ctl->dirty[1] = 0;
     fence_mbar_init();
   }
   if (warp == kProducerWarp && lane == 0) {
@@ -568,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 finite_part<kHalf>(z.w));
               }
             }
-            if (bad) *reinterpret_cast<volatile uint32_t*>(&ctl->dirty) = ne + 1;
+            if (bad) *reinterpret_cast<volatile uint32_t*>(&ctl->dirty[(ne + 1) & 1]) = ne + 1;
             fence_proxy_async_smem();
             __syncwarp();
           };
@@ -743,6 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float f0 = 1.f, f1 = 0.f;
       named_sync(kBarF + t, kBarRelay);  // O is complete: this slot's, and for slot 0 of a joined item both
+      dbg_late(ctx);
       if (join) {
         // slot 1's rows go to the threads of slot 0, which own the same TMEM lanes; the readers of the sums before these
         // are through, since this item's first P V waited for them
@@ -775,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       if (busy) {
         const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
-        const bool dirty = *reinterpret_cast<volatile uint32_t*>(&ctl->dirty) == job.ne;
+        const bool dirty = *reinterpret_cast<volatile uint32_t*>(&ctl->dirty[job.ne & 1]) == job.ne;
         const int slot = part_of(cta, job.j0);
         if (!join && !dirty && !part && nt > 0) {  // the usual way, 64 columns at a time
 #pragma unroll 1
@@ -974,12 +978,17 @@ int launch(const char* fn, const SeqArgs& a, const Parts& parts, cudaStream_t st
   if ((st = get_dev_ctx(&ctx))) return st;
   auto kern = seq_fwd_kernel<D, kPaged, kHalf>;
   const int smem = FwdLayout<D>::kSmem, ctas = device_sms();
-  static const int regs = [&] {
+  static std::atomic<bool> checked{false};
+  cudaError_t e;
+  if (!checked.load(std::memory_order_relaxed)) {
     cudaFuncAttributes f{};
-    return cudaFuncGetAttributes(&f, kern) == cudaSuccess ? f.numRegs : 0;
-  }();
-  if (regs != kLaunchRegs) return set_error(UAA_ERR_CUDA, "%s: built with %d registers, not %d", fn, regs, kLaunchRegs);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if ((e = cudaFuncGetAttributes(&f, kern)) != cudaSuccess)
+      return set_error(UAA_ERR_CUDA, "%s: kernel attributes: %s", fn, cudaGetErrorString(e));
+    if (f.numRegs != kLaunchRegs)
+      return set_error(UAA_ERR_CUDA, "%s: built with %d registers a thread, not %d", fn, f.numRegs, kLaunchRegs);
+    checked.store(true, std::memory_order_relaxed);
+  }
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return set_error(UAA_ERR_CUDA, "%s: smem attribute: %s", fn, cudaGetErrorString(e));
   kern<<<ctas, kThreads, smem, stream>>>(mq, mk, mv, mo, a, parts, s.scale * kLog2e, ctx);
   if ((st = check_launch(fn))) return st;
@@ -1004,7 +1013,7 @@ template <bool kPaged>
 int seq_fwd(const char* fn, const uaa_seqs* s, void* workspace, size_t bytes, cudaStream_t stream) {
   int st = check_seqs(fn, s, kPaged);
   if (st) return st;
-  if (s->T == 0 || s->B == 0) return UAA_OK;
+  if (s->T == 0 || (s->B == 0 && !s->rest)) return UAA_OK;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return set_error(UAA_ERR_INVALID_ARG, "%s: workspace is NULL or not 256-byte aligned", fn);
   const SeqArgs a = seq_args(*s);

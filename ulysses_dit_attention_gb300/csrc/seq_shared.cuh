@@ -106,6 +106,7 @@ __device__ __forceinline__ void store16(void* p, size_t at, float x, int fp16) {
 // in the middle of an item where it falls so.  A kind of row says how many tiles a sequence has, how many inner tiles a
 // tile has and what the first p tiles weigh.
 constexpr int kBN = 128;  // keys of a tile
+constexpr int kMostTokens = 1 << 30;  // of a tensor, or of a sequence's pages: places are 32-bit sums of them and a tile
 // The least inner tiles of a share, and of a part.
 constexpr int kLeastShare = 4, kLeastTiles = 2;
 
@@ -413,9 +414,11 @@ int check_seqs(const char* fn, const uaa_seqs* s, bool paged, bool bwd = false) 
   if (s->B > 65535 || s->Hq > 65535) return set_error(UAA_ERR_UNSUPPORTED, "%s: B and Hq must be <= 65535", fn);
   if ((long long)s->T * s->Hq >= (1LL << 32) - 1 || (long long)s->Tk * s->Hk >= (1LL << 32) - 1)
     return set_error(UAA_ERR_UNSUPPORTED, "%s: 2^32 rows of one head or more", fn);
+  if (s->T > kMostTokens || s->Tk > kMostTokens || (paged && (long long)s->width * s->page > kMostTokens))
+    return set_error(UAA_ERR_UNSUPPORTED, "%s: more than 2^30 tokens", fn);
   if (!(s->scale > 0.f) || !isfinite(s->scale))
     return set_error(UAA_ERR_INVALID_ARG, "%s: scale must be positive and finite", fn);
-  if (s->B == 0 || (s->T == 0 && !(bwd && s->Tk > 0))) return UAA_OK;
+  if ((s->B == 0 && !s->rest) || (s->T == 0 && !(bwd && s->Tk > 0))) return UAA_OK;
   int st;
   const bool keys = paged ? s->pages > 0 : s->Tk > 0;
   if (keys && ((st = check_dev_ptr(fn, "k", s->k)) || (st = check_dev_ptr(fn, "v", s->v)))) return st;
