@@ -905,13 +905,6 @@ __global__ void __launch_bounds__(256, 4) seq_join_kernel(const __grid_constant_
   for (int x = 0; x < kCols; ++x) acc[x] = 0.f;
   const int at = valid ? r : 0;
   each_part(parts.first, c, ctas, nt, [&](const int (&ids)[kBatch]) {
-    float x[kBatch];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) x[u] = ids[u] < 0 ? -INFINITY : part_stat(parts, ids[u])[at].x;
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) top = fmaxf(top, x[u]);
-  });
-  each_part(parts.first, c, ctas, nt, [&](const int (&ids)[kBatch]) {
     float2 st[kBatch];
     float o[kBatch][kCols];
 #pragma unroll
@@ -920,6 +913,16 @@ __global__ void __launch_bounds__(256, 4) seq_join_kernel(const __grid_constant_
       st[u] = part_stat(parts, ids[u])[at];
 #pragma unroll
       for (int x = 0; x < kCols; ++x) o[u][x] = part_o<D>(parts, ids[u])[(size_t)(col + x) * parts.rows + at];
+    }
+    const float before = top;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (ids[u] >= 0) top = fmaxf(top, st[u].x);
+    if (before != -INFINITY && top != before) {
+      const float f = ex2(before - top);
+      sum *= f;
+#pragma unroll
+      for (int x = 0; x < kCols; ++x) acc[x] *= f;
     }
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
