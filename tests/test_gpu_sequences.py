@@ -233,6 +233,24 @@ def test_values_that_are_not_finite_in_every_item(D):
         assert torch.isfinite(out).all(), warp
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_late_warp_changes_nothing_with_fewer_keys_than_queries(D):
+    """Items whose first tile reads no key behind items whose second tile has a step more than the first."""
+    if not uaa.debug_build():
+        pytest.skip("runs in the child process that loads the debug build")
+    x = draw([256] * 800, [256, 128] * 400, 1, 1, D, seed=54)
+    want = step(x)
+    check(want, against(x), ALL)
+    for warp in range(12):
+        uaa.debug_late_warp(warp, 20000)
+        try:
+            got = step(x)
+        finally:
+            uaa.debug_late_warp()
+        for n in ALL:
+            assert np.array_equal(bits(got[n]), bits(want[n])), (warp, n)
+
+
 @pytest.mark.parametrize("news,lens", [([1] * 30, [900] * 30), ([1, 200, 7, 1], [3000, 700, 129, 1])], ids=["tokens", "chunks"])
 def test_a_late_warp_changes_nothing_over_pages(news, lens):
     if not uaa.debug_build():

@@ -148,14 +148,16 @@ __device__ __forceinline__ Item item_of(const SeqArgs& a, const Walk<Pairs>& w) 
     it.n[0] = (it.c + 1) / 2;
     it.n[1] = it.c / 2;
   } else {
-    it.n[0] = held_in(tiles_in(keys_of(a.s, w.q, t0 + TT - 1), kBN) - w.j0, 0, it.c);
+    // (a first tile that reads no key takes one all the same, masked: slot 1 may still be in the item before, and slot 0
+    // without a step could not tell the phases of its barriers apart)
+    it.n[0] = held_in(tiles_in(keys_of(a.s, w.q, t0 + TT - 1), kBN) - w.j0, min(1, it.c), it.c);
     it.n[1] = it.c;
   }
   return it;
 }
 // The key tile whose K slot slot 0 takes its rows out through: every S that reads it comes before slot 0's last P V (before
-// slot 1's, where slot 0 works on the same tile or on none, and waits for slot 1).
-__device__ __forceinline__ int stage_k(const Item& it) { return (it.split || it.n[0] == 0 ? it.c : it.n[0]) - 1; }
+// slot 1's, where both work on the same tile and slot 0 waits for slot 1).
+__device__ __forceinline__ int stage_k(const Item& it) { return (it.split ? it.c : it.n[0]) - 1; }
 
 // What the softmax warps of a slot have to know of an item.
 enum { kSplit = 1, kPart = 2, kJoin = 4, kFull = 8 };  // kFull: every token of the slot's tile is there
@@ -781,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
         const bool dirty = *reinterpret_cast<volatile uint32_t*>(&ctl->dirty[job.ne & 1]) == job.ne;
         const int slot = part_of(cta, job.j0);
-        if (!join && !dirty && !part && nt > 0) {  // the usual way, 64 columns at a time
+        if (!join && !dirty && !part) {  // the usual way, 64 columns at a time
 #pragma unroll 1
           for (int e = 0; e < D / 64; ++e) {
             float y[64];
@@ -797,10 +799,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < D / 32; ++e) {
           float y[32];
           tmem_ld32(tl + 256 + t * D + 32 * e, y);
-          if (nt == 0) {  // this tile reads no key of the part
-#pragma unroll
-            for (int f = 0; f < 32; ++f) y[f] = 0.f;
-          }
           if (join) {
             float z[32];
             tmem_ld32(tl + 256 + D + 32 * e, z);
