@@ -924,7 +924,8 @@ def attn_packed_bwd(q, k, v, out, dout, lse, starts, starts_k=None, causal=True,
                     workspace=None):
     """``uaa_attn_packed_bwd``: the gradients ``(dq, dk, dv)`` of :func:`attn_packed_fwd` (bf16).
 
-    An infinity or a NaN of a token may show in the gradients of any token of its own sequence; other sequences' stay clean."""
+    An infinity or a NaN of a token may show in the gradients of any token of its own sequence; other sequences' stay
+    clean."""
     if out is None or lse is None:
         raise ValueError("out and lse are the forward's results")
     return _packed_bwd(q, k, v, out, dout, lse, starts, starts_k, causal, scale, dq, dk, dv, workspace, 0)
@@ -1033,7 +1034,8 @@ def cache_write(k, v, k_pages, v_pages, starts, table, lens, seqs=None):
     dev = _same_device(k, v, k_pages, v_pages, starts, table, lens, seqs)
     if k.element_size() != 2 or any(t.dtype != k.dtype for t in (v, k_pages, v_pages)):
         raise TypeError("k, v and the pages must have one 2-byte type")
-    if k.shape != v.shape or k_pages.shape != v_pages.shape or k.dim() != 3 or k_pages.dim() != 4 or k.shape[1:] != k_pages.shape[2:]:
+    if (k.shape != v.shape or k_pages.shape != v_pages.shape or k.dim() != 3 or k_pages.dim() != 4 or
+            k.shape[1:] != k_pages.shape[2:]):
         raise ValueError(f"k {tuple(k.shape)}, v {tuple(v.shape)} and pages {tuple(k_pages.shape)}, "
                          f"{tuple(v_pages.shape)} do not fit")
     (k0, k1, _), (v0, v1, _) = _rows16("k", k, 3), _rows16("v", v, 3)

@@ -7,11 +7,12 @@
 // tiles (a pair) of one sequence and key head, against tiles of 128 keys.
 //
 // Work.  A persistent CTA per SM; the items of all sequences in a row, weighed by
-// the keys that they read plus kItemWork, are cut into equal shares, one a CTA, in
-// the middle of an item where it falls so: long prompts, many short ones and one
-// token over a long past fill the card alike, and the lengths stay on the device
-// (every CTA adds up the weights itself when it starts).  The parts of an item that
-// was cut go to the workspace, unnormalised, and a second kernel joins them in order.
+// the keys that they read plus what an item costs beside them, are cut into equal
+// shares, one a CTA, in the middle of an item where it falls so: long prompts, many
+// short ones and one token over a long past fill the card alike, and the lengths stay
+// on the device (every CTA adds up the weights itself when it starts, 3 to 5 us).
+// The parts of an item that was cut go to the workspace, unnormalised, and a second
+// kernel joins them in order.
 //   warp 8     TMA producer: the item's Q tiles, then K_j, V_j through a ring
 //   warp 9     tcgen05 issuer (one elected lane)
 //   warps 0-3  softmax of slot 0, warps 4-7 of slot 1: thread r owns row r (a TMEM
@@ -28,6 +29,16 @@
 // Keys outside a row's border get P = 0.  P V multiplies that 0 by what V holds, so in
 // the tiles that the border crosses the relay warps look at V first: an infinity or a
 // NaN there becomes a zero, and the epilogue adds it to the rows that do read it.
+//
+// Bound and times (GB300, bf16, on the device).  Long sequences: the matrix pipe; a
+// step of a pair at D = 128 takes 1.44 us, four products of 128 x 128 x 128 and
+// 32768 exponentials, 1.1 us of it products: 8192 x 8192, 24 heads, 512 us = 1610
+// TFLOP/s; 16389 tokens, 40 / 8 heads, causal 1690 us = 1630; 2048 new tokens over
+// 27280 keys in pages 725 us = 1520.  At D = 64 the exponentials weigh as much as the
+// products: 8192 x 8192, 24 heads, 433 us = 950 TFLOP/s.  Short sequences: filling and
+// draining, 4.4 us an item beside its steps (images of 300 to 1100 tokens, D = 64, 24
+// heads: 82 us at 16 % of the matrix pipe).  New tokens: memory, 16 tokens over
+// 222000 keys, 8 key heads: 164 us, 5.5 TB/s.
 #include <float.h>
 
 #include <atomic>
@@ -110,6 +121,11 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&v);
   }
+}
+template <bool kHalf>
+__device__ __forceinline__ uint4 pack8(const float* x, float f) {
+  return make_uint4(pack2<kHalf>(x[0] * f, x[1] * f), pack2<kHalf>(x[2] * f, x[3] * f), pack2<kHalf>(x[4] * f, x[5] * f),
+                    pack2<kHalf>(x[6] * f, x[7] * f));
 }
 // 16-bit floats, two a word: whether one of them is an infinity or a NaN; and the word without them
 template <bool kHalf>
@@ -361,7 +377,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool drop = (int)n == ctx.drop_load;
             if constexpr (kPaged) {
               if (lane == 0) {
-                if (kind == 1) *reinterpret_cast<uint4*>(ctl->words[slot]) = make_uint4(words[0], words[1], words[2], words[3]);
+                if (kind == 1)
+                  *reinterpret_cast<uint4*>(ctl->words[slot]) = make_uint4(words[0], words[1], words[2], words[3]);
                 if (!drop) {
                   if (there) mbar_arrive_expect_tx(&ctl->bar_kv_full[slot], there * rows * 128 * kChunks);
                   else mbar_arrive(&ctl->bar_kv_full[slot]);
@@ -538,7 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c = it.c;
         if (c > 0) {
           // V of step i: an infinity or a NaN in a row of V that not every row of the item reads becomes a zero, and the
-          // epilogue adds it to the rows that read it (dirty).  Slot 0 does it where the slots share V, since its product comes first.
+          // epilogue adds it to the rows that read it (dirty).  Slot 0 does it where the slots share V, since its product
+          // comes first.
           auto look = [&](int i) {
             const uint32_t o = it.split ? 2 * i + t : i, nv = base + 2 * o + 1;
             const int j = w.j0 + (int)o;
@@ -556,8 +574,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int x = 0; x < 8 * kChunks; ++x) y[x] = v[(x / 8) * (kChunkBytes / 16) + (x % 8) * 32];
               uint32_t sum = 0;  // 0 as long as all are finite: an infinity or a NaN times 0 is a NaN
 #pragma unroll
-              for (int x = 0; x < 8 * kChunks; ++x)
-                sum = times0_plus<kHalf>(y[x].x, times0_plus<kHalf>(y[x].y, times0_plus<kHalf>(y[x].z, times0_plus<kHalf>(y[x].w, sum))));
+              for (int x = 0; x < 8 * kChunks; ++x) {
+                sum = times0_plus<kHalf>(y[x].z, times0_plus<kHalf>(y[x].w, sum));
+                sum = times0_plus<kHalf>(y[x].x, times0_plus<kHalf>(y[x].y, sum));
+              }
               if (!__any_sync(0xffffffffu, not_finite<kHalf>(sum))) continue;
               const uint32_t mw = wr < 64 ? (wr < 32 ? words.x : words.y) : (wr < 96 ? words.z : words.w);
 #pragma unroll 1
@@ -566,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint4* p = v + (x / 8) * (kChunkBytes / 16) + (x % 8) * 32;
                 const uint4 z = *p;
                 if (key < it.lo && ((mw >> r) & 1u)) continue;  // every row reads it
-                if (!(not_finite<kHalf>(z.x) || not_finite<kHalf>(z.y) || not_finite<kHalf>(z.z) || not_finite<kHalf>(z.w)))
+                if (!not_finite<kHalf>(z.x) && !not_finite<kHalf>(z.y) && !not_finite<kHalf>(z.z) && !not_finite<kHalf>(z.w))
                   continue;
                 bad = true;
                 *p = make_uint4(finite_part<kHalf>(z.x), finite_part<kHalf>(z.y), finite_part<kHalf>(z.z),
@@ -666,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (store) {
 #pragma unroll 1
           for (int x = 0; x < D / 8; ++x)
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(s.out) + (size_t)orow * D + 8 * x) = make_uint4(0u, 0u, 0u, 0u);
+            reinterpret_cast<uint4*>(static_cast<uint16_t*>(s.out) + (size_t)orow * D)[x] = make_uint4(0u, 0u, 0u, 0u);
           s.lse[lo] = -INFINITY;
         }
         continue;
@@ -789,47 +809,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             float y[64];
             tmem_ld32x2(tl + 256 + t * D + 64 * e, tl + 256 + t * D + 64 * e + 32, y);
 #pragma unroll
-            for (int f = 0; f < 8; ++f)
-              *piece(lane, 8 * e + f) =
-                  make_uint4(pack2<kHalf>(y[8 * f + 0] * inv, y[8 * f + 1] * inv), pack2<kHalf>(y[8 * f + 2] * inv, y[8 * f + 3] * inv),
-                             pack2<kHalf>(y[8 * f + 4] * inv, y[8 * f + 5] * inv), pack2<kHalf>(y[8 * f + 6] * inv, y[8 * f + 7] * inv));
+            for (int f = 0; f < 8; ++f) *piece(lane, 8 * e + f) = pack8<kHalf>(&y[8 * f], inv);
           }
         } else {
 #pragma unroll 1
-        for (int e = 0; e < D / 32; ++e) {
-          float y[32];
-          tmem_ld32(tl + 256 + t * D + 32 * e, y);
-          if (join) {
-            float z[32];
-            tmem_ld32(tl + 256 + D + 32 * e, z);
+          for (int e = 0; e < D / 32; ++e) {
+            float y[32];
+            tmem_ld32(tl + 256 + t * D + 32 * e, y);
+            if (join) {
+              float z[32];
+              tmem_ld32(tl + 256 + D + 32 * e, z);
 #pragma unroll
-            for (int f = 0; f < 32; ++f) y[f] = y[f] * f0 + z[f] * f1;
-          }
-          if (dirty && valid) {
+              for (int f = 0; f < 32; ++f) y[f] = y[f] * f0 + z[f] * f1;
+            }
+            if (dirty && valid) {
 #pragma unroll 1
-            for (int k = max(job.lo, job.j0 * kBN); k < min(lim, (job.j0 + job.c) * kBN); ++k) {
-              const uint16_t* v = value_row<kPaged>(a, job.q, job.h, k);
-              if (!v) continue;
+              for (int k = max(job.lo, job.j0 * kBN); k < min(lim, (job.j0 + job.c) * kBN); ++k) {
+                const uint16_t* v = value_row<kPaged>(a, job.q, job.h, k);
+                if (!v) continue;
 #pragma unroll
-              for (int f = 0; f < 32; ++f) {
-                const float z = load16(v, 32 * e + f, kHalf);
-                if (!isfinite(z)) y[f] += z;
+                for (int f = 0; f < 32; ++f) {
+                  const float z = load16(v, 32 * e + f, kHalf);
+                  if (!isfinite(z)) y[f] += z;
+                }
               }
             }
-          }
-          if (part) {
-            float* po = part_o<D>(parts, slot) + t * 128 + row;
-            if (valid)
+            if (part) {
+              float* po = part_o<D>(parts, slot) + t * 128 + row;
+              if (valid)
 #pragma unroll
-              for (int f = 0; f < 32; ++f) po[(size_t)(32 * e + f) * parts.rows] = y[f];
-          } else {
+                for (int f = 0; f < 32; ++f) po[(size_t)(32 * e + f) * parts.rows] = y[f];
+            } else {
 #pragma unroll
-            for (int f = 0; f < 4; ++f)
-              *piece(lane, 4 * e + f) =
-                  make_uint4(pack2<kHalf>(y[8 * f + 0] * inv, y[8 * f + 1] * inv), pack2<kHalf>(y[8 * f + 2] * inv, y[8 * f + 3] * inv),
-                             pack2<kHalf>(y[8 * f + 4] * inv, y[8 * f + 5] * inv), pack2<kHalf>(y[8 * f + 6] * inv, y[8 * f + 7] * inv));
+              for (int f = 0; f < 4; ++f) *piece(lane, 4 * e + f) = pack8<kHalf>(&y[8 * f], inv);
+            }
           }
-        }
         }
         if (!part && !(job.flags & kFull)) {
           __syncwarp();
@@ -880,7 +894,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------------------
 // Joins the parts of the items that were cut.  Block (c - 1, x, y): the item that CTA c's share begins inside of, if no
-// earlier share does, rows 32 x .. 32 x + 31, columns 64 y .. 64 y + 63: a lane a row, a warp 8 columns.
+// earlier share does, rows 32 x .. 32 x + 31, columns 64 y .. 64 y + 63: a lane a row, a warp 8 columns, four parts' loads
+// in flight together (one part at a time, all columns: 60 us for one token over 16000 keys by 125 parts, now 31 with the
+// attention itself).
 template <int D, bool kPaged, bool kHalf>
 __global__ void __launch_bounds__(256, 4) seq_join_kernel(const __grid_constant__ SeqArgs a, const Parts parts, int ctas,
                                                           DevCtx ctx) {
@@ -937,9 +953,7 @@ __global__ void __launch_bounds__(256, 4) seq_join_kernel(const __grid_constant_
   if (!guard_store(ctx, oo, kCols, (size_t)s.T * s.Hq * D) || !guard_store(ctx, lo, 1, (size_t)s.Hq * s.T)) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   uint16_t* out = static_cast<uint16_t*>(s.out) + oo;
-  *reinterpret_cast<uint4*>(out) =
-      make_uint4(pack2<kHalf>(acc[0] * inv, acc[1] * inv), pack2<kHalf>(acc[2] * inv, acc[3] * inv),
-                 pack2<kHalf>(acc[4] * inv, acc[5] * inv), pack2<kHalf>(acc[6] * inv, acc[7] * inv));
+  *reinterpret_cast<uint4*>(out) = pack8<kHalf>(acc, inv);
   if (col == 0) s.lse[lo] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
 }
 

@@ -78,9 +78,10 @@ __device__ __forceinline__ int seq_of_token(const int* starts, int B, int t) {
 // Zeros to the tokens of no sequence, before starts[0] and behind starts[B], of a (T, row) tensor of 16-bit elements: the
 // calling threads, `n` of them a block, take 16-byte pieces in turn.  lse: -inf beside them, of `heads` heads.
 __device__ __noinline__ void clear_rest(const int* starts, int B, int T, void* x, long long row, float* lse, int heads,
-                                           int thread, int n) {
+                                        int thread, int n) {
   const int a = held_in(starts[0], 0, T), b = held_in(starts[B], a, T);
-  const long long head = (long long)a * row / 8, all = head + (long long)(T - b) * row / 8, skip = (long long)(b - a) * row / 8;
+  const long long head = (long long)a * row / 8, skip = (long long)(b - a) * row / 8;
+  const long long all = head + (long long)(T - b) * row / 8;
   for (long long i = (long long)blockIdx.x * n + thread; i < all; i += (long long)gridDim.x * n)
     static_cast<uint4*>(x)[i < head ? i : i + skip] = make_uint4(0u, 0u, 0u, 0u);
   const long long none = T - (b - a);
