@@ -10,7 +10,7 @@
 // the keys that they read plus what an item costs beside them, are cut into equal
 // shares, one a CTA, in the middle of an item where it falls so: long prompts, many
 // short ones and one token over a long past fill the card alike, and the lengths stay
-// on the device (every CTA adds up the weights itself when it starts, 3 to 5 us).
+// on the device (every CTA adds up the weights itself when it starts, about 3 us).
 // The parts of an item that was cut go to the workspace, unnormalised, and a second
 // kernel joins them in order.
 //   warp 8     TMA producer: the item's Q tiles, then K_j, V_j through a ring

@@ -23,10 +23,15 @@ int check_dev_ptr(const char* fn, const char* name, const void* p);
 
 namespace {
 
+// What the row of items depends on.
+struct Shape {
+  int causal, Hk, TT;
+};
 struct SeqArgs {
   uaa_seqs s;
   int g;   // query heads of a key head
   int TT;  // tokens of a tile of 128 rows, a row being one head of one token
+  __device__ __forceinline__ operator Shape() const { return Shape{s.causal, s.Hk, TT}; }
 };
 
 __device__ __forceinline__ int held_in(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
@@ -60,9 +65,10 @@ __device__ __forceinline__ Seq load_seq(const uaa_seqs& s, int b, bool* bad = nu
 }
 
 // Keys that query i of the sequence reads.
-__device__ __forceinline__ int keys_of(const uaa_seqs& s, const Seq& q, int i) {
-  return s.causal ? held_in(q.m - q.n + i + 1, 0, q.m) : q.m;
+__device__ __forceinline__ int keys_of(int causal, const Seq& q, int i) {
+  return causal ? held_in(q.m - q.n + i + 1, 0, q.m) : q.m;
 }
+__device__ __forceinline__ int keys_of(const uaa_seqs& s, const Seq& q, int i) { return keys_of(s.causal, q, i); }
 
 // The sequence that token t belongs to, or -1 behind the last one (binary search; starts must not decrease).
 __device__ __forceinline__ int seq_of_token(const int* starts, int B, int t) {
@@ -113,26 +119,33 @@ constexpr int kLeastShare = 4, kLeastTiles = 2;
 
 __device__ __forceinline__ int tiles_in(int x, int per) { return (x + per - 1) / per; }
 
+// (of a guess that is put right)
+__device__ __forceinline__ float root(float x) {
+  float y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Tiles of W query tokens, inner tiles of keys: tile p's last query reads the most keys (the last tile weighs as if it
 // were full).  Of a causal sequence with fewer keys than queries the first `none` tiles read no key.
 template <int kTilesOf2>  // tiles of 128 rows: 1 or 2 (a pair)
 struct QueryRow {
-  static __device__ __forceinline__ int width(const SeqArgs& a) { return kTilesOf2 * a.TT; }
-  static __device__ __forceinline__ int tiles(const SeqArgs& a, const Seq& q) { return tiles_in(q.n, width(a)); }
-  static __device__ __forceinline__ int inner(const SeqArgs& a, const Seq& q, int p) {
-    return tiles_in(keys_of(a.s, q, min(q.n, (p + 1) * width(a)) - 1), kBN);
+  static __device__ __forceinline__ int width(const Shape& a) { return kTilesOf2 * a.TT; }
+  static __device__ __forceinline__ int tiles(const Shape& a, const Seq& q) { return tiles_in(q.n, width(a)); }
+  static __device__ __forceinline__ int inner(const Shape& a, const Seq& q, int p) {
+    return tiles_in(keys_of(a.causal, q, min(q.n, (p + 1) * width(a)) - 1), kBN);
   }
-  static __device__ __forceinline__ int unit(const SeqArgs&) { return kBN; }  // tokens of an inner tile
+  static __device__ __forceinline__ int unit(const Shape&) { return kBN; }  // tokens of an inner tile
   // A pair's costs 3 key tiles' time (4.4 us beside 1.44 us at D = 128) and the half tile that is rounded up; a single
   // tile's (dQ) was measured: of 2, 3, 4 and 5 tiles 3 is the fastest or within 1 %.
   static constexpr int item = kTilesOf2 == 2 ? 7 * kBN / 2 : 3 * kBN;
   int none;
   long long flat, slope;  // item none + (P = p - none) flat + slope P (P + 1) / 2
-  __device__ __forceinline__ QueryRow(const SeqArgs& a, const Seq& q) {
+  __device__ __forceinline__ QueryRow(const Shape& a, const Seq& q) {
     const int W = width(a), off = q.m - q.n;
-    none = a.s.causal && off < 0 ? -off / W : 0;
-    flat = item + (a.s.causal ? (long long)off + (long long)none * W : q.m);
-    slope = a.s.causal ? W : 0;
+    none = a.causal && off < 0 ? -off / W : 0;
+    flat = item + (a.causal ? (long long)off + (long long)none * W : q.m);
+    slope = a.causal ? W : 0;
   }
   __device__ __forceinline__ long long of(int p) const {
     const long long P = p - none;
@@ -140,28 +153,28 @@ struct QueryRow {
   }
   __device__ __forceinline__ int guess(long long w) const {
     const float x = (float)(w - (long long)item * none);
-    if (x <= 0.f) return (int)((float)w / item);
-    if (!slope) return (int)(none + x / (float)flat);
+    if (x <= 0.f) return (int)((float)w * (1.f / item));
+    if (!slope) return none + (int)__fdividef(x, (float)flat);
     const float h = 0.5f * (float)slope, f = (float)flat + h;
-    return (int)(none + 2.f * x / (f + sqrtf(f * f + 4.f * h * x)));
+    return none + (int)__fdividef(2.f * x, f + root(f * f + 4.f * h * x));
   }
 };
 
 // Tiles of 128 keys, inner tiles of TT query tokens: min(n, m - 128 p) queries read keys of tile p.
 struct KeyRow {
-  static __device__ __forceinline__ int tiles(const SeqArgs&, const Seq& q) { return tiles_in(q.m, kBN); }
-  static __device__ __forceinline__ int first(const SeqArgs& a, const Seq& q, int p) {  // the first inner tile
-    return a.s.causal ? max(0, p * kBN - (q.m - q.n)) / a.TT : 0;
+  static __device__ __forceinline__ int tiles(const Shape&, const Seq& q) { return tiles_in(q.m, kBN); }
+  static __device__ __forceinline__ int first(const Shape& a, const Seq& q, int p) {  // the first inner tile
+    return a.causal ? max(0, p * kBN - (q.m - q.n)) / a.TT : 0;
   }
-  static __device__ __forceinline__ int inner(const SeqArgs& a, const Seq& q, int p) {
+  static __device__ __forceinline__ int inner(const Shape& a, const Seq& q, int p) {
     return max(0, tiles_in(q.n, a.TT) - first(a, q, p));
   }
-  static __device__ __forceinline__ int unit(const SeqArgs& a) { return a.TT; }
+  static __device__ __forceinline__ int unit(const Shape& a) { return a.TT; }
   int item;  // (of 1.5 to 8 inner tiles 4 to 7 are the fastest within 2 %)
   int full;  // the first tiles, which all queries read
   long long n, m;
-  __device__ __forceinline__ KeyRow(const SeqArgs& a, const Seq& q) : item(11 * a.TT / 2), n(q.n), m(q.m) {
-    full = !a.s.causal ? INT32_MAX : q.m >= q.n ? (q.m - q.n) / kBN + 1 : 0;
+  __device__ __forceinline__ KeyRow(const Shape& a, const Seq& q) : item(11 * a.TT / 2), n(q.n), m(q.m) {
+    full = !a.causal ? INT32_MAX : q.m >= q.n ? (q.m - q.n) / kBN + 1 : 0;
   }
   __device__ __forceinline__ long long of(int p) const {
     const long long f = min(p, full), P = p;
@@ -170,10 +183,10 @@ struct KeyRow {
   __device__ __forceinline__ int guess(long long w) const {
     const long long f = (long long)full * (item + n);
     const float flat = (float)(item + n);
-    if (w <= f) return (int)((float)w / flat);
+    if (w <= f) return (int)__fdividef((float)w, flat);
     // behind the full tiles: x = b P - 64 P (P - 1) with P = p - full
     const float x = (float)(w - f), b = (float)(item + m - (long long)kBN * full) + kBN / 2;
-    return full + (int)(2.f * x / (b + sqrtf(fmaxf(b * b - 2.f * kBN * x, 0.f))));
+    return full + (int)__fdividef(2.f * x, b + root(fmaxf(b * b - 2.f * kBN * x, 0.f)));
   }
 };
 
@@ -191,15 +204,13 @@ struct Found {  // weight w of sequence b
   int b;
 };
 
-// The place at weight w of a sequence.  (One copy of the code: a share's end has to be the next one's beginning.)
+// The place at weight w of a sequence.  (Called from one place: a share's end has to be the next one's beginning.)
 template <class Row>
-__device__ __noinline__ Cut cut_at(const SeqArgs& a, const Found& f) {
-  const Seq q = f.q;
-  long long w = f.w;
+__device__ __forceinline__ Cut cut_at(const Shape& a, const Seq& q, long long w, int b) {
   const int np = Row::tiles(a, q);
   const Row row(a, q);
   const long long head = row.of(np);
-  Cut c{f.b, min((int)((float)w / (float)head), a.s.Hk - 1), 0, 0};
+  Cut c{b, min((int)__fdividef((float)w, (float)head), a.Hk - 1), 0, 0};
   while (c.h > 0 && c.h * head > w) --c.h;
   while ((c.h + 1) * head <= w) ++c.h;
   w -= c.h * head;
@@ -208,14 +219,14 @@ __device__ __noinline__ Cut cut_at(const SeqArgs& a, const Found& f) {
   while (c.p + 1 < np && row.of(c.p + 1) <= w) ++c.p;
   const long long first = row.of(c.p);
   const int nt = Row::inner(a, q, c.p);
-  c.j = min((int)((float)(w - first) / (float)(row.of(c.p + 1) - first) * nt + 0.5f), nt);
+  c.j = min((int)(__fdividef((float)(w - first), (float)(row.of(c.p + 1) - first)) * nt + 0.5f), nt);
   if (c.j < kLeastTiles) {
     c.j = 0;
   } else if (nt - c.j < kLeastTiles) {
     c.j = 0;
     if (++c.p == np) {
       c.p = 0;
-      if (++c.h == a.s.Hk) {
+      if (++c.h == a.Hk) {
         c.h = 0;
         ++c.b;
       }
@@ -245,64 +256,87 @@ __device__ __forceinline__ Share find_share(const SeqArgs& a, uint8_t* scratch, 
     const int np = Row::tiles(a, q);
     return np > 0 ? s.Hk * Row(a, q).of(np) : 0LL;
   };
-  // The weights where this share begins and ends; false: there are fewer shares.
+  // The weights where this share begins and ends; false: there are fewer shares.  (A border is the same number in both of
+  // its shares, and that is all that has to hold: 32-bit floats, which do not decrease with c.)
   auto borders = [&](long long total, long long& w0, long long& w1) {
-    const long long most = total / (kLeastShare * Row::unit(a));
-    const int shares = most < 1 ? 1 : most < ctas ? (int)most : ctas;
+    const int least = kLeastShare * Row::unit(a);
+    const int shares = total >= (long long)least * ctas ? ctas : max((int)total / least, 1);
     if (cta >= shares) return false;
-    const long long each = total / shares;
-    const int rest = (int)(total - each * shares);
-    w0 = each * cta + rest * cta / shares;
-    w1 = each * (cta + 1) + rest * (cta + 1) / shares;
+    const float each = __fdividef(1.f, (float)shares), all = (float)total;
+    w0 = (long long)(all * ((float)cta * each));
+    w1 = cta + 1 == shares ? total : (long long)(all * ((float)(cta + 1) * each));
     return true;
   };
   long long* sums = reinterpret_cast<long long*>(scratch);  // a sum a warp
   Found* found = reinterpret_cast<Found*>(scratch + 256);
   Cut* cuts = reinterpret_cast<Cut*>(scratch + 384);
-  if (threadIdx.x < 2) {
-    found[threadIdx.x].b = -1;
-    cuts[threadIdx.x] = Cut{s.B, 0, 0, 0};
-  }
-  auto scan = [&](long long x, long long& all) {  // sum of the threads before this one; `all`: of all
-    long long run = x;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const long long y = __shfl_up_sync(0xffffffffu, run, o);
-      if (lane >= o) run += y;
-    }
-    __syncthreads();
-    if (lane == 31) sums[warp] = run;
-    __syncthreads();
-    long long ahead = 0;
-    all = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) ahead += sums[w];
-      all += sums[w];
-    }
-    return ahead + run - x;
-  };
+  // Up to 32 sequences are one warp's work, the others wait; up to kThreads are weighed and added up once.  (With all warps'
+  // barriers and two scans this took 3.8 to 5.5 us from a kernel's start, now 2.7 to 3.4: mostly code read for the first
+  // time.  One token over 700 keys 22.1 -> 20.7 us.)
+  const bool few = s.B <= 32;
   Seq q{};  // of sequence threadIdx.x, if there are no more than threads
-  long long w = 0, w0 = 0, w1 = 0;
-#pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {  // the total; then the sequences that the share begins and ends in
-    long long done = 0, all;
+  if (!few || warp == 0) {
+    if (threadIdx.x < 2) {
+      found[threadIdx.x].b = -1;
+      cuts[threadIdx.x] = Cut{s.B, 0, 0, 0};
+    }
+    __syncwarp();
+    auto scan = [&](long long x, long long& all) {  // sum of the threads before this one; `all`: of all
+      long long run = x;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const long long y = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += y;
+      }
+      if (few) {
+        all = __shfl_sync(0xffffffffu, run, 31);
+        return run - x;
+      }
+      __syncthreads();
+      if (lane == 31) sums[warp] = run;
+      __syncthreads();
+      long long ahead = 0;
+      all = 0;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) ahead += sums[w];
+        all += sums[w];
+      }
+      return ahead + run - x;
+    };
+    long long w = 0, at = 0, total = 0, all, w0 = 0, w1 = 0;
+    auto mark = [&](int b) {  // the sequences that the share begins and ends in
+      if (w > 0 && w0 >= at && w0 < at + w) found[0] = Found{q, w0 - at, b};
+      if (w > 0 && w1 >= at && w1 < at + w) found[1] = Found{q, w1 - at, b};
+    };
 #pragma unroll 1
     for (int b0 = 0; b0 < s.B; b0 += kThreads) {
       const int b = b0 + threadIdx.x;
-      if (pass == 0 || s.B > kThreads) {
-        w = b < s.B ? weigh(b, q, true) : 0;
-      }
-      const long long at = done + scan(w, all);
-      if (pass == 1 && w > 0) {
-        if (w0 >= at && w0 < at + w) found[0] = Found{q, w0 - at, b};
-        if (w1 >= at && w1 < at + w) found[1] = Found{q, w1 - at, b};
-      }
-      done += all;
+      w = b < s.B ? weigh(b, q, true) : 0;
+      at = total + scan(w, all);
+      total += all;
     }
-    if (pass == 0 && !borders(done, w0, w1)) break;
+    if (borders(total, w0, w1)) {
+      if (s.B <= kThreads) {
+        mark(threadIdx.x);
+      } else {
+        long long done = 0;
+#pragma unroll 1
+        for (int b0 = 0; b0 < s.B; b0 += kThreads) {
+          const int b = b0 + threadIdx.x;
+          w = b < s.B ? weigh(b, q, false) : 0;
+          at = done + scan(w, all);
+          mark(b);
+          done += all;
+        }
+      }
+    }
+    if (few) __syncwarp();
+    else __syncthreads();
+    if (threadIdx.x < 2 && found[threadIdx.x].b >= 0) {
+      const Found f = found[threadIdx.x];
+      cuts[threadIdx.x] = cut_at<Row>(a, f.q, f.w, f.b);
+    }
   }
-  __syncthreads();
-  if (lane == 0 && warp < 2 && found[warp].b >= 0) cuts[warp] = cut_at<Row>(a, found[warp]);
   __syncthreads();
   Share r{cuts[0], cuts[1], nullptr};
   const int held = min(r.to.b, s.B - 1) - r.from.b + 1;  // its sequences (none: from.b = B)
