@@ -32,10 +32,10 @@
 //
 // Bound and times (GB300, bf16, on the device).  Long sequences: the matrix pipe; a
 // step of a pair at D = 128 takes 1.44 us, four products of 128 x 128 x 128 and
-// 32768 exponentials, 1.1 us of it products: 8192 x 8192, 24 heads, 512 us = 1610
+// 32768 exponentials, 1.1 us of it products: 8192 x 8192, 24 heads, 516 us = 1600
 // TFLOP/s; 16389 tokens, 40 / 8 heads, causal 1690 us = 1630; 2048 new tokens over
-// 27280 keys in pages 725 us = 1520.  At D = 64 the exponentials weigh as much as the
-// products: 8192 x 8192, 24 heads, 433 us = 950 TFLOP/s.  Short sequences: filling and
+// 27280 keys in pages 718 us = 1540.  At D = 64 the exponentials weigh as much as the
+// products: 8192 x 8192, 24 heads, 457 us = 900 TFLOP/s.  Short sequences: filling and
 // draining, 4.4 us an item beside its steps (images of 300 to 1100 tokens, D = 64, 24
 // heads: 82 us at 16 % of the matrix pipe).  New tokens: memory, 16 tokens over
 // 222000 keys, 8 key heads: 164 us, 5.5 TB/s.

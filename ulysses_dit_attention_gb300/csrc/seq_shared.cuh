@@ -114,8 +114,10 @@ __device__ __forceinline__ void store16(void* p, size_t at, float x, int fp16) {
 // tile has and what the first p tiles weigh.
 constexpr int kBN = 128;  // keys of a tile
 constexpr int kMostTokens = 1 << 30;  // of a tensor, or of a sequence's pages: places are 32-bit sums of them and a tile
-// The least inner tiles of a share, and of a part.
-constexpr int kLeastShare = 4, kLeastTiles = 2;
+// The least inner tiles of a part (1: images of 300 to 1100 tokens 94 us instead of 87).  A share may weigh as little as one,
+// and an item weighs several, so that small calls have an item or a part a CTA (at least 4: one token over 700 keys 18.4 us
+// instead of 16.2 in a graph, prompts of 150, 8 and 10 tokens 15.8 instead of 11.6).
+constexpr int kLeastTiles = 2;
 
 __device__ __forceinline__ int tiles_in(int x, int per) { return (x + per - 1) / per; }
 
@@ -259,7 +261,7 @@ __device__ __forceinline__ Share find_share(const SeqArgs& a, uint8_t* scratch, 
   // The weights where this share begins and ends; false: there are fewer shares.  (A border is the same number in both of
   // its shares, and that is all that has to hold: 32-bit floats, which do not decrease with c.)
   auto borders = [&](long long total, long long& w0, long long& w1) {
-    const int least = kLeastShare * Row::unit(a);
+    const int least = Row::unit(a);
     const int shares = total >= (long long)least * ctas ? ctas : max((int)total / least, 1);
     if (cta >= shares) return false;
     const float each = __fdividef(1.f, (float)shares), all = (float)total;
