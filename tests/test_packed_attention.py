@@ -1,6 +1,7 @@
 """Attention over packed sequences against the float64 definition, within the error that the operands' roundings allow."""
 import ctypes
 import itertools
+import weakref
 
 import numpy as np
 import pytest
@@ -99,6 +100,35 @@ def test_refusals_of_the_call():
     assert bwd(B=0, q=0) == 0 and bwd(T=0, Tk=0, q=0) == 0
     assert uaa.attn_packed_bwd_workspace_bytes(-1, 4, 4, 2, 64) == 0 and uaa.attn_packed_bwd_workspace_bytes(1, 4, 4, 2, 96) == 0
     assert uaa.attn_seqs_workspace_bytes(1, -1, 4, 2, 64) == 0
+
+
+def test_the_workspace_outlives_the_launch(monkeypatch):
+    """Freed before the launch, another thread's tensor could take its place on the same stream."""
+    made, seen, empty = [], [], torch.empty
+
+    def make(*a, **kw):
+        t = empty(*a, **kw)
+        made.append((weakref.ref(t), t.data_ptr()))
+        return t
+
+    def call(dev, name, *a):
+        live = [r() for r, _ in made]
+        assert all(t is not None for t in live), name
+        seen.append(name)
+        assert any(t.data_ptr() in a for t in live), name
+
+    q, kv = torch.zeros(5, 4, 64, dtype=torch.bfloat16), torch.zeros(5, 2, 64, dtype=torch.bfloat16)
+    starts, lens = torch.tensor([0, 5], dtype=torch.int32), torch.tensor([5], dtype=torch.int32)
+    pool = torch.zeros(2, 16, 2, 64, dtype=torch.bfloat16)
+    monkeypatch.setattr(uaa, "_same_device", lambda *ts: ts[0].device)
+    monkeypatch.setattr(uaa, "_call", call)
+    monkeypatch.setattr(torch, "empty", make)
+    out, lse = uaa.attn_packed_fwd(q, kv, kv, starts)
+    made.clear()
+    uaa.attn_packed_bwd(q, kv, kv, out, q, lse, starts)
+    made.clear()
+    uaa.attn_paged_fwd(q, pool, pool, starts, torch.zeros(1, 2, dtype=torch.int32), lens)
+    assert seen == ["uaa_attn_packed_fwd", "uaa_attn_packed_bwd", "uaa_attn_paged_fwd"]
 
 
 @pytest.mark.parametrize("kw", [dict(T=2 ** 30 + 1, Hq=1, Hk=1), dict(Tk=2 ** 30 + 1, Hq=1, Hk=1)])

@@ -877,7 +877,7 @@ def attn_seqs_workspace_bytes(B, T, Hq, Hk, D) -> int:
 def _seqs_workspace(workspace, B, T, Hq, Hk, D, dev):
     if workspace is None:
         workspace = torch.empty(attn_seqs_workspace_bytes(B, T, Hq, Hk, D), dtype=torch.uint8, device=dev)
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace
 
 
 def _packed_args(q, k, v, starts, starts_k, causal, scale, out, lse, half=True, rest=0):
@@ -912,7 +912,8 @@ def _packed_fwd(q, k, v, starts, starts_k, causal, scale, out, lse, workspace, r
     dev = _same_device(q, k, v, starts, starts_k, out, lse, workspace)
     args, out, lse = _packed_args(q, k, v, starts, starts_k, causal, scale, out, lse, rest=rest)
     T, Hq, D = q.shape
-    _call(dev, "uaa_attn_packed_fwd", args, *_seqs_workspace(workspace, starts.shape[0] - 1, T, Hq, k.shape[1], D, dev))
+    workspace = _seqs_workspace(workspace, starts.shape[0] - 1, T, Hq, k.shape[1], D, dev)  # held until the launch
+    _call(dev, "uaa_attn_packed_fwd", args, workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out, lse
 
 
@@ -1021,7 +1022,8 @@ def attn_paged_fwd(q, k_pages, v_pages, starts, table, lens, seqs=None, causal=T
                       starts.data_ptr(), 0, table.data_ptr(), lens.data_ptr(), 0 if seqs is None else seqs.data_ptr(),
                       q0, q1, k1, k2, v1, v2, k0, v0, B, T, 0, Hq, Hk, D, dtype, 1 if causal else 0, N, page, rows,
                       width, 0, scale)
-    _call(dev, "uaa_attn_paged_fwd", args, *_seqs_workspace(workspace, B, T, Hq, Hk, D, dev))
+    workspace = _seqs_workspace(workspace, B, T, Hq, Hk, D, dev)  # held until the launch
+    _call(dev, "uaa_attn_paged_fwd", args, workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out, lse
 
 
