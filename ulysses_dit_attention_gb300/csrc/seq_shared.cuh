@@ -70,17 +70,6 @@ __device__ __forceinline__ int keys_of(int causal, const Seq& q, int i) {
 }
 __device__ __forceinline__ int keys_of(const uaa_seqs& s, const Seq& q, int i) { return keys_of(s.causal, q, i); }
 
-// The sequence that token t belongs to, or -1 behind the last one (binary search; starts must not decrease).
-__device__ __forceinline__ int seq_of_token(const int* starts, int B, int t) {
-  int lo = 0, hi = B;  // the last b with starts[b] <= t
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (starts[mid] <= t) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo < B && starts[lo] <= t ? lo : -1;
-}
-
 // Zeros to the tokens of no sequence, before starts[0] and behind starts[B], of a (T, row) tensor of 16-bit elements: the
 // calling threads, `n` of them a block, take 16-byte pieces in turn.  lse: -inf beside them, of `heads` heads.
 __device__ __noinline__ void clear_rest(const int* starts, int B, int T, void* x, long long row, float* lse, int heads,
@@ -99,10 +88,6 @@ __device__ __noinline__ void clear_rest(const int* starts, int B, int T, void* x
 
 __device__ __forceinline__ float load16(const void* p, size_t at, int fp16) {
   return fp16 ? __half2float(static_cast<const __half*>(p)[at]) : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]);
-}
-__device__ __forceinline__ void store16(void* p, size_t at, float x, int fp16) {
-  if (fp16) static_cast<__half*>(p)[at] = __float2half_rn(x);
-  else static_cast<__nv_bfloat16*>(p)[at] = __float2bfloat16_rn(x);
 }
 
 // ---------------------------------------------------------------------------
