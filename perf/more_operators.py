@@ -243,64 +243,55 @@ def _turn(st):
 
 
 # --------------------------------------------------------------------------- plain forms, 32 bits
-def _runs(Hk, cells):
-    """Runs of key heads that are computed together: as many as keep a few GB of scores."""
-    step = max(1, min(Hk, (1 << 29) // max(1, cells)))
-    return [slice(h, min(Hk, h + step)) for h in range(0, Hk, step)]
-
-
-def _by_head(x, Hk):
-    """(n, H, D) as 32-bit (Hk, H // Hk, n, D)."""
-    return x.float().unflatten(1, (Hk, -1)).permute(1, 2, 0, 3)
-
-
 def _attend(q, k, v, causal):
-    """q (n, Hq, D), k, v (m, Hk, D): the last query stands at the last key.  Out in 32 bits, the log-sum-exp and the
-    probabilities of every run of key heads."""
+    """q (n, Hq, D), k, v (m, Hk, D): the last query stands at the last key.  Out in 32 bits and the log-sum-exp."""
     n, Hq, D = q.shape
     m, Hk, _ = k.shape
-    q, k, v = (_by_head(x, Hk) for x in (q, k, v))
-    out = torch.empty((n, Hk, Hq // Hk, D), dtype=torch.float32, device=q.device)
-    lse = torch.empty((Hk, Hq // Hk, n), dtype=torch.float32, device=q.device)
+    out = torch.empty((n, Hq, D), dtype=torch.float32, device=q.device)
+    lse = torch.empty((Hq, n), dtype=torch.float32, device=q.device)
     hidden = None
     if causal and n > 1:
         hidden = torch.arange(m, device=q.device)[None, :] > torch.arange(m - n, m, device=q.device)[:, None]
     probs = []
-    for h in _runs(Hk, Hq // Hk * n * m):
-        s = torch.matmul(q[h], k[h].transpose(-1, -2)) * (1.0 / math.sqrt(D))
+    for h in range(Hk):
+        heads = slice(h * (Hq // Hk), (h + 1) * (Hq // Hk))
+        s = torch.matmul(q[:, heads].float().transpose(0, 1), k[:, h].float().T) * (1.0 / math.sqrt(D))
         if hidden is not None:
             s.masked_fill_(hidden, -math.inf)
         top = s.amax(-1, keepdim=True)
         p = torch.exp(s - top)
         total = p.sum(-1, keepdim=True)
-        lse[h] = (top + torch.log(total)).squeeze(-1)
+        lse[heads] = (top + torch.log(total)).squeeze(-1)
         p = p / total
-        out[:, h] = torch.matmul(p, v[h]).permute(2, 0, 1, 3)
-        probs.append((h, p))
-    return out.flatten(1, 2), lse.flatten(0, 1), probs
+        out[:, heads] = torch.matmul(p, v[:, h].float()).transpose(0, 1)
+        probs.append(p)
+    return out, lse, probs
 
 
 def _plain_packed(st):
     case, dt = st["case"], st["q"].dtype
     outs, lses, dqs, dks, dvs, at = [], [], [], [], [], 0
-    Hk, scale = case["Hk"], 1.0 / math.sqrt(case["D"])
+    g = case["Hq"] // case["Hk"]
+    scale = 1.0 / math.sqrt(case["D"])
     for n in st["lens"]:
         q, k, v = (st[x][at: at + n] for x in ("q", "k", "v"))
         out, lse, probs = _attend(q, k, v, case["causal"])
         outs.append(out.to(dt))
         lses.append(lse)
         if case["grad"]:
-            do = _by_head(st["dout"][at: at + n], Hk)
-            q, k, v = (_by_head(x, Hk) for x in (q, k, v))
-            dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-            for h, p in probs:
-                dv[h] = torch.matmul(p.transpose(-1, -2), do[h]).sum(1, keepdim=True)
-                ds = torch.matmul(do[h], v[h].transpose(-1, -2))
+            do = st["dout"][at: at + n].float()
+            dq, dk, dv = torch.empty_like(out), torch.empty_like(k, dtype=torch.float32), torch.empty_like(v, dtype=torch.float32)
+            for h, p in enumerate(probs):
+                heads = slice(h * g, h * g + g)
+                d = do[:, heads].transpose(0, 1)
+                dv[:, h] = torch.matmul(p.transpose(-1, -2), d).sum(0)
+                ds = torch.matmul(d, v[:, h].float().T)
                 ds = p * (ds - (p * ds).sum(-1, keepdim=True))
-                dq[h] = torch.matmul(ds, k[h]) * scale
-                dk[h] = (torch.matmul(ds.transpose(-1, -2), q[h]) * scale).sum(1, keepdim=True)
-            for x, to in ((dq, dqs), (dk, dks), (dv, dvs)):
-                to.append(x.permute(2, 0, 1, 3).flatten(1, 2).to(dt))
+                dq[:, heads] = (torch.matmul(ds, k[:, h].float()) * scale).transpose(0, 1)
+                dk[:, h] = (torch.matmul(ds.transpose(-1, -2), q[:, heads].float().transpose(0, 1)) * scale).sum(0)
+            dqs.append(dq.to(dt))
+            dks.append(dk.to(dt))
+            dvs.append(dv.to(dt))
         del probs
         at += n
     if case["grad"]:
