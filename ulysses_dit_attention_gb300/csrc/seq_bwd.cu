@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
     tmem_alloc(&ctl->tmem_base, 512);
     tmem_relinquish();
   }
-  // rows of a query tile that no copy fills
+  // rows of a query tile that no copy fills (and, at an item's end, that its way out has been through)
   if (rows < 128 && warp < L::kQStages + L::kDStages)
     zero_rows<D>(smem + L::kQ + warp * L::kTileBytes, rows, 128, lane);
   const Share share = find_share<KeyRow, false, kDkdvThreads, L::kSeqs>(a, smem + L::kLse, smem + L::kKept, x.w.seqs_kv,
@@ -594,6 +594,15 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
             bulk_commit_group();
             bulk_wait_read_all();
           }
+        }
+        __syncwarp();
+        // dV and dK were put in all rows of the two tiles.  Those that no copy fills are zeros again before the tiles are a
+        // stage again: the next item's products read them, and an infinity or a NaN there would reach all of its rows.
+        if (rows < 128 && !w.part) {
+          zero_rows<D>(out[0], rows, 128, lane);
+          zero_rows<D>(out[1], rows, 128, lane);
+        }
+        if (lane == 0) {
           mbar_arrive(&ctl->bar_do_empty[gl % L::kDStages]);
           mbar_arrive(&ctl->bar_q_empty[gl % L::kQStages]);
         }
