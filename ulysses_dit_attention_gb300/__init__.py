@@ -1059,7 +1059,8 @@ class PagedCache:
     on the device, for :func:`attn_paged_fwd`.  A sequence is a number below ``seqs`` and has ``width`` pages at most.
     The lowest free pages are taken first.  A call that cannot be done raises before anything changes
     (``UAA_ERR_NO_PAGES`` where pages are short).  The device's side is changed on the current stream, by small
-    launches that hold their data; these calls are made outside of graph captures, between replays.
+    launches that hold their data; these calls are made outside of graph captures, between replays.  A cache is not copied
+    or pickled.
 
     A step of a model::
 
@@ -1097,6 +1098,9 @@ class PagedCache:
         if getattr(self, "_h", None) and _lib is not None:
             _lib.uaa_pages_destroy(self._h)
             self._h = None
+
+    def __reduce_ex__(self, protocol):  # a copy would share the handle, which either of the two frees
+        raise TypeError("a PagedCache cannot be copied or pickled")
 
     @property
     def free_pages(self):
