@@ -957,8 +957,6 @@ class PackedAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, starts, starts_k=None, causal=True, scale=None, saved=None):
         _check_saved(saved)
-        if q.dtype != torch.bfloat16 and any(ctx.needs_input_grad):
-            raise TypeError("gradients are built for bfloat16")
         out, lse = _packed_fwd(q, k, v, starts, starts_k, causal, scale, None, None, None, 1)
         if saved == "int8":  # the checkpoint takes contiguous rows
             q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
@@ -989,6 +987,9 @@ def packed_attention(q, k, v, starts, starts_k=None, causal=True, scale=None, sa
 
     To capture a step with its gradients in a CUDA graph, warm up on another stream and let no eager autograd graph
     of the same leaves live: PyTorch ties a leaf's gradients to the stream of the first graph that holds it."""
+    # (asked here: inside of a Function the grad mode is off, and a leaf says that it needs a gradient under no_grad too)
+    if q.dtype != torch.bfloat16 and torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v)):
+        raise TypeError("gradients are built for bfloat16")
     return PackedAttention.apply(q, k, v, starts, starts_k, causal, scale, saved)
 
 
