@@ -497,9 +497,12 @@ int uaa_attn_packed_bwd(const uaa_seqs* args, const void* dout, void* dq, void* 
  * A cache keeps the keys and values of `seqs` sequences in pages of `page` tokens.  Which page holds what is kept on
  * the host, by this object, and copied to the device: table (seqs, width), -1 behind a sequence's pages, and lens.
  * Pages may be shared (a fork); the lowest free page is always taken first.  The calls check everything before they
- * change anything; then they enqueue the device's changes on `stream`, a few small launches.  They are made outside
- * of graph captures (a captured one would be replayed without the host's part); the attention and write calls, which
- * read table and lens on the device, may be captured.  One thread at a time per object is not required: calls lock. */
+ * change anything; then they enqueue the device's changes on `stream`, a few small launches.  Should one of these fail
+ * (UAA_ERR_CUDA), the host's side has changed and the device's has not, or in part: further calls with pools are then
+ * refused (UAA_ERR_CUDA), and the object is to be destroyed and the pools, table and lens given up with it.  The calls
+ * are made outside of graph captures (a captured one would be replayed without the host's part); the attention and
+ * write calls, which read table and lens on the device, may be captured.  One thread at a time per object is not
+ * required: calls lock. */
 typedef struct uaa_pages uaa_pages;
 
 /* The device's side; `pools` NULL in the calls below: the host's side alone. */
@@ -578,6 +581,10 @@ void uaa_set_wait_timeout_ms(unsigned int ms);
  * uaa_check_device_status() reports UAA_ERR_TIMEOUT.  No copy is ever issued
  * with a bad address: the load is simply not issued.  n < 0 turns it off. */
 void uaa_debug_drop_load(int n);
+
+/* Diagnostic, for tests of a cache whose device did not follow (off by default): while n >= 0, the n-th launch (counted
+ * from 0) of every uaa_pages_* call is not made, and the call fails there with UAA_ERR_CUDA.  n < 0 turns it off. */
+void uaa_debug_fail_launch(int n);
 
 /* Diagnostic of the debug build, for tests of the order of waits: while warp >= 0,
  * that warp of every block of the attention kernels launched afterwards comes `ns`

@@ -28,7 +28,7 @@ from .build import DEBUG_LIB_PATH, LIB_PATH
 __all__ = [
     "UAAError", "lib", "attn_fwd", "attn_bwd", "attn_bwd_workspace_bytes", "attn_bwd_fused_workspace_bytes", "seq_to_head", "head_to_seq",
     "assemble_key_mask", "check_device_status", "watchdog_selftest", "set_wait_timeout_ms", "debug_drop_load",
-    "debug_late_warp",
+    "debug_late_warp", "debug_fail_launch",
     "set_bwd_profile_events", "Attention", "attn_fwd_groups", "attn_bwd_groups",
     "attention", "UlyssesAttention", "ulysses_attention", "STATUS", "debug_build", "debug_exp2_fma2",
     "RotaryPlan", "rotary_fwd", "rotary_bwd", "Rotary", "rotary", "shard_positions", "Act8", "act8_pack", "act8_unpack",
@@ -124,6 +124,7 @@ _SIGS = {
     "uaa_watchdog_selftest": (_I, [ctypes.c_uint, _P]),
     "uaa_set_wait_timeout_ms": (None, [ctypes.c_uint]),
     "uaa_debug_drop_load": (None, [_I]),
+    "uaa_debug_fail_launch": (None, [_I]),
     "uaa_debug_late_warp": (_I, [_I, ctypes.c_uint]),
     "uaa_set_bwd_profile_events": (None, [_P, _P, _P]),
     "uaa_last_error": (ctypes.c_char_p, []),
@@ -1060,8 +1061,9 @@ class PagedCache:
     on the device, for :func:`attn_paged_fwd`.  A sequence is a number below ``seqs`` and has ``width`` pages at most.
     The lowest free pages are taken first.  A call that cannot be done raises before anything changes
     (``UAA_ERR_NO_PAGES`` where pages are short).  The device's side is changed on the current stream, by small
-    launches that hold their data; these calls are made outside of graph captures, between replays.  A cache is not copied
-    or pickled.
+    launches that hold their data; these calls are made outside of graph captures, between replays.  Should such a launch
+    fail (``UAA_ERR_CUDA``), the device has not followed the host: the cache refuses further changes and is to be given
+    up.  A cache is not copied or pickled.
 
     A step of a model::
 
@@ -1282,6 +1284,12 @@ def set_wait_timeout_ms(ms: int):
 def debug_drop_load(n: int):
     """Diagnostic: the attention kernels' producers skip their n-th ring load (-1: off)."""
     lib().uaa_debug_drop_load(int(n))
+
+
+def debug_fail_launch(n: int = -1):
+    """Diagnostic: the n-th launch of every call that changes a :class:`PagedCache` is not made, and the call fails (-1:
+    off)."""
+    lib().uaa_debug_fail_launch(int(n))
 
 
 def debug_late_warp(warp: int = -1, ns: int = 0):

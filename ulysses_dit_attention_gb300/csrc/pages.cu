@@ -13,6 +13,7 @@
 // are launches: a fork of 8 sequences by 5, with one token more for each, is 35 MB in
 // 8 launches, 112 to 127 us, nearly all of it on the host.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cstdint>
 #include <mutex>
@@ -152,7 +153,10 @@ int check_pools(const char* fn, const uaa_pools* d, cudaStream_t stream) {
                      d->row_bytes);
   cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
   const cudaError_t e = cudaStreamIsCapturing(stream, &capture);
-  if (e != cudaSuccess) return set_error(UAA_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+  if (e != cudaSuccess) {
+    cudaGetLastError();  // reported here, not by a later call's launch
+    return set_error(UAA_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+  }
   if (capture != cudaStreamCaptureStatusNone)
     return set_error(UAA_ERR_UNSUPPORTED, "%s: not inside a graph capture: the pages are kept on the host", fn);
   return UAA_OK;
@@ -176,6 +180,7 @@ struct uaa_pages {
   std::vector<Move> moves;
   std::vector<unsigned> seen;  // the call that last named a sequence
   unsigned call = 0;
+  bool lost = false;  // a launch failed when the host's side had changed: the device's side is another one
 
   int need(int tokens) const { return (int)(((long long)tokens + page - 1) / page); }
   int take() {
@@ -218,8 +223,25 @@ struct uaa_pages {
 
 namespace {
 
+std::atomic<int> g_fail_launch{-1};  // diagnostic: the launch of every call that is not made and counts as failed
+
+// One launch of a call, its `index`-th.  What it returns is asked, not the last error: that may be an older call's.
+template <typename A>
+int send_one(const char* fn, void (*kernel)(A), dim3 grid, int threads, const A& a, int index, cudaStream_t s) {
+  if (index == g_fail_launch.load(std::memory_order_relaxed))
+    return set_error(UAA_ERR_CUDA, "%s: launch failed: left out by uaa_debug_fail_launch", fn);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+  if (e == cudaSuccess) return UAA_OK;
+  cudaGetLastError();
+  return set_error(UAA_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+}
+
 template <int N>
-int send_moves(const char* fn, const uaa_pools& d, const uaa_pages& p, const Move* m, int n, cudaStream_t s) {
+int send_moves(const char* fn, const uaa_pools& d, const uaa_pages& p, const Move* m, int n, int index, cudaStream_t s) {
   MoveArgs<N> a;
   a.k = static_cast<uint4*>(d.k);
   a.v = static_cast<uint4*>(d.v);
@@ -229,12 +251,12 @@ int send_moves(const char* fn, const uaa_pools& d, const uaa_pages& p, const Mov
   a.n = n;
   std::copy(m, m + n, a.m);
   const long long parts = (a.page + kCopy * kCopyThreads - 1) / (kCopy * kCopyThreads);
-  page_copy_kernel<N><<<dim3(n, (unsigned)std::min(parts, 64LL), 2 * d.layers), kCopyThreads, 0, s>>>(a);
-  return check_launch(fn);
+  return send_one(fn, page_copy_kernel<N>, dim3(n, (unsigned)std::min(parts, 64LL), 2 * d.layers), kCopyThreads, a, index, s);
 }
 
 template <int N>
-int send_edits(const char* fn, const uaa_pools& d, int32_t* starts, int32_t* seqs, const Edit* e, int n, cudaStream_t s) {
+int send_edits(const char* fn, const uaa_pools& d, int32_t* starts, int32_t* seqs, const Edit* e, int n, int index,
+               cudaStream_t s) {
   EditArgs<N> a;
   a.to[kTable] = d.table;
   a.to[kLens] = d.lens;
@@ -242,25 +264,34 @@ int send_edits(const char* fn, const uaa_pools& d, int32_t* starts, int32_t* seq
   a.to[kSeqs] = seqs;
   a.n = n;
   std::copy(e, e + n, a.e);
-  table_edit_kernel<N><<<(n + 7) / 8, 256, 0, s>>>(a);
-  return check_launch(fn);
+  return send_one(fn, table_edit_kernel<N>, dim3((n + 7) / 8), 256, a, index, s);
 }
 
-// The call's copies and table changes, enqueued.
-int send(const char* fn, const uaa_pages& p, const uaa_pools* d, int32_t* starts, int32_t* seqs, cudaStream_t s) {
+// The call's copies and table changes, enqueued.  The host's side has changed already: a launch that fails leaves the two
+// apart, and as the copies of shared pages may be among what is missing, the object takes no further call.
+int send(const char* fn, uaa_pages& p, const uaa_pools* d, int32_t* starts, int32_t* seqs, cudaStream_t s) {
   if (!d) return UAA_OK;
-  for (size_t i = 0; i < p.moves.size(); i += kMany) {
+  int index = 0;
+  for (size_t i = 0; i < p.moves.size(); i += kMany, ++index) {
     const int n = (int)std::min(p.moves.size() - i, (size_t)kMany);
     const Move* m = p.moves.data() + i;
-    if (int st = n <= kFew ? send_moves<kFew>(fn, *d, p, m, n, s) : send_moves<kMany>(fn, *d, p, m, n, s)) return st;
+    const int st = n <= kFew ? send_moves<kFew>(fn, *d, p, m, n, index, s) : send_moves<kMany>(fn, *d, p, m, n, index, s);
+    if (st) return p.lost = true, st;
   }
-  for (size_t i = 0; i < p.edits.size(); i += kMany) {
+  for (size_t i = 0; i < p.edits.size(); i += kMany, ++index) {
     const int n = (int)std::min(p.edits.size() - i, (size_t)kMany);
     const Edit* e = p.edits.data() + i;
-    if (int st = n <= kFew ? send_edits<kFew>(fn, *d, starts, seqs, e, n, s)
-                           : send_edits<kMany>(fn, *d, starts, seqs, e, n, s))
-      return st;
+    const int st = n <= kFew ? send_edits<kFew>(fn, *d, starts, seqs, e, n, index, s)
+                             : send_edits<kMany>(fn, *d, starts, seqs, e, n, index, s);
+    if (st) return p.lost = true, st;
   }
+  return UAA_OK;
+}
+
+int check_lost(const char* fn, const uaa_pages& p, const uaa_pools* d) {
+  if (d && p.lost)
+    return set_error(UAA_ERR_CUDA, "%s: a launch of an earlier call failed: the device's table is not the host's; "
+                     "destroy the cache", fn);
   return UAA_OK;
 }
 
@@ -331,6 +362,7 @@ extern "C" int uaa_pages_append(uaa_pages* p, const uaa_pools* pools, int n, con
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (st || (st = check_pools(fn, pools, s))) return st;
     std::lock_guard<std::mutex> lock(p->mu);
+    if ((st = check_lost(fn, *p, pools))) return st;
     p->begin();
     long long want = 0, total = 0, entries = 0;
     std::unordered_map<int, int> left;  // holders of a shared last page, less those that this call takes off it
@@ -410,6 +442,7 @@ extern "C" int uaa_pages_fork(uaa_pages* p, const uaa_pools* pools, int n, const
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (st || (st = check_pools(fn, pools, s))) return st;
     std::lock_guard<std::mutex> lock(p->mu);
+    if ((st = check_lost(fn, *p, pools))) return st;
     p->begin();
     size_t entries = 0;
     for (int i = 0; i < n; ++i) {
@@ -443,6 +476,7 @@ extern "C" int uaa_pages_truncate(uaa_pages* p, const uaa_pools* pools, int n, c
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (st || (st = check_pools(fn, pools, s))) return st;
     std::lock_guard<std::mutex> lock(p->mu);
+    if ((st = check_lost(fn, *p, pools))) return st;
     p->begin();
     for (int i = 0; i < n; ++i) {
       const int q = seqs[i];
@@ -475,6 +509,7 @@ extern "C" int uaa_pages_compact(uaa_pages* p, const uaa_pools* pools, uaa_strea
     int st = check_pools(fn, pools, s);
     if (st) return st;
     std::lock_guard<std::mutex> lock(p->mu);
+    if ((st = check_lost(fn, *p, pools))) return st;
     p->begin();
     const int used = p->pages - p->unused;
     std::unordered_map<int, size_t> to;  // page -> its move
@@ -508,6 +543,8 @@ extern "C" int uaa_pages_compact(uaa_pages* p, const uaa_pools* pools, uaa_strea
     return send(fn, *p, pools, nullptr, nullptr, s);
   });
 }
+
+extern "C" void uaa_debug_fail_launch(int n) { g_fail_launch.store(n < 0 ? -1 : n); }
 
 extern "C" int uaa_pages_row(uaa_pages* p, int seq, int* out, int most) {
   const char* fn = "uaa_pages_row";
