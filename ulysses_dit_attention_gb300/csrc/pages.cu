@@ -359,6 +359,8 @@ extern "C" int uaa_pages_append(uaa_pages* p, const uaa_pools* pools, int n, con
   const char* fn = "uaa_pages_append";
   return guarded(fn, [&] {
     int st = check_list(fn, p, n, seqs, counts);
+    if (!st && ((reinterpret_cast<uintptr_t>(starts) | reinterpret_cast<uintptr_t>(seqs_dev)) & 3u))
+      st = set_error(UAA_ERR_INVALID_ARG, "%s: starts or seqs_dev is not 4-byte aligned", fn);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (st || (st = check_pools(fn, pools, s))) return st;
     std::lock_guard<std::mutex> lock(p->mu);
