@@ -40,11 +40,6 @@ constexpr int kMmaWarp = 9;
 constexpr int kMmaWarp1 = 10;  // the dQ kernel's second issuer
 constexpr int kDkdvThreads = 320, kDqThreads = 352;
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<uint32_t*>(&v);
@@ -58,16 +53,6 @@ __device__ __forceinline__ void store_packed64(uint32_t taddr, const float (&x)[
 }
 // TMEM column of the A operand for K step kk when each half of the 128 columns lies packed at its own half's start.
 __device__ __forceinline__ uint32_t packed_a_col(int kk) { return kk < 4 ? kk * 8 : 64 + (kk - 4) * 8; }
-
-// 4-D tiled tensor store from shared memory (bulk-group completion).
-__device__ __forceinline__ void tma_store_4d(const void* smem_src, const CUtensorMap* map, int c0, int c1, int c2,
-                                             int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
-          reinterpret_cast<uint64_t>(map)),
-      "r"(smem_u32(smem_src)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-      : "memory");
-}
 
 // The way out of a gradient tile: this thread's half row (columns hf D / 2 ..) in 16-bit pieces, swizzled as a tensor copy
 // takes them.  A tile whose rows all exist leaves by one; of others each warp stores its 32 half rows, a row by D / 16 lanes.

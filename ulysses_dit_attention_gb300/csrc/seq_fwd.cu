@@ -88,22 +88,6 @@ struct FwdCtl {
 };
 static_assert(sizeof(FwdCtl) <= 512, "control block");
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// 4-D tiled tensor store from shared memory (bulk-group completion).
-__device__ __forceinline__ void tma_store_4d(const void* smem_src, const CUtensorMap* map, int c0, int c1, int c2,
-                                             int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
-          reinterpret_cast<uint64_t>(map)),
-      "r"(smem_u32(smem_src)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-      : "memory");
-}
-
 // The softmax warps take registers that the other four do not need: 256 x 200 + 128 x 96 of the 384 x 168 that the block is
 // launched with, which the host makes sure of (the softmax warps would wait for ever otherwise).  It keeps spills out of
 // their loop: 2048 tokens over 27280 keys 755 -> 729 us, 24 sequences in chunks 152 -> 145, 8192 tokens at D = 64 433 -> 425.
