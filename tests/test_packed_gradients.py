@@ -1,11 +1,11 @@
 """Gradients of packed attention over long sequences, whose items are cut several times, by their mean error.
 
 The bounds of each element (oracle/seqs.py) add up every rounding at its worst, which for hundreds of keys is a good part of
-the value.  Independent roundings add up by squares instead.  One to bf16 is uniform within half a step, at most 2^-8 of the
-value, so its mean square is at most (2^-8)^2 / 3 of the value's.  With normal inputs the terms of a sum are uncorrelated,
-and the sum of rounded terms is off by the same share of its own mean square.  There are at most three on the way to a
-result: of P or dS, of out where Delta = dout . out uses it, and of the result.  So the error's mean square is at most
-3 (2^-8)^2 / 3 of the result's: 2^-8.
+the value.  Independent roundings add up by squares instead.  One to bf16 is uniform within half a step, 2^-8 of the binade's
+lowest value; with mantissas x of density 1 / (x ln 2) its mean square is (2^-8)^2 / 3 times 3 / (8 ln 2), (0.425 * 2^-8)^2, of
+the value's.  With normal inputs the terms of a sum are uncorrelated, and a sum of rounded terms is off by the same share of
+its own mean square.  There are at most four on the way to a result: of dS, of P and of out where Delta = dout . out uses
+them, and of the result.  Together: (2 * 0.425 * 2^-8)^2, below (2^-8)^2.
 """
 import numpy as np
 import pytest
