@@ -2,14 +2,15 @@
 // is shared out stand in seq_shared.cuh).  No atomics: the same bits every time.
 //  1. seq_stats_kernel: Delta = rowsum(dO * O) and -L log2(e) of every row, in tiles
 //     of 128 rows as the others read them (row r of a tile: head r % g of token r / g).
-//  2. seq_dkdv_kernel: an item is a tile of 128 keys of one sequence and key head; it
+//  2. seq_dq_kernel: an item is a tile of query rows; it walks the key tiles that the
+//     rows read, with Q and dO in TMEM: S, dP, dQ += dS K.  Rows that read one key tile
+//     only get Delta = sum P dP, without the roundings of P and O.
+//  3. seq_dkdv_kernel: an item is a tile of 128 keys of one sequence and key head; it
 //     walks the tiles of query rows that read it:
 //        S^T = K Q^T,  P^T = exp2(S^T c - L log2 e),  dP^T = V dO^T,
 //        dS^T = P^T (dP^T - Delta),  dV += P^T dO,  dK += dS^T Q   (in TMEM)
-//     The rows of the g query heads that share the key head are rows of one tile, so
-//     their gradients add up in the accumulator.
-//  3. seq_dq_kernel: an item is a tile of query rows; it walks the key tiles that the
-//     rows read, with Q and dO in TMEM: S and dP once more, dQ += dS K.
+//     S and dP once more.  The rows of the g query heads that share the key head are
+//     rows of one tile, so their gradients add up in the accumulator.
 //  4. seq_bwd_join_kernel: items that were cut between two shares.
 // Seven products where five would do; the alternative, dQ by 32-bit reductions from
 // the dK/dV kernel, is slower and has no fixed order.
@@ -27,6 +28,8 @@
 // an item costs 5.5 steps beside its own: images of 300 to 1100 tokens, D = 64, 24
 // heads: 123 + 93 us at 20 %.  The rows' statistics: memory, 20 us for 215 MB.
 #include <math.h>
+
+#include <type_traits>
 
 #include "seq_shared.cuh"
 
@@ -162,7 +165,7 @@ __global__ void __launch_bounds__(256) seq_stats_kernel(const __grid_constant__ 
 }
 
 // ---------------------------------------------------------------------------
-// 2. dK / dV
+// 3. dK / dV
 template <int D>
 struct DkdvLayout {
   static constexpr int kTileBytes = 128 * D * 2;
@@ -275,7 +278,7 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (threadIdx.x == 0) x.w.first_kv[blockIdx.x] = share.from;
-  await_previous();  // the rows' statistics
+  await_previous();  // the rows' statistics, and the dQ kernel's corrections of them
   allow_next();
   const uint32_t tmem = ctl->tmem_base;
   const MmaGuard mg = mma_guard(ctx, sbase, L::kSmem, tmem, 512);  // debug builds' operand checks
@@ -623,7 +626,7 @@ __global__ void __launch_bounds__(kDkdvThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// 3. dQ
+// 2. dQ
 template <int D>
 struct DqLayout {
   // K and V in rings of their own: a K slot is freed only by dQ, late in a key tile's processing, a V slot already by dP.
@@ -636,8 +639,10 @@ struct DqLayout {
   static constexpr int kDO = kQ + kTileBytes;
   static constexpr int kCtl = kDO + kTileBytes;
   static constexpr int kKept = kCtl + 512;
-  static constexpr int kScratch = kKept + kKeptSeqs * 16;
-  static constexpr int kSmem = kScratch + kShareBytes;
+  static constexpr int kSeqs = D == 128 ? 32 : kKeptSeqs;  // as many as there is room for
+  static constexpr int kSums = kKept + kSeqs * 16;  // of the rows' two halves; find_share's scratch before
+  static constexpr int kSmem = kSums + 2 * 128 * 8;
+  static_assert(kShareBytes <= 2 * 128 * 8, "scratch");
   static_assert(kSmem <= 232448, "dQ shared memory exceeds the per-CTA limit");
 };
 
@@ -645,13 +650,16 @@ struct DqCtl {
   uint64_t bar_qdo_ready;
   uint64_t bar_kv_full[16], bar_kv_empty[16];
   uint64_t bar_s_full, bar_s_read, bar_dp_full, bar_ds_ready;
-  uint64_t bar_dq_done, bar_dq_free, bar_final[2], bar_dq_step, bar_tail, bar_out, bar_qd_full, bar_qd_free;
+  uint64_t bar_dq_done, bar_dq_free, bar_final[2], bar_dq_step, bar_tail, bar_out, bar_qd_full, bar_qd_free,
+      bar_sums;
   uint32_t tmem_base;
   int abort;
 };
 static_assert(sizeof(DqCtl) <= 512, "control block");
 
 using Rows = QueryRow<1>;
+// What a row's P may add up to beside one: the error of its scores and of lse.
+constexpr float kNearOne = 1.f / 1024;
 
 template <int D>
 __global__ void __launch_bounds__(kDqThreads, 1)
@@ -701,6 +709,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     mbar_init(&ctl->bar_out, kComputeThreads);
     mbar_init(&ctl->bar_qd_full, 1);
     mbar_init(&ctl->bar_qd_free, kComputeThreads);
+    mbar_init(&ctl->bar_sums, kComputeThreads);
     mbar_init(&ctl->bar_final[0], 1);
     mbar_init(&ctl->bar_final[1], 1);
     ctl->abort = 0;
@@ -716,8 +725,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     tmem_alloc(&ctl->tmem_base, 512);
     tmem_relinquish();
   }
-  const Share share = find_share<Rows, false, kDqThreads>(a, smem + L::kScratch, smem + L::kKept, x.w.seqs_q,
-                                                          ctx.status);
+  const Share share = find_share<Rows, false, kDqThreads, L::kSeqs>(a, smem + L::kSums, smem + L::kKept, x.w.seqs_q,
+                                                                    ctx.status);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -897,7 +906,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     bool ok = true;
     uint32_t g = 0, it = 0;
     if (s.rest) clear_rest(s.starts, s.B, s.T, x.dq, (long long)s.Hq * D, nullptr, 0, threadIdx.x, kComputeThreads);
-    await_previous();  // the rows' statistics, which the dK/dV kernel waited for before it let this one start
+    await_previous();  // the rows' statistics
+    uint32_t alone = 0;  // items of one key tile
     Walk<Rows> w(share);
     while (ok && w.next(a)) {
       const int tok = w.at.p * a.TT + rt, hq = w.at.h * a.g + rh;
@@ -937,21 +947,24 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         tc_fence_before();
         mbar_arrive(&ctl->bar_qdo_ready);
       }
-      const size_t prow = ((size_t)w.at.h * x.w.slots + first_slot(a, w.q.q0, w.at.b) + w.at.p) * 128 + row;
-      const float nl2 = x.w.nl2[prow];
-      const float dl = x.w.delta[prow];
-      for (int i = 0; i < ntl; ++i) {
+      auto prow = [&] { return ((size_t)w.at.h * x.w.slots + first_slot(a, w.q.q0, w.at.b) + w.at.p) * 128 + row; };
+      const float nl2 = x.w.nl2[prow()];
+      float dl = x.w.delta[prow()];
+      // A key tile; kAlone: the only one that the rows read (a body of its own: as a branch of the other one images of 300 to
+      // 1100 tokens, which have none of these, take 326 us a step instead of 320).
+      auto tile = [&](auto only, int i) {
+        constexpr bool kAlone = decltype(only)::value;
         const int j = w.j0 + i;
         // K and V of the next tile are read by the products that this tile's s_read and ds_ready release; they normally
         // land long before, and waiting for them here keeps these waits off the issuing threads.
-        if (i + 1 < ntl) {
+        if (!kAlone && i + 1 < ntl) {
           bool okw = wait_or_abort(&ctl->bar_kv_full[kslot(g + 1)], kpar(g + 1), ctx, ctl);
           if (okw) okw = wait_or_abort(&ctl->bar_kv_full[vslot(g + 1)], vpar(g + 1), ctx, ctl);
           ok = __all_sync(0xffffffffu, okw);
-          if (!ok) break;
+          if (!ok) return;
         }
         ok = __all_sync(0xffffffffu, wait_or_abort(&ctl->bar_s_full, g & 1, ctx, ctl));
-        if (!ok) break;
+        if (!ok) return;
         tc_fence_after();
         float p[64];
         tmem_ld32x2(tl + kColS + 64 * hf, tl + kColS + 64 * hf + 32, p);
@@ -970,8 +983,37 @@ __global__ void __launch_bounds__(kDqThreads, 1)
           }
         }
         ok = __all_sync(0xffffffffu, wait_or_abort(&ctl->bar_dp_full, g & 1, ctx, ctl));
-        if (!ok) break;
+        if (!ok) return;
         tc_fence_after();
+        if constexpr (kAlone) {
+          // Delta = sum P dP, from both halves of the row, which the dK/dV kernel reads too.  Where few keys are read, what
+          // dout . out is off by (the roundings of P and of out) shows in dS: dQ and dK of sequences of 2, 9 and 40 tokens,
+          // causal, are off by 0.0044, 0.0033 and 0.0029 with it and by 0.0024 without; of 32 sequences of 60 to 128 tokens
+          // a step takes 124 us instead of 120.  (P that do not add up to one are of a call over some of the keys with the
+          // lse of all of them, or of a checkpoint: dout . out is their Delta.)
+          float sum[4] = {}, both[4] = {};  // of every fourth key: short chains
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float y[32];
+            tmem_ld32(tl + kColDP + 64 * hf + 32 * e, y);
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (32 * e + c < left) {
+                sum[c & 3] += p[32 * e + c];
+                both[c & 3] = fmaf(p[32 * e + c], y[c], both[c & 3]);
+              }
+          }
+          float2* sums = reinterpret_cast<float2*>(smem + L::kSums) + row;
+          sums[hf * 128] = make_float2((sum[0] + sum[1]) + (sum[2] + sum[3]), (both[0] + both[1]) + (both[2] + both[3]));
+          mbar_arrive(&ctl->bar_sums);
+          ok = __all_sync(0xffffffffu, wait_or_abort(&ctl->bar_sums, alone & 1, ctx, ctl));
+          if (!ok) return;
+          ++alone;
+          if (fabsf(sums[0].x + sums[128].x - 1.f) < kNearOne) {
+            dl = sums[0].y + sums[128].y;
+            if (hf == 0) x.w.delta[prow()] = dl;
+          }
+        }
         float dp[64];
         tmem_ld32x2(tl + kColDP + 64 * hf, tl + kColDP + 64 * hf + 32, dp);
         {
@@ -992,6 +1034,11 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         tc_fence_before();
         mbar_arrive(&ctl->bar_ds_ready);
         ++g;
+      };
+      if (ntl == 1 && !w.part) {
+        tile(std::true_type{}, 0);
+      } else {
+        for (int i = 0; ok && i < ntl; ++i) tile(std::false_type{}, i);
       }
       if (!ok) break;
       // epilogue: dQ = scale (dS K)
@@ -1182,11 +1229,11 @@ int launch_bwd(const char* fn, const BwdArgs& x, cudaStream_t stream) {
   const float c = s.scale * kLog2e;
   seq_stats_kernel<D><<<dim3(x.w.slots, s.Hk), 256, 0, stream>>>(x);
   if ((st = check_launch(fn))) return st;
-  if ((st = launch_after(fn, seq_dkdv_kernel<D>, dim3(ctas), kDkdvThreads, DkdvLayout<D>::kSmem, stream, mq, mk, mv, md, ok,
-                         ov, x, c, ctx)))
-    return st;
   if (some && (st = launch_after(fn, seq_dq_kernel<D>, dim3(ctas), kDqThreads, DqLayout<D>::kSmem, stream, mq, md, mk, mv,
                                  oq, x, c, ctx)))
+    return st;
+  if ((st = launch_after(fn, seq_dkdv_kernel<D>, dim3(ctas), kDkdvThreads, DkdvLayout<D>::kSmem, stream, mq, mk, mv, md, ok,
+                         ov, x, c, ctx)))
     return st;
   if (!some) return UAA_OK;  // nothing was cut: no tile has an inner one
   return launch_after(fn, seq_bwd_join_kernel<D>, dim3(ctas - 1, 4, 2), 256, 0, stream, x, ctas, ctx);
