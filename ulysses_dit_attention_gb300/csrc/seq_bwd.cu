@@ -991,6 +991,9 @@ __global__ void __launch_bounds__(kDqThreads, 1)
           // causal, are off by 0.0044, 0.0033 and 0.0029 with it and by 0.0024 without; of 32 sequences of 60 to 128 tokens
           // a step takes 124 us instead of 120.  (P that do not add up to one are of a call over some of the keys with the
           // lse of all of them, or of a checkpoint: dout . out is their Delta.)
+          // A softmax over one key is constant: with P = 1 Delta is dP itself, so dS is 0, here and in the dK/dV kernel, whose dP
+          // is the same sum of the same products.
+          if (lim == 1 && hf == 0 && fabsf(p[0] - 1.f) < kNearOne) p[0] = 1.f;
           float sum[4] = {}, both[4] = {};  // of every fourth key: short chains
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
