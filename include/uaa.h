@@ -480,7 +480,8 @@ int uaa_attn_packed_fwd(const uaa_seqs* args, void* workspace, size_t workspace_
 int uaa_attn_paged_fwd(const uaa_seqs* args, void* workspace, size_t workspace_bytes, uaa_stream_t stream);
 
 /* Gradients of uaa_attn_packed_fwd (bf16), deterministic (no atomics).
- *   args           : the forward's, with its out and lse
+ *   args           : the forward's, with its out and lse (or with some of the keys only, and the out and lse of all of them:
+ *                    a part of dq, and dk and dv of those keys)
  *   dout           : device, contiguous (T, Hq, D)
  *   dq; dk, dv     : device, contiguous (T, Hq, D); (Tk, Hk, D), written for the tokens of the sequences; they must not
  *                    overlap the inputs nor each other
@@ -502,7 +503,9 @@ int uaa_attn_packed_bwd(const uaa_seqs* args, const void* dout, void* dq, void* 
  * refused (UAA_ERR_CUDA), and the object is to be destroyed and the pools, table and lens given up with it.  The calls
  * are made outside of graph captures (a captured one would be replayed without the host's part); the attention and
  * write calls, which read table and lens on the device, may be captured.  One thread at a time per object is not
- * required: calls lock. */
+ * required: calls lock.  The lock keeps the host's side in order; the device's follows the order of the streams, so the
+ * calls for one object, and the attention and write calls over its table, go to one stream or to streams that wait for
+ * one another. */
 typedef struct uaa_pages uaa_pages;
 
 /* The device's side; `pools` NULL in the calls below: the host's side alone. */

@@ -926,6 +926,8 @@ def attn_packed_bwd(q, k, v, out, dout, lse, starts, starts_k=None, causal=True,
                     workspace=None):
     """``uaa_attn_packed_bwd``: the gradients ``(dq, dk, dv)`` of :func:`attn_packed_fwd` (bf16).
 
+    ``k`` and ``v`` may be some of the keys that ``out`` and ``lse`` are of: then ``dq`` is a part, ``dk`` and ``dv`` are those
+    keys'.
     An infinity or a NaN of a token may show in the gradients of any token of its own sequence; other sequences' stay
     clean."""
     if out is None or lse is None:
@@ -1063,7 +1065,8 @@ class PagedCache:
     (``UAA_ERR_NO_PAGES`` where pages are short).  The device's side is changed on the current stream, by small
     launches that hold their data; these calls are made outside of graph captures, between replays.  Should such a launch
     fail (``UAA_ERR_CUDA``), the device has not followed the host: the cache refuses further changes and is to be given
-    up.  A cache is not copied or pickled.
+    up.  A cache is not copied or pickled.  Calls from several threads lock the host's side; the device's follows the order of
+    the streams, so a cache is used on one stream or on streams that wait for one another.
 
     A step of a model::
 

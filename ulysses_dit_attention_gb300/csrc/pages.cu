@@ -11,7 +11,7 @@
 // GB300: 24 sequences that end, 24 others written to their places and the rest closed
 // up, 921 MB in four layers of 8 heads of 128: 175 us, 5.3 TB/s.  Calls of a few pages
 // are launches: a fork of 8 sequences by 5, with one token more for each, is 35 MB in
-// 8 launches, 112 to 127 us, nearly all of it on the host.
+// 9 launches, 116 to 131 us, nearly all of it on the host.
 #include <algorithm>
 #include <atomic>
 #include <climits>

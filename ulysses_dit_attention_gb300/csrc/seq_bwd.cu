@@ -4,7 +4,8 @@
 //     of 128 rows as the others read them (row r of a tile: head r % g of token r / g).
 //  2. seq_dq_kernel: an item is a tile of query rows; it walks the key tiles that the
 //     rows read, with Q and dO in TMEM: S, dP, dQ += dS K.  Rows that read one key tile
-//     only get Delta = sum P dP, without the roundings of P and O.
+//     only get Delta = sum P dP, without the roundings of P and O (with many keys Delta
+//     is small beside dP, and so is what they make of it).
 //  3. seq_dkdv_kernel: an item is a tile of 128 keys of one sequence and key head; it
 //     walks the tiles of query rows that read it:
 //        S^T = K Q^T,  P^T = exp2(S^T c - L log2 e),  dP^T = V dO^T,
@@ -24,9 +25,9 @@
 // time a CTA: 8192 x 8192, 24 heads, D = 128: 1990 us, by the seven products 1450
 // TFLOP/s; 8191 tokens, 24 / 8 heads, causal: dK/dV 541 us (a step 1.65 us for 1.1 us
 // of products), dQ 470.  The matrix pipe is active for 58 % (dK/dV) and 45 % (dQ) on
-// texts of 326 to 4100 tokens (226 + 215 us).  Short sequences: filling and draining,
+// texts of 326 to 4100 tokens (224 + 215 us).  Short sequences: filling and draining,
 // an item costs 5.5 steps beside its own: images of 300 to 1100 tokens, D = 64, 24
-// heads: 123 + 93 us at 20 %.  The rows' statistics: memory, 20 us for 215 MB.
+// heads: 124 + 96 us at 20 %.  The rows' statistics: memory, 22 us for 108 MB.
 #include <math.h>
 
 #include <type_traits>
