@@ -4,8 +4,8 @@ off by shows in dS = P (dP - Delta).
 The tolerance, by mean squares.  A value rounded to bf16 is off by at most half a step, evenly spread: 2^-8 / sqrt(3) of its
 binade's lowest value, so with mantissas x in [1, 2) of density 1 / (x ln 2) the mean square is (2^-8)^2 / 3 times the
 integral of 1 / (x^3 ln 2), 3 / (8 ln 2), which is (0.4247 * 2^-8)^2 of the value's.  dQ and dK have two such roundings, of
-dS and of the result: sqrt(2) * 0.4247 * 2^-8 = 0.00235.  A tenth more is for samples that are not spread like that.  (The
-roundings of P and of out within Delta = dout . out would make 0.0044 of it for two keys and 0.0027 for a hundred.)
+dS and of the result: sqrt(2) * 0.4247 * 2^-8 = 0.00235.  A tenth more is for samples that are not spread like that.  (With
+the roundings of P and of out within Delta = dout . out the kernels had 0.0037 for two tokens and 0.0027 for forty, causal.)
 """
 import numpy as np
 import pytest
